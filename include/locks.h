@@ -34,7 +34,9 @@
  *    library allocates nothing, frees nothing and never synchronises the
  *    stream (except locks_get_device_error, which reads back one word).
  *  - Element types: keys, values, queries, outputs and summaries are bf16
- *    (raw 16-bit patterns), lengths and indices int32, scores float32.
+ *    (raw 16-bit patterns), lengths and indices int32, scores float32.  The
+ *    cache's pages may hold keys and values in 4 bits instead
+ *    (locks_cache_t.kv_format); every call that reads a cache takes both.
  *  - Supported sizes: head_dim d = 128, page_size P = 64 or 16 (the
  *    explainer's §2 "Kernmechanisme" gives a page size of 16), group size
  *    G = num_q_heads / num_kv_heads in 1..16, summary rank r even in 2..16
@@ -83,6 +85,7 @@ typedef enum {
 #define LOCKS_DEVERR_LENGTHS     0x4  /* seq_len > max_pages * P or n_summarized > seq_len / P (clamped) */
 #define LOCKS_DEVERR_PAGE_ID     0x8  /* builder page id outside [0, pages_total) */
 #define LOCKS_DEVERR_TIMEOUT     0x10 /* a bounded wait on a TMA copy gave up (should never happen) */
+#define LOCKS_DEVERR_POSITION    0x20 /* a token's position lies outside the rotation table (lockskv.h) */
 
 #define LOCKS_DTYPE_BF16 0
 #define LOCKS_DTYPE_F32 1
@@ -95,6 +98,14 @@ typedef enum {
 #define LOCKS_Q4_BLOCK_BYTES(r, P) ((((72 * (r)) + ((P) * (r)) + 132) + 15) / 16 * 16)
 #define LOCKS_Q4_PAGE_HEAD_BYTES(r) LOCKS_Q4_BLOCK_BYTES(r, 64)
 
+/* Formats of a cache's pages (locks_cache_t.kv_format). */
+#define LOCKS_KV_BF16 0
+#define LOCKS_KV_Q4 1
+
+/* Bytes of one page-head of a LOCKS_KV_Q4 cache (keys and values together,
+ * head_dim 128): 144 per token, 28% of the 512 of a bf16 token. */
+#define LOCKS_KV_Q4_BLOCK_BYTES(P) (144 * (P))
+
 /* Paged KV cache.  K and V pools hold whole pages for all KV heads:
  *   k_pool, v_pool  bf16 [pages_total][num_kv_heads][page_size][head_dim]
  *                   (one page-head = P x d contiguous, 16 KiB at P=64, d=128,
@@ -106,7 +117,32 @@ typedef enum {
  *   n_summarized    int32 [batch]: leading full pages whose summaries are
  *                   valid; pages from n_summarized on (full or partial) form
  *                   the open tail and are always attended.  May be NULL for
- *                   calls that do not select (dense decode, builder). */
+ *                   calls that do not select (dense decode, builder).
+ *   kv_format       LOCKS_KV_BF16 (0): the pools above.
+ *                   LOCKS_KV_Q4: k_pool points to one block of
+ *                   LOCKS_KV_Q4_BLOCK_BYTES(page_size) bytes per page-head,
+ *                   [pages_total][num_kv_heads][bytes], base 16-byte aligned,
+ *                   with the page's keys and values; v_pool is unused.  Each
+ *                   32 consecutive dimensions (32j .. 32j+31) of a token's key
+ *                   and of its value have a half-precision scale s >= 0 and 32
+ *                   codes in [-7, 7], stored as code + 8; the element is
+ *                   s * code.  Token t of the page, dimension d, j = d/32:
+ *                     byte 0      key codes, 64 bytes per token: element d in
+ *                                 the little-endian 32-bit word at 64 t +
+ *                                 16 ((d%32)/8) + 4 j, bits
+ *                                 4((d%8)/2) + 16(d%2) .. +3
+ *                     byte 64P    key scales, 8 bytes per token: s_j at 8 t + 2 j
+ *                     byte 72P    value codes, 1024 bytes per 16 tokens; with
+ *                                 u = t%16: element d in the little-endian
+ *                                 16-bit word at 1024 (t/16) + 512 (u/8) +
+ *                                 64 ((d%32)/4) + 16 ((u%8)/2) + 4 j +
+ *                                 2 (u%2), bits 4(d%4) .. +3
+ *                     byte 136P   value scales, 128 bytes per 16 tokens: s_j at
+ *                                 128 (t/16) + 32 ((u%8)/2) + 16 (u/8) + 4 j +
+ *                                 2 (u%2)
+ *                   (the orders put the pieces one lane of a matrix
+ *                   instruction needs side by side).  A NaN scale makes its 32
+ *                   elements NaN. */
 typedef struct locks_cache {
   const void* k_pool;
   const void* v_pool;
@@ -119,6 +155,7 @@ typedef struct locks_cache {
   int32_t page_size;
   int32_t pages_total;
   int32_t max_pages;
+  int32_t kv_format;
 } locks_cache_t;
 
 /* Resident page summaries, indexed by PHYSICAL page like the pools:
@@ -210,8 +247,9 @@ LOCKS_API locks_status_t locks_workspace_init(void* ws, size_t bytes, void* stre
  * singular value <= 1e-6 sigma_1 are zero.  page_ids: device int32 [n];
  * an id outside [0, pages_total) is skipped and, when `ws` is given, sets
  * LOCKS_DEVERR_PAGE_ID.  `ws` may be NULL (then such errors are silent).
- * Reads k_pool only; block_table, seq_lens and v_pool are not used.
- * Capturable. */
+ * Reads k_pool only; block_table, seq_lens and v_pool are not used.  Of a
+ * LOCKS_KV_Q4 page the keys summarised are the stored ones, s * code rounded
+ * to bf16.  Capturable. */
 LOCKS_API locks_status_t locks_build_summaries(const locks_cache_t* cache, locks_summary_t* summary,
                                      const int32_t* page_ids, int32_t n,
                                      void* ws, size_t ws_bytes, void* stream);

@@ -24,7 +24,8 @@ LIB = os.path.join(OUT_DIR, "liblocks.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "--expt-relaxed-constexpr"]
-SOURCES = ["api.cu", "scan.cu", "topk.cu", "attend.cu", "build.cu", "static_ws.cu"]
+SOURCES = ["api.cu", "scan.cu", "topk.cu", "attend.cu", "build.cu", "static_ws.cu", "attend_q4.cu",
+           "kv_append.cu", "prompt.cu"]
 
 
 def nvcc() -> str:
@@ -48,7 +49,8 @@ def build(verbose: bool = False, extra_flags=(), force: bool = False) -> str:
     is newer than every source and header."""
     os.makedirs(OUT_DIR, exist_ok=True)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(os.path.dirname(HERE), "include", "locks.h"))
+    include = os.path.join(os.path.dirname(HERE), "include")
+    deps += [os.path.join(include, f) for f in os.listdir(include)]
     if not force and os.path.exists(LIB):
         lib_t = os.path.getmtime(LIB)
         if all(os.path.getmtime(d) < lib_t for d in deps):

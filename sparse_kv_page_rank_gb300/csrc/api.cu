@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/locks.h"
+#include "../../include/lockskv.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -37,20 +38,26 @@ struct Plan {
   int tk_chunk = 0, n_tk = 0;
   size_t tk_keys = 0;
   int sparse_cluster = 1, dense_cluster = 1, dense_nc = 1, lse_splits = 1;
+  // LOCKS_KV_Q4 caches: clusters, CTAs and tiles per turn of attend_q4.cu
+  int q4_sparse_cluster = 1, q4_sparse_tiles = 1, q4_dense_cluster = 1, q4_dense_nc = 1, q4_dense_tiles = 1;
   bool fused = false;     // decode step as scan + one attention kernel that selects the pages itself
   int fused_cluster = 1;
   size_t off_err = 0, off_cnt_tk = 0, off_cnt_att = 0, off_shat = 0, off_part = 0, off_ckey = 0,
          off_cidx = 0, off_sel = 0, off_selcnt = 0, off_selphys = 0, off_pml = 0, off_po = 0, total = 0;
 };
 
+bool is_q4(const locks_cache_t* c) { return c->kv_format == LOCKS_KV_Q4; }
+
 locks_status_t check_cache(const locks_cache_t* c, bool need_kv) {
   if (!c) return LOCKS_ERR_INVALID_ARG;
   if (c->batch <= 0 || c->num_kv_heads <= 0 || c->pages_total <= 0 || c->max_pages <= 0)
     return LOCKS_ERR_INVALID_ARG;
   if (c->head_dim != kHeadDim || (c->page_size != kPage && c->page_size != 16)) return LOCKS_ERR_UNSUPPORTED;
+  if (c->kv_format != LOCKS_KV_BF16 && c->kv_format != LOCKS_KV_Q4) return LOCKS_ERR_INVALID_ARG;
   if (need_kv) {
-    if (!c->k_pool || !c->v_pool || !c->block_table || !c->seq_lens) return LOCKS_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(c->k_pool) | reinterpret_cast<uintptr_t>(c->v_pool)) & 15)
+    const void* v_pool = is_q4(c) ? c->k_pool : c->v_pool;  // a 4-bit block holds both
+    if (!c->k_pool || !v_pool || !c->block_table || !c->seq_lens) return LOCKS_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(c->k_pool) | reinterpret_cast<uintptr_t>(v_pool)) & 15)
       return LOCKS_ERR_INVALID_ARG;
   }
   // TMA row coordinate and 32-bit page-head offsets
@@ -87,6 +94,41 @@ locks_status_t check_summary(const locks_summary_t* s, bool for_scan) {
 
 float scale_of(const locks_params_t* p) {
   return p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)kHeadDim);
+}
+
+// Launch shapes of attend_q4.cu.  A warp takes 64 tokens at a time where a CTA has
+// at least two turns of them for its seven warps, else 16 tokens, so that a few
+// pages still keep every warp busy.
+constexpr long long kQ4WholeSlots = 14;
+
+void plan_q4(const locks_cache_t* c, Plan& pl, int sms, long long max_tiles, int ppt) {
+  const int P = c->page_size;
+  const long long BH = pl.BH, resident = (long long)attend_q4_ctas_per_sm(pl.G) * sms;
+  auto tiles_for = [](long long slots_per_cta) { return slots_per_cta >= kQ4WholeSlots ? 4 : 1; };
+  {
+    // page list: one cluster per problem, the largest with which all are resident at once
+    const long long slots = ((long long)pl.k_max + 2 + ppt - 1) / ppt;
+    int cs = attend_q4_max_cluster(kAttendSparse, pl.G, P, 1);
+    while (cs > 1 && (cs > slots || BH > attend_q4_active_clusters(kAttendSparse, pl.G, P, 1, cs))) cs /= 2;
+    pl.q4_sparse_cluster = cs;
+    pl.q4_sparse_tiles = tiles_for((slots + cs - 1) / cs);
+  }
+  {
+    // every page: the (cluster, clusters per problem) with the most CTAs in one
+    // wave, none with less than two slots; among equals the larger cluster
+    const int cs_max = attend_q4_max_cluster(kAttendDense, pl.G, P, 4);
+    const long long want = std::max<long long>(1, std::min<long long>(resident / BH, (max_tiles + 1) / 2));
+    long long best = 0;
+    for (int cs = cs_max; cs >= 1; cs /= 2) {
+      const long long nc = want / cs;
+      if (nc >= 1 && cs * nc > best) {
+        best = cs * nc;
+        pl.q4_dense_cluster = cs;
+        pl.q4_dense_nc = (int)nc;
+      }
+    }
+    pl.q4_dense_tiles = tiles_for((max_tiles + best - 1) / best);
+  }
 }
 
 Plan make_plan(const locks_cache_t* c, const locks_params_t* p) {
@@ -170,7 +212,7 @@ Plan make_plan(const locks_cache_t* c, const locks_params_t* p) {
     // problem count (GB300: 8K context with 256 problems, 50.3 us with the
     // separate top-k and 52.0 us fused; 32K with 64 problems, 34.4 and 37.5;
     // 128K with 8 problems, 23.7 and 29.4).
-    if (P == kPage && pl.k_max <= kFusedMaxK && (p->flags & LOCKS_FLAG_FUSED)) {
+    if (P == kPage && pl.k_max <= kFusedMaxK && (p->flags & LOCKS_FLAG_FUSED) && !is_q4(c)) {
       const int cs_max = attend_max_cluster(kAttendFused, P);
       const long long need = ((long long)c->max_pages + kAttendThreads - 1) / kAttendThreads;
       int csf = 1;
@@ -183,12 +225,14 @@ Plan make_plan(const locks_cache_t* c, const locks_params_t* p) {
       }
     }
   }
+  if (is_q4(c)) plan_q4(c, pl, sms, max_tiles, ppt);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     size_t o = off;
     off = align_up(off + std::max<size_t>(bytes, 1));
     return o;
   };
+  const int nc = is_q4(c) ? pl.q4_dense_nc : pl.dense_nc;
   pl.off_err = take(sizeof(int));
   pl.off_cnt_tk = take(sizeof(unsigned) * BH);
   pl.off_cnt_att = take(sizeof(unsigned) * BH);
@@ -199,8 +243,8 @@ Plan make_plan(const locks_cache_t* c, const locks_params_t* p) {
   pl.off_sel = take(sizeof(int32_t) * BH * std::max(pl.k_max, 1));
   pl.off_selcnt = take(sizeof(int32_t) * BH);
   pl.off_selphys = take(sizeof(int32_t) * BH * std::max(pl.k_max, 1));
-  pl.off_pml = take(sizeof(float2) * BH * pl.dense_nc * pl.G);
-  pl.off_po = take(sizeof(float) * BH * pl.dense_nc * pl.G * kHeadDim);
+  pl.off_pml = take(sizeof(float2) * BH * nc * pl.G);
+  pl.off_po = take(sizeof(float) * BH * nc * pl.G * kHeadDim);
   pl.total = off;
   return pl;
 }
@@ -315,11 +359,6 @@ locks_status_t run_select(const locks_cache_t* c, const locks_summary_t* s, cons
 locks_status_t run_attend(const locks_cache_t* c, const locks_params_t* p, const Plan& pl, const void* q,
                           int32_t* sel, int32_t* selcnt, void* out, float* lse, float* page_lse,
                           void* ws, int mode, cudaStream_t st, bool inputs_early = false) {
-  CUtensorMap tk, tv;
-  std::memset(&tk, 0, sizeof(tk));
-  std::memset(&tv, 0, sizeof(tv));
-  if (!encode_pool(&tk, c->k_pool, c)) return LOCKS_ERR_CUDA;
-  if (mode != kAttendPageLse && !encode_pool(&tv, c->v_pool, c)) return LOCKS_ERR_CUDA;
   AttendArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.block_table = c->block_table;
@@ -384,7 +423,92 @@ locks_status_t run_attend(const locks_cache_t* c, const locks_params_t* p, const
   }
 #endif
   a.page_size = c->page_size;
+  if (is_q4(c)) {
+    int tiles = 4;
+    if (mode == kAttendSparse) {
+      a.cluster = a.n_splits = pl.q4_sparse_cluster;
+      tiles = pl.q4_sparse_tiles;
+    } else if (mode == kAttendDense) {
+      a.cluster = pl.q4_dense_cluster;
+      a.n_splits = pl.q4_dense_cluster * pl.q4_dense_nc;
+      tiles = pl.q4_dense_tiles;
+    }
+    return cuda_status(launch_attend_q4(a, mode, tiles, st));
+  }
+  CUtensorMap tk, tv;
+  std::memset(&tk, 0, sizeof(tk));
+  std::memset(&tv, 0, sizeof(tv));
+  if (!encode_pool(&tk, c->k_pool, c)) return LOCKS_ERR_CUDA;
+  if (mode != kAttendPageLse && !encode_pool(&tv, c->v_pool, c)) return LOCKS_ERR_CUDA;
   return cuda_status(launch_attend(a, tk, tv, mode, st, true));
+}
+
+locks_status_t check_tokens(const locks_cache_t* c, const lockskv_tokens_t* t) {
+  if (!t || t->total < 0 || t->max_tokens < 0) return LOCKS_ERR_INVALID_ARG;
+  if (!t->cu_tokens && (t->total != c->batch || t->max_tokens > 1)) return LOCKS_ERR_INVALID_ARG;
+  return LOCKS_OK;
+}
+
+// bf16 token rows: 16-byte aligned, `stride` elements apart, `row` elements long.
+locks_status_t check_rows(const void* p, int64_t stride, int64_t row) {
+  if ((reinterpret_cast<uintptr_t>(p) & 15) || stride < row || (stride & 7)) return LOCKS_ERR_INVALID_ARG;
+  return LOCKS_OK;
+}
+
+// A workspace that only holds the error word (or none).
+locks_status_t check_err_ws(void* ws, size_t bytes) {
+  if (ws && (bytes < sizeof(int) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))) return LOCKS_ERR_WORKSPACE;
+  return LOCKS_OK;
+}
+
+// Launch shape and workspace of lockskv_prompt_attend.
+constexpr long long kPromptCounters = 1024;
+struct PromptPlan {
+  int n_qtiles = 1, n_splits = 1;
+  size_t off_counters = 0, off_ml = 0, off_o = 0, total = 0;
+};
+
+// Tiles of 2 * (128 / G) tokens; where there are fewer of them than SMs, the keys
+// are cut as well, down to about two blocks of 128 per CTA.
+locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, const lockskv_tokens_t* t, PromptPlan* pl) {
+  const int G = p->num_q_heads / c->num_kv_heads, per_cta = 2 * (128 / G);
+  const long long BH = (long long)c->batch * c->num_kv_heads;
+  pl->n_qtiles = std::max(1, (t->max_tokens + per_cta - 1) / per_cta);
+  if (pl->n_qtiles > 65535) return LOCKS_ERR_UNSUPPORTED;
+  const long long ctas = BH * pl->n_qtiles, sms = device_sm_count();
+  const long long blocks = ((long long)c->max_pages * c->page_size + 127) / 128;
+  pl->n_splits = (int)std::max<long long>(1, std::min<long long>(sms / ctas, (blocks + 1) / 2));
+  if (BH * pl->n_splits > 0x7fffffffLL) return LOCKS_ERR_UNSUPPORTED;
+  // The error word, then the counters (problems are split only while there are at
+  // most half as many as SMs), in the same place for every shape: one workspace
+  // serves calls of different lengths, whose partial results never lie on a counter.
+  size_t off = kAlign;
+  if (ctas > kPromptCounters) pl->n_splits = 1;
+  const size_t parts = pl->n_splits > 1 ? (size_t)ctas * pl->n_splits * 256 : 0;
+  pl->off_counters = off;
+  off = align_up(off + sizeof(unsigned) * kPromptCounters);
+  pl->off_ml = off;
+  off = align_up(off + sizeof(float2) * parts);
+  pl->off_o = off;
+  pl->total = align_up(off + sizeof(float) * parts * kHeadDim);
+  return LOCKS_OK;
+}
+
+KvTokenArgs token_args(const locks_cache_t* c, const lockskv_tokens_t* t, void* ws) {
+  KvTokenArgs a;
+  a.cu_tokens = t->cu_tokens;
+  a.block_table = c->block_table;
+  a.seq_lens = c->seq_lens;
+  a.err = static_cast<int*>(ws);
+  a.batch = c->batch;
+  a.num_kv_heads = c->num_kv_heads;
+  a.max_pages = c->max_pages;
+  a.pages_total = c->pages_total;
+  a.page_size = c->page_size;
+  a.total = t->total;
+  a.max_tokens = t->max_tokens;
+  a.q4 = is_q4(c) ? 1 : 0;
+  return a;
 }
 
 }  // namespace
@@ -444,6 +568,7 @@ locks_status_t locks_build_summaries(const locks_cache_t* cache, locks_summary_t
   a.format = summary->dtype;
   a.err = ws ? static_cast<int*>(ws) : nullptr;  // the error word is at offset 0 of every workspace
   a.page_size = cache->page_size;
+  a.kv_q4 = is_q4(cache) ? 1 : 0;
   return cuda_status(launch_build(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -568,6 +693,128 @@ locks_status_t locks_get_device_error(void* ws, int32_t* code, void* stream) {
   if (cudaMemsetAsync(ws, 0, sizeof(int), s) != cudaSuccess) return LOCKS_ERR_CUDA;
   *code = v;
   return v ? LOCKS_ERR_DEVICE : LOCKS_OK;
+}
+
+locks_status_t lockskv_append(const locks_cache_t* cache, const lockskv_tokens_t* tokens,
+                              const lockskv_append_t* ap, void* ws, size_t ws_bytes, void* stream) {
+  locks_status_t st = check_cache(cache, true);
+  if (st != LOCKS_OK) return st;
+  if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
+  if ((st = check_err_ws(ws, ws_bytes)) != LOCKS_OK) return st;
+  if (!ap || !ap->k || !ap->v || (ap->q == nullptr) != (ap->q_out == nullptr)) return LOCKS_ERR_INVALID_ARG;
+  const int64_t kv_row = (int64_t)cache->num_kv_heads * kHeadDim;
+  if ((st = check_rows(ap->k, ap->k_stride, kv_row)) != LOCKS_OK) return st;
+  if ((st = check_rows(ap->v, ap->v_stride, kv_row)) != LOCKS_OK) return st;
+  if (ap->q) {
+    if (ap->num_q_heads <= 0) return LOCKS_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)ap->num_q_heads * kHeadDim;
+    if ((st = check_rows(ap->q, ap->q_stride, q_row)) != LOCKS_OK) return st;
+    if ((st = check_rows(ap->q_out, ap->q_out_stride, q_row)) != LOCKS_OK) return st;
+    if (ap->q == ap->q_out && ap->q_stride != ap->q_out_stride) return LOCKS_ERR_INVALID_ARG;
+  }
+  if (ap->rotary_dim < 0) return LOCKS_ERR_INVALID_ARG;
+  if (ap->rotary_dim % 16 || ap->rotary_dim > kHeadDim) return LOCKS_ERR_UNSUPPORTED;
+  if ((ap->rotary_dim > 0) != (ap->rope != nullptr)) return LOCKS_ERR_INVALID_ARG;
+  if (ap->rope && (ap->rope_rows <= 0 || (reinterpret_cast<uintptr_t>(ap->rope) & 15))) return LOCKS_ERR_INVALID_ARG;
+  if ((ap->interleaved & ~1) != 0) return LOCKS_ERR_INVALID_ARG;
+  if (tokens->total == 0 || tokens->max_tokens == 0) return LOCKS_OK;
+  KvAppendArgs a;
+  a.tok = token_args(cache, tokens, ws);
+  a.k_pool = const_cast<void*>(cache->k_pool);
+  a.v_pool = const_cast<void*>(cache->v_pool);
+  a.k = static_cast<const uint16_t*>(ap->k);
+  a.v = static_cast<const uint16_t*>(ap->v);
+  a.q = static_cast<const uint16_t*>(ap->q);
+  a.q_out = static_cast<uint16_t*>(ap->q_out);
+  a.rope = ap->rope;
+  a.positions = ap->positions;
+  a.k_stride = ap->k_stride;
+  a.v_stride = ap->v_stride;
+  a.q_stride = ap->q_stride;
+  a.q_out_stride = ap->q_out_stride;
+  a.num_q_heads = ap->num_q_heads;
+  a.rope_rows = ap->rope_rows;
+  a.rotary_dim = ap->rotary_dim;
+  a.interleaved = ap->interleaved;
+  return cuda_status(launch_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+locks_status_t lockskv_read(const locks_cache_t* cache, const lockskv_tokens_t* tokens, void* k_out, void* v_out,
+                            void* ws, size_t ws_bytes, void* stream) {
+  locks_status_t st = check_cache(cache, true);
+  if (st != LOCKS_OK) return st;
+  if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
+  if ((st = check_err_ws(ws, ws_bytes)) != LOCKS_OK) return st;
+  if (!k_out && !v_out) return LOCKS_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15) return LOCKS_ERR_INVALID_ARG;
+  if (tokens->total == 0 || tokens->max_tokens == 0) return LOCKS_OK;
+  KvReadArgs a;
+  a.tok = token_args(cache, tokens, ws);
+  a.k_pool = cache->k_pool;
+  a.v_pool = cache->v_pool;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.v_out = static_cast<uint16_t*>(v_out);
+  return cuda_status(launch_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+locks_status_t lockskv_prompt_workspace_size(const locks_cache_t* cache, const locks_params_t* params,
+                                             const lockskv_tokens_t* tokens, size_t* bytes) {
+  if (!bytes) return LOCKS_ERR_INVALID_ARG;
+  locks_status_t st = check_cache(cache, false);
+  if (st != LOCKS_OK) return st;
+  if ((st = check_params(cache, params)) != LOCKS_OK) return st;
+  if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
+  PromptPlan pl;
+  if ((st = plan_prompt(cache, params, tokens, &pl)) != LOCKS_OK) return st;
+  *bytes = pl.total;
+  return LOCKS_OK;
+}
+
+locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_params_t* params,
+                                     const lockskv_tokens_t* tokens, const void* q, int64_t q_stride, void* out,
+                                     float* lse, void* ws, size_t ws_bytes, void* stream) {
+  locks_status_t st = check_cache(cache, true);
+  if (st != LOCKS_OK) return st;
+  if ((st = check_params(cache, params)) != LOCKS_OK) return st;
+  if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
+  if (!q || !out || (reinterpret_cast<uintptr_t>(out) & 15)) return LOCKS_ERR_INVALID_ARG;
+  if ((st = check_rows(q, q_stride, (int64_t)params->num_q_heads * kHeadDim)) != LOCKS_OK) return st;
+  PromptPlan pl;
+  if ((st = plan_prompt(cache, params, tokens, &pl)) != LOCKS_OK) return st;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) || ws_bytes < pl.total) return LOCKS_ERR_WORKSPACE;
+  if (tokens->total == 0 || tokens->max_tokens == 0) return LOCKS_OK;
+  CUtensorMap tk, tv;
+  std::memset(&tk, 0, sizeof(tk));
+  std::memset(&tv, 0, sizeof(tv));
+  if (!is_q4(cache) && (!encode_pool(&tk, cache->k_pool, cache) || !encode_pool(&tv, cache->v_pool, cache)))
+    return LOCKS_ERR_CUDA;
+  PromptArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.k_pool = cache->k_pool;
+  a.v_pool = cache->v_pool;
+  a.cu_tokens = tokens->cu_tokens;
+  a.block_table = cache->block_table;
+  a.seq_lens = cache->seq_lens;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.part_o = at<float>(ws, pl.off_o);
+  a.part_ml = at<float2>(ws, pl.off_ml);
+  a.counters = at<unsigned>(ws, pl.off_counters);
+  a.err = at<int>(ws, 0);
+  a.batch = cache->batch;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.group = params->num_q_heads / cache->num_kv_heads;
+  a.max_pages = cache->max_pages;
+  a.pages_total = cache->pages_total;
+  a.page_size = cache->page_size;
+  a.total = tokens->total;
+  a.max_tokens = tokens->max_tokens;
+  a.n_qtiles = pl.n_qtiles;
+  a.n_splits = pl.n_splits;
+  a.scale_log2 = scale_of(params) * kLog2e;
+  a.q4 = is_q4(cache) ? 1 : 0;
+  return cuda_status(launch_prompt(a, tk, tv, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

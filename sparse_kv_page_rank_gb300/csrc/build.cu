@@ -35,6 +35,8 @@
 // Each basis vector, coefficient column and the centroid then get one
 // symmetric float32 scale s = max|x| / qmax (qmax 7 for int4, 127 for int8)
 // and codes rint(x / s), packed as LOCKS_Q4_BLOCK_BYTES(r, P) bytes.
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -129,9 +131,24 @@ __global__ void __launch_bounds__(kBT) build_kernel(const BuildArgs a) {
   const uint16_t* kg = a.k_pool + ph * P * kHeadDim;
 
   // 0. K -> shared memory (bf16, padded rows)
-  for (int e = tid; e < P * kHeadDim / 8; e += kBT) {
-    const int row = e / 16, col = (e % 16) * 8;
-    *reinterpret_cast<uint4*>(&s.K[row * kKS + col]) = __ldg(reinterpret_cast<const uint4*>(kg + row * kHeadDim + col));
+  if (a.kv_q4) {
+    // the stored keys, scale * code, rounded to bf16
+    const uint8_t* block = reinterpret_cast<const uint8_t*>(a.k_pool) + ph * LOCKS_KV_Q4_BLOCK_BYTES(P);
+    for (int e = tid; e < P * kHeadDim / 8; e += kBT) {
+      const int row = e / 16, ch = e % 16, j = ch / 4;
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(block + 64 * row + 16 * (ch % 4) + 4 * j));
+      const float z = __half2float(*reinterpret_cast<const __half*>(block + 64 * P + 8 * row + 2 * j));
+      uint32_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = pack_bf16(z * (float)((int)((w >> (4 * i)) & 15u) - 8), z * (float)((int)((w >> (4 * i + 16)) & 15u) - 8));
+      *reinterpret_cast<uint4*>(&s.K[row * kKS + 8 * ch]) = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+  } else {
+    for (int e = tid; e < P * kHeadDim / 8; e += kBT) {
+      const int row = e / 16, col = (e % 16) * 8;
+      *reinterpret_cast<uint4*>(&s.K[row * kKS + col]) = __ldg(reinterpret_cast<const uint4*>(kg + row * kHeadDim + col));
+    }
   }
   const bool q4 = a.format == LOCKS_DTYPE_Q4;
   if (q4) {

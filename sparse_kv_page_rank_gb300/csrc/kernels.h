@@ -79,7 +79,7 @@ struct AttendArgs {
   const float* shat;          // ws: [B*Hkv][max_pages][G] natural log
   const float2* part;         // ws: [B*Hkv][n_scan_chunks][G] (max, sum) of base-2 LSE
   int n_scan_chunks;
-  const uint16_t* k_pool16;   // fused mode: pool bases for L2 prefetches of likely pages
+  const uint16_t* k_pool16;   // fused mode: pool bases for L2 prefetches of likely pages; LOCKS_KV_Q4: the blocks
   const uint16_t* v_pool16;
   int32_t* sel_pages_out;     // fused mode: the page list it selected, [B*Hkv][k_max] (as locks_select)
   int32_t* sel_count_out;     // fused mode: [B*Hkv]
@@ -95,7 +95,7 @@ constexpr int kFusedPrefetch = 4;  // each CTA's best pages whose K/V are prefet
 
 // Summary builder.
 struct BuildArgs {
-  const uint16_t* k_pool;
+  const uint16_t* k_pool;  // bf16 pages, or LOCKS_KV_Q4 blocks
   void* basis_t;
   void* coeffs;
   const int32_t* page_ids;
@@ -103,7 +103,72 @@ struct BuildArgs {
   int format;  // LOCKS_DTYPE_BF16 / _F32 (basis_t + coeffs) or _Q4 (packed blocks in basis_t)
   int* err;
   int page_size;
+  int kv_q4;  // 1: the pages are LOCKS_KV_Q4 blocks
 };
+
+// The newest tokens of a batch (lockskv.h), as the cache-writing kernels see them.
+struct KvTokenArgs {
+  const int32_t* cu_tokens;  // [batch + 1], or null: one token per sequence
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int* err;
+  int batch, num_kv_heads, max_pages, pages_total, page_size;
+  int total, max_tokens;
+  int q4;  // 1: k_pool holds LOCKS_KV_Q4 blocks (v_pool unused)
+};
+struct KvAppendArgs {
+  KvTokenArgs tok;
+  void* k_pool;
+  void* v_pool;
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* q;  // or null
+  uint16_t* q_out;
+  const float* rope;
+  const int32_t* positions;  // or null: the position in the sequence
+  long long k_stride, v_stride, q_stride, q_out_stride;  // elements
+  int num_q_heads, rope_rows, rotary_dim, interleaved;
+};
+struct KvReadArgs {
+  KvTokenArgs tok;
+  const void* k_pool;
+  const void* v_pool;
+  uint16_t* k_out;  // or null
+  uint16_t* v_out;  // or null
+};
+
+// Causal attention of the newest tokens (prompt.cu).
+struct PromptArgs {
+  const uint16_t* q;         // bf16 [total][Hq][d], rows q_stride elements apart
+  long long q_stride;
+  const void* k_pool;        // LOCKS_KV_Q4: the blocks
+  const void* v_pool;
+  const int32_t* cu_tokens;  // or null
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  uint16_t* out;
+  float* lse;                // or null
+  float* part_o;             // ws: [B*Hkv*n_qtiles][n_splits][256][d]
+  float2* part_ml;           // ws: the same without d: (reference, sum), base 2
+  unsigned* counters;        // ws: [B*Hkv*n_qtiles]
+  int* err;
+  int batch, num_kv_heads, group, max_pages, pages_total, page_size;
+  int total, max_tokens;
+  int n_qtiles;              // CTAs along a sequence's new tokens (256 rows each)
+  int n_splits;              // CTAs along the keys
+  float scale_log2;
+  int q4;
+};
+
+cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t s);
+cudaError_t launch_read(const KvReadArgs& a, cudaStream_t s);
+// Attention over a LOCKS_KV_Q4 cache, one query token per sequence.  `tiles`:
+// 16-token tiles a warp takes at once (4, or 1 where a CTA has few pages).
+cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStream_t s);
+int attend_q4_max_cluster(int mode, int group, int page_size, int tiles);
+int attend_q4_active_clusters(int mode, int group, int page_size, int tiles, int cs);
+int attend_q4_ctas_per_sm(int group);
 
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_topk(const TopkArgs& a, cudaStream_t s, bool pdl);

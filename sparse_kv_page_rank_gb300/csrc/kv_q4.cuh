@@ -1,0 +1,47 @@
+// The 4-bit page format (LOCKS_KV_Q4 in locks.h) as the kernels that compute on it
+// see it, and the fp16-pair arithmetic that takes its codes apart.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace locks {
+
+constexpr int kQ4Slot = LOCKS_KV_Q4_BLOCK_BYTES(64);  // 64 tokens: one page, or four 16-token pages
+
+// Byte offset of 16-token tile t's part in a 64-token slot: a 64-token page keeps
+// each of the four parts of all its tokens together, a 16-token page is one tile.
+template <int P>
+struct Q4Tile {
+  __device__ static uint32_t key_codes(int t) { return P == 64 ? 1024 * t : 2304 * t; }
+  __device__ static uint32_t key_scales(int t) { return P == 64 ? 4096 + 128 * t : 2304 * t + 1024; }
+  __device__ static uint32_t value_codes(int t) { return P == 64 ? 4608 + 1024 * t : 2304 * t + 1152; }
+  __device__ static uint32_t value_scales(int t) { return P == 64 ? 8704 + 128 * t : 2304 * t + 2176; }
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float f16_lo(uint32_t w) { return __low2float(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ float f16_hi(uint32_t w) { return __high2float(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Fields 0 and 1 (bits 0-3, 4-7) of both halves of w, each holding code + 8, as
+// fp16 pairs of codes: a field under the exponent of 1024 (or, four bits up, of
+// 64) is the number 1024 + u (64 + u) exactly, from which 1032 (72) is taken.
+__device__ __forceinline__ void q4_codes01(uint32_t w, uint32_t& f0, uint32_t& f1) {
+  f0 = sub_f16x2((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
+  f1 = sub_f16x2((w & 0x00f000f0u) | 0x54005400u, 0x54805480u);
+}
+
+}  // namespace locks

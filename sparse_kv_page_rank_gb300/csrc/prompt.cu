@@ -1,0 +1,731 @@
+// Causal attention of the newest tokens of every sequence over the paged cache
+// (a prompt, the next chunk of one, or a few draft tokens), bf16 or 4-bit pages.
+//
+// Mathematics.  Rows are (token, query head of the group): the G heads of a KV head
+// share its keys, so a tile of 128 rows holds 128 / G tokens and its products are
+// S = Q K^T and O += P V with the online softmax between them; row r of token i at
+// position p sees the keys t <= p.
+//
+// What bounds it: 4 * 128 operations per visible (row, key) at the tensor cores'
+// rate; for few rows over a long cache, the cache's bytes.
+//
+// Layout.  A CTA takes two tiles (256 rows) of one KV head, so that one tile's
+// softmax runs while the other's products do, and walks the keys in blocks of 128.
+// Tensor memory (512 columns): S of both tiles, 128 columns each, whose first 64
+// columns P overwrites (16-bit pairs, the A operand of the second product), and O
+// of both tiles, 128 columns each.  Warps: 0 issues the matrix instructions, 1 the
+// copies; 4-7 and 8-11 are the softmax of the two tiles, one thread per row, so
+// neither maximum nor sum needs a shuffle; 12-15 (4-bit pages) turn codes into the
+// fp16 operands.  Matrix instructions of one CTA execute in the order of issue, so
+// S of the next block may be issued right behind the product that reads P from the
+// same columns, and a softmax that has seen S of block j knows that O holds all
+// blocks before j: it rescales O in place, and only when a row's maximum has grown
+// by more than 2^8 since its last reference.
+//
+// bf16 pages arrive by TMA in the operands' own order (64-column boxes, 128-byte
+// swizzle).  4-bit pages arrive as whole page-heads and are converted to s * code
+// in fp16 (one rounding, 2^-11), with q scaled into fp16 by a power of two and the
+// weights scaled by 2^6, so that weights 2^-30 of the largest still count.
+//
+// Values that a row does not see must not reach it, not even as 0 * NaN: in the
+// blocks that straddle a tile's diagonal or the end of the sequence, value rows past
+// the end are zeroed in shared memory, and a visible token's non-finite values are
+// zeroed there too and added, as they are, to the rows that see the token at the
+// end.
+//
+// Few rows: the keys of a problem are cut among several CTAs, whose partial
+// (reference, sum, O) go to the workspace; the last one to finish joins them.
+#include "common.cuh"
+#include "kernels.h"
+#include "kv_q4.cuh"
+#include "tcgen05.cuh"
+
+namespace locks {
+
+namespace {
+
+constexpr int kRows = 128;                   // rows of a tile
+constexpr int kBlock = 128;                  // keys of a block
+constexpr int kHalf = kBlock * 128;          // bytes of 64 columns of 128 16-bit rows
+constexpr int kOperand = 2 * kHalf;          // one tile of Q, K or V: 32 KiB
+constexpr int kKvStages = 2;
+constexpr int kRawSlots = 3;                 // 4-bit pages: 64-token slots of codes
+constexpr int kSkipRing = 4;                 // the copies run at most three blocks ahead of the softmax
+constexpr int kMaxBad = 2 * kRows;           // tokens near a diagonal: no more than a CTA has
+constexpr float kLazy = 8.f;                 // growth of a maximum (base 2) that O's reference tolerates
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;             // S: columns 0 and 128; O: 256 and 384
+
+struct PromptShared {
+  uint64_t q_full, k_full[kKvStages], v_full[kKvStages], k_empty[kKvStages], v_empty[kKvStages];
+  uint64_t s_full[2], p_ready[2], o_full[2], drain;
+  uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+  uint32_t tmem;
+  int skip[kSkipRing];      // 16-token groups of a block whose page is outside the pool (bits)
+  int raw_skip[kRawSlots];  // the same of a slot
+  int abort;                // a bounded wait gave up
+  int n_bad, bad[kMaxBad];
+  int last;
+};
+
+// Waits for phase `parity`; gives up after the iteration limit, or once another
+// role has given up.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, PromptShared& sh) {
+  const uint32_t addr = smem_u32(bar);
+  for (uint32_t it = 0; it < kMbarSpinLimit; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
+  }
+  *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+  return false;
+}
+
+// The same by a whole warp, which goes on or gives up as one.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, PromptShared& sh) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, sh));
+}
+
+// Byte offset of 16-byte chunk `cc` (0..7) of row `row` in a 64-column half-tile
+// (128-byte swizzle).
+__device__ __forceinline__ uint32_t swz(int row, int cc) { return row * 128 + ((cc ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};\n" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+
+// The four fields of both halves of w as fp16 pairs of codes.
+__device__ __forceinline__ void q4_codes(uint32_t w, uint32_t (&f)[4]) {
+  q4_codes01(w, f[0], f[1]);
+  q4_codes01(w >> 8, f[2], f[3]);
+}
+
+// What one CTA works on.
+struct PromptPlace {
+  int b, hkv, split;
+  int row0;          // first token row of the sequence in the token arrays
+  int len;           // tokens in the cache
+  int start;         // position of the sequence's first new token
+  int tok0, n_tok;   // new tokens of this CTA
+  int n_tiles;
+  int kv_end;        // keys that its last token sees
+  int j0, j1;        // its blocks of keys
+};
+
+// Index of a CTA's partial results (of 256 rows each): its sequence, head, tiles and split.
+__device__ __forceinline__ size_t part_row(const PromptArgs& a, const PromptPlace& w, int y) {
+  return (((size_t)w.b * a.num_kv_heads + w.hkv) * a.n_qtiles + y) * a.n_splits + w.split;
+}
+
+// One value of the cache (bf16 pages: any; 4-bit pages: with its scale).
+template <bool Q4, int P>
+__device__ float value_at(const PromptArgs& a, const PromptPlace& w, int t, int d) {
+  const int phys = __ldg(a.block_table + (size_t)w.b * a.max_pages + t / P);
+  const size_t ph = (size_t)phys * a.num_kv_heads + w.hkv;
+  const int slot = t % P;
+  if (!Q4) {
+    const uint16_t x = __ldg(static_cast<const uint16_t*>(a.v_pool) + (ph * P + slot) * kHeadDim + d);
+    return __uint_as_float((uint32_t)x << 16);
+  }
+  const int u = slot & 15, j = d / 32;
+  const uint8_t* p = static_cast<const uint8_t*>(a.k_pool) + ph * (size_t)LOCKS_KV_Q4_BLOCK_BYTES(P);
+  const uint16_t c = *reinterpret_cast<const uint16_t*>(p + 72 * P + 1024 * (slot / 16) + 512 * (u / 8) +
+                                                        64 * ((d % 32) / 4) + 16 * ((u % 8) / 2) + 4 * j + 2 * (u % 2));
+  const __half s = *reinterpret_cast<const __half*>(p + 136 * P + 128 * (slot / 16) + 32 * ((u % 8) / 2) +
+                                                    16 * (u / 8) + 4 * j + 2 * (u % 2));
+  return __half2float(s) * (float)(((c >> (4 * (d % 4))) & 15) - 8);
+}
+
+// ---- warp 1: the copies ---------------------------------------------------------
+template <bool Q4, int P>
+__device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUtensorMap* tk, const CUtensorMap* tv,
+                          PromptShared& sh, uint8_t* kv, uint8_t* raw) {
+  constexpr int kPPB = kBlock / P;  // pages of a block
+  constexpr int kAtOnce = 32 / kPPB;
+  const int lane = threadIdx.x & 31;
+  const int n_pages = (w.len + P - 1) / P;
+  int nk = 0, nv = 0, nr = 0;  // blocks (slots) asked for
+  bool ok = true;
+  for (int jb = w.j0; jb < w.j1 && ok; jb += kAtOnce) {
+    // the pages of several blocks at a time, one per lane
+    const int lp = jb * kPPB + lane;
+    int phys = -1;
+    if (lp < n_pages && lp < w.j1 * kPPB) {
+      phys = __ldg(a.block_table + (size_t)w.b * a.max_pages + lp);
+      if (phys < 0 || phys >= a.pages_total) {
+        set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
+        phys = -1;
+      }
+    }
+    for (int j = jb; j < min(jb + kAtOnce, w.j1) && ok; ++j) {
+      const int n = j - w.j0, st = n % kKvStages;
+      int pg[kPPB], skip = 0;
+#pragma unroll
+      for (int i = 0; i < kPPB; ++i) {
+        pg[i] = __shfl_sync(0xffffffffu, phys, (j - jb) * kPPB + i);
+        if (pg[i] < 0) skip |= ((1 << (P / 16)) - 1) << (i * (P / 16));
+      }
+      if constexpr (!Q4) {
+        const int copies = kPPB - __popc(skip) / (P / 16);
+        uint8_t* kd = kv + st * 2 * kOperand;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {  // keys, then values
+          uint64_t* full = v ? &sh.v_full[st] : &sh.k_full[st];
+          uint64_t* empty = v ? &sh.v_empty[st] : &sh.k_empty[st];
+          if (n >= kKvStages && !wait_warp(empty, (n / kKvStages - 1) & 1, sh)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            if (!v) sh.skip[n % kSkipRing] = skip;
+            mbar_arrive_expect_tx(full, (uint32_t)copies * P * 256);
+#pragma unroll
+            for (int i = 0; i < kPPB; ++i) {
+              if (pg[i] < 0) continue;
+              const int y = (pg[i] * a.num_kv_heads + w.hkv) * P;
+              uint8_t* dst = kd + v * kOperand + i * P * 128;
+              tma_load_2d(dst, v ? tv : tk, full, 0, y);
+              tma_load_2d(dst + kHalf, v ? tv : tk, full, 64, y);
+            }
+          }
+          __syncwarp();
+          if (v) nv = n + 1; else nk = n + 1;
+        }
+      } else {
+        // two 64-token slots of codes; the converters hand `skip` on with the block
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int s = 2 * n + hh, rs = s % kRawSlots;
+          if (s >= kRawSlots && !wait_warp(&sh.raw_empty[rs], (s / kRawSlots - 1) & 1, sh)) {
+            ok = false;
+            break;
+          }
+          const int part = (skip >> (4 * hh)) & 15;
+          if (lane == 0) {
+            sh.raw_skip[rs] = part;
+            mbar_arrive_expect_tx(&sh.raw_full[rs],
+                                  (uint32_t)(kPPB / 2 - __popc(part) / (P / 16)) * LOCKS_KV_Q4_BLOCK_BYTES(P));
+#pragma unroll
+            for (int i = 0; i < kPPB / 2; ++i) {
+              const int ph = pg[hh * (kPPB / 2) + i];
+              if (ph < 0) continue;
+              bulk_load(smem_u32(raw) + rs * kQ4Slot + i * LOCKS_KV_Q4_BLOCK_BYTES(P),
+                        static_cast<const uint8_t*>(a.k_pool) +
+                            ((size_t)ph * a.num_kv_heads + w.hkv) * (size_t)LOCKS_KV_Q4_BLOCK_BYTES(P),
+                        LOCKS_KV_Q4_BLOCK_BYTES(P), &sh.raw_full[rs]);
+            }
+          }
+          __syncwarp();
+          nr = s + 1;
+        }
+      }
+    }
+  }
+  if (!ok && lane == 0) {
+    // let the copies in flight land before the memory is given back
+    for (int n = max(0, nk - kKvStages); n < nk; ++n) (void)mbar_wait(&sh.k_full[n % kKvStages], (n / kKvStages) & 1);
+    for (int n = max(0, nv - kKvStages); n < nv; ++n) (void)mbar_wait(&sh.v_full[n % kKvStages], (n / kKvStages) & 1);
+    for (int s = max(0, nr - kRawSlots); s < nr; ++s) (void)mbar_wait(&sh.raw_full[s % kRawSlots], (s / kRawSlots) & 1);
+  }
+}
+
+// ---- warps 12-15: codes to fp16 operands -----------------------------------------
+template <int P>
+__device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t kv, uint32_t raw) {
+  using At = Q4Tile<P>;
+  const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+  for (int n = 0; n < w.j1 - w.j0; ++n) {
+    const int st = n % kKvStages;
+    const uint32_t kd = kv + st * 2 * kOperand, vd = kd + kOperand;
+    if (n >= kKvStages && !wait_warp(&sh.k_empty[st], (n / kKvStages - 1) & 1, sh)) return;
+#pragma unroll 1
+    for (int hh = 0; hh < 2; ++hh) {
+      const int s = 2 * n + hh, rs = s % kRawSlots;
+      if (!wait_warp(&sh.raw_full[rs], (s / kRawSlots) & 1, sh)) return;
+      if (tid == 0) {
+        if (hh == 0) sh.skip[n % kSkipRing] = sh.raw_skip[rs];
+        else sh.skip[n % kSkipRing] |= sh.raw_skip[rs] << 4;
+      }
+      const uint32_t src = raw + rs * kQ4Slot;
+      // a warp takes a 16-token tile, 8 tokens at a time; lane: 16 bytes of codes
+      // (piece c) of one token, the eight lanes of a store phase on rows r and r + 4
+      const int c = lane & 3;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * i + ((lane >> 2) & 1) * 4 + (lane >> 3);
+        const uint4 x = lds128(src + At::key_codes(warp) + 64 * r + 16 * c);
+        const uint2 z = lds64(src + At::key_scales(warp) + 8 * r);
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+        const int row = 64 * hh + 16 * warp + r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t zz = __byte_perm(j < 2 ? z.x : z.y, 0, j & 1 ? 0x3232 : 0x1010);
+          uint32_t f[4];
+          q4_codes(words[j], f);
+          sts128(kd + (j >> 1) * kHalf + swz(row, (j & 1) * 4 + c), mul_f16x2(f[0], zz), mul_f16x2(f[1], zz),
+                 mul_f16x2(f[2], zz), mul_f16x2(f[3], zz));
+        }
+      }
+    }
+    fence_proxy_async();
+    mbar_arrive(&sh.k_full[st]);
+    if (n >= kKvStages && !wait_warp(&sh.v_empty[st], (n / kKvStages - 1) & 1, sh)) return;
+#pragma unroll 1
+    for (int hh = 0; hh < 2; ++hh) {
+      const int s = 2 * n + hh, rs = s % kRawSlots;
+      const uint32_t src = raw + rs * kQ4Slot;
+      // lane (g, c): dimensions 32 j + 4 g .. + 3 of tokens 2c, 2c + 1 (+ 8)
+      const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) {
+        const uint4 x = lds128(src + At::value_codes(warp) + 512 * hi + 16 * lane);
+        const uint4 z = lds128(src + At::value_scales(warp) + 32 * c + 16 * hi);
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w}, zw[4] = {z.x, z.y, z.z, z.w};
+        const int row = 64 * hh + 16 * warp + 8 * hi + 2 * c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t f[4];
+          q4_codes(words[j], f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = mul_f16x2(f[i], zw[j]);
+          const uint32_t base = vd + (j >> 1) * kHalf + (g & 1) * 8;
+          const int cc = (j & 1) * 4 + (g >> 1);
+          sts64(base + swz(row, cc), __byte_perm(f[0], f[1], 0x5410), __byte_perm(f[2], f[3], 0x5410));
+          sts64(base + swz(row + 1, cc), __byte_perm(f[0], f[1], 0x7632), __byte_perm(f[2], f[3], 0x7632));
+        }
+      }
+      mbar_arrive(&sh.raw_empty[rs]);
+    }
+    fence_proxy_async();
+    mbar_arrive(&sh.v_full[st]);
+  }
+}
+
+// ---- warp 0, one thread: the matrix instructions ------------------------------------
+template <bool Q4>
+__device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uint32_t kv, uint32_t tmem) {
+  constexpr uint32_t kIdS = umma_idesc(kRows, kBlock, !Q4, false), kIdO = umma_idesc(kRows, kHeadDim, !Q4, true);
+  const int n_blocks = w.j1 - w.j0;
+  auto scores = [&](int t, int st) {  // S_t = Q_t K^T
+    const uint32_t k = kv + st * 2 * kOperand, qt = q + t * kOperand;
+#pragma unroll
+    for (int s = 0; s < kHeadDim / 16; ++s) {
+      const uint32_t off = (s / 4) * kHalf + (s % 4) * 32;
+      umma_ss(tmem + t * kBlock, umma_desc(qt + off, 16, 1024), umma_desc(k + off, 16, 1024), kIdS, s > 0);
+    }
+  };
+  auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
+    const uint32_t v = kv + st * 2 * kOperand + kOperand;
+#pragma unroll
+    for (int s = 0; s < kBlock / 16; ++s)
+      umma_ts(tmem + kTmemO + t * kHeadDim, tmem + t * kBlock + s * 8, umma_desc(v + s * 16 * 128, kHalf, 1024), kIdO,
+              !first || s > 0);
+  };
+  bool ok = wait_bar(&sh.q_full, 0, sh) && wait_bar(&sh.k_full[0], 0, sh);
+  if (ok) {
+    tc_fence_after();
+    for (int t = 0; t < w.n_tiles; ++t) {
+      scores(t, 0);
+      umma_commit(&sh.s_full[t]);
+    }
+    umma_commit(&sh.k_empty[0]);
+  }
+  for (int n = 0; ok && n < n_blocks; ++n) {
+    const int st = n % kKvStages, sn = (n + 1) % kKvStages;
+    if (!(ok = wait_bar(&sh.v_full[st], (n / kKvStages) & 1, sh))) break;
+    for (int t = 0; t < w.n_tiles; ++t) {
+      if (!(ok = wait_bar(&sh.p_ready[t], n & 1, sh))) break;
+      tc_fence_after();
+      values(t, st, n == 0);
+      if (t == w.n_tiles - 1) umma_commit(&sh.v_empty[st]);
+      if (n + 1 < n_blocks) {
+        if (t == 0) {
+          if (!(ok = wait_bar(&sh.k_full[sn], ((n + 1) / kKvStages) & 1, sh))) break;
+          tc_fence_after();
+        }
+        scores(t, sn);
+        umma_commit(&sh.s_full[t]);
+        if (t == w.n_tiles - 1) umma_commit(&sh.k_empty[sn]);
+      } else {
+        umma_commit(&sh.o_full[t]);
+      }
+    }
+  }
+  if (!ok) {
+    // what was issued must end before its memory is given back
+    umma_commit(&sh.drain);
+    (void)mbar_wait(&sh.drain, 0);
+  }
+}
+
+// ---- warps 4-11: one softmax row per thread -------------------------------------------
+template <bool Q4, int P>
+__device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptShared& sh, uint8_t* smem, uint32_t tmem_base) {
+  constexpr float kOffset = Q4 ? 6.f : 0.f;  // weights are scaled by 2^kOffset
+  const int warp = threadIdx.x >> 5, t = (warp - 4) / 4;
+  if (t >= w.n_tiles) return;
+  const int row = threadIdx.x & 127;
+  const int G = a.group, tpt = kRows / G, Hq = a.num_kv_heads * G;
+  const int ti = row / G, h = row - ti * G;
+  const int i = t * tpt + ti;  // token of this CTA
+  const bool valid = ti < tpt && i < w.n_tok;
+  const int tok = w.tok0 + i;
+  const int pos = w.start + tok;
+  const int limit = valid ? max(0, pos + 1) : w.kv_end;  // keys that this row sees
+  const size_t qrow = (size_t)w.row0 + tok;
+  const uint32_t tmem = tmem_base + ((uint32_t)(warp & 3) << 21);
+  float factor = a.scale_log2;
+
+  // the row's query into the operand's order
+  {
+    const uint16_t* src = a.q + qrow * a.q_stride + (size_t)(w.hkv * G + h) * kHeadDim;
+    const uint32_t dst = smem_u32(smem) + t * kOperand;
+    uint4 x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + k) : make_uint4(0, 0, 0, 0);
+    float down = 1.f;
+    if (Q4) {
+      uint32_t m = 0;  // largest magnitude, as bf16 bits
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max(m, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
+      }
+      int e = (int)(m >> 7) - 127;
+      e = m == 0 || e > 127 ? 0 : min(max(e, -100), 126);
+      down = __uint_as_float((uint32_t)(127 - e) << 23);
+      factor *= __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      if (Q4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
+      }
+      sts128(dst + (k >> 3) * kHalf + swz(row, k & 7), v[0], v[1], v[2], v[3]);
+    }
+    fence_proxy_async();
+    mbar_arrive(&sh.q_full);
+  }
+
+  float m = -INFINITY, l = 0.f;  // reference (base 2), sum of the weights
+  const int first_limit = max(0, w.start + w.tok0 + 1);  // keys that every row of the CTA sees
+  const int n_blocks = w.j1 - w.j0;
+  for (int n = 0; n < n_blocks; ++n) {
+    const int kv0 = (w.j0 + n) * kBlock;
+    if (!wait_warp(&sh.s_full[t], n & 1, sh)) return;
+    tc_fence_after();
+    const int skip = *reinterpret_cast<volatile int*>(&sh.skip[n % kSkipRing]);
+    // values that some row must not see (tile 0's threads, one token each)
+    if (t == 0 && (kv0 + kBlock > first_limit || kv0 + kBlock > w.len || skip)) {
+      const int st = n % kKvStages;
+      if (!wait_warp(&sh.v_full[st], (n / kKvStages) & 1, sh)) return;
+      uint8_t* v = smem + 2 * kOperand + st * 2 * kOperand + kOperand + row * 128;
+      const int at = kv0 + row;
+      bool zero = at >= w.kv_end || at >= w.len || ((skip >> (row / 16)) & 1);
+      if (!zero && at >= first_limit) {
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + (k >> 3) * kHalf + (k & 7) * 16);
+          const uint32_t e = Q4 ? 0x7c007c00u : 0x7f807f80u;
+          // an exponent of all ones in either half of a word
+          auto inf = [&](uint32_t y) { return __vcmpeq2(y & e, e) != 0; };
+          bad |= inf(x.x) | inf(x.y) | inf(x.z) | inf(x.w);
+        }
+        if (bad) {
+          const int k = atomicAdd(&sh.n_bad, 1);
+          if (k < kMaxBad) sh.bad[k] = at;
+          zero = true;
+        }
+      }
+      if (zero) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(v + (k >> 3) * kHalf + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async();
+    }
+
+    const int lim = limit - kv0;
+    const bool masked = __any_sync(0xffffffffu, lim < kBlock) || skip;
+    auto hide = [&](uint32_t (&s)[32], int c0) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (c0 + k >= lim || ((skip >> ((c0 + k) / 16)) & 1)) s[k] = 0xff800000u;  // -infinity
+    };
+    const uint32_t ts = tmem + t * kBlock, to = tmem + kTmemO + t * kHeadDim;
+    // the block's maximum
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c0 = 0; c0 < kBlock; c0 += 32) {
+      uint32_t s[32];
+      tmem_ld32(s, ts + c0);
+      tmem_wait_ld32(s);
+      if (masked) hide(s, c0);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
+    }
+    mx *= factor;  // positive
+    if (__any_sync(0xffffffffu, mx > m + kLazy || (m == -INFINITY && mx > m))) {
+      const float mn = fmaxf(m, mx);
+      const float al = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+      m = mn;
+      l *= al;
+      if (n > 0) {  // O holds every block before this one
+#pragma unroll
+        for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(o, to + c0);
+          tmem_wait_ld32(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+          tmem_st32(to + c0, o);
+        }
+      }
+    }
+    const float ref = m == -INFINITY ? 0.f : m - kOffset;
+#pragma unroll
+    for (int c0 = 0; c0 < kBlock; c0 += 32) {
+      uint32_t s[32], p[16];
+      tmem_ld32(s, ts + c0);
+      tmem_wait_ld32(s);
+      if (masked) hide(s, c0);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float x = fast_exp2(fmaf(__uint_as_float(s[2 * k]), factor, -ref));
+        const float y = fast_exp2(fmaf(__uint_as_float(s[2 * k + 1]), factor, -ref));
+        l += x + y;
+        p[k] = Q4 ? pack_f16(x, y) : pack_bf16(x, y);
+      }
+      tmem_st16(ts + c0 / 2, p);  // behind the columns of S that are still to be read
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(&sh.p_ready[t]);
+  }
+
+  // ---- the rows' results ----
+  if (n_blocks > 0) {
+    if (!wait_warp(&sh.o_full[t], 0, sh)) return;
+    tc_fence_after();
+  }
+  const int n_bad = min(*reinterpret_cast<volatile int*>(&sh.n_bad), kMaxBad);
+  const float lse2 = (m == -INFINITY ? 0.f : m - kOffset) + fast_log2(l);
+  const size_t oi = qrow * Hq + (size_t)w.hkv * G + h;
+  const size_t pi = a.n_splits > 1 ? part_row(a, w, blockIdx.y) * (2 * kRows) + t * kRows + row : 0;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+    uint32_t o[32];
+    if (n_blocks > 0) {
+      tmem_ld32(o, tmem + kTmemO + t * kHeadDim + c0);
+      tmem_wait_ld32(o);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = 0u;
+    }
+    for (int x = 0; x < n_bad; ++x) {
+      const int at = sh.bad[x];
+      if (!valid || at >= limit) continue;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float v = value_at<Q4, P>(a, w, at, c0 + k);
+        if (!isfinite(v)) o[k] = __float_as_uint(__uint_as_float(o[k]) + v);
+      }
+    }
+    if (!valid) continue;
+    if (a.n_splits > 1) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        *reinterpret_cast<uint4*>(a.part_o + pi * kHeadDim + c0 + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; k += 8) {
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y[e] = pack_bf16(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
+        *reinterpret_cast<uint4*>(a.out + oi * kHeadDim + c0 + k) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+  }
+  if (valid) {
+    if (a.n_splits > 1) a.part_ml[pi] = make_float2(l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m - kOffset), l);
+    else if (a.lse) a.lse[oi] = l == 0.f ? -INFINITY : lse2 * kLn2;
+  }
+}
+
+template <bool Q4, int P>
+__global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PromptArgs a) {
+  extern __shared__ uint8_t dyn_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ PromptShared sh;
+  uint8_t* kv = smem + 2 * kOperand;
+  uint8_t* raw = kv + kKvStages * 2 * kOperand;
+  const int tid = threadIdx.x, warp = tid >> 5;
+
+  pdl_wait();
+  PromptPlace w;
+  {
+    const int x = blockIdx.x / a.n_splits;
+    w.split = blockIdx.x % a.n_splits;
+    w.hkv = x % a.num_kv_heads;
+    w.b = x / a.num_kv_heads;
+    const int qt = gridDim.y - 1 - blockIdx.y;  // the tiles with the most keys first
+    const bool says = tid == 0 && blockIdx.y == 0 && w.split == 0;
+    int len = a.seq_lens[w.b];
+    if (len < 0 || len > a.max_pages * P) {
+      if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+      len = len < 0 ? 0 : a.max_pages * P;
+    }
+    int c0 = w.b, c1 = w.b + (len > 0 ? 1 : 0);
+    if (a.cu_tokens) {
+      c0 = a.cu_tokens[w.b];
+      c1 = a.cu_tokens[w.b + 1];
+    }
+    int n = c1 - c0;
+    if (c0 < 0 || n < 0 || c1 > a.total) {
+      if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+      n = 0;
+    }
+    if (says && (n > len || n > a.max_tokens)) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+    const int mine = min(n, a.max_tokens), per_cta = 2 * (kRows / a.group);
+    w.row0 = c0;
+    w.len = len;
+    w.start = len - n;
+    w.tok0 = qt * per_cta;
+    if (w.tok0 >= mine) return;  // the whole CTA
+    w.n_tok = min(per_cta, mine - w.tok0);
+    w.n_tiles = w.n_tok > kRows / a.group ? 2 : 1;
+    w.kv_end = max(0, min(len, w.start + w.tok0 + w.n_tok));
+    const long long nb = (w.kv_end + kBlock - 1) / kBlock;
+    w.j0 = (int)(nb * w.split / a.n_splits);
+    w.j1 = (int)(nb * (w.split + 1) / a.n_splits);
+  }
+  if (tid == 0) {
+    mbar_init(&sh.q_full, kRows * w.n_tiles);
+    for (int s = 0; s < kKvStages; ++s) {
+      mbar_init(&sh.k_full[s], Q4 ? 128 : 1);
+      mbar_init(&sh.v_full[s], Q4 ? 128 : 1);
+      mbar_init(&sh.k_empty[s], 1);
+      mbar_init(&sh.v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_ready[t], kRows);
+      mbar_init(&sh.o_full[t], 1);
+    }
+    mbar_init(&sh.drain, 1);
+    for (int s = 0; s < kRawSlots; ++s) {
+      mbar_init(&sh.raw_full[s], 1);
+      mbar_init(&sh.raw_empty[s], 128);
+    }
+    fence_mbar_init();
+    sh.abort = 0;
+    sh.n_bad = 0;
+  }
+  if (warp == 0) tmem_alloc(&sh.tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 0) {
+    if ((tid & 31) == 0 && w.j1 > w.j0) mma_role<Q4>(w, sh, smem_u32(smem), smem_u32(kv), tmem);
+    __syncwarp();
+  } else if (warp == 1) {
+    load_role<Q4, P>(a, w, &tk, &tv, sh, kv, raw);
+  } else if (warp >= 12) {
+    if constexpr (Q4) convert_role<P>(w, sh, smem_u32(kv), smem_u32(raw));
+  } else if (warp >= 4) {
+    softmax_role<Q4, P>(a, w, sh, smem, tmem);
+  }
+  __syncwarp();
+  __threadfence();  // partial results, before the ticket
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+  pdl_launch_dependents();
+  if (tid == 0 && sh.abort) set_error(a.err, kDevErrTimeout);
+  if (a.n_splits == 1) return;
+
+  // ---- the last CTA of the tiles joins the partial results ----
+  const size_t prob = part_row(a, w, blockIdx.y) / a.n_splits;
+  if (tid == 0) sh.last = atomicAdd(a.counters + prob, 1u) == (unsigned)(a.n_splits - 1);
+  __syncthreads();
+  if (!sh.last) return;
+  __threadfence();
+  const int G = a.group, tpt = kRows / G, lane = tid & 31;
+  for (int r = warp; r < w.n_tiles * kRows; r += blockDim.x / 32) {
+    const int ti = (r % kRows) / G, h = (r % kRows) % G, i = (r / kRows) * tpt + ti;
+    if (ti >= tpt || i >= w.n_tok) continue;
+    float M = -INFINITY;
+    for (int s = 0; s < a.n_splits; ++s)
+      M = fmaxf(M, __ldcg(a.part_ml + (prob * a.n_splits + s) * (2 * kRows) + r).x);
+    float L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < a.n_splits; ++s) {
+      const size_t pi = (prob * a.n_splits + s) * (2 * kRows) + r;
+      const float2 ml = __ldcg(a.part_ml + pi);
+      if (ml.y == 0.f) continue;  // saw no key
+      const float f = fast_exp2(ml.x - M);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + pi * kHeadDim) + lane);
+      L = fmaf(ml.y, f, L);
+      O.x = fmaf(v.x, f, O.x);
+      O.y = fmaf(v.y, f, O.y);
+      O.z = fmaf(v.z, f, O.z);
+      O.w = fmaf(v.w, f, O.w);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t oi = ((size_t)w.row0 + w.tok0 + i) * ((size_t)a.num_kv_heads * G) + (size_t)w.hkv * G + h;
+    *reinterpret_cast<uint2*>(a.out + oi * kHeadDim + 4 * lane) =
+        make_uint2(pack_bf16(O.x * inv, O.y * inv), pack_bf16(O.z * inv, O.w * inv));
+    if (a.lse && lane == 0) a.lse[oi] = L == 0.f ? -INFINITY : (M + fast_log2(L)) * kLn2;
+  }
+  if (tid == 0) a.counters[prob] = 0;  // ready for the next call
+}
+
+size_t smem_bytes(bool q4) {
+  return 1024 + 2 * kOperand + (size_t)kKvStages * 2 * kOperand + (q4 ? kRawSlots * kQ4Slot : 0);
+}
+
+template <bool Q4, int P>
+cudaError_t launch(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  auto kern = prompt_kernel<Q4, P>;
+  const size_t smem = smem_bytes(Q4);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.batch * a.num_kv_heads * a.n_splits, a.n_qtiles, 1);
+  cfg.blockDim = dim3(Q4 ? 512 : 384, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  if (a.q4) return a.page_size == 16 ? launch<true, 16>(a, tk, tv, s) : launch<true, 64>(a, tk, tv, s);
+  return a.page_size == 16 ? launch<false, 16>(a, tk, tv, s) : launch<false, 64>(a, tk, tv, s);
+}
+
+}  // namespace locks

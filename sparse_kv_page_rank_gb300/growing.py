@@ -44,7 +44,7 @@ class GrowingLoop:
 
     def __init__(self, rt: LocksRuntime, q: torch.Tensor, snapshot_step: int | None = None):
         self.rt, self.q = rt, q
-        self.P = rt.k_pool.shape[2]
+        self.P = rt.page_size
         dev = rt.device
         self.main = torch.cuda.Stream(device=dev)
         self.side = torch.cuda.Stream(device=dev)

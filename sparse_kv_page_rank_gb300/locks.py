@@ -30,6 +30,8 @@ LOCKS_DTYPE_BF16 = 0
 LOCKS_DTYPE_F32 = 1
 LOCKS_DTYPE_Q4 = 2
 LOCKS_DTYPE_BF16_PACKED = 3
+LOCKS_KV_BF16 = 0
+LOCKS_KV_Q4 = 1
 LOCKS_FLAG_UNFUSED = 0x1
 LOCKS_FLAG_FUSED = 0x2
 
@@ -37,11 +39,19 @@ LOCKS_FLAG_FUSED = 0x2
 def q4_page_head_bytes(rank: int, page_size: int = 64) -> int:
     """Bytes of one page-head of a LOCKS_DTYPE_Q4 summary (LOCKS_Q4_BLOCK_BYTES)."""
     return (72 * rank + page_size * rank + 132 + 15) // 16 * 16
+
+
+def kv_q4_block_bytes(page_size: int = 64) -> int:
+    """Bytes of one page-head of a LOCKS_KV_Q4 cache (LOCKS_KV_Q4_BLOCK_BYTES)."""
+    return 144 * page_size
+
+
 LOCKS_DEVERR_BLOCK_TABLE = 0x1
 LOCKS_DEVERR_SEL_PAGE = 0x2
 LOCKS_DEVERR_LENGTHS = 0x4
 LOCKS_DEVERR_PAGE_ID = 0x8
 LOCKS_DEVERR_TIMEOUT = 0x10
+LOCKS_DEVERR_POSITION = 0x20
 
 
 class LocksError(RuntimeError):
@@ -56,7 +66,7 @@ class locks_cache_t(ctypes.Structure):
                 ("n_summarized", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("pages_total", ctypes.c_int32),
-                ("max_pages", ctypes.c_int32)]
+                ("max_pages", ctypes.c_int32), ("kv_format", ctypes.c_int32)]
 
 
 class locks_summary_t(ctypes.Structure):
@@ -67,6 +77,18 @@ class locks_summary_t(ctypes.Structure):
 class locks_params_t(ctypes.Structure):
     _fields_ = [("num_q_heads", ctypes.c_int32), ("budget_tokens", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class lockskv_tokens_t(ctypes.Structure):
+    _fields_ = [("cu_tokens", ctypes.c_void_p), ("total", ctypes.c_int32), ("max_tokens", ctypes.c_int32)]
+
+
+class lockskv_append_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("rope", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("num_q_heads", ctypes.c_int32), ("rope_rows", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -83,6 +105,7 @@ def lib() -> ctypes.CDLL:
         P = ctypes.POINTER
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         C, S, R = P(locks_cache_t), P(locks_summary_t), P(locks_params_t)
+        T, A, i64 = P(lockskv_tokens_t), P(lockskv_append_t), ctypes.c_int64
         sig = {
             "locks_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "locks_workspace_size": (ctypes.c_int, [C, S, R, P(sz)]),
@@ -97,6 +120,10 @@ def lib() -> ctypes.CDLL:
             "locks_exact_page_lse": (ctypes.c_int, [C, R, vp, vp, vp]),
             "locks_get_device_error": (ctypes.c_int, [vp, P(i32), vp]),
             "locks_decode_step_static": (ctypes.c_int, [C, S, R, vp, vp, vp, vp, vp, vp, vp]),
+            "lockskv_append": (ctypes.c_int, [C, T, A, vp, sz, vp]),
+            "lockskv_read": (ctypes.c_int, [C, T, vp, vp, vp, sz, vp]),
+            "lockskv_prompt_workspace_size": (ctypes.c_int, [C, R, T, P(sz)]),
+            "lockskv_prompt_attend": (ctypes.c_int, [C, R, T, vp, i64, vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -128,7 +155,8 @@ def _ptr(x) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -141,12 +169,48 @@ def _check(status: int, what: str):
 
 def make_cache(k_pool, v_pool, block_table, seq_lens, n_summarized=None, *, pages_total=None,
                num_kv_heads=None) -> locks_cache_t:
-    """C struct for a paged cache given as tensors [pages_total][Hkv][P][d]."""
-    pt, hkv, P, d = (k_pool.shape if k_pool is not None and hasattr(k_pool, "shape")
-                     else (pages_total, num_kv_heads, 64, 128))
+    """C struct for a paged cache given as tensors [pages_total][Hkv][P][d], or as
+    4-bit blocks uint8 [pages_total][Hkv][kv_q4_block_bytes(P)] (v_pool None)."""
+    fmt = LOCKS_KV_BF16
+    if k_pool is not None and hasattr(k_pool, "shape"):
+        if k_pool.dim() == 3:
+            pt, hkv, nbytes = k_pool.shape
+            P, d, fmt = nbytes // 144, 128, LOCKS_KV_Q4
+            if nbytes != kv_q4_block_bytes(P):
+                raise ValueError(f"{nbytes} bytes are no 4-bit block of whole tokens")
+        else:
+            pt, hkv, P, d = k_pool.shape
+    else:
+        pt, hkv, P, d = pages_total, num_kv_heads, 64, 128
     return locks_cache_t(_ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seq_lens),
                          _ptr(n_summarized), int(block_table.shape[0]), int(hkv), int(d), int(P),
-                         int(pt), int(block_table.shape[1]))
+                         int(pt), int(block_table.shape[1]), fmt)
+
+
+def make_tokens(cu_tokens, total: int, max_tokens: int) -> lockskv_tokens_t:
+    """The newest tokens of a batch; cu_tokens None: one per sequence."""
+    return lockskv_tokens_t(_ptr(cu_tokens), int(total), int(max_tokens))
+
+
+def _row_stride(x, what: str) -> int:
+    """Elements between the token rows of x [total][heads][128] (bf16, heads contiguous)."""
+    import torch
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[2] != 128:
+        raise ValueError(f"{what} must be bf16 [tokens][heads][128]")
+    if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != 128):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * 128
+
+
+def make_append(k, v, q=None, q_out=None, rope=None, rotary_dim: int = 0, positions=None,
+                interleaved: bool = False) -> lockskv_append_t:
+    """C struct of what lockskv_append writes, from tensors [total][heads][128]."""
+    return lockskv_append_t(_ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(rope), _ptr(positions),
+                            _row_stride(k, "k"), _row_stride(v, "v"),
+                            _row_stride(q, "q") if q is not None else 0,
+                            _row_stride(q_out, "q_out") if q_out is not None else 0,
+                            q.shape[1] if q is not None else 0, rope.shape[0] if rope is not None else 0,
+                            int(rotary_dim), int(interleaved))
 
 
 def make_summary(basis_t, coeffs, rank: int, dtype: int = LOCKS_DTYPE_BF16) -> locks_summary_t:
@@ -231,3 +295,26 @@ def locks_get_device_error(ws, stream=None) -> int:
     if st not in (LOCKS_OK, LOCKS_ERR_DEVICE):
         raise LocksError(st, "locks_get_device_error")
     return int(code.value)
+
+
+def lockskv_append(cache, tokens, append, ws=None, ws_bytes: int = 0, stream=None):
+    _check(lib().lockskv_append(ctypes.byref(cache), ctypes.byref(tokens), ctypes.byref(append), _ptr(ws),
+                                int(ws_bytes), _stream(stream)), "lockskv_append")
+
+
+def lockskv_read(cache, tokens, k_out, v_out, ws=None, ws_bytes: int = 0, stream=None):
+    _check(lib().lockskv_read(ctypes.byref(cache), ctypes.byref(tokens), _ptr(k_out), _ptr(v_out), _ptr(ws),
+                              int(ws_bytes), _stream(stream)), "lockskv_read")
+
+
+def lockskv_prompt_workspace_size(cache, params, tokens) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lockskv_prompt_workspace_size(ctypes.byref(cache), ctypes.byref(params), ctypes.byref(tokens),
+                                               ctypes.byref(n)), "lockskv_prompt_workspace_size")
+    return int(n.value)
+
+
+def lockskv_prompt_attend(cache, params, tokens, q, q_stride: int, out, lse, ws, ws_bytes: int, stream=None):
+    _check(lib().lockskv_prompt_attend(ctypes.byref(cache), ctypes.byref(params), ctypes.byref(tokens), _ptr(q),
+                                       int(q_stride), _ptr(out), _ptr(lse), _ptr(ws), int(ws_bytes),
+                                       _stream(stream)), "lockskv_prompt_attend")

@@ -15,7 +15,9 @@ from . import locks as L
 class LocksRuntime:
     """Holds a paged cache on ``device`` and calls liblocks.so on it.
 
-    k_pool, v_pool: bf16 [pages_total][Hkv][P][128] with P = 64 or 16;
+    k_pool, v_pool: bf16 [pages_total][Hkv][P][128] with P = 64 or 16; or, for
+    a cache held in 4 bits (LOCKS_KV_Q4), k_pool uint8 [pages_total][Hkv]
+    [kv_q4_block_bytes(P)] and v_pool None.
     block_table int32 [B][max_pages]; seq_lens, n_summarized int32 [B].
     Summaries are allocated here.  bf16: one LOCKS_DTYPE_BF16_PACKED block per
     page-head (basis rows, then coefficients), with ``basis_t`` [pages_total]
@@ -28,17 +30,22 @@ class LocksRuntime:
     kernels, or as two wherever the size limits allow).
     """
 
-    def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
+    def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor | None, block_table: torch.Tensor,
                  seq_lens: torch.Tensor, n_summarized: torch.Tensor, num_q_heads: int, rank: int,
                  budget_tokens: int, scale: float = 0.0, quantized: bool = False, form: str = "auto",
                  split: bool = False):
-        assert k_pool.dtype == torch.bfloat16 and v_pool.dtype == torch.bfloat16
+        if v_pool is None:
+            assert k_pool.dtype == torch.uint8 and k_pool.dim() == 3 and k_pool.is_contiguous()
+        else:
+            assert k_pool.dtype == torch.bfloat16 and v_pool.dtype == torch.bfloat16
         assert block_table.dtype == torch.int32 and seq_lens.dtype == torch.int32
         self.device = k_pool.device
         self.k_pool, self.v_pool = k_pool, v_pool
         self.block_table, self.seq_lens = block_table, seq_lens
         self.n_summarized = n_summarized.to(torch.int32)
-        pt, hkv, P, d = k_pool.shape
+        self.cache = L.make_cache(k_pool, v_pool, block_table, seq_lens, self.n_summarized)
+        pt, hkv, P, d = self.cache.pages_total, self.cache.num_kv_heads, self.cache.page_size, self.cache.head_dim
+        self.page_size = P
         self.batch = block_table.shape[0]
         self.num_kv_heads, self.num_q_heads = hkv, num_q_heads
         self.rank = rank
@@ -57,7 +64,6 @@ class LocksRuntime:
             self.basis_t = self.blocks[:, :, :rank * d].unflatten(-1, (rank, d))
             self.coeffs = self.blocks[:, :, rank * d:].unflatten(-1, (P, rank))
             self.summary = L.make_summary(self.blocks, None, rank, L.LOCKS_DTYPE_BF16_PACKED)
-        self.cache = L.make_cache(k_pool, v_pool, block_table, seq_lens, self.n_summarized)
         flags = {"auto": 0, "unfused": L.LOCKS_FLAG_UNFUSED, "fused": L.LOCKS_FLAG_FUSED}[form]
         self.params = L.make_params(num_q_heads, budget_tokens, scale, flags)
         self.k_max = min(budget_tokens // P, block_table.shape[1])
@@ -71,6 +77,13 @@ class LocksRuntime:
         self.build_ws = torch.zeros(512, dtype=torch.uint8, device=self.device)
         off = (-self.build_ws.data_ptr()) % 256
         self.build_ws = self.build_ws[off:off + 256]
+        # the error word of the calls that write and read tokens, and the prompt
+        # attention's workspace (grown to the largest call seen)
+        self.kv_ws = torch.zeros(512, dtype=torch.uint8, device=self.device)
+        off = (-self.kv_ws.data_ptr()) % 256
+        self.kv_ws = self.kv_ws[off:off + 256]
+        self.prompt_ws = None
+        self._prompt_need = {}
         B = self.batch
         self.sel_pages = torch.zeros((B, hkv, max(self.k_max, 1)), dtype=torch.int32, device=self.device)
         self.sel_count = torch.zeros((B, hkv), dtype=torch.int32, device=self.device)
@@ -126,7 +139,94 @@ class LocksRuntime:
         L.locks_exact_page_lse(self.cache, self.params, q, pl, stream)
         return pl
 
+    def _tokens(self, total: int, cu_tokens: torch.Tensor | None, max_tokens: int | None):
+        if cu_tokens is None:
+            return L.make_tokens(None, total, 1)
+        if cu_tokens.dtype != torch.int32 or cu_tokens.numel() != self.batch + 1 or not cu_tokens.is_contiguous():
+            raise ValueError("cu_tokens must be contiguous int32 [batch + 1]")
+        return L.make_tokens(cu_tokens, total, total if max_tokens is None else max_tokens)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None, *,
+               rope: torch.Tensor | None = None, rotary_dim: int | None = None, interleaved: bool = False,
+               positions: torch.Tensor | None = None, cu_tokens: torch.Tensor | None = None,
+               max_tokens: int | None = None, q_out: torch.Tensor | None = None, stream=None):
+        """Writes the newest tokens of every sequence into the cache (seq_lens
+        already counts them) and rotates their keys and queries.
+
+        k, v: bf16 [total][Hkv][128], q: bf16 [total][Hq][128] (views into a
+        fused projection are fine); rope: float32 [positions][rotary_dim], the
+        cosines, then the sines; cu_tokens int32 [batch + 1] gives each
+        sequence's rows and max_tokens the most that one has (default: total);
+        without cu_tokens there is one token per sequence.  Returns the
+        rotated queries (``q_out``, by default a new tensor; ``q`` itself
+        rotates in place), or None without q."""
+        total = k.shape[0]
+        if k.shape[1] != self.num_kv_heads or v.shape != k.shape:
+            raise ValueError(f"k and v must be [tokens][{self.num_kv_heads}][128]")
+        if q is not None:
+            if q.shape[0] != total or q.shape[1] != self.num_q_heads:
+                raise ValueError(f"q must be [{total}][{self.num_q_heads}][128]")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            elif q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if rope is None:
+            rotary_dim = rotary_dim or 0
+        else:
+            if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+                raise ValueError("rope must be contiguous float32 [positions][rotary_dim]")
+            rotary_dim = rope.shape[1] if rotary_dim is None else rotary_dim
+            if rotary_dim != rope.shape[1]:
+                raise ValueError("rope must have rotary_dim columns")
+        if positions is not None and (positions.dtype != torch.int32 or positions.numel() != total
+                                      or not positions.is_contiguous()):
+            raise ValueError("positions must be contiguous int32 [tokens]")
+        L.lockskv_append(self.cache, self._tokens(total, cu_tokens, max_tokens),
+                         L.make_append(k, v, q, q_out, rope, rotary_dim, positions, interleaved),
+                         self.kv_ws, 256, stream)
+        return q_out
+
+    def read_tokens(self, total: int, *, cu_tokens: torch.Tensor | None = None, max_tokens: int | None = None,
+                    stream=None):
+        """The newest tokens' keys and values as the cache holds them: two new
+        bf16 tensors [total][Hkv][128] (rows of nobody are left unwritten)."""
+        k, v = (torch.empty((total, self.num_kv_heads, 128), dtype=torch.bfloat16, device=self.device)
+                for _ in range(2))
+        L.lockskv_read(self.cache, self._tokens(total, cu_tokens, max_tokens), k, v, self.kv_ws, 256, stream)
+        return k, v
+
+    def prompt_attend(self, q: torch.Tensor, *, cu_tokens: torch.Tensor | None = None,
+                      max_tokens: int | None = None, out=None, lse=None, stream=None):
+        """Causal attention of the newest tokens, already in the cache, over it:
+        q bf16 [total][Hq][128] -> out bf16 [total][Hq][128], lse float32
+        [total][Hq] (new tensors by default)."""
+        total = q.shape[0]
+        if q.shape[1] != self.num_q_heads:
+            raise ValueError(f"q must be [tokens][{self.num_q_heads}][128]")
+        stride = L._row_stride(q, "q")
+        tokens = self._tokens(total, cu_tokens, max_tokens)
+        if out is None:
+            out = torch.empty((total, self.num_q_heads, 128), dtype=torch.bfloat16, device=self.device)
+        if lse is None:
+            lse = torch.empty((total, self.num_q_heads), dtype=torch.float32, device=self.device)
+        need = self._prompt_need.get((total, tokens.max_tokens))
+        if need is None:
+            need = L.lockskv_prompt_workspace_size(self.cache, self.params, tokens)
+            self._prompt_need[(total, tokens.max_tokens)] = need
+        if self.prompt_ws is None or self.prompt_ws.numel() < need:
+            ws = torch.zeros(need + 256, dtype=torch.uint8, device=self.device)
+            off = (-ws.data_ptr()) % 256
+            self.prompt_ws = ws[off:off + need]
+        L.lockskv_prompt_attend(self.cache, self.params, tokens, q, stride, out, lse, self.prompt_ws,
+                                self.prompt_ws.numel(), stream)
+        return out, lse
+
     def device_error(self, stream=None) -> int:
         """LOCKS_DEVERR_* bits set since the last read, by the calls on the
-        main workspace and by the builder (both words are cleared)."""
-        return L.locks_get_device_error(self.ws, stream) | L.locks_get_device_error(self.build_ws, stream)
+        main workspace, by the builder and by the calls on tokens and prompts
+        (all words are cleared)."""
+        err = L.locks_get_device_error(self.ws, stream) | L.locks_get_device_error(self.build_ws, stream)
+        err |= L.locks_get_device_error(self.kv_ws, stream)
+        return err | (L.locks_get_device_error(self.prompt_ws, stream) if self.prompt_ws is not None else 0)
