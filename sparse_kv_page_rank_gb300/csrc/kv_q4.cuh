@@ -36,6 +36,11 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 // Fields 0 and 1 (bits 0-3, 4-7) of both halves of w, each holding code + 8, as
 // fp16 pairs of codes: a field under the exponent of 1024 (or, four bits up, of
 // 64) is the number 1024 + u (64 + u) exactly, from which 1032 (72) is taken.

@@ -23,9 +23,14 @@
 // by more than 2^8 since its last reference.
 //
 // bf16 pages arrive by TMA in the operands' own order (64-column boxes, 128-byte
-// swizzle).  4-bit pages arrive as whole page-heads and are converted to s * code
-// in fp16 (one rounding, 2^-11), with q scaled into fp16 by a power of two and the
-// weights scaled by 2^6, so that weights 2^-30 of the largest still count.
+// swizzle).  4-bit pages arrive as whole page-heads and are converted to fp16, with q
+// scaled into fp16 by a power of two.  A key s * code has up to 14 significant bits:
+// it is held as the nearest half and the remainder, both exact, and S is the sum of
+// the products with both (one half alone would put 2^-11 of sum |q||k| into every
+// logit).  Values are s * code rounded once (2^-11), weights are scaled by 2^6, so
+// that those 2^-30 of the largest still count.  The two operands of the keys leave
+// room for one block of keys in shared memory, which is converted while the products
+// with the values run.
 //
 // Values that a row does not see must not reach it, not even as 0 * NaN: in the
 // blocks that straddle a tile's diagonal or the end of the sequence, value rows past
@@ -48,7 +53,11 @@ constexpr int kRows = 128;                   // rows of a tile
 constexpr int kBlock = 128;                  // keys of a block
 constexpr int kHalf = kBlock * 128;          // bytes of 64 columns of 128 16-bit rows
 constexpr int kOperand = 2 * kHalf;          // one tile of Q, K or V: 32 KiB
-constexpr int kKvStages = 2;
+constexpr int kKvBytes = 4 * kOperand;       // keys and values: two operands each
+constexpr int kKvStages = 2;                 // blocks of values in flight, and of bf16 keys
+template <bool Q4>
+constexpr int kKeyStages = Q4 ? 1 : kKvStages;
+constexpr uint32_t kValues = 2 * kOperand;   // offset of the values behind the keys
 constexpr int kRawSlots = 3;                 // 4-bit pages: 64-token slots of codes
 constexpr int kSkipRing = 4;                 // the copies run at most three blocks ahead of the softmax
 constexpr int kMaxBad = 2 * kRows;           // tokens near a diagonal: no more than a CTA has
@@ -57,7 +66,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;             // S: columns 0 and 128; O: 256 and 384
 
 struct PromptShared {
-  uint64_t q_full, k_full[kKvStages], v_full[kKvStages], k_empty[kKvStages], v_empty[kKvStages];
+  uint64_t q_full, k_full[2], v_full[2], k_empty[2], v_empty[2];
   uint64_t s_full[2], p_ready[2], o_full[2], drain;
   uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
   uint32_t tmem;
@@ -175,7 +184,6 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
       }
       if constexpr (!Q4) {
         const int copies = kPPB - __popc(skip) / (P / 16);
-        uint8_t* kd = kv + st * 2 * kOperand;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {  // keys, then values
           uint64_t* full = v ? &sh.v_full[st] : &sh.k_full[st];
@@ -191,7 +199,7 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
             for (int i = 0; i < kPPB; ++i) {
               if (pg[i] < 0) continue;
               const int y = (pg[i] * a.num_kv_heads + w.hkv) * P;
-              uint8_t* dst = kd + v * kOperand + i * P * 128;
+              uint8_t* dst = kv + v * kValues + st * kOperand + i * P * 128;
               tma_load_2d(dst, v ? tv : tk, full, 0, y);
               tma_load_2d(dst + kHalf, v ? tv : tk, full, 64, y);
             }
@@ -244,8 +252,8 @@ __device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t kv
   const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   for (int n = 0; n < w.j1 - w.j0; ++n) {
     const int st = n % kKvStages;
-    const uint32_t kd = kv + st * 2 * kOperand, vd = kd + kOperand;
-    if (n >= kKvStages && !wait_warp(&sh.k_empty[st], (n / kKvStages - 1) & 1, sh)) return;
+    const uint32_t kd = kv, vd = kv + kValues + st * kOperand;
+    if (n >= 1 && !wait_warp(&sh.k_empty[0], (n - 1) & 1, sh)) return;
 #pragma unroll 1
     for (int hh = 0; hh < 2; ++hh) {
       const int s = 2 * n + hh, rs = s % kRawSlots;
@@ -270,13 +278,20 @@ __device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t kv
           const uint32_t zz = __byte_perm(j < 2 ? z.x : z.y, 0, j & 1 ? 0x3232 : 0x1010);
           uint32_t f[4];
           q4_codes(words[j], f);
-          sts128(kd + (j >> 1) * kHalf + swz(row, (j & 1) * 4 + c), mul_f16x2(f[0], zz), mul_f16x2(f[1], zz),
-                 mul_f16x2(f[2], zz), mul_f16x2(f[3], zz));
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            hi[e] = mul_f16x2(f[e], zz);
+            lo[e] = fma_f16x2(f[e], zz, hi[e] ^ 0x80008000u);  // s * code - hi, exact
+          }
+          const uint32_t at = kd + (j >> 1) * kHalf + swz(row, (j & 1) * 4 + c);
+          sts128(at, hi[0], hi[1], hi[2], hi[3]);
+          sts128(at + kOperand, lo[0], lo[1], lo[2], lo[3]);
         }
       }
     }
     fence_proxy_async();
-    mbar_arrive(&sh.k_full[st]);
+    mbar_arrive(&sh.k_full[0]);
     if (n >= kKvStages && !wait_warp(&sh.v_empty[st], (n / kKvStages - 1) & 1, sh)) return;
 #pragma unroll 1
     for (int hh = 0; hh < 2; ++hh) {
@@ -313,51 +328,61 @@ __device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t kv
 template <bool Q4>
 __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uint32_t kv, uint32_t tmem) {
   constexpr uint32_t kIdS = umma_idesc(kRows, kBlock, !Q4, false), kIdO = umma_idesc(kRows, kHeadDim, !Q4, true);
+  constexpr int kKS = kKeyStages<Q4>;
   const int n_blocks = w.j1 - w.j0;
-  auto scores = [&](int t, int st) {  // S_t = Q_t K^T
-    const uint32_t k = kv + st * 2 * kOperand, qt = q + t * kOperand;
+  auto scores = [&](int t, int n) {  // S_t = Q_t K^T (4-bit pages: both halves of K)
+    const uint32_t k = kv + (n % kKS) * kOperand, qt = q + t * kOperand;
 #pragma unroll
-    for (int s = 0; s < kHeadDim / 16; ++s) {
-      const uint32_t off = (s / 4) * kHalf + (s % 4) * 32;
-      umma_ss(tmem + t * kBlock, umma_desc(qt + off, 16, 1024), umma_desc(k + off, 16, 1024), kIdS, s > 0);
-    }
+    for (int part = 0; part < (Q4 ? 2 : 1); ++part)
+#pragma unroll
+      for (int s = 0; s < kHeadDim / 16; ++s) {
+        const uint32_t off = (s / 4) * kHalf + (s % 4) * 32;
+        umma_ss(tmem + t * kBlock, umma_desc(qt + off, 16, 1024), umma_desc(k + part * kOperand + off, 16, 1024), kIdS,
+                part + s > 0);
+      }
+    umma_commit(&sh.s_full[t]);
+    if (t == w.n_tiles - 1) umma_commit(&sh.k_empty[n % kKS]);
   };
-  auto values = [&](int t, int st, bool first) {  // O_t (+)= P_t V
-    const uint32_t v = kv + st * 2 * kOperand + kOperand;
+  auto values = [&](int t, int n) {  // O_t (+)= P_t V
+    const uint32_t v = kv + kValues + (n % kKvStages) * kOperand;
 #pragma unroll
     for (int s = 0; s < kBlock / 16; ++s)
       umma_ts(tmem + kTmemO + t * kHeadDim, tmem + t * kBlock + s * 8, umma_desc(v + s * 16 * 128, kHalf, 1024), kIdO,
-              !first || s > 0);
+              n > 0 || s > 0);
+    if (t == w.n_tiles - 1) umma_commit(&sh.v_empty[n % kKvStages]);
+    if (n == n_blocks - 1) umma_commit(&sh.o_full[t]);
   };
   bool ok = wait_bar(&sh.q_full, 0, sh) && wait_bar(&sh.k_full[0], 0, sh);
   if (ok) {
     tc_fence_after();
-    for (int t = 0; t < w.n_tiles; ++t) {
-      scores(t, 0);
-      umma_commit(&sh.s_full[t]);
-    }
-    umma_commit(&sh.k_empty[0]);
+    for (int t = 0; t < w.n_tiles; ++t) scores(t, 0);
   }
   for (int n = 0; ok && n < n_blocks; ++n) {
-    const int st = n % kKvStages, sn = (n + 1) % kKvStages;
-    if (!(ok = wait_bar(&sh.v_full[st], (n / kKvStages) & 1, sh))) break;
-    for (int t = 0; t < w.n_tiles; ++t) {
-      if (!(ok = wait_bar(&sh.p_ready[t], n & 1, sh))) break;
-      tc_fence_after();
-      values(t, st, n == 0);
-      if (t == w.n_tiles - 1) umma_commit(&sh.v_empty[st]);
-      if (n + 1 < n_blocks) {
-        if (t == 0) {
-          if (!(ok = wait_bar(&sh.k_full[sn], ((n + 1) / kKvStages) & 1, sh))) break;
-          tc_fence_after();
-        }
-        scores(t, sn);
-        umma_commit(&sh.s_full[t]);
-        if (t == w.n_tiles - 1) umma_commit(&sh.k_empty[sn]);
-      } else {
-        umma_commit(&sh.o_full[t]);
+    if (!(ok = wait_bar(&sh.v_full[n % kKvStages], (n / kKvStages) & 1, sh) && wait_bar(&sh.p_ready[0], n & 1, sh))) break;
+    tc_fence_after();
+    values(0, n);
+    // the next scores of tile 0 and the values of tile 1, whichever can go first
+    bool next = n + 1 < n_blocks, second = w.n_tiles == 2;
+    const bool more = next;
+    uint32_t it = 0;
+    while (next || second) {
+      if (next && mbar_test(&sh.k_full[(n + 1) % kKS], ((n + 1) / kKS) & 1)) {
+        tc_fence_after();
+        scores(0, n + 1);
+        next = false;
+      }
+      if (second && mbar_test(&sh.p_ready[1], n & 1)) {
+        tc_fence_after();
+        values(1, n);
+        second = false;
+      }
+      if (++it > kMbarSpinLimit || *reinterpret_cast<volatile int*>(&sh.abort)) {
+        *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+        ok = false;
+        break;
       }
     }
+    if (ok && more && w.n_tiles == 2) scores(1, n + 1);
   }
   if (!ok) {
     // what was issued must end before its memory is given back
@@ -431,7 +456,7 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
     if (t == 0 && (kv0 + kBlock > first_limit || kv0 + kBlock > w.len || skip)) {
       const int st = n % kKvStages;
       if (!wait_warp(&sh.v_full[st], (n / kKvStages) & 1, sh)) return;
-      uint8_t* v = smem + 2 * kOperand + st * 2 * kOperand + kOperand + row * 128;
+      uint8_t* v = smem + 2 * kOperand + kValues + st * kOperand + row * 128;
       const int at = kv0 + row;
       bool zero = at >= w.kv_end || at >= w.len || ((skip >> (row / 16)) & 1);
       if (!zero && at >= first_limit) {
@@ -573,7 +598,7 @@ __global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PromptShared sh;
   uint8_t* kv = smem + 2 * kOperand;
-  uint8_t* raw = kv + kKvStages * 2 * kOperand;
+  uint8_t* raw = kv + kKvBytes;
   const int tid = threadIdx.x, warp = tid >> 5;
 
   pdl_wait();
@@ -699,7 +724,7 @@ __global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
 }
 
 size_t smem_bytes(bool q4) {
-  return 1024 + 2 * kOperand + (size_t)kKvStages * 2 * kOperand + (q4 ? kRawSlots * kQ4Slot : 0);
+  return 1024 + 2 * kOperand + (size_t)kKvBytes + (q4 ? kRawSlots * kQ4Slot : 0);
 }
 
 template <bool Q4, int P>

@@ -3,8 +3,8 @@ against a 64-bit reference.
 
 Tolerances.  bf16 pages: weights rounded to bf16 (2^-8), outputs to bf16 (2^-8),
 logits sums of 128 exact products in fp32 (at most 2^-23 of the running magnitude
-each: 2^-16 of sum |q||k|).  4-bit pages: keys and values s * code rounded to fp16
-(2^-11 of each, so 2^-11 of sum |q||k| in a logit), weights to fp16 (2^-11).  A logit
+each: 2^-16 of sum |q||k|).  4-bit pages: keys exact, in two halves (256 products,
+2^-15), values s * code rounded to fp16 (2^-11), weights to fp16 (2^-11).  A logit
 error e changes normalised weights by at most 2 e.  fp16 is no finer than 2^-24 below
 2^-14: weights are held times 2^6 relative to a reference that is at most the row's
 maximum, so the largest is at least 2^6 and each weight is off by another 2^-25 / 2^6
@@ -56,7 +56,7 @@ def check(case, new, q, out, lse, first_bad=None):
                 qq = q[row:row + n, g][rows]
                 ro, rl, av, mag, _ = attend64(qq, kk, vv, hidden[rows][:, :kk.shape[0]])
                 m = kk.shape[0]
-                e = 2.0 ** -16 * mag + 2.0 ** -22 * (mag + 16) + (2.0 ** -11 * mag if q4 else 0)
+                e = 2.0 ** (-15 if q4 else -16) * mag + 2.0 ** -22 * (mag + 16)
                 to = 2.0 ** -8 * ro.abs() + ((2.0 ** -10 if q4 else 2.0 ** -8) + 2 * e + m * 2.0 ** -23)[:, None] * av
                 if q4:
                     to = to + m * 2.0 ** -31 * vv.abs().max()
