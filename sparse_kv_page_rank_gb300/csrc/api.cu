@@ -39,7 +39,7 @@ struct Plan {
   size_t tk_keys = 0;
   int sparse_cluster = 1, dense_cluster = 1, dense_nc = 1, lse_splits = 1;
   // LOCKS_KV_Q4 caches: clusters, CTAs and tiles per turn of attend_q4.cu
-  int q4_sparse_cluster = 1, q4_sparse_tiles = 1, q4_dense_cluster = 1, q4_dense_nc = 1, q4_dense_tiles = 1;
+  int q4_sparse_cluster = 1, q4_sparse_tiles = 1, q4_dense_ctas = 0, q4_dense_tiles = 1;
   bool fused = false;     // decode step as scan + one attention kernel that selects the pages itself
   int fused_cluster = 1;
   size_t off_err = 0, off_cnt_tk = 0, off_cnt_att = 0, off_shat = 0, off_part = 0, off_ckey = 0,
@@ -97,37 +97,27 @@ float scale_of(const locks_params_t* p) {
 }
 
 // Launch shapes of attend_q4.cu.  A warp takes 64 tokens at a time where a CTA has
-// at least two turns of them for its seven warps, else 16 tokens, so that a few
+// at least two turns of them for its six warps, else 16 tokens, so that a few
 // pages still keep every warp busy.
-constexpr long long kQ4WholeSlots = 14;
+constexpr long long kQ4WholeSlots = 12;
 
 void plan_q4(const locks_cache_t* c, Plan& pl, int sms, long long max_tiles, int ppt) {
   const int P = c->page_size;
-  const long long BH = pl.BH, resident = (long long)attend_q4_ctas_per_sm(pl.G) * sms;
+  const long long BH = pl.BH;
   auto tiles_for = [](long long slots_per_cta) { return slots_per_cta >= kQ4WholeSlots ? 4 : 1; };
   {
     // page list: one cluster per problem, the largest with which all are resident at once
     const long long slots = ((long long)pl.k_max + 2 + ppt - 1) / ppt;
-    int cs = attend_q4_max_cluster(kAttendSparse, pl.G, P, 1);
-    while (cs > 1 && (cs > slots || BH > attend_q4_active_clusters(kAttendSparse, pl.G, P, 1, cs))) cs /= 2;
+    int cs = 16;
+    while (cs > 1 && (cs > slots || BH > attend_q4_active_clusters(pl.G, P, 1, cs))) cs /= 2;
     pl.q4_sparse_cluster = cs;
     pl.q4_sparse_tiles = tiles_for((slots + cs - 1) / cs);
   }
   {
-    // every page: the (cluster, clusters per problem) with the most CTAs in one
-    // wave, none with less than two slots; among equals the larger cluster
-    const int cs_max = attend_q4_max_cluster(kAttendDense, pl.G, P, 4);
-    const long long want = std::max<long long>(1, std::min<long long>(resident / BH, (max_tiles + 1) / 2));
-    long long best = 0;
-    for (int cs = cs_max; cs >= 1; cs /= 2) {
-      const long long nc = want / cs;
-      if (nc >= 1 && cs * nc > best) {
-        best = cs * nc;
-        pl.q4_dense_cluster = cs;
-        pl.q4_dense_nc = (int)nc;
-      }
-    }
-    pl.q4_dense_tiles = tiles_for((max_tiles + best - 1) / best);
+    // every page: as many CTAs as are resident at once, but no more than slots
+    const long long slots = BH * max_tiles;
+    pl.q4_dense_ctas = (int)std::min<long long>((long long)kQ4CtasPerSm * sms, slots);
+    pl.q4_dense_tiles = tiles_for(slots / pl.q4_dense_ctas);
   }
 }
 
@@ -232,10 +222,12 @@ Plan make_plan(const locks_cache_t* c, const locks_params_t* p) {
     off = align_up(off + std::max<size_t>(bytes, 1));
     return o;
   };
-  const int nc = is_q4(c) ? pl.q4_dense_nc : pl.dense_nc;
+  // partial results of the dense decode, and its tickets
+  const long long parts = is_q4(c) ? 2LL * pl.q4_dense_ctas : BH * pl.dense_nc;
+  const long long tickets = BH + 2LL * pl.q4_dense_ctas;
   pl.off_err = take(sizeof(int));
   pl.off_cnt_tk = take(sizeof(unsigned) * BH);
-  pl.off_cnt_att = take(sizeof(unsigned) * BH);
+  pl.off_cnt_att = take(sizeof(unsigned) * tickets);
   pl.off_shat = take(sizeof(float) * BH * c->max_pages * pl.G);
   pl.off_part = take(sizeof(float2) * BH * pl.n_scan * pl.G);
   pl.off_ckey = take(sizeof(uint32_t) * BH * pl.n_tk * std::max(pl.k_max, 1));
@@ -243,8 +235,8 @@ Plan make_plan(const locks_cache_t* c, const locks_params_t* p) {
   pl.off_sel = take(sizeof(int32_t) * BH * std::max(pl.k_max, 1));
   pl.off_selcnt = take(sizeof(int32_t) * BH);
   pl.off_selphys = take(sizeof(int32_t) * BH * std::max(pl.k_max, 1));
-  pl.off_pml = take(sizeof(float2) * BH * nc * pl.G);
-  pl.off_po = take(sizeof(float) * BH * nc * pl.G * kHeadDim);
+  pl.off_pml = take(sizeof(float2) * parts * pl.G);
+  pl.off_po = take(sizeof(float) * parts * pl.G * kHeadDim);
   pl.total = off;
   return pl;
 }
@@ -429,8 +421,8 @@ locks_status_t run_attend(const locks_cache_t* c, const locks_params_t* p, const
       a.cluster = a.n_splits = pl.q4_sparse_cluster;
       tiles = pl.q4_sparse_tiles;
     } else if (mode == kAttendDense) {
-      a.cluster = pl.q4_dense_cluster;
-      a.n_splits = pl.q4_dense_cluster * pl.q4_dense_nc;
+      a.cluster = 1;
+      a.n_splits = pl.q4_dense_ctas;
       tiles = pl.q4_dense_tiles;
     }
     return cuda_status(launch_attend_q4(a, mode, tiles, st));

@@ -13,13 +13,14 @@
 // tile (2304 bytes) arrives every ~98 clocks per SM at the measured copy rate, in
 // which its four schedulers issue ~390 warp instructions; a tile costs a warp
 // about 220, so the codes have to be taken apart cheaply:
-//  - Codes are stored as u = code + 8.  A pair of 4-bit fields under a fixed fp16
-//    exponent is the pair (64 + u) or (1024 + u) exactly: one logical operation.
-//  - Keys: the matrix instruction runs on (64 + u) = code + 72 and its accumulator
-//    starts at -72 sum_d q_d (per head and scale group), so nothing is subtracted
-//    from the codes.  Values, whose sums run over all tokens, are freed of the
-//    offset by one packed subtraction (an offset carried through thousands of
-//    accumulations would cost digits).
+//  - Codes are stored as u = code + 8.  A 4-bit field under a fixed fp16 exponent is
+//    1024 + u (or, four bits up, 64 + u) exactly: one logical operation for two.
+//  - Keys: the matrix instruction runs on 64 + u = code + 72 and its accumulator
+//    starts at -72 sum_d q_d (per head and scale group), which takes the offset out.
+//    Values, whose sums run over all tokens, are freed of it by a packed subtraction
+//    (an offset carried through thousands of accumulations would cost digits).
+//    e4m3 operands would need fewer operations (0000uuuu is the number u 2^-9), but
+//    this instruction has no 8-bit form of its own here: 128K took 46 us, not 42.
 //  - The products have M = tokens (or dimensions) and N = 8 query heads, so that
 //    the group's few heads sit on the instruction's short side, and the pages store
 //    the codes in the order in which a lane needs them: 16 bytes per lane, 512
@@ -34,14 +35,22 @@
 // largest value scale seen, so that weight * scale stays below 2^16 and weights
 // 2^-30 below the largest still count.
 //
-// Work split: grid (CS * NC, B * Hkv), clusters of CS CTAs, as attend.cu: each CTA
-// takes a contiguous range of the problem's pages.  Eight warps: one issues the
-// bulk copies of whole page-heads (9216 or 2304 contiguous bytes) into a ring of
-// 64-token slots, seven consume.  With many pages per CTA a warp takes a whole slot
-// (one maximum and at most one rescale per 64 tokens); with few, 16 tokens, so that
-// all warps work on two slots.  Partial states meet in shared memory, then
-// across the cluster, then (several clusters per problem) in the workspace, where
-// the last cluster to finish joins them.
+// Buffers.  Every warp copies for itself: its lane 0 issues bulk copies of whole pages
+// into the warp's own two 64-token buffers (9216 or 4 x 2304 contiguous bytes; with
+// few pages per CTA eight 16-token buffers, so that a page occupies four warps).  A
+// warp waits for its own copies in order and refills a buffer only when it is done
+// with it, so no warp waits for another.  Two CTAs of six warps per SM hold 221 KB of
+// buffers, half of them in flight at any time.
+//
+// Work split.  Over every page: the 64-token slots of all sequences and heads in one
+// line, cut into equal parts, one per CTA (two CTAs per SM), so that ragged lengths and
+// any number of problems fill every SM.  A CTA whose part ends inside a problem writes
+// its partial (R, sum, O) to the workspace; the last CTA of a problem to finish joins
+// them (in two levels where they would be many).  Over a page list, a few pages of
+// each problem: one thread-block cluster per problem, whose CTAs push their partial
+// states to each other through distributed shared memory.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "kv_q4.cuh"
@@ -50,20 +59,21 @@ namespace locks {
 
 namespace {
 
-constexpr int kW = 7;                           // consumer warps
-constexpr int kThreads = (kW + 1) * 32;         // and the producer
-constexpr int kStages = 11;                     // 101,376 bytes: two CTAs per SM
-constexpr int kOStride = 132;                   // padded row of a warp's outputs (floats)
-constexpr int kRing = kStages * kQ4Slot;
-constexpr int kRecvMl = 16 * 16 * 8;            // their (R, sum), [rank][head]
+constexpr int kW = 6;                                    // warps
+constexpr int kThreads = kW * 32;
+constexpr int kTileBytes = LOCKS_KV_Q4_BLOCK_BYTES(16);  // 16 tokens
+constexpr int kWarpTiles = 8;                            // tiles of buffers per warp
+constexpr int kRing = kW * kWarpTiles * kTileBytes;      // 110,592 bytes: two CTAs per SM
+constexpr int kOStride = 132;                            // padded row of a warp's outputs (floats)
+constexpr int kRecvMl = 16 * 16 * 8;                     // (R, sum) received from the cluster, [rank][head]
 constexpr int kSmem = kRing + 128;
 
 struct Q4Shared {
-  uint64_t full[kStages], empty[kStages], recv;
-  int len[kStages][4], lp[kStages];
+  uint64_t full[kW][kWarpTiles], recv, join;
+  int len[kW][kWarpTiles][4], lp[kW][kWarpTiles];
   float m[kW][16], l[kW][16], f[kW][16];
   float cta_m[16], cta_l[16];
-  int failed, last;
+  int last;
 };
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -71,186 +81,99 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(x));
   return d;
 }
-// Field i (0..3) of both halves of w as the fp16 pair 64 + u (exact).
-template <int I>
-__device__ __forceinline__ uint32_t field64(uint32_t w) {
-  const uint32_t x = I == 0 ? w << 4 : (I == 1 ? w : (I == 2 ? w >> 4 : w >> 8));
-  return (x & 0x00f000f0u) | 0x54005400u;
+// The four fields of both halves of w as fp16 pairs 64 + u (exact).
+__device__ __forceinline__ void fields64(uint32_t w, uint32_t (&f)[4]) {
+  const uint32_t v = w >> 8;
+  f[0] = sub_f16x2(field_under<0x000f000fu, 0x64006400u>(w), 0x63806380u);  // 1024 + u, less 960
+  f[1] = field_under<0x00f000f0u, 0x54005400u>(w);
+  f[2] = sub_f16x2(field_under<0x000f000fu, 0x64006400u>(v), 0x63806380u);
+  f[3] = field_under<0x00f000f0u, 0x54005400u>(v);
 }
+// D = A B + C with an accumulator that is not overwritten.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
 // Mask of a packed pair of tokens (t, t + 1) that keeps those inside `len`.
 __device__ __forceinline__ uint32_t pair_mask(int t, int len) {
   return (t < len ? 0x0000ffffu : 0u) | (t + 1 < len ? 0xffff0000u : 0u);
 }
 
-// TPU: 16-token tiles per warp and turn (4: a whole slot, 1: a quarter).
-// NT: blocks of 8 query heads.
-template <int MODE, int P, int TPU, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_q4_kernel(const AttendArgs a) {
-  constexpr bool LSE = MODE == kAttendPageLse;
-  constexpr int kPPS = kPage / P;  // pages per slot
-  constexpr uint32_t kPageBytes = LSE ? 72 * P : 144 * P;
-  using At = Q4Tile<P>;
-  extern __shared__ __align__(128) uint8_t ring_raw[];
-  __shared__ Q4Shared sh;
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ring_raw) + 127) & ~uintptr_t(127));
-  const uint32_t rbase = smem_u32(ring);
+// One warp's share of a problem.  TPU: 16-token tiles per turn (one buffer); NT:
+// blocks of 8 query heads.
+template <int P, int TPU, int NT, bool LSE>
+struct Q4Warp {
+  static constexpr int TP = P / 16;                        // tiles of a page
+  static constexpr int kPages = TP >= TPU ? 1 : TPU / TP;  // pages a unit touches
+  static constexpr int kUPP = TP >= TPU ? TP / TPU : 1;    // units of a page
+  static constexpr int kBufs = kWarpTiles / TPU;
+  static constexpr int kBufBytes = TPU * kTileBytes;
+  // one block of heads has the registers to start its products at the codes' offset
+  static constexpr bool kBiased = NT == 1;
+  static_assert(!LSE || (kPages == 1 && kUPP == 1), "a unit of the page LSE is one page");
+  using At = Q4Tile<P, TPU>;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x, bh = blockIdx.y;
-  const int b = bh / a.num_kv_heads, hkv = bh % a.num_kv_heads;
-  const int G = a.group, Hq = a.num_kv_heads * G;
+  Q4Shared& sh;
+  const int warp, lane, g, c, group;
+  const uint32_t wbase;  // this warp's buffers
+  // q of head 8 nt + g, dimensions 32 j + 8 c .. + 7, scaled into fp16
+  uint32_t qf[NT][4][4];
+  float init[NT][4][4];  // -72 sum of q over the scale group's 32 dimensions, heads 2c, 2c + 1 (twice)
+  float fac[NT][2];      // logit factor of heads 2c, 2c + 1
+  float R[NT][2], l[NT][2];  // their softmax reference (base 2) and sum
+  float o[4][2][NT][4];  // their outputs: dimensions 32 j + 4 g + 2 half, + 1 (rows)
+  int x;                 // exponent offset of the weights, lowered by large value scales
+  int seq;               // units consumed so far: buffer seq % kBufs, phase seq / kBufs
+  float* page_lse;       // LSE only
+  size_t lse_stride;
 
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], TPU == 4 ? 1 : 4);
+  __device__ __forceinline__ Q4Warp(Q4Shared& s, uint32_t ring, int grp)
+      : sh(s), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2), c(threadIdx.x & 3),
+        group(grp), wbase(ring + (threadIdx.x >> 5) * kWarpTiles * kTileBytes), x(15), seq(0), page_lse(nullptr),
+        lse_stride(0) {}
+
+  __device__ __forceinline__ void reset() {
+    x = 15;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      R[nt][0] = R[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][hf][nt][e] = 0.f;
     }
-    mbar_init(&sh.recv, a.cluster);
-    fence_mbar_init();
-    sh.failed = 0;
-  }
-  __syncthreads();
-  if (!LSE) cluster_arrive();  // matched by the wait before the first remote access
-  pdl_wait();
-
-  int L = a.seq_lens[b];
-  if (L < 0 || L > a.max_pages * P) {
-    if (tid == 0 && split == 0) set_error(a.err, LOCKS_DEVERR_LENGTHS);
-    L = L < 0 ? 0 : a.max_pages * P;
-  }
-  const int n_pages = (L + P - 1) / P;
-  int ns = 0, cnt = 0, n_items = n_pages;
-  if (MODE == kAttendSparse) {
-    const int cap = min(L / P, a.max_pages);
-    ns = min(max(a.n_summarized[b], 0), cap);
-    const int kcap = min(a.k_max, ns);
-    cnt = a.sel_count[bh];
-    if (cnt < 0 || cnt > kcap) {
-      if (tid == 0) set_error(a.err, LOCKS_DEVERR_SEL_PAGE);
-      cnt = cnt < 0 ? 0 : kcap;
-    }
-    n_items = cnt + (n_pages - ns);
-  }
-  // this CTA's pages: a whole number of slots
-  const int ipc = ((n_items + a.n_splits - 1) / a.n_splits + kPPS - 1) / kPPS * kPPS;
-  const int i0 = min(n_items, split * ipc), i1 = min(n_items, i0 + ipc);
-  const int n_slots = (i1 - i0 + kPPS - 1) / kPPS;
-
-  float R[NT][2], l[NT][2];   // softmax reference (base 2) and sum of heads 8 nt + 2c, + 1
-  float o[4][2][NT][4];       // outputs: dimensions 32 j + 4 g + 2 half, + 1 (rows) of those heads
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    R[nt][0] = R[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][hf][nt][e] = 0.f;
   }
 
-  if (warp == kW) {
-    // ---- producer: resolve 32 pages at a time, then copy them slot by slot ----
-    bool ok = true;
-    int issued = 0;
-    for (int base = 0; base < i1 - i0 && ok; base += 32) {
-      const int i = i0 + base + lane;
-      int phys = -1, len = 0, lp = -1;
-      if (i < i1) {
-        if (MODE == kAttendSparse && i < cnt) {
-          lp = a.sel_pages[(size_t)bh * a.k_max + i];
-          if (a.sel_phys) phys = a.sel_phys[(size_t)bh * a.k_max + i];
-          if (lp < 0 || lp >= ns) {
-            set_error(a.err, LOCKS_DEVERR_SEL_PAGE);
-            lp = -1;
-          } else if (!a.sel_phys) {
-            phys = a.block_table[(size_t)b * a.max_pages + lp];
-          }
-        } else {
-          lp = MODE == kAttendSparse ? ns + (i - cnt) : i;
-          phys = a.block_table[(size_t)b * a.max_pages + lp];
-        }
-        if (lp >= 0 && (phys < 0 || phys >= a.pages_total)) {
-          set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
-          lp = -1;
-        }
-        if (lp >= 0) len = min(P, L - lp * P);
-      }
-      const int here = min(32, i1 - i0 - base);
-      for (int k = 0; k < here; k += kPPS) {
-        const int s = (base + k) / kPPS, st = s % kStages;
-        if (s >= kStages && !mbar_wait(&sh.empty[st], (s / kStages - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int w = 0; w < kPPS; ++w) {
-          const int ln = __shfl_sync(0xffffffffu, len, (k + w) & 31);
-          if (lane == 0) sh.len[st][w] = k + w < here ? ln : 0;
-          if (k + w < here && ln > 0) bytes += kPageBytes;
-        }
-        const int lp0 = __shfl_sync(0xffffffffu, lp, k);
-        if (lane == 0) {
-          if (kPPS == 1) sh.lp[st] = lp0;
-          mbar_arrive_expect_tx(&sh.full[st], bytes);
-        }
-        if (LSE && kPPS > 1) {
-          // the pages of the slot in the order of the list; page numbers follow from the first item
-          if (lane == 0) sh.lp[st] = i0 + base + k;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int w = 0; w < kPPS; ++w) {
-          const int ln = __shfl_sync(0xffffffffu, len, (k + w) & 31);
-          const int ph = __shfl_sync(0xffffffffu, phys, (k + w) & 31);
-          if (lane == 0 && k + w < here && ln > 0)
-            bulk_load(rbase + st * kQ4Slot + w * LOCKS_KV_Q4_BLOCK_BYTES(P),
-                      reinterpret_cast<const uint8_t*>(a.k_pool16) +
-                          ((size_t)ph * a.num_kv_heads + hkv) * (size_t)LOCKS_KV_Q4_BLOCK_BYTES(P),
-                      kPageBytes, &sh.full[st]);
-        }
-        issued = s + 1;
-      }
-    }
-    if (!ok) {
-      // consumers gave up: let the copies in flight land before the ring is reused
-      if (lane == 0) {
-        set_error(a.err, kDevErrTimeout);
-        sh.failed = 1;
-        for (int s = max(0, issued - kStages); s < issued; ++s) (void)mbar_wait(&sh.full[s % kStages], (s / kStages) & 1);
-      }
-    }
-  } else {
-    // ---- consumers ----
-    // q of head 8 nt + g, dimensions 32 j + 8 c .. + 7, scaled into fp16
-    uint32_t qf[NT][4][4];
-    float init[NT][4][2];   // -72 sum of q over the group's 32 dimensions, heads 2c, 2c + 1
-    float fac[NT][2];       // logit factor of heads 2c, 2c + 1
+  // The group's queries (rows q, bf16).
+  __device__ __forceinline__ void load_q(const uint16_t* q, float scale_log2) {
+    const int G = group;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int h = 8 * nt + g;
       uint4 raw[4];
-      float mx = 0.f;
+      uint32_t mx = 0;  // largest magnitude, as bf16 bits
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         raw[j] = make_uint4(0, 0, 0, 0);
         if (h < G)
-          raw[j] = __ldg(reinterpret_cast<const uint4*>(a.q + ((size_t)b * Hq + (size_t)hkv * G + h) * kHeadDim +
-                                                        32 * j + 8 * c));
+          raw[j] = __ldg(reinterpret_cast<const uint4*>(q + h * kHeadDim + 32 * j + 8 * c));
         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+        for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       // 2^-e with e the exponent of the largest element (0 for a zero or
       // non-finite row), kept away from the ends of fp32's range
-      int e = (int)(__float_as_uint(mx) >> 23) - 127;
-      e = mx == 0.f || e > 127 ? 0 : min(max(e, -100), 126);
+      int e = (int)(mx >> 7) - 127;
+      e = mx == 0 || e > 127 ? 0 : min(max(e, -100), 126);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       float sum[4];
 #pragma unroll
@@ -264,226 +187,311 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_q4_kernel(co
         }
         sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
         sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+        if constexpr (kBiased)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) init[nt][j][k] = -72.f * __shfl_sync(0xffffffffu, sum[j], 8 * c + 4 * k);
+          for (int k = 0; k < 2; ++k)
+            init[nt][j][k] = init[nt][j][2 + k] = -72.f * __shfl_sync(0xffffffffu, sum[j], 8 * c + 4 * k);
       }
-      const float up = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+      const float up = scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
       for (int k = 0; k < 2; ++k) fac[nt][k] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * k);
     }
+  }
 
-    float m[NT][2];
+  // One unit in buffer `buf`; WHOLE: all its tokens are inside the sequence, else
+  // left[t] counts those of tile t (two copies of the code, so that whole units
+  // carry no masks).
+  template <bool WHOLE>
+  __device__ __forceinline__ void unit(uint32_t base, int buf, const int (&left)[TPU]) {
+    float sc[TPU][NT][4];
+    float mx[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
-    int x = 15;  // exponent offset of the weights, lowered by large value scales
-
-    const int n_units = TPU == 4 ? n_slots : 4 * n_slots;
-    for (int u = warp; u < n_units; u += kW) {
-      const int s = TPU == 4 ? u : u >> 2, st = s % kStages, t0 = TPU == 4 ? 0 : u & 3;
-      if (!mbar_wait(&sh.full[st], (s / kStages) & 1)) {
-        if (lane == 0) {
-          set_error(a.err, kDevErrTimeout);
-          sh.failed = 1;
+    for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+    // ---- logits of the unit's tokens (rows g, g + 8 of each tile) ----
+#pragma unroll
+    for (int t = 0; t < TPU; ++t) {
+      const uint4 k0 = lds128(base + At::key_codes(t) + lane * 16), k1 = lds128(base + At::key_codes(t) + 512 + lane * 16);
+      const uint2 s0 = lds64(base + At::key_scales(t) + g * 8), s1 = lds64(base + At::key_scales(t) + 64 + g * 8);
+      const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+      const float z0[4] = {f16_lo(s0.x), f16_hi(s0.x), f16_lo(s0.y), f16_hi(s0.y)};
+      const float z1[4] = {f16_lo(s1.x), f16_hi(s1.x), f16_lo(s1.y), f16_hi(s1.y)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t f0[4], f1[4];
+        if constexpr (kBiased) {
+          fields64(kw0[j], f0);
+          fields64(kw1[j], f1);
+        } else {
+          q4_codes01(kw0[j], f0[0], f0[1]);
+          q4_codes01(kw0[j] >> 8, f0[2], f0[3]);
+          q4_codes01(kw1[j], f1[0], f1[1]);
+          q4_codes01(kw1[j] >> 8, f1[2], f1[3]);
         }
-        break;
-      }
-      const uint32_t base = rbase + st * kQ4Slot;
-      // tokens of the tile, or of the slot at P = 64 (from its first token)
-      int len[TPU];
-      bool whole = true, any = false;
 #pragma unroll
-      for (int t = 0; t < TPU; ++t) {
-        const int ln = P == 64 ? sh.len[st][0] - 16 * (t0 + t) : sh.len[st][t0 + t];
-        len[t] = ln;
-        whole &= ln >= 16;
-        any |= ln > 0;
-      }
-      if (any) {
-        float sc[TPU][NT][4];
-        float mx[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
-        // ---- logits of the unit's tokens (rows g, g + 8 of each tile) ----
-#pragma unroll
-        for (int t = 0; t < TPU; ++t) {
-          const uint4 k0 = lds128(base + At::key_codes(t0 + t) + lane * 16), k1 = lds128(base + At::key_codes(t0 + t) + 512 + lane * 16);
-          const uint2 s0 = lds64(base + At::key_scales(t0 + t) + g * 8), s1 = lds64(base + At::key_scales(t0 + t) + 64 + g * 8);
-          const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
-          const float z0[4] = {f16_lo(s0.x), f16_hi(s0.x), f16_lo(s0.y), f16_hi(s0.y)};
-          const float z1[4] = {f16_lo(s1.x), f16_hi(s1.x), f16_lo(s1.y), f16_hi(s1.y)};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a00 = field64<0>(kw0[j]), a01 = field64<1>(kw0[j]), a02 = field64<2>(kw0[j]), a03 = field64<3>(kw0[j]);
-            const uint32_t a10 = field64<0>(kw1[j]), a11 = field64<1>(kw1[j]), a12 = field64<2>(kw1[j]), a13 = field64<3>(kw1[j]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float acc[4] = {init[nt][j][0], init[nt][j][1], init[nt][j][0], init[nt][j][1]};
-              mma_16816_f16(acc, a00, a10, a01, a11, qf[nt][j][0], qf[nt][j][1]);
-              mma_16816_f16(acc, a02, a12, a03, a13, qf[nt][j][2], qf[nt][j][3]);
-              if (j == 0) {
-                sc[t][nt][0] = z0[0] * acc[0];
-                sc[t][nt][1] = z0[0] * acc[1];
-                sc[t][nt][2] = z1[0] * acc[2];
-                sc[t][nt][3] = z1[0] * acc[3];
-              } else {
-                sc[t][nt][0] = fmaf(z0[j], acc[0], sc[t][nt][0]);
-                sc[t][nt][1] = fmaf(z0[j], acc[1], sc[t][nt][1]);
-                sc[t][nt][2] = fmaf(z1[j], acc[2], sc[t][nt][2]);
-                sc[t][nt][3] = fmaf(z1[j], acc[3], sc[t][nt][3]);
-              }
-            }
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4];
+          if constexpr (kBiased) {
+            mma_from(acc, f0[0], f1[0], f0[1], f1[1], qf[nt][j][0], qf[nt][j][1], init[nt][j]);
+          } else {
+            acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+            mma_16816_f16(acc, f0[0], f1[0], f0[1], f1[1], qf[nt][j][0], qf[nt][j][1]);
           }
-          if (!whole) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (g >= len[t]) sc[t][nt][0] = sc[t][nt][1] = -INFINITY;
-              if (g + 8 >= len[t]) sc[t][nt][2] = sc[t][nt][3] = -INFINITY;
-            }
+          mma_16816_f16(acc, f0[2], f1[2], f0[3], f1[3], qf[nt][j][2], qf[nt][j][3]);
+          if (j == 0) {
+            sc[t][nt][0] = z0[0] * acc[0];
+            sc[t][nt][1] = z0[0] * acc[1];
+            sc[t][nt][2] = z1[0] * acc[2];
+            sc[t][nt][3] = z1[0] * acc[3];
+          } else {
+            sc[t][nt][0] = fmaf(z0[j], acc[0], sc[t][nt][0]);
+            sc[t][nt][1] = fmaf(z0[j], acc[1], sc[t][nt][1]);
+            sc[t][nt][2] = fmaf(z1[j], acc[2], sc[t][nt][2]);
+            sc[t][nt][3] = fmaf(z1[j], acc[3], sc[t][nt][3]);
           }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) mx[nt][k] = fmaxf(mx[nt][k], fmaxf(sc[t][nt][k], sc[t][nt][2 + k]));
         }
+      }
+      if constexpr (!WHOLE) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (g >= left[t]) sc[t][nt][0] = sc[t][nt][1] = -INFINITY;
+          if (g + 8 >= left[t]) sc[t][nt][2] = sc[t][nt][3] = -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) mx[nt][k] = fmaxf(mx[nt][k], fmaxf(sc[t][nt][k], sc[t][nt][2 + k]));
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 4));
+        mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 8));
+        mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 16));
+        mx[nt][k] *= fac[nt][k];  // the factor is positive
+      }
+    if constexpr (LSE) {
+      // a unit is one page (a slot of P = 64, a tile of P = 16)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float ps = 0.f;
+#pragma unroll
+          for (int t = 0; t < TPU; ++t)
+            ps += fast_exp2(fmaf(sc[t][nt][k], fac[nt][k], -mx[nt][k])) +
+                  fast_exp2(fmaf(sc[t][nt][2 + k], fac[nt][k], -mx[nt][k]));
+          ps += __shfl_xor_sync(0xffffffffu, ps, 4);
+          ps += __shfl_xor_sync(0xffffffffu, ps, 8);
+          ps += __shfl_xor_sync(0xffffffffu, ps, 16);
+          const int h = 8 * nt + 2 * c + k;
+          if (g == 0 && h < group) {
+            page_lse[(size_t)h * lse_stride + sh.lp[warp][buf]] = (mx[nt][k] + fast_log2(ps)) * kLn2;
+          }
+        }
+    } else {
+      int xn;
+      // ---- the weights' exponent offset: the largest value scale, below 2^(e+1),
+      // times weights of up to 2^x stays below 2^15 ----
+      {
+        uint32_t top = 0;
+        if (lane < 8 * TPU) {
+          const int t = lane >> 3;  // this lane's 16 bytes of scales
+          uint4 w = lds128(base + At::value_scales(t) + (lane & 7) * 16);
+          if constexpr (!WHOLE) {
+            // each word: tokens 8 (lane%2) + (lane%8)/2 2, + 1 of tile t
+            const int ln = P == 64 ? sh.len[warp][buf][0] - 16 * t : sh.len[warp][buf][t];
+            const uint32_t msk = pair_mask(8 * (lane & 1) + 2 * ((lane & 7) >> 1), ln);
+            w.x &= msk; w.y &= msk; w.z &= msk; w.w &= msk;
+          }
+          const uint32_t v0 = __vmaxu2(w.x, w.y), v1 = __vmaxu2(w.z, w.w);
+          const uint32_t v = __vmaxu2(v0, v1);
+          top = max(v & 0xffffu, v >> 16);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        // half bits -> exponent; a NaN scale (its product is NaN anyway) counts as the largest
+        const int e = min((int)(top >> 10), 29) - 15;
+        xn = min(x, min(15, 14 - e));
+      }
+      bool moved = false;
+      float Rn[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          Rn[nt][k] = fmaxf(R[nt][k] + (float)x, mx[nt][k]) - (float)xn;
+          moved |= Rn[nt][k] != R[nt][k];
+        }
+      if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 4));
-            mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 8));
-            mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 16));
-            mx[nt][k] *= fac[nt][k];  // the factor is positive
-          }
-        if constexpr (LSE) {
-          // a unit is one page (a slot of P = 64, a tile of P = 16)
+            const float al = Rn[nt][k] == -INFINITY ? 1.f : fast_exp2(R[nt][k] - Rn[nt][k]);
+            R[nt][k] = Rn[nt][k];
+            l[nt][k] *= al;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float ps = 0.f;
-#pragma unroll
-              for (int t = 0; t < TPU; ++t)
-                ps += fast_exp2(fmaf(sc[t][nt][k], fac[nt][k], -mx[nt][k])) +
-                      fast_exp2(fmaf(sc[t][nt][2 + k], fac[nt][k], -mx[nt][k]));
-              ps += __shfl_xor_sync(0xffffffffu, ps, 4);
-              ps += __shfl_xor_sync(0xffffffffu, ps, 8);
-              ps += __shfl_xor_sync(0xffffffffu, ps, 16);
-              const int h = 8 * nt + 2 * c + k;
-              if (g == 0 && h < G) {
-                const int lp = sh.lp[st] + (kPPS > 1 ? t0 : 0);
-                a.page_lse[((size_t)b * Hq + (size_t)hkv * G + h) * a.max_pages + lp] = (mx[nt][k] + fast_log2(ps)) * kLn2;
-              }
-            }
-        } else {
-          // ---- the weights' exponent offset: the largest value scale, below 2^(e+1),
-          // times weights of up to 2^x stays below 2^15 ----
-          {
-            uint32_t top = 0;
-            if (TPU == 4 || lane < 8) {
-              const int t = TPU == 4 ? lane >> 3 : 0;  // this lane's 16 bytes of scales
-              uint4 w = lds128(base + At::value_scales(t0 + t) + (lane & 7) * 16);
-              if (!whole) {
-                // each word: tokens 8 (lane%2) + (lane%8)/2 2, + 1 of tile t
-                const int ln = P == 64 ? sh.len[st][0] - 16 * (t0 + t) : sh.len[st][t0 + t];
-                const uint32_t msk = pair_mask(8 * (lane & 1) + 2 * ((lane & 7) >> 1), ln);
-                w.x &= msk; w.y &= msk; w.z &= msk; w.w &= msk;
-              }
-              const uint32_t v0 = __vmaxu2(w.x, w.y), v1 = __vmaxu2(w.z, w.w);
-              const uint32_t v = __vmaxu2(v0, v1);
-              top = max(v & 0xffffu, v >> 16);
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            // half bits -> exponent; a NaN scale (its product is NaN anyway) counts as the largest
-            const int e = min((int)(top >> 10), 29) - 15;
-            x = min(x, min(15, 14 - e));
-          }
-          bool moved = false;
-          float Rn[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              m[nt][k] = fmaxf(m[nt][k], mx[nt][k]);
-              Rn[nt][k] = m[nt][k] - (float)x;
-              moved |= Rn[nt][k] != R[nt][k];
-            }
-          if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float al = Rn[nt][k] == -INFINITY ? 1.f : fast_exp2(R[nt][k] - Rn[nt][k]);
-                R[nt][k] = Rn[nt][k];
-                l[nt][k] *= al;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int hf = 0; hf < 2; ++hf) {
-                    o[j][hf][nt][k] *= al;
-                    o[j][hf][nt][2 + k] *= al;
-                  }
+              for (int hf = 0; hf < 2; ++hf) {
+                o[j][hf][nt][k] *= al;
+                o[j][hf][nt][2 + k] *= al;
               }
           }
-          // ---- weights and the values they weight ----
+      }
+      x = xn;
+      // ---- weights and the values they weight ----
 #pragma unroll
-          for (int t = 0; t < TPU; ++t) {
-            uint32_t pb[NT][2];
+      for (int t = 0; t < TPU; ++t) {
+        uint32_t pb[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float p[4];
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                p[k] = fast_exp2(fmaf(sc[t][nt][k], fac[nt][k & 1], -R[nt][k & 1]));
-                l[nt][k & 1] += p[k];
-              }
-              pb[nt][0] = transpose8x8(pack_f16(p[0], p[1]));  // tokens 2c, 2c + 1 of head g
-              pb[nt][1] = transpose8x8(pack_f16(p[2], p[3]));  // tokens 8 + 2c, + 1
-            }
-            const uint4 v0 = lds128(base + At::value_codes(t0 + t) + lane * 16), v1 = lds128(base + At::value_codes(t0 + t) + 512 + lane * 16);
-            uint4 z0 = lds128(base + At::value_scales(t0 + t) + c * 32), z1 = lds128(base + At::value_scales(t0 + t) + c * 32 + 16);
-            if (!whole) {
-              // scales past the end may be anything, a NaN too
-              const uint32_t m0 = pair_mask(2 * c, len[t]), m1 = pair_mask(8 + 2 * c, len[t]);
-              z0.x &= m0; z0.y &= m0; z0.z &= m0; z0.w &= m0;
-              z1.x &= m1; z1.y &= m1; z1.z &= m1; z1.w &= m1;
-            }
-            const uint32_t vw0[4] = {v0.x, v0.y, v0.z, v0.w}, vw1[4] = {v1.x, v1.y, v1.z, v1.w};
-            const uint32_t zw0[4] = {z0.x, z0.y, z0.z, z0.w}, zw1[4] = {z1.x, z1.y, z1.z, z1.w};
+          for (int k = 0; k < 4; ++k) {
+            p[k] = fast_exp2(fmaf(sc[t][nt][k], fac[nt][k & 1], -R[nt][k & 1]));
+            l[nt][k & 1] += p[k];
+          }
+          pb[nt][0] = transpose8x8(pack_f16(p[0], p[1]));  // tokens 2c, 2c + 1 of head g
+          pb[nt][1] = transpose8x8(pack_f16(p[2], p[3]));  // tokens 8 + 2c, + 1
+        }
+        const uint4 v0 = lds128(base + At::value_codes(t) + lane * 16), v1 = lds128(base + At::value_codes(t) + 512 + lane * 16);
+        uint4 z0 = lds128(base + At::value_scales(t) + c * 32), z1 = lds128(base + At::value_scales(t) + c * 32 + 16);
+        if constexpr (!WHOLE) {
+          // scales past the end may be anything, a NaN too
+          const uint32_t m0 = pair_mask(2 * c, left[t]), m1 = pair_mask(8 + 2 * c, left[t]);
+          z0.x &= m0; z0.y &= m0; z0.z &= m0; z0.w &= m0;
+          z1.x &= m1; z1.y &= m1; z1.z &= m1; z1.w &= m1;
+        }
+        const uint32_t vw0[4] = {v0.x, v0.y, v0.z, v0.w}, vw1[4] = {v1.x, v1.y, v1.z, v1.w};
+        const uint32_t zw0[4] = {z0.x, z0.y, z0.z, z0.w}, zw1[4] = {z1.x, z1.y, z1.z, z1.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-              q4_codes01(vw0[j], a0, a1);
-              q4_codes01(vw1[j], a2, a3);
-              q4_codes01(vw0[j] >> 8, b0, b1);
-              q4_codes01(vw1[j] >> 8, b2, b3);
+        for (int j = 0; j < 4; ++j) {
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          q4_codes01(vw0[j], a0, a1);
+          q4_codes01(vw1[j], a2, a3);
+          q4_codes01(vw0[j] >> 8, b0, b1);
+          q4_codes01(vw1[j] >> 8, b2, b3);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t p0 = mul_f16x2(pb[nt][0], zw0[j]), p1 = mul_f16x2(pb[nt][1], zw1[j]);
-                mma_16816_f16(o[j][0][nt], a0, a1, a2, a3, p0, p1);
-                mma_16816_f16(o[j][1][nt], b0, b1, b2, b3, p0, p1);
-              }
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t p0 = mul_f16x2(pb[nt][0], zw0[j]), p1 = mul_f16x2(pb[nt][1], zw1[j]);
+            mma_16816_f16(o[j][0][nt], a0, a1, a2, a3, p0, p1);
+            mma_16816_f16(o[j][1][nt], b0, b1, b2, b3, p0, p1);
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.empty[st]);
     }
   }
-  if (LSE) {
-    pdl_launch_dependents();
-    return;
-  }
-  __syncthreads();  // the ring is no longer read or written by copies
-  pdl_launch_dependents();
 
-  // ---- merge the warps of this CTA ----
-  float* so = reinterpret_cast<float*>(ring);  // [kW][8 NT][kOStride]
-  float* octa = so + kW * 8 * NT * kOStride;   // [16][128]
-  float* recv_o = octa + 16 * kHeadDim;
-  float2* recv_ml = reinterpret_cast<float2*>(recv_o + 16 * kHeadDim);
-  static_assert((kW * 8 * NT * kOStride + 32 * kHeadDim) * 4 + kRecvMl <= kRing, "the merge fits the ring");
-  if (warp < kW) {
+  // n_pages pages, dealt out to the CTA's warps: page_of(i, lp, phys, len) gives page i
+  // (len 0: left out); meanwhile() runs while the first copies are under way.  Called by
+  // whole warps.
+  template <typename PageOf, typename Meanwhile>
+  __device__ __forceinline__ void run(const uint8_t* blocks, size_t head_stride, int hkv, int n_pages, int* err,
+                                      PageOf page_of, Meanwhile meanwhile) {
+    const int n_units = (n_pages + kPages - 1) / kPages * kUPP;
+    const int n_mine = (n_units - warp + kW - 1) / kW;  // units warp, warp + 6, ...
+    // the pages of units m0 .. m0 + 31 of this warp, one unit per lane
+    int phys[kPages], len[kPages], lp0 = -1;
+    auto resolve = [&](int m0) {
+      const int u = warp + kW * (m0 + lane);
+#pragma unroll
+      for (int w = 0; w < kPages; ++w) {
+        const int i = u / kUPP * kPages + w;
+        phys[w] = 0;
+        len[w] = 0;
+        if (u < n_units && i < n_pages) {
+          int lp = -1, ph = 0, ln = 0;
+          page_of(i, lp, ph, ln);
+          if (w == 0) lp0 = lp;
+          phys[w] = ph;
+          len[w] = max(0, ln - u % kUPP * TPU * 16);  // tokens from the unit's first tile on
+        }
+      }
+    };
+    // unit m into its buffer (all lanes; the copies are lane 0's)
+    auto issue = [&](int m) {
+      const int src = m & 31, buf = (seq + m) % kBufs;
+      int ph[kPages], ln[kPages];
+#pragma unroll
+      for (int w = 0; w < kPages; ++w) {
+        ph[w] = __shfl_sync(0xffffffffu, phys[w], src);
+        ln[w] = __shfl_sync(0xffffffffu, len[w], src);
+      }
+      const int lp = LSE ? __shfl_sync(0xffffffffu, lp0, src) : 0;
+      if (lane == 0) {
+        constexpr uint32_t kBytes = (kUPP > 1 ? kBufBytes : LOCKS_KV_Q4_BLOCK_BYTES(P)) / (LSE ? 2 : 1);
+        uint64_t* bar = &sh.full[warp][buf];
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int w = 0; w < kPages; ++w) {
+          sh.len[warp][buf][w] = ln[w];
+          bytes += ln[w] > 0 ? kBytes : 0u;
+        }
+        if (LSE) sh.lp[warp][buf] = lp;
+        mbar_arrive_expect_tx(bar, bytes);
+        const uint32_t dst = wbase + buf * kBufBytes;
+#pragma unroll
+        for (int w = 0; w < kPages; ++w) {
+          if (ln[w] <= 0) continue;
+          const uint8_t* block = blocks + (size_t)ph[w] * head_stride + (size_t)hkv * LOCKS_KV_Q4_BLOCK_BYTES(P);
+          if constexpr (kUPP == 1) {
+            bulk_load(dst + w * LOCKS_KV_Q4_BLOCK_BYTES(P), block, kBytes, bar);
+          } else {
+            // the unit's tiles of the page's four parts
+            const int t = (warp + kW * m) % kUPP * TPU;
+            bulk_load(dst, block + 1024 * t, 1024 * TPU, bar);
+            bulk_load(dst + 1024 * TPU, block + 64 * P + 128 * t, 128 * TPU, bar);
+            bulk_load(dst + 1152 * TPU, block + 72 * P + 1024 * t, 1024 * TPU, bar);
+            bulk_load(dst + 2176 * TPU, block + 136 * P + 128 * t, 128 * TPU, bar);
+          }
+        }
+      }
+    };
+    int issued = 0, done = 0;
+    if (n_mine > 0) resolve(0);
+    for (; issued < min(kBufs, n_mine); ++issued) issue(issued);
+    meanwhile();
+    for (; done < n_mine; ++done) {
+      const int s = seq + done, buf = s % kBufs;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[warp][buf], (s / kBufs) & 1))) {
+        if (lane == 0) set_error(err, kDevErrTimeout);
+        break;
+      }
+      // tokens from each tile's first on (one page's, or a page per tile)
+      int left[TPU];
+      bool whole = true, any = false;
+#pragma unroll
+      for (int t = 0; t < TPU; ++t) {
+        left[t] = P == 64 ? sh.len[warp][buf][0] - 16 * t : sh.len[warp][buf][t];
+        whole &= left[t] >= 16;
+        any |= left[t] > 0;
+      }
+      const uint32_t base = wbase + buf * kBufBytes;
+      if (whole) unit<true>(base, buf, left);
+      else if (any) unit<false>(base, buf, left);
+      __syncwarp();  // every lane is done with the buffer
+      if (issued < n_mine) {
+        if ((issued & 31) == 0) resolve(issued);
+        issue(issued);
+        ++issued;
+      }
+    }
+    // after a failed wait: let the copies in flight land before the memory is reused
+    if (done < n_mine && lane == 0)
+      for (int m = done; m < issued; ++m) (void)mbar_wait(&sh.full[warp][(seq + m) % kBufs], ((seq + m) / kBufs) & 1);
+    __syncwarp();
+    seq += issued;
+  }
+
+  // The six warps' states to the CTA's: (R, sum) in sh.cta_m, sh.cta_l and O [16][128]
+  // in octa (shared memory over the buffers; whole CTA, ends with a barrier).
+  __device__ __forceinline__ float* merge(uint8_t* ring) {
+    float* so = reinterpret_cast<float*>(ring);  // [kW][8 NT][kOStride]
+    float* octa = so + kW * 8 * NT * kOStride;   // [16][128]
+    const int tid = threadIdx.x, G = group;
+    __syncthreads();  // the buffers are no longer read, nor written by copies
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -497,135 +505,417 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_q4_kernel(co
           sh.m[warp][h] = R[nt][k];
           sh.l[warp][h] = s;
         }
+        if (h < G)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(so + (warp * 8 * NT + h) * kOStride + 32 * j + 4 * g) =
-              make_float4(o[j][0][nt][k], o[j][0][nt][2 + k], o[j][1][nt][k], o[j][1][nt][2 + k]);
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float4*>(so + (warp * 8 * NT + h) * kOStride + 32 * j + 4 * g) =
+                make_float4(o[j][0][nt][k], o[j][0][nt][2 + k], o[j][1][nt][k], o[j][1][nt][2 + k]);
       }
-  }
-  __syncthreads();
-  if (tid < G) {
-    float M = -INFINITY;
+    __syncthreads();
+    if (tid < G) {
+      float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) M = fmaxf(M, sh.m[w][tid]);
-    float Ls = 0.f;
+      for (int w = 0; w < kW; ++w) M = fmaxf(M, sh.m[w][tid]);
+      float Ls = 0.f;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      const float f = M == -INFINITY ? 1.f : fast_exp2(sh.m[w][tid] - M);
-      sh.f[w][tid] = f;
-      Ls += sh.l[w][tid] * f;
+      for (int w = 0; w < kW; ++w) {
+        const float f = M == -INFINITY ? 1.f : fast_exp2(sh.m[w][tid] - M);
+        sh.f[w][tid] = f;
+        Ls = fmaf(sh.l[w][tid], f, Ls);
+      }
+      sh.cta_m[tid] = M;
+      sh.cta_l[tid] = Ls;
     }
-    sh.cta_m[tid] = M;
-    sh.cta_l[tid] = Ls;
-  }
-  __syncthreads();
-  const int CS = a.cluster, NC = a.n_splits / a.cluster;
-  const uint32_t rank = cluster_ctarank();
-  const int cols = kHeadDim / CS;
-  cluster_wait();  // every CTA of the cluster has set up its receive barrier
-  // Before anybody's ring may be written from outside, its owner must be done with
-  // it: the second cluster barrier.
-  cluster_arrive();
-  for (int e = tid; e < G * (kHeadDim / 4); e += kThreads) {
-    const int h = e / (kHeadDim / 4), d4 = 4 * (e % (kHeadDim / 4));
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    for (int e = tid; e < G * (kHeadDim / 4); e += kThreads) {
+      const int h = e / (kHeadDim / 4), d4 = 4 * (e % (kHeadDim / 4));
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      const float f = sh.f[w][h];
-      const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 * NT + h) * kOStride + d4);
-      O.x = fmaf(v.x, f, O.x);
-      O.y = fmaf(v.y, f, O.y);
-      O.z = fmaf(v.z, f, O.z);
-      O.w = fmaf(v.w, f, O.w);
+      for (int w = 0; w < kW; ++w) {
+        const float f = sh.f[w][h];
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * 8 * NT + h) * kOStride + d4);
+        O.x = fmaf(v.x, f, O.x);
+        O.y = fmaf(v.y, f, O.y);
+        O.z = fmaf(v.z, f, O.z);
+        O.w = fmaf(v.w, f, O.w);
+      }
+      *reinterpret_cast<float4*>(octa + h * kHeadDim + d4) = O;
     }
-    *reinterpret_cast<float4*>(octa + h * kHeadDim + d4) = O;
+    __syncthreads();
+    return octa;
   }
-  __syncthreads();
-  cluster_wait();
-  // ---- push this CTA's state to the owners of its columns ----
-  const uint32_t ro = smem_u32(recv_o), rml = smem_u32(recv_ml);
-  for (int e = tid; e < G * (kHeadDim / 4); e += kThreads) {
-    const int h = e / (kHeadDim / 4), c4 = 4 * (e % (kHeadDim / 4));
-    const float4 v = *reinterpret_cast<const float4*>(octa + h * kHeadDim + c4);
-    st_dsmem_f4(dsmem_addr(ro + 4 * (((int)rank * G + h) * cols + c4 % cols), c4 / cols), v);
-  }
-  for (int e = tid; e < CS * G; e += kThreads) {
-    const int dst = e / G, h = e % G;
-    st_dsmem_f2(dsmem_addr(rml + 8 * ((int)rank * 16 + h), dst), make_float2(sh.cta_m[h], sh.cta_l[h]));
-  }
-  __syncthreads();  // the whole CTA's stores precede the release arrivals
-  if (tid < CS) mbar_arrive_remote(dsmem_addr(smem_u32(&sh.recv), tid));
-  if (!mbar_wait_cluster(&sh.recv, 0) && tid == 0) set_error(a.err, kDevErrTimeout);
-  const int q = split / CS;
-  for (int e = tid; e < G * cols; e += kThreads) {
-    const int h = e / cols, cc = e % cols, col = (int)rank * cols + cc;
-    float M = -INFINITY;
-    for (int rr = 0; rr < CS; ++rr) M = fmaxf(M, recv_ml[rr * 16 + h].x);
-    float Ls = 0.f, O = 0.f;
-    for (int rr = 0; rr < CS; ++rr) {
-      const float2 ml = recv_ml[rr * 16 + h];
-      const float f = M == -INFINITY ? 1.f : fast_exp2(ml.x - M);
-      Ls = fmaf(ml.y, f, Ls);
-      O = fmaf(recv_o[(rr * G + h) * cols + cc], f, O);
-    }
-    const size_t oi = (size_t)b * Hq + (size_t)hkv * G + h;
-    if (NC == 1) {
-      a.out[oi * kHeadDim + col] = __bfloat16_as_ushort(__float2bfloat16_rn(Ls == 0.f ? 0.f : O / Ls));
-      if (a.lse && col == 0) a.lse[oi] = Ls == 0.f ? -INFINITY : (M + fast_log2(Ls)) * kLn2;
-    } else {
-      const size_t pi = ((size_t)bh * NC + q) * G + h;
-      a.part_o[pi * kHeadDim + col] = O;
-      if (col == 0) a.part_ml[pi] = make_float2(M, Ls);
-    }
-  }
-  if (NC == 1) return;
+};
 
-  // ---- several clusters per problem: the last one to finish joins them ----
-  __threadfence();
-  cluster_sync();
-  if (rank == 0 && tid == 0) {
-    const int last = atomicAdd(a.counters + bh, 1u) == (unsigned)(NC - 1);
-    for (int rr = 0; rr < CS; ++rr) st_dsmem(dsmem_addr(smem_u32(&sh.last), rr), last);
-  }
-  cluster_sync();
-  if (!sh.last) return;
-  __threadfence();
-  for (int e = tid; e < G * cols; e += kThreads) {
-    const int h = e / cols, col = (int)rank * cols + e % cols;
-    const size_t p0 = (size_t)bh * NC * G + h;
-    float M = -INFINITY;
-    for (int qq = 0; qq < NC; ++qq) M = fmaxf(M, __ldcg(a.part_ml + p0 + (size_t)qq * G).x);
-    float Ls = 0.f, O = 0.f;
-    for (int qq = 0; qq < NC; ++qq) {
-      const float2 ml = __ldcg(a.part_ml + p0 + (size_t)qq * G);
-      const float f = M == -INFINITY ? 1.f : fast_exp2(ml.x - M);
-      Ls = fmaf(ml.y, f, Ls);
-      O = fmaf(__ldcg(a.part_o + (p0 + (size_t)qq * G) * kHeadDim + col), f, O);
+__device__ __forceinline__ uint8_t* align_ring(uint8_t* raw) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+}
+__device__ __forceinline__ int checked_length(const AttendArgs& a, int b, int P, bool says) {
+  const int L = a.seq_lens[b];
+  if (L >= 0 && L <= a.max_pages * P) return L;
+  if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+  return L < 0 ? 0 : a.max_pages * P;
+}
+// Physical page of logical page lp of sequence b, -1 (reported) when there is none.
+__device__ __forceinline__ int physical_page(const AttendArgs& a, int b, int lp) {
+  const int ph = a.block_table[(size_t)b * a.max_pages + lp];
+  if (ph >= 0 && ph < a.pages_total) return ph;
+  set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
+  return -1;
+}
+__device__ __forceinline__ void store_result(const AttendArgs& a, size_t row, int col, float O, float M, float Ls) {
+  a.out[row * kHeadDim + col] = __bfloat16_as_ushort(__float2bfloat16_rn(Ls == 0.f ? 0.f : O / Ls));
+  if (a.lse && col == 0) a.lse[row] = Ls == 0.f ? -INFINITY : (M + fast_log2(Ls)) * kLn2;
+}
+
+// ---- every page ------------------------------------------------------------------
+// Partial results a.part_ml, a.part_o: two per CTA (its first problem, which another
+// CTA began, and the one it begins itself), [2 CTA + begins][G].  Tickets a.counters:
+// [B*Hkv] per problem, then two per CTA for groups of partials.
+constexpr int kJoinBytes = 80 * 1024;  // partials one CTA reads at a time
+
+// Joins n partials (the first in slot s0, the others in s1, s1 + step, ...) into the
+// result rows (row >= 0) or into the first slot.  The outputs come into shared memory
+// as bulk copies, all in flight at once, while the weights are made.
+__device__ void join_partials(const AttendArgs& a, Q4Shared& sh, uint8_t* ring, int n, size_t s0, size_t s1, size_t step,
+                              long long row, int& phase) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.group;
+  auto slot = [&](int i) { return i == 0 ? s0 : s1 + step * (size_t)(i - 1); };
+  const float* po = reinterpret_cast<const float*>(ring);  // [at_once][G][128]
+  float* f = reinterpret_cast<float*>(ring + kJoinBytes);  // [n][G]: at most two per SM and 16 heads
+  static_assert(kJoinBytes + 16 * 4 * 448 <= kRing, "weights of 448 partials");
+  const int at_once = kJoinBytes / (G * kHeadDim * 4);
+  auto ask = [&](int i0) {  // warp 0: partials i0 .. i0 + at_once - 1
+    const int m = min(at_once, n - i0);
+    if (lane == 0) mbar_arrive_expect_tx(&sh.join, (uint32_t)(m * G * kHeadDim * 4));
+    __syncwarp();
+    for (int i = lane; i < m; i += 32)
+      bulk_load(smem_u32(ring) + i * G * kHeadDim * 4, a.part_o + slot(i0 + i) * G * kHeadDim, G * kHeadDim * 4, &sh.join);
+  };
+  // the partials were written with ordinary stores (here: the ring too)
+  asm volatile("fence.proxy.async;\n" ::: "memory");
+  __syncthreads();
+  if (warp == 0) ask(0);
+  for (int h = warp; h < G; h += kW) {
+    float M = -INFINITY, Ls = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.part_ml + slot(i) * G + h).x);
+    M = warp_max(M);
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = __ldcg(a.part_ml + slot(i) * G + h);
+      const float e = M == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+      Ls = fmaf(ml.y, e, Ls);
+      f[i * G + h] = e;
     }
-    const size_t oi = (size_t)b * Hq + (size_t)hkv * G + h;
-    a.out[oi * kHeadDim + col] = __bfloat16_as_ushort(__float2bfloat16_rn(Ls == 0.f ? 0.f : O / Ls));
-    if (a.lse && col == 0) a.lse[oi] = Ls == 0.f ? -INFINITY : (M + fast_log2(Ls)) * kLn2;
+    Ls = warp_sum(Ls);
+    if (lane == 0) {
+      sh.cta_m[h] = M;
+      sh.cta_l[h] = Ls;
+    }
   }
-  if (rank == 0 && tid == 0) a.counters[bh] = 0;  // ready for the next call
+  constexpr int kPairs = 16 * kHeadDim / 2 / kThreads + 1;
+  float2 O[kPairs];
+#pragma unroll
+  for (int k = 0; k < kPairs; ++k) O[k] = make_float2(0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += at_once) {
+    const bool ok = mbar_wait(&sh.join, phase);
+    phase ^= 1;
+    if (!ok && tid == 0) set_error(a.err, kDevErrTimeout);
+    __syncthreads();  // and the weights are there
+    const int m = min(at_once, n - i0);
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      const int e = 2 * (tid + k * kThreads);
+      if (e >= G * kHeadDim) break;
+#pragma unroll 4
+      for (int i = 0; i < m; ++i) {
+        const float2 y = *reinterpret_cast<const float2*>(po + (size_t)i * G * kHeadDim + e);
+        const float x = f[(i0 + i) * G + e / kHeadDim];
+        O[k].x = fmaf(y.x, x, O[k].x);
+        O[k].y = fmaf(y.y, x, O[k].y);
+      }
+    }
+    __syncthreads();  // read, before it is overwritten
+    if (warp == 0 && i0 + at_once < n) ask(i0 + at_once);
+  }
+#pragma unroll
+  for (int k = 0; k < kPairs; ++k) {
+    const int e = 2 * (tid + k * kThreads);
+    if (e >= G * kHeadDim) break;
+    const int h = e / kHeadDim, col = e % kHeadDim;
+    if (row >= 0) {
+      store_result(a, (size_t)row + h, col, O[k].x, sh.cta_m[h], sh.cta_l[h]);
+      store_result(a, (size_t)row + h, col + 1, O[k].y, sh.cta_m[h], sh.cta_l[h]);
+    } else {
+      *reinterpret_cast<float2*>(a.part_o + s0 * G * kHeadDim + e) = O[k];
+      if (col == 0) a.part_ml[s0 * G + h] = make_float2(sh.cta_m[h], sh.cta_l[h]);
+    }
+  }
+}
+
+template <int P, int TPU, int NT>
+__global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const AttendArgs a) {
+  extern __shared__ __align__(128) uint8_t ring_raw[];
+  __shared__ Q4Shared sh;
+  uint8_t* ring = align_ring(ring_raw);
+  constexpr int kPPS = kPage / P;  // pages of a slot
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int G = a.group, hkv_n = a.num_kv_heads;
+  Q4Warp<P, TPU, NT, false> w(sh, smem_u32(ring), G);
+  if (lane == 0) {
+    for (int s = 0; s < kWarpTiles; ++s) mbar_init(&sh.full[w.warp][s], 1);
+    if (w.warp == 0) mbar_init(&sh.join, 1);
+    fence_mbar_init();
+  }
+  int join_phase = 0;
+  __syncthreads();
+  pdl_wait();
+
+  // all slots in one line: sequence by sequence, head by head
+  auto slots_of = [&](int b) { return (checked_length(a, b, P, blockIdx.x == 0 && tid < 32) + kPage - 1) / kPage; };
+  long long total = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    int n = b0 + lane < a.batch ? slots_of(b0 + lane) : 0;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+    total += n;
+  }
+  total *= hkv_n;
+  // with fewer slots than CTAs the last CTAs get none, so that no part is empty
+  const long long C = min((long long)gridDim.x, max(total, 1LL)), cta = blockIdx.x;
+  long long at = cta < C ? total * cta / C : total;
+  const long long end = cta < C ? total * (cta + 1) / C : total;
+  auto owner = [&](long long y) { return ((y + 1) * C - 1) / total; };  // the CTA whose part holds slot y
+
+  if (cta == 0) {
+    // sequences without a token have no slots and get their rows here
+    for (int b = 0; b < a.batch; ++b)
+      if (a.seq_lens[b] <= 0)
+        for (int e = tid; e < hkv_n * G * kHeadDim; e += kThreads)
+          store_result(a, (size_t)b * hkv_n * G + e / kHeadDim, e % kHeadDim, 0.f, 0.f, 0.f);
+  }
+
+  // the sequence that holds slot `at`, and the line's position of its first slot
+  int b = 0;
+  long long first = 0;
+  int nb = 0;  // its slots per head
+  auto seek = [&](long long y) {
+    while (b < a.batch) {
+      nb = slots_of(b);
+      if (y < first + (long long)nb * hkv_n) return;
+      first += (long long)nb * hkv_n;
+      ++b;
+    }
+  };
+  {
+    // whole blocks of 32 sequences at a time
+    while (b + 32 <= a.batch) {
+      int n = slots_of(b + lane);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+      if (at < first + (long long)n * hkv_n) break;
+      first += (long long)n * hkv_n;
+      b += 32;
+    }
+  }
+  while (at < end) {
+    seek(at);
+    const int h = (int)((at - first) / nb);
+    const long long p0 = first + (long long)h * nb, p1 = p0 + nb;  // the problem's slots in the line
+    const int s0 = (int)(at - p0), s1 = (int)(min(end, p1) - p0);  // this CTA's of them
+    const int L = checked_length(a, b, P, false);
+    const int pg0 = s0 * kPPS, pg1 = min(s1 * kPPS, (L + P - 1) / P);
+    const size_t row = ((size_t)b * hkv_n + h) * G;
+    w.run(reinterpret_cast<const uint8_t*>(a.k_pool16), (size_t)hkv_n * LOCKS_KV_Q4_BLOCK_BYTES(P), h, pg1 - pg0, a.err,
+          [&](int i, int& lp, int& phys, int& len) {
+            lp = pg0 + i;
+            phys = physical_page(a, b, lp);
+            len = phys >= 0 ? min(P, L - lp * P) : 0;
+          },
+          [&] {
+            w.reset();
+            w.load_q(a.q + row * kHeadDim, a.scale_log2);
+          });
+    if (p0 + s1 >= end) pdl_launch_dependents();
+    const float* octa = w.merge(ring);
+    if (s0 == 0 && s1 == nb) {
+      for (int e = tid; e < G * kHeadDim; e += kThreads)
+        store_result(a, row + e / kHeadDim, e % kHeadDim, octa[e], sh.cta_m[e / kHeadDim], sh.cta_l[e / kHeadDim]);
+    } else {
+      // the problem's CTAs c0 .. c1; c0 begins it
+      const long long c0 = owner(p0), c1 = owner(p1 - 1);
+      const size_t mine = 2 * (size_t)cta + (s0 == 0 ? 1 : 0);
+      for (int e = tid; e < G * (kHeadDim / 4); e += kThreads)
+        reinterpret_cast<float4*>(a.part_o + mine * G * kHeadDim)[e] = reinterpret_cast<const float4*>(octa)[e];
+      if (tid < G) a.part_ml[mine * G + tid] = make_float2(sh.cta_m[tid], sh.cta_l[tid]);
+      __threadfence();
+      __syncthreads();
+      const int n = (int)(c1 - c0) + 1;
+      // partials of a group: all of them where they are two loads' worth, else 16
+      const int gs = n <= 2 * (kJoinBytes / (G * kHeadDim * 4)) ? n : 16;
+      const int i = (int)(cta - c0), grp = i / gs, n_grp = (n + gs - 1) / gs;
+      const size_t g0 = grp == 0 ? 2 * (size_t)c0 + 1 : 2 * ((size_t)c0 + (size_t)grp * gs);
+      const int in_grp = min(gs, n - grp * gs);
+      unsigned* ticket = n_grp == 1 ? a.counters + (size_t)b * hkv_n + h : a.counters + (size_t)a.batch * hkv_n + g0;
+      if (tid == 0) sh.last = atomicAdd(ticket, 1u) == (unsigned)(in_grp - 1);
+      __syncthreads();
+      if (sh.last) {
+        __threadfence();
+        if (tid == 0) *ticket = 0;  // ready for the next call
+        join_partials(a, sh, ring, in_grp, g0, 2 * ((size_t)c0 + (size_t)grp * gs + 1), 2,
+                      n_grp == 1 ? (long long)row : -1, join_phase);
+        if (n_grp > 1) {
+          __threadfence();
+          __syncthreads();
+          unsigned* top = a.counters + (size_t)b * hkv_n + h;
+          if (tid == 0) sh.last = atomicAdd(top, 1u) == (unsigned)(n_grp - 1);
+          __syncthreads();
+          if (sh.last) {
+            __threadfence();
+            if (tid == 0) *top = 0;
+            join_partials(a, sh, ring, n_grp, 2 * (size_t)c0 + 1, 2 * ((size_t)c0 + gs), 2 * (size_t)gs, (long long)row, join_phase);
+          }
+        }
+      }
+    }
+    at = p0 + s1;
+    // the buffers were written with ordinary stores: before the next copies into them
+    fence_proxy_async();
+    __syncthreads();
+  }
+}
+
+// ---- a page list, or the exact page log-sum-exp ------------------------------------
+// Grid (CTAs of the cluster, B * Hkv); for the page LSE (splits, B * Hkv), no clusters.
+template <int MODE, int P, int TPU, int NT>
+__global__ void __launch_bounds__(kThreads, 2) attend_q4_kernel(const AttendArgs a) {
+  constexpr bool LSE = MODE == kAttendPageLse;
+  extern __shared__ __align__(128) uint8_t ring_raw[];
+  __shared__ Q4Shared sh;
+  uint8_t* ring = align_ring(ring_raw);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int split = blockIdx.x, bh = blockIdx.y;
+  const int b = bh / a.num_kv_heads, hkv = bh % a.num_kv_heads;
+  const int G = a.group;
+  Q4Warp<P, TPU, NT, LSE> w(sh, smem_u32(ring), G);
+  constexpr int kPages = Q4Warp<P, TPU, NT, LSE>::kPages;
+  if (lane == 0) {
+    for (int s = 0; s < kWarpTiles; ++s) mbar_init(&sh.full[w.warp][s], 1);
+    if (w.warp == 0) mbar_init(&sh.recv, a.cluster);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (!LSE) cluster_arrive();  // matched by the wait before the first remote access
+  pdl_wait();
+
+  const int L = checked_length(a, b, P, tid == 0 && split == 0);
+  const int n_pages = (L + P - 1) / P;
+  int ns = 0, cnt = 0, n_items = n_pages;
+  if (!LSE) {
+    const int cap = min(L / P, a.max_pages);
+    ns = min(max(a.n_summarized[b], 0), cap);
+    const int kcap = min(a.k_max, ns);
+    cnt = a.sel_count[bh];
+    if (cnt < 0 || cnt > kcap) {
+      if (tid == 0) set_error(a.err, LOCKS_DEVERR_SEL_PAGE);
+      cnt = cnt < 0 ? 0 : kcap;
+    }
+    n_items = cnt + (n_pages - ns);
+  }
+  // this CTA's pages (whole units)
+  const int ipc = ((n_items + a.n_splits - 1) / a.n_splits + kPages - 1) / kPages * kPages;
+  const int i0 = min(n_items, split * ipc), i1 = min(n_items, i0 + ipc);
+  const size_t row = (size_t)b * a.num_kv_heads * G + (size_t)hkv * G;
+  if (LSE) {
+    w.page_lse = a.page_lse + row * a.max_pages;
+    w.lse_stride = a.max_pages;
+  }
+  w.run(reinterpret_cast<const uint8_t*>(a.k_pool16), (size_t)a.num_kv_heads * LOCKS_KV_Q4_BLOCK_BYTES(P), hkv, i1 - i0,
+        a.err, [&](int k, int& lp, int& phys, int& len) {
+          const int i = i0 + k;
+          if (!LSE && i < cnt) {
+            lp = a.sel_pages[(size_t)bh * a.k_max + i];
+            // inside the decode step the top-k also wrote the physical pages
+            phys = a.sel_phys ? a.sel_phys[(size_t)bh * a.k_max + i] : 0;
+            if (lp < 0 || lp >= ns) {
+              set_error(a.err, LOCKS_DEVERR_SEL_PAGE);
+              return;
+            }
+            if (!a.sel_phys) {
+              phys = physical_page(a, b, lp);
+            } else if (phys < 0 || phys >= a.pages_total) {
+              set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
+              phys = -1;
+            }
+          } else {
+            lp = LSE ? i : ns + (i - cnt);
+            phys = physical_page(a, b, lp);
+          }
+          len = phys >= 0 ? min(P, L - lp * P) : 0;
+        },
+        [&] {
+          w.reset();
+          w.load_q(a.q + row * kHeadDim, a.scale_log2);
+        });
+  pdl_launch_dependents();
+  if constexpr (!LSE) {
+    const float* octa = w.merge(ring);
+    float* recv_o = reinterpret_cast<float*>(ring) + kW * 8 * NT * kOStride + 16 * kHeadDim;
+    float2* recv_ml = reinterpret_cast<float2*>(recv_o + 16 * kHeadDim);
+    static_assert((kW * 8 * NT * kOStride + 32 * kHeadDim) * 4 + kRecvMl <= kRing, "the merge fits the buffers");
+    const int CS = a.cluster;
+    const uint32_t rank = cluster_ctarank();
+    const int cols = kHeadDim / CS;
+    cluster_wait();  // every CTA of the cluster has set up its receive barrier
+    cluster_sync();  // and is done with its buffers, which the others now write
+    const uint32_t ro = smem_u32(recv_o), rml = smem_u32(recv_ml);
+    for (int e = tid; e < G * (kHeadDim / 4); e += kThreads) {
+      const int h = e / (kHeadDim / 4), c4 = 4 * (e % (kHeadDim / 4));
+      const float4 v = *reinterpret_cast<const float4*>(octa + h * kHeadDim + c4);
+      st_dsmem_f4(dsmem_addr(ro + 4 * (((int)rank * G + h) * cols + c4 % cols), c4 / cols), v);
+    }
+    for (int e = tid; e < CS * G; e += kThreads) {
+      const int dst = e / G, h = e % G;
+      st_dsmem_f2(dsmem_addr(rml + 8 * ((int)rank * 16 + h), dst), make_float2(sh.cta_m[h], sh.cta_l[h]));
+    }
+    __syncthreads();  // the whole CTA's stores precede the release arrivals
+    if (tid < CS) mbar_arrive_remote(dsmem_addr(smem_u32(&sh.recv), tid));
+    if (!mbar_wait_cluster(&sh.recv, 0) && tid == 0) set_error(a.err, kDevErrTimeout);
+    for (int e = tid; e < G * cols; e += kThreads) {
+      const int h = e / cols, cc = e % cols;
+      float M = -INFINITY;
+      for (int rr = 0; rr < CS; ++rr) M = fmaxf(M, recv_ml[rr * 16 + h].x);
+      float Ls = 0.f, O = 0.f;
+      for (int rr = 0; rr < CS; ++rr) {
+        const float2 ml = recv_ml[rr * 16 + h];
+        const float f = M == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+        Ls = fmaf(ml.y, f, Ls);
+        O = fmaf(recv_o[(rr * G + h) * cols + cc], f, O);
+      }
+      store_result(a, row + h, (int)rank * cols + cc, O, M, Ls);
+    }
+  }
 }
 
 using Kern = void (*)(const AttendArgs);
 
 template <int MODE, int P>
 Kern pick(int group, int tiles) {
-  if (group <= 8) return tiles == 4 ? attend_q4_kernel<MODE, P, 4, 1> : attend_q4_kernel<MODE, P, 1, 1>;
-  return tiles == 4 ? attend_q4_kernel<MODE, P, 4, 2> : attend_q4_kernel<MODE, P, 1, 2>;
+  if constexpr (MODE == kAttendPageLse) {
+    // a unit is one page: four tiles, or one
+    return group <= 8 ? attend_q4_kernel<MODE, P, P / 16, 1> : attend_q4_kernel<MODE, P, P / 16, 2>;
+  } else if constexpr (MODE == kAttendSparse) {
+    if (group <= 8) return tiles == 4 ? attend_q4_kernel<MODE, P, 4, 1> : attend_q4_kernel<MODE, P, 1, 1>;
+    return tiles == 4 ? attend_q4_kernel<MODE, P, 2, 2> : attend_q4_kernel<MODE, P, 1, 2>;
+  } else {
+    if (group <= 8) return tiles == 4 ? attend_q4_dense_kernel<P, 4, 1> : attend_q4_dense_kernel<P, 1, 1>;
+    return tiles == 4 ? attend_q4_dense_kernel<P, 2, 2> : attend_q4_dense_kernel<P, 1, 2>;
+  }
 }
 
 Kern kernel_of(int mode, int group, int page_size, int tiles) {
-  if (mode == kAttendPageLse) {
-    // a unit is one page: a slot, or a tile of it
-    if (page_size == 16)
-      return group <= 8 ? attend_q4_kernel<kAttendPageLse, 16, 1, 1> : attend_q4_kernel<kAttendPageLse, 16, 1, 2>;
-    return group <= 8 ? attend_q4_kernel<kAttendPageLse, 64, 4, 1> : attend_q4_kernel<kAttendPageLse, 64, 4, 2>;
-  }
-  if (page_size == 16) return mode == kAttendSparse ? pick<kAttendSparse, 16>(group, tiles) : pick<kAttendDense, 16>(group, tiles);
-  return mode == kAttendSparse ? pick<kAttendSparse, 64>(group, tiles) : pick<kAttendDense, 64>(group, tiles);
+  const bool p16 = page_size == 16;
+  if (mode == kAttendSparse) return p16 ? pick<kAttendSparse, 16>(group, tiles) : pick<kAttendSparse, 64>(group, tiles);
+  if (mode == kAttendDense) return p16 ? pick<kAttendDense, 16>(group, tiles) : pick<kAttendDense, 64>(group, tiles);
+  return p16 ? pick<kAttendPageLse, 16>(group, tiles) : pick<kAttendPageLse, 64>(group, tiles);
 }
 
 bool prepare(Kern k, int cluster) {
@@ -656,32 +946,24 @@ int active_clusters(Kern k, int cs) {
 
 }  // namespace
 
-int attend_q4_ctas_per_sm(int group) { return group <= 8 ? 2 : 1; }
-
-int attend_q4_active_clusters(int mode, int group, int page_size, int tiles, int cs) {
+int attend_q4_active_clusters(int group, int page_size, int tiles, int cs) {
   // one entry per kernel variant, cluster size and device; the answer depends on nothing else
-  static int cache[2][2][2][2][5][64] = {};
+  static int cache[2][2][2][5][64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || cs < 1 || cs > 16) return 1;
-  int& slot = cache[mode == kAttendSparse][group > 8][page_size == 16][tiles == 4][31 - __builtin_clz((unsigned)cs)][dev];
+  int& slot = cache[group > 8][page_size == 16][tiles == 4][31 - __builtin_clz((unsigned)cs)][dev];
   if (slot == 0) {
-    const int n = active_clusters(kernel_of(mode, group, page_size, tiles), cs);
+    const int n = active_clusters(kernel_of(kAttendSparse, group, page_size, tiles), cs);
     slot = n > 0 ? n : -1;
   }
   return slot > 0 ? slot : 0;
-}
-
-int attend_q4_max_cluster(int mode, int group, int page_size, int tiles) {
-  for (int cs = 16; cs > 1; cs /= 2)
-    if (attend_q4_active_clusters(mode, group, page_size, tiles, cs) > 0) return cs;
-  return 1;
 }
 
 cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStream_t s) {
   const Kern k = kernel_of(mode, a.group, a.page_size, tiles);
   if (!prepare(k, a.cluster)) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.n_splits, a.batch * a.num_kv_heads, 1);
+  cfg.gridDim = dim3(a.n_splits, mode == kAttendDense ? 1 : a.batch * a.num_kv_heads, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;

@@ -164,11 +164,13 @@ cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& tk, const CUte
 cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t s);
 cudaError_t launch_read(const KvReadArgs& a, cudaStream_t s);
 // Attention over a LOCKS_KV_Q4 cache, one query token per sequence.  `tiles`:
-// 16-token tiles a warp takes at once (4, or 1 where a CTA has few pages).
+// 4 for many 16-token tiles per warp and turn, 1 where a CTA has few pages.
+// Page list: a.cluster = a.n_splits CTAs per problem.  Every page: a.n_splits CTAs in
+// all, a.part_* hold two partials per CTA, a.counters B*Hkv + two tickets per CTA.
 cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStream_t s);
-int attend_q4_max_cluster(int mode, int group, int page_size, int tiles);
-int attend_q4_active_clusters(int mode, int group, int page_size, int tiles, int cs);
-int attend_q4_ctas_per_sm(int group);
+// Clusters of cs CTAs of the page-list kernel that the device holds at once.
+int attend_q4_active_clusters(int group, int page_size, int tiles, int cs);
+constexpr int kQ4CtasPerSm = 2;
 
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_topk(const TopkArgs& a, cudaStream_t s, bool pdl);
