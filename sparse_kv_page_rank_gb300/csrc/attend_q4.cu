@@ -31,9 +31,10 @@
 // Precision.  q is scaled by a power of two to fit fp16 (bf16's 8 bits are exact
 // there); logits, maxima, sums and outputs are fp32.  Weights are rounded to fp16
 // twice (2^-11 each, before and after their scale).  They are kept in fp16's range
-// by the reference of the softmax: R = (running maximum) - x with x chosen from the
-// largest value scale seen, so that weight * scale stays below 2^16 and weights
-// 2^-30 below the largest still count.
+// by the reference R of the softmax, from which weights grow up to 2^x, x chosen from
+// the largest value scale seen, so that weight * scale stays below 2^15 and weights
+// 2^-30 below the largest still count.  R moves only when a token outgrows it, so the
+// usual unit needs no maximum across lanes, only a vote.
 //
 // Buffers.  Every warp copies for itself: its lane 0 issues bulk copies of whole pages
 // into the warp's own two 64-token buffers (9216 or 4 x 2304 contiguous bytes; with
@@ -262,17 +263,21 @@ struct Q4Warp {
 #pragma unroll
         for (int k = 0; k < 2; ++k) mx[nt][k] = fmaxf(mx[nt][k], fmaxf(sc[t][nt][k], sc[t][nt][2 + k]));
     }
+    // the unit's maximum per head, base 2 (the lanes of a column hold different tokens)
+    auto whole_max = [&] {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 4));
-        mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 8));
-        mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 16));
-        mx[nt][k] *= fac[nt][k];  // the factor is positive
-      }
+        for (int k = 0; k < 2; ++k) {
+          mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 4));
+          mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 8));
+          mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], 16));
+          mx[nt][k] *= fac[nt][k];  // the factor is positive
+        }
+    };
     if constexpr (LSE) {
       // a unit is one page (a slot of P = 64, a tile of P = 16)
+      whole_max();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -291,45 +296,39 @@ struct Q4Warp {
           }
         }
     } else {
-      int xn;
-      // ---- the weights' exponent offset: the largest value scale, below 2^(e+1),
-      // times weights of up to 2^x stays below 2^15 ----
-      {
-        uint32_t top = 0;
-        if (lane < 8 * TPU) {
-          const int t = lane >> 3;  // this lane's 16 bytes of scales
-          uint4 w = lds128(base + At::value_scales(t) + (lane & 7) * 16);
-          if constexpr (!WHOLE) {
-            // each word: tokens 8 (lane%2) + (lane%8)/2 2, + 1 of tile t
-            const int ln = P == 64 ? sh.len[warp][buf][0] - 16 * t : sh.len[warp][buf][t];
-            const uint32_t msk = pair_mask(8 * (lane & 1) + 2 * ((lane & 7) >> 1), ln);
-            w.x &= msk; w.y &= msk; w.z &= msk; w.w &= msk;
-          }
-          const uint32_t v0 = __vmaxu2(w.x, w.y), v1 = __vmaxu2(w.z, w.w);
-          const uint32_t v = __vmaxu2(v0, v1);
-          top = max(v & 0xffffu, v >> 16);
+      // The weights 2^(s - R) have to stay below 2^x, and 2^x times the largest value
+      // scale below 2^15.  R is moved, and x lowered, only when a token or a scale of
+      // the unit breaks that; then the largest weight becomes 2^(x - 4).
+      uint32_t top = 0;  // largest scale of this lane's 16 bytes, as half bits
+      if (lane < 8 * TPU) {
+        const int t = lane >> 3;
+        uint4 w = lds128(base + At::value_scales(t) + (lane & 7) * 16);
+        if constexpr (!WHOLE) {
+          // each word: tokens 8 (lane%2) + (lane%8)/2 2, + 1 of tile t
+          const int ln = P == 64 ? sh.len[warp][buf][0] - 16 * t : sh.len[warp][buf][t];
+          const uint32_t msk = pair_mask(8 * (lane & 1) + 2 * ((lane & 7) >> 1), ln);
+          w.x &= msk; w.y &= msk; w.z &= msk; w.w &= msk;
         }
-        top = __reduce_max_sync(0xffffffffu, top);
-        // half bits -> exponent; a NaN scale (its product is NaN anyway) counts as the largest
-        const int e = min((int)(top >> 10), 29) - 15;
-        xn = min(x, min(15, 14 - e));
+        const uint32_t v = __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w));
+        top = max(v & 0xffffu, v >> 16);
       }
-      bool moved = false;
-      float Rn[NT][2];
+      const float fx = (float)x;
+      bool moved = (int)(top >> 10) > 29 - x;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          Rn[nt][k] = fmaxf(R[nt][k] + (float)x, mx[nt][k]) - (float)xn;
-          moved |= Rn[nt][k] != R[nt][k];
-        }
+        for (int k = 0; k < 2; ++k) moved |= fmaf(mx[nt][k], fac[nt][k], -R[nt][k]) > fx;
       if (__any_sync(0xffffffffu, moved)) {
+        whole_max();
+        // half bits -> exponent; a NaN scale (its product is NaN anyway) counts as the largest
+        x = min(x, 29 - min((int)(__reduce_max_sync(0xffffffffu, top) >> 10), 29));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float al = Rn[nt][k] == -INFINITY ? 1.f : fast_exp2(R[nt][k] - Rn[nt][k]);
-            R[nt][k] = Rn[nt][k];
+            const float Rn = fmaxf(R[nt][k], mx[nt][k] - (float)(x - 4));
+            const float al = Rn == -INFINITY ? 1.f : fast_exp2(R[nt][k] - Rn);
+            R[nt][k] = Rn;
             l[nt][k] *= al;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -340,7 +339,6 @@ struct Q4Warp {
               }
           }
       }
-      x = xn;
       // ---- weights and the values they weight ----
 #pragma unroll
       for (int t = 0; t < TPU; ++t) {
