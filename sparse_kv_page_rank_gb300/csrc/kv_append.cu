@@ -14,11 +14,13 @@
 // one round trip of dependent loads (lengths, block table, table row, data) plus
 // the launch for a decode step.
 //
-// Split: a CTA takes one token; 16 threads take a row of 128 elements, 8 (16
-// bytes) each, so a thread's dimensions, and with them its cosines and sines, are
-// the same for every row it visits.  The partner of a (d, d + rot/2) pair is read
-// a second time, from L1.  A 32-dimension group is 4 neighbouring threads, whose
-// maximum takes two shuffles.
+// Split: 16 threads take a row of 128 elements, 8 (16 bytes) each, so a thread's
+// dimensions, and with them its cosines and sines, are the same for every row of a
+// token.  The partner of a (d, d + rot/2) pair is read a second time, from L1.  A
+// 32-dimension group is 4 neighbouring threads, whose maximum takes two shuffles.  A
+// prompt's token is one warp's, which has four pairs of rows in flight while it finds
+// the token's place; a decode step's few tokens are a CTA's each, whose eight warps
+// load all rows at once.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -29,8 +31,9 @@ namespace locks {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kRowThreads = kHeadDim / 8;                  // threads of one row
-constexpr int kRowsAtOnce = kAppendThreads / kRowThreads;  // rows a CTA visits at once
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kRowThreads = kHeadDim / 8;  // threads of one row: two rows per warp and step
+constexpr int kInFlight = 4;               // steps whose rows are loaded together
 
 // The sequence of token row t and its place: position, physical page, slot.
 struct TokenPlace {
@@ -38,30 +41,30 @@ struct TokenPlace {
   bool ok;
 };
 
-// Every thread computes the same thing (a few broadcast loads).
+// Whole warps; every lane gets the same answer.
 __device__ __forceinline__ TokenPlace token_place(const KvTokenArgs& a, int t, bool report) {
   TokenPlace r;
   r.ok = false;
   r.pos = r.phys = r.slot = 0;
+  r.b = t;
   int n_b = 1, i = 0;
   if (a.cu_tokens) {
-    // the last b with cu_tokens[b] <= t
-    int lo = 0, hi = a.batch;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.cu_tokens + mid) <= t) lo = mid; else hi = mid - 1;
+    // the last b with cu_tokens[b] <= t: 32 sequences at a time
+    const int lane = threadIdx.x & 31;
+    r.b = 0;
+    for (int b0 = 1; b0 <= a.batch; b0 += 32) {
+      const int n = __popc(__ballot_sync(0xffffffffu, b0 + lane <= a.batch && __ldg(a.cu_tokens + b0 + lane) <= t));
+      r.b += n;
+      if (n < 32) break;
     }
-    r.b = lo;
-    if (lo >= a.batch) return r;  // a row behind the last sequence
-    const int c0 = __ldg(a.cu_tokens + lo), c1 = __ldg(a.cu_tokens + lo + 1);
+    if (r.b >= a.batch) return r;  // a row behind the last sequence
+    const int c0 = __ldg(a.cu_tokens + r.b), c1 = __ldg(a.cu_tokens + r.b + 1);
     n_b = c1 - c0;
     i = t - c0;
     if (i < 0 || i >= n_b || i >= a.max_tokens) {
       if (report) set_error(a.err, LOCKS_DEVERR_LENGTHS);
       return r;
     }
-  } else {
-    r.b = t;
   }
   const int len = __ldg(a.seq_lens + r.b);
   if (!a.cu_tokens && len == 0) return r;  // an idle slot of a padded batch
@@ -159,22 +162,44 @@ __device__ __forceinline__ void put_v_q4(uint8_t* block, int P, int slot, int ch
                                2 * (t & 1)) = s;
 }
 
-template <bool Q4>
+// WPT: warps of a token (1 or 8).
+template <bool Q4, int WPT>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppendArgs a) {
-  const int t = blockIdx.x;
-  const int ch = threadIdx.x % kRowThreads, r0 = threadIdx.x / kRowThreads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (kAppendWarps / WPT) + warp / WPT;
+  const int ch = lane % kRowThreads, r0 = warp % WPT * 2 + lane / kRowThreads;
   pdl_wait();
-  const TokenPlace tp = token_place(a.tok, t, threadIdx.x == 0);
-  if (!tp.ok) return;
+  pdl_launch_dependents();
+  if (t >= a.tok.total) return;
   const int hkv = a.tok.num_kv_heads, P = a.tok.page_size;
   const int half = a.rotary_dim / 2, d0 = 8 * ch;
   const bool turns = d0 < a.rotary_dim;
   const bool upper = !a.interleaved && d0 >= half;
+  // rows of the token: keys, values, then queries
+  const int rows = 2 * hkv + (a.q ? a.num_q_heads : 0);
+  const uint16_t* kr = a.k + (size_t)t * a.k_stride + d0;
+  const uint16_t* vr = a.v + (size_t)t * a.v_stride + d0 - hkv * kHeadDim;
+  const uint16_t* qr = a.q + (size_t)t * a.q_stride + d0 - 2 * hkv * kHeadDim;
+  const int to_mate = upper ? -half : half;
+  uint4 x[kInFlight], mate[kInFlight];
+  auto load = [&](int r) {
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k, r += 2 * WPT) {
+      if (r >= rows) continue;
+      const uint16_t* src = (r < hkv ? kr : (r < 2 * hkv ? vr : qr)) + r * kHeadDim;
+      x[k] = *reinterpret_cast<const uint4*>(src);
+      if (turns && !a.interleaved && (r < hkv || r >= 2 * hkv)) mate[k] = *reinterpret_cast<const uint4*>(src + to_mate);
+    }
+  };
+  load(r0);  // under way while the token's place is looked up
+  const bool says = lane == 0 && warp % WPT == 0;
+  const TokenPlace tp = token_place(a.tok, t, says);
+  if (!tp.ok) return;
   Turn tr;
   if (a.rotary_dim) {
     const int row = a.positions ? __ldg(a.positions + t) : tp.pos;
     if (row < 0 || row >= a.rope_rows) {
-      if (threadIdx.x == 0) set_error(a.tok.err, LOCKS_DEVERR_POSITION);
+      if (says) set_error(a.tok.err, LOCKS_DEVERR_POSITION);
       return;
     }
     if (turns) {
@@ -190,53 +215,52 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppendAr
       }
     }
   }
-  // rows of this token: keys, values, then queries
-  const int rows = 2 * hkv + (a.q ? a.num_q_heads : 0);
-  for (int r = r0; r < (rows + kRowsAtOnce - 1) / kRowsAtOnce * kRowsAtOnce; r += kRowsAtOnce) {
-    const bool in = r < rows;
-    const bool is_k = r < hkv, is_v = !is_k && r < 2 * hkv;
-    const int h = is_k ? r : (is_v ? r - hkv : r - 2 * hkv);
-    const uint16_t* src = is_k ? a.k + (size_t)t * a.k_stride
-                               : (is_v ? a.v + (size_t)t * a.v_stride : a.q + (size_t)t * a.q_stride);
-    uint4 x = make_uint4(0, 0, 0, 0), mate = x;
-    if (in) {
-      x = *reinterpret_cast<const uint4*>(src + h * kHeadDim + d0);
-      if (turns && !is_v && !a.interleaved)
-        mate = *reinterpret_cast<const uint4*>(src + h * kHeadDim + (upper ? d0 - half : d0 + half));
-    }
-    // queries rotated in place: both partners are read before either is written
+  const size_t page = (size_t)tp.phys * hkv;
+  uint16_t* q_out = a.q_out + (size_t)t * a.q_out_stride + d0 - 2 * hkv * kHeadDim;
+  // both rows of a warp's step exist or end together but for the last one
+  for (int rb = r0; rb - lane / kRowThreads < rows; rb += 2 * WPT * kInFlight) {
+    if (rb != r0) load(rb);
+    // queries may be rotated in place: a row's partners are read before either is written
     __syncwarp();
-    if (turns && !is_v) x = rotate8(x, mate, tr, a.interleaved, upper);
-    const size_t ph = (size_t)tp.phys * hkv + h;
-    if (Q4) {
-      // the shuffles of the quantiser need whole groups; a warp's two rows may
-      // be of different kinds
-      uint8_t* block = reinterpret_cast<uint8_t*>(a.k_pool) + ph * (size_t)LOCKS_KV_Q4_BLOCK_BYTES(P);
-      const bool any_kv = __any_sync(0xffffffffu, in && (is_k || is_v));
-      if (any_kv) {
-        int u[8];
-        const __half s = quantise8(x, u);
-        if (in && is_k) put_k_q4(block, P, tp.slot, ch, u, s);
-        if (in && is_v) put_v_q4(block, P, tp.slot, ch, u, s);
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      const int r = rb + 2 * WPT * k;
+      const bool in = r < rows, is_kv = r < 2 * hkv, is_v = is_kv && r >= hkv;
+      uint4 y = in ? x[k] : make_uint4(0, 0, 0, 0);
+      if (in && turns && !is_v) y = rotate8(y, mate[k], tr, a.interleaved, upper);
+      const size_t ph = page + (is_v ? r - hkv : r);
+      if (Q4) {
+        // the shuffles of the quantiser are a whole warp's, whose two rows may be of
+        // different kinds
+        if (__any_sync(0xffffffffu, in && is_kv)) {
+          uint8_t* block = reinterpret_cast<uint8_t*>(a.k_pool) + ph * (size_t)LOCKS_KV_Q4_BLOCK_BYTES(P);
+          int u[8];
+          const __half s = quantise8(y, u);
+          if (in && is_kv && !is_v) put_k_q4(block, P, tp.slot, ch, u, s);
+          if (in && is_v) put_v_q4(block, P, tp.slot, ch, u, s);
+        }
+      } else if (in && is_kv) {
+        uint16_t* pool = reinterpret_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool);
+        *reinterpret_cast<uint4*>(pool + (ph * P + tp.slot) * kHeadDim + d0) = y;
       }
-    } else if (in && (is_k || is_v)) {
-      uint16_t* pool = reinterpret_cast<uint16_t*>(is_k ? a.k_pool : a.v_pool);
-      *reinterpret_cast<uint4*>(pool + (ph * P + tp.slot) * kHeadDim + d0) = x;
+      if (in && !is_kv) *reinterpret_cast<uint4*>(q_out + (size_t)r * kHeadDim) = y;
     }
-    if (in && !is_k && !is_v) *reinterpret_cast<uint4*>(a.q_out + (size_t)t * a.q_out_stride + h * kHeadDim + d0) = x;
   }
-  pdl_launch_dependents();
 }
 
-template <bool Q4>
+template <bool Q4, int WPT>
 __global__ void __launch_bounds__(kAppendThreads) read_kernel(const KvReadArgs a) {
-  const int t = blockIdx.x;
-  const int ch = threadIdx.x % kRowThreads, r0 = threadIdx.x / kRowThreads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (kAppendWarps / WPT) + warp / WPT;
+  const int ch = lane % kRowThreads, r0 = warp % WPT * 2 + lane / kRowThreads;
   pdl_wait();
-  const TokenPlace tp = token_place(a.tok, t, threadIdx.x == 0);
+  pdl_launch_dependents();
+  if (t >= a.tok.total) return;
+  const TokenPlace tp = token_place(a.tok, t, lane == 0 && warp % WPT == 0);
   if (!tp.ok) return;
   const int hkv = a.tok.num_kv_heads, P = a.tok.page_size, slot = tp.slot;
-  for (int r = r0; r < 2 * hkv; r += kRowsAtOnce) {
+#pragma unroll 4
+  for (int r = r0; r < 2 * hkv; r += 2 * WPT) {
     const bool is_k = r < hkv;
     const int h = is_k ? r : r - hkv;
     uint16_t* out = is_k ? a.k_out : a.v_out;
@@ -273,13 +297,18 @@ __global__ void __launch_bounds__(kAppendThreads) read_kernel(const KvReadArgs a
     }
     *reinterpret_cast<uint4*>(out + ((size_t)t * hkv + h) * kHeadDim + 8 * ch) = x;
   }
-  pdl_launch_dependents();
 }
 
+// A CTA per token while that many CTAs are resident at once (eight per SM), so that a
+// decode step takes one round of loads; beyond that a warp per token.
+constexpr int kWideTokens = 8 * 152;
+
 template <typename K, typename A>
-cudaError_t launch_tokens(K kern, const A& a, cudaStream_t s) {
+cudaError_t launch_tokens(K wide, K narrow, const A& a, cudaStream_t s) {
+  const bool w = a.tok.total <= kWideTokens;
+  const K kern = w ? wide : narrow;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.tok.total, 1, 1);
+  cfg.gridDim = dim3(w ? a.tok.total : (a.tok.total + kAppendWarps - 1) / kAppendWarps, 1, 1);
   cfg.blockDim = dim3(kAppendThreads, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -293,11 +322,13 @@ cudaError_t launch_tokens(K kern, const A& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t s) {
-  return a.tok.q4 ? launch_tokens(append_kernel<true>, a, s) : launch_tokens(append_kernel<false>, a, s);
+  return a.tok.q4 ? launch_tokens(append_kernel<true, 8>, append_kernel<true, 1>, a, s)
+                  : launch_tokens(append_kernel<false, 8>, append_kernel<false, 1>, a, s);
 }
 
 cudaError_t launch_read(const KvReadArgs& a, cudaStream_t s) {
-  return a.tok.q4 ? launch_tokens(read_kernel<true>, a, s) : launch_tokens(read_kernel<false>, a, s);
+  return a.tok.q4 ? launch_tokens(read_kernel<true, 8>, read_kernel<true, 1>, a, s)
+                  : launch_tokens(read_kernel<false, 8>, read_kernel<false, 1>, a, s);
 }
 
 }  // namespace locks

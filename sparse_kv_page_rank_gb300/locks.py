@@ -192,25 +192,36 @@ def make_tokens(cu_tokens, total: int, max_tokens: int) -> lockskv_tokens_t:
     return lockskv_tokens_t(_ptr(cu_tokens), int(total), int(max_tokens))
 
 
+_bf16 = None
+
+
 def _row_stride(x, what: str) -> int:
     """Elements between the token rows of x [total][heads][128] (bf16, heads contiguous)."""
-    import torch
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[2] != 128:
+    global _bf16
+    if _bf16 is None:
+        import torch
+        _bf16 = torch.bfloat16
+    if x.dtype is not _bf16 or x.dim() != 3:
         raise ValueError(f"{what} must be bf16 [tokens][heads][128]")
-    if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != 128):
+    n, h, d = x.shape
+    row, head, one = x.stride()
+    if d != 128:
+        raise ValueError(f"{what} must be bf16 [tokens][heads][128]")
+    if one != 1 or (head != 128 and h > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * 128
+    return row if n > 1 else h * 128
 
 
 def make_append(k, v, q=None, q_out=None, rope=None, rotary_dim: int = 0, positions=None,
                 interleaved: bool = False) -> lockskv_append_t:
     """C struct of what lockskv_append writes, from tensors [total][heads][128]."""
-    return lockskv_append_t(_ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(rope), _ptr(positions),
-                            _row_stride(k, "k"), _row_stride(v, "v"),
-                            _row_stride(q, "q") if q is not None else 0,
-                            _row_stride(q_out, "q_out") if q_out is not None else 0,
-                            q.shape[1] if q is not None else 0, rope.shape[0] if rope is not None else 0,
-                            int(rotary_dim), int(interleaved))
+    qs = qos = heads = rows = 0
+    if q is not None:
+        heads, qs, qos = q.shape[1], _row_stride(q, "q"), _row_stride(q_out, "q_out")
+    if rope is not None:
+        rows = rope.shape[0]
+    return lockskv_append_t(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), _ptr(rope), _ptr(positions),
+                            _row_stride(k, "k"), _row_stride(v, "v"), qs, qos, heads, rows, rotary_dim, interleaved)
 
 
 def make_summary(basis_t, coeffs, rank: int, dtype: int = LOCKS_DTYPE_BF16) -> locks_summary_t:

@@ -160,25 +160,29 @@ class LocksRuntime:
         without cu_tokens there is one token per sequence.  Returns the
         rotated queries (``q_out``, by default a new tensor; ``q`` itself
         rotates in place), or None without q."""
-        total = k.shape[0]
-        if k.shape[1] != self.num_kv_heads or v.shape != k.shape:
+        shape = k.shape
+        total = shape[0]
+        if shape[1] != self.num_kv_heads or v.shape != shape:
             raise ValueError(f"k and v must be [tokens][{self.num_kv_heads}][128]")
         if q is not None:
-            if q.shape[0] != total or q.shape[1] != self.num_q_heads:
+            shape = q.shape
+            if shape[0] != total or shape[1] != self.num_q_heads:
                 raise ValueError(f"q must be [{total}][{self.num_q_heads}][128]")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            elif q_out.shape != q.shape:
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            elif q_out.shape != shape:
                 raise ValueError("q_out must have q's shape")
         elif q_out is not None:
             raise ValueError("q_out without q")
         if rope is None:
             rotary_dim = rotary_dim or 0
         else:
-            if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+            if rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
                 raise ValueError("rope must be contiguous float32 [positions][rotary_dim]")
-            rotary_dim = rope.shape[1] if rotary_dim is None else rotary_dim
-            if rotary_dim != rope.shape[1]:
+            cols = rope.shape[1]
+            if rotary_dim is None:
+                rotary_dim = cols
+            elif rotary_dim != cols:
                 raise ValueError("rope must have rotary_dim columns")
         if positions is not None and (positions.dtype != torch.int32 or positions.numel() != total
                                       or not positions.is_contiguous()):
@@ -208,7 +212,7 @@ class LocksRuntime:
         stride = L._row_stride(q, "q")
         tokens = self._tokens(total, cu_tokens, max_tokens)
         if out is None:
-            out = torch.empty((total, self.num_q_heads, 128), dtype=torch.bfloat16, device=self.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if lse is None:
             lse = torch.empty((total, self.num_q_heads), dtype=torch.float32, device=self.device)
         need = self._prompt_need.get((total, tokens.max_tokens))
