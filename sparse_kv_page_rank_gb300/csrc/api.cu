@@ -265,12 +265,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2-D view of a pool of 128-column bf16 rows (rows = pages_total * Hkv *
-// rows_per_page); 64-column boxes of box_rows rows with 128-byte swizzle.
-bool encode_rows(CUtensorMap* m, const void* pool, const locks_cache_t* c, int rows_per_page, int box_rows) {
+// 2-D view of 128-column 16-bit rows; 64-column boxes of box_rows rows with
+// 128-byte swizzle.  (Copies move bits, so the type only says their size.)
+bool encode_matrix(CUtensorMap* m, const void* pool, size_t rows, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)c->pages_total * c->num_kv_heads * rows_per_page};
+  cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * 2};
   cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
@@ -278,6 +278,11 @@ bool encode_rows(CUtensorMap* m, const void* pool, const locks_cache_t* c, int r
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// A pool of bf16 pages (rows = pages_total * Hkv * rows_per_page).
+bool encode_rows(CUtensorMap* m, const void* pool, const locks_cache_t* c, int rows_per_page, int box_rows) {
+  return encode_matrix(m, pool, (size_t)c->pages_total * c->num_kv_heads * rows_per_page, box_rows);
 }
 
 // K or V pool: boxes of one page-head's rows x 64 columns (one page-head is
@@ -455,20 +460,29 @@ locks_status_t check_err_ws(void* ws, size_t bytes) {
 
 // Launch shape and workspace of lockskv_prompt_attend.
 constexpr long long kPromptCounters = 1024;
+// 4-bit pages: from this many row tiles of a head on, its keys and values are
+// converted once for all of them, where the planes take no more than this.
+constexpr int kPlaneTiles = 4;
+constexpr long long kPlaneBytes = 4LL << 30;
 struct PromptPlan {
-  int n_qtiles = 1, n_splits = 1;
-  size_t off_counters = 0, off_ml = 0, off_o = 0, total = 0;
+  int n_qtiles = 1, n_splits = 1, plane_rows = 0;
+  bool planes = false;
+  size_t off_counters = 0, off_ml = 0, off_o = 0, off_planes = 0, total = 0;
 };
 
-// Tiles of 2 * (128 / G) tokens; where there are fewer of them than SMs, the keys
-// are cut as well, down to about two blocks of 128 per CTA.
+// Where there are fewer row tiles than SMs, the keys are cut as well, down to about
+// two blocks of 128 per CTA.
 locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, const lockskv_tokens_t* t, PromptPlan* pl) {
-  const int G = p->num_q_heads / c->num_kv_heads, per_cta = 2 * (128 / G);
+  const int G = p->num_q_heads / c->num_kv_heads, per_tile = 128 / G;  // tokens of a 128-row tile
   const long long BH = (long long)c->batch * c->num_kv_heads;
-  pl->n_qtiles = std::max(1, (t->max_tokens + per_cta - 1) / per_cta);
+  const long long blocks = ((long long)c->max_pages * c->page_size + 127) / 128;
+  const long long tiles = std::max(1, (t->max_tokens + per_tile - 1) / per_tile);
+  const long long plane_bytes = 3 * BH * blocks * 128 * kHeadDim * 2;
+  pl->planes = is_q4(c) && tiles >= kPlaneTiles && plane_bytes <= kPlaneBytes;
+  pl->plane_rows = (int)(blocks * 128);
+  pl->n_qtiles = (int)(is_q4(c) && !pl->planes ? tiles : (tiles + 1) / 2);
   if (pl->n_qtiles > 65535) return LOCKS_ERR_UNSUPPORTED;
   const long long ctas = BH * pl->n_qtiles, sms = device_sm_count();
-  const long long blocks = ((long long)c->max_pages * c->page_size + 127) / 128;
   pl->n_splits = (int)std::max<long long>(1, std::min<long long>(sms / ctas, (blocks + 1) / 2));
   if (BH * pl->n_splits > 0x7fffffffLL) return LOCKS_ERR_UNSUPPORTED;
   // The error word, then the counters (problems are split only while there are at
@@ -482,7 +496,9 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
   pl->off_ml = off;
   off = align_up(off + sizeof(float2) * parts);
   pl->off_o = off;
-  pl->total = align_up(off + sizeof(float) * parts * kHeadDim);
+  off = align_up(off + sizeof(float) * parts * kHeadDim);
+  pl->off_planes = off;
+  pl->total = align_up(off + (pl->planes ? (size_t)plane_bytes : 0));
   return LOCKS_OK;
 }
 
@@ -780,7 +796,12 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   std::memset(&tv, 0, sizeof(tv));
   if (!is_q4(cache) && (!encode_pool(&tk, cache->k_pool, cache) || !encode_pool(&tv, cache->v_pool, cache)))
     return LOCKS_ERR_CUDA;
+  if (pl.planes && !encode_matrix(&tk, at<uint16_t>(ws, pl.off_planes),
+                                  3 * (size_t)cache->batch * cache->num_kv_heads * pl.plane_rows, 128))
+    return LOCKS_ERR_CUDA;
   PromptArgs a;
+  a.planes = pl.planes ? at<uint16_t>(ws, pl.off_planes) : nullptr;
+  a.plane_rows = pl.plane_rows;
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_stride;
   a.k_pool = cache->k_pool;

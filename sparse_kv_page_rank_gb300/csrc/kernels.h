@@ -154,12 +154,15 @@ struct PromptArgs {
   int* err;
   int batch, num_kv_heads, group, max_pages, pages_total, page_size;
   int total, max_tokens;
-  int n_qtiles;              // CTAs along a sequence's new tokens (256 rows each)
+  int n_qtiles;              // CTAs along a sequence's new tokens (256 rows each; 128 for 4-bit codes)
   int n_splits;              // CTAs along the keys
   float scale_log2;
   int q4;
+  uint16_t* planes;          // 4-bit pages, many rows: ws [3][B][Hkv][plane_rows][d] fp16; else null
+  int plane_rows;            // tokens of a plane, whole blocks of 128
 };
 
+// tk, tv: the pools; with planes tk is their tensor map (boxes of 128 rows x 64 columns).
 cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
 cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t s);
 cudaError_t launch_read(const KvReadArgs& a, cudaStream_t s);

@@ -9,28 +9,31 @@
 // What bounds it: 4 * 128 operations per visible (row, key) at the tensor cores'
 // rate; for few rows over a long cache, the cache's bytes.
 //
-// Layout.  A CTA takes two tiles (256 rows) of one KV head, so that one tile's
-// softmax runs while the other's products do, and walks the keys in blocks of 128.
-// Tensor memory (512 columns): S of both tiles, 128 columns each, whose first 64
-// columns P overwrites (16-bit pairs, the A operand of the second product), and O
-// of both tiles, 128 columns each.  Warps: 0 issues the matrix instructions, 1 the
-// copies; 4-7 and 8-11 are the softmax of the two tiles, one thread per row, so
-// neither maximum nor sum needs a shuffle; 12-15 (4-bit pages) turn codes into the
-// fp16 operands.  Matrix instructions of one CTA execute in the order of issue, so
-// S of the next block may be issued right behind the product that reads P from the
-// same columns, and a softmax that has seen S of block j knows that O holds all
-// blocks before j: it rescales O in place, and only when a row's maximum has grown
-// by more than 2^8 since its last reference.
+// Layout.  Tensor memory (512 columns): two S buffers of 128 columns, whose first 64
+// columns P overwrites (16-bit pairs, the A operand of the second product), and one or
+// two O of 128 columns.  Keys and values come as 32 KiB operands (128 tokens in the
+// instructions' 128-byte swizzle) through a ring of five, so that copies run one to
+// two blocks ahead.  Warps: 0 issues the matrix instructions, 1 the copies, 4 and up
+// are the softmax of a tile, one thread per row, so neither maximum nor sum needs a
+// shuffle.  Matrix instructions of one CTA execute in the order of issue, so S of the
+// next block may be issued right behind the product that reads P from the same
+// columns.  O is rescaled in place by the softmax warps, and only when a row's
+// maximum has grown by more than 2^8 since its last reference.
 //
-// bf16 pages arrive by TMA in the operands' own order (64-column boxes, 128-byte
-// swizzle).  4-bit pages arrive as whole page-heads and are converted to fp16, with q
-// scaled into fp16 by a power of two.  A key s * code has up to 14 significant bits:
-// it is held as the nearest half and the remainder, both exact, and S is the sum of
-// the products with both (one half alone would put 2^-11 of sum |q||k| into every
-// logit).  Values are s * code rounded once (2^-11), weights are scaled by 2^6, so
-// that those 2^-30 of the largest still count.  The two operands of the keys leave
-// room for one block of keys in shared memory, which is converted while the products
-// with the values run.
+// Three sources of the operands:
+//  - bf16 pages: TMA copies of the pages (64-column boxes).  A CTA takes two tiles
+//    (256 rows), so that one tile's softmax runs while the other's products do.
+//  - 4-bit pages, many rows: each key is needed by many CTAs, so one kernel first
+//    writes the sequence's keys and values as fp16 planes into the workspace, and
+//    TMA copies fetch those; else as above.
+//  - 4-bit pages, few rows: eight warps turn the pages' codes into operands in shared
+//    memory.  A CTA takes one tile and both S buffers, so that S of the next block is
+//    made while the softmax of this one runs.
+// fp16 operands: q is scaled by a power of two.  A key s * code has up to 14
+// significant bits: it is held as the nearest half and the remainder, both exact, and
+// S is the sum of the products with both (one half alone would put 2^-11 of
+// sum |q||k| into every logit).  Values are s * code rounded once (2^-11), weights are
+// scaled by 2^6, so that those 2^-30 of the largest still count.
 //
 // Values that a row does not see must not reach it, not even as 0 * NaN: in the
 // blocks that straddle a tile's diagonal or the end of the sequence, value rows past
@@ -53,25 +56,30 @@ constexpr int kRows = 128;                   // rows of a tile
 constexpr int kBlock = 128;                  // keys of a block
 constexpr int kHalf = kBlock * 128;          // bytes of 64 columns of 128 16-bit rows
 constexpr int kOperand = 2 * kHalf;          // one tile of Q, K or V: 32 KiB
-constexpr int kKvBytes = 4 * kOperand;       // keys and values: two operands each
-constexpr int kKvStages = 2;                 // blocks of values in flight, and of bf16 keys
-template <bool Q4>
-constexpr int kKeyStages = Q4 ? 1 : kKvStages;
-constexpr uint32_t kValues = 2 * kOperand;   // offset of the values behind the keys
+constexpr int kSlots = 5;                    // operands in the ring of keys and values
 constexpr int kRawSlots = 3;                 // 4-bit pages: 64-token slots of codes
-constexpr int kSkipRing = 4;                 // the copies run at most three blocks ahead of the softmax
+constexpr int kSkipRing = 8;                 // the copies run at most five operands ahead of the products
 constexpr int kMaxBad = 2 * kRows;           // tokens near a diagonal: no more than a CTA has
 constexpr float kLazy = 8.f;                 // growth of a maximum (base 2) that O's reference tolerates
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;             // S: columns 0 and 128; O: 256 and 384
 
+// Where the operands come from.
+enum Source { kBf16Pages, kPlanes, kCodes };
+template <Source S>
+constexpr int kTiles = S == kCodes ? 1 : 2;   // tiles of a CTA
+template <Source S>
+constexpr int kUnits = S == kBf16Pages ? 2 : 3;  // operands of a block: keys (two halves), values
+template <Source S>
+constexpr int kThreadsOf = S == kCodes ? 512 : 384;
+
 struct PromptShared {
-  uint64_t q_full, k_full[2], v_full[2], k_empty[2], v_empty[2];
-  uint64_t s_full[2], p_ready[2], o_full[2], drain;
+  uint64_t q_full, full[kSlots], empty[kSlots];
+  uint64_t s_full[2], p_ready[2], o_full[2], pv_done, drain;
   uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
   uint32_t tmem;
-  int skip[kSkipRing];      // 16-token groups of a block whose page is outside the pool (bits)
-  int raw_skip[kRawSlots];  // the same of a slot
+  int skip[2][kSkipRing];   // per half of a block: 16-token groups whose page is outside the pool (bits)
+  int raw_skip[kRawSlots];  // the same of a slot of codes
   int abort;                // a bounded wait gave up
   int n_bad, bad[kMaxBad];
   int last;
@@ -154,14 +162,14 @@ __device__ float value_at(const PromptArgs& a, const PromptPlace& w, int t, int 
 }
 
 // ---- warp 1: the copies ---------------------------------------------------------
-template <bool Q4, int P>
+template <Source S, int P>
 __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUtensorMap* tk, const CUtensorMap* tv,
-                          PromptShared& sh, uint8_t* kv, uint8_t* raw) {
+                          PromptShared& sh, uint8_t* ring, uint8_t* raw) {
   constexpr int kPPB = kBlock / P;  // pages of a block
   constexpr int kAtOnce = 32 / kPPB;
   const int lane = threadIdx.x & 31;
   const int n_pages = (w.len + P - 1) / P;
-  int nk = 0, nv = 0, nr = 0;  // blocks (slots) asked for
+  int asked = 0;  // operands (slots of codes) asked for
   bool ok = true;
   for (int jb = w.j0; jb < w.j1 && ok; jb += kAtOnce) {
     // the pages of several blocks at a time, one per lane
@@ -175,44 +183,54 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
       }
     }
     for (int j = jb; j < min(jb + kAtOnce, w.j1) && ok; ++j) {
-      const int n = j - w.j0, st = n % kKvStages;
+      const int n = j - w.j0;
       int pg[kPPB], skip = 0;
 #pragma unroll
       for (int i = 0; i < kPPB; ++i) {
         pg[i] = __shfl_sync(0xffffffffu, phys, (j - jb) * kPPB + i);
         if (pg[i] < 0) skip |= ((1 << (P / 16)) - 1) << (i * (P / 16));
       }
-      if constexpr (!Q4) {
+      if constexpr (S != kCodes) {
         const int copies = kPPB - __popc(skip) / (P / 16);
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {  // keys, then values
-          uint64_t* full = v ? &sh.v_full[st] : &sh.k_full[st];
-          uint64_t* empty = v ? &sh.v_empty[st] : &sh.k_empty[st];
-          if (n >= kKvStages && !wait_warp(empty, (n / kKvStages - 1) & 1, sh)) {
+        for (int u = 0; u < kUnits<S>; ++u, ++asked) {  // keys, then values
+          const int slot = asked % kSlots;
+          if (asked >= kSlots && !wait_warp(&sh.empty[slot], (asked / kSlots - 1) & 1, sh)) {
             ok = false;
             break;
           }
           if (lane == 0) {
-            if (!v) sh.skip[n % kSkipRing] = skip;
-            mbar_arrive_expect_tx(full, (uint32_t)copies * P * 256);
+            uint64_t* full = &sh.full[slot];
+            uint8_t* dst = ring + slot * kOperand;
+            if (u == 0) {
+              sh.skip[0][n % kSkipRing] = skip & 15;
+              sh.skip[1][n % kSkipRing] = skip >> 4;
+            }
+            if constexpr (S == kPlanes) {
+              // plane u of this sequence and head
+              const int y = (int)(((long long)u * a.batch + w.b) * a.num_kv_heads + w.hkv) * a.plane_rows + j * kBlock;
+              mbar_arrive_expect_tx(full, kOperand);
+              tma_load_2d(dst, tk, full, 0, y);
+              tma_load_2d(dst + kHalf, tk, full, 64, y);
+            } else {
+              mbar_arrive_expect_tx(full, (uint32_t)copies * P * 256);
 #pragma unroll
-            for (int i = 0; i < kPPB; ++i) {
-              if (pg[i] < 0) continue;
-              const int y = (pg[i] * a.num_kv_heads + w.hkv) * P;
-              uint8_t* dst = kv + v * kValues + st * kOperand + i * P * 128;
-              tma_load_2d(dst, v ? tv : tk, full, 0, y);
-              tma_load_2d(dst + kHalf, v ? tv : tk, full, 64, y);
+              for (int i = 0; i < kPPB; ++i) {
+                if (pg[i] < 0) continue;
+                const int y = (pg[i] * a.num_kv_heads + w.hkv) * P;
+                tma_load_2d(dst + i * P * 128, u ? tv : tk, full, 0, y);
+                tma_load_2d(dst + kHalf + i * P * 128, u ? tv : tk, full, 64, y);
+              }
             }
           }
           __syncwarp();
-          if (v) nv = n + 1; else nk = n + 1;
         }
       } else {
         // two 64-token slots of codes; the converters hand `skip` on with the block
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int s = 2 * n + hh, rs = s % kRawSlots;
-          if (s >= kRawSlots && !wait_warp(&sh.raw_empty[rs], (s / kRawSlots - 1) & 1, sh)) {
+        for (int hh = 0; hh < 2; ++hh, ++asked) {
+          const int rs = asked % kRawSlots;
+          if (asked >= kRawSlots && !wait_warp(&sh.raw_empty[rs], (asked / kRawSlots - 1) & 1, sh)) {
             ok = false;
             break;
           }
@@ -232,146 +250,228 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
             }
           }
           __syncwarp();
-          nr = s + 1;
         }
       }
     }
   }
   if (!ok && lane == 0) {
     // let the copies in flight land before the memory is given back
-    for (int n = max(0, nk - kKvStages); n < nk; ++n) (void)mbar_wait(&sh.k_full[n % kKvStages], (n / kKvStages) & 1);
-    for (int n = max(0, nv - kKvStages); n < nv; ++n) (void)mbar_wait(&sh.v_full[n % kKvStages], (n / kKvStages) & 1);
-    for (int s = max(0, nr - kRawSlots); s < nr; ++s) (void)mbar_wait(&sh.raw_full[s % kRawSlots], (s / kRawSlots) & 1);
+    constexpr int kRing = S == kCodes ? kRawSlots : kSlots;
+    for (int i = max(0, asked - kRing); i < asked; ++i)
+      (void)mbar_wait(S == kCodes ? &sh.raw_full[i % kRing] : &sh.full[i % kRing], (i / kRing) & 1);
   }
 }
 
-// ---- warps 12-15: codes to fp16 operands -----------------------------------------
+// ---- codes to fp16 --------------------------------------------------------------
+// The keys of a 16-byte piece c of one token's codes (its 8-byte scales z): for each
+// scale group j the eight dimensions 32 j + 8 c .. + 7 as the nearest halves and the
+// remainders; out(j, hi, lo).
+template <typename Out>
+__device__ __forceinline__ void convert_keys(uint4 x, uint2 z, Out out) {
+  const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t zz = __byte_perm(j < 2 ? z.x : z.y, 0, j & 1 ? 0x3232 : 0x1010);
+    uint32_t f[4], hi[4], lo[4];
+    q4_codes(words[j], f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hi[e] = mul_f16x2(f[e], zz);
+      lo[e] = fma_f16x2(f[e], zz, hi[e] ^ 0x80008000u);  // s * code - hi, exact
+    }
+    out(j, hi, lo);
+  }
+}
+// The values of a lane's 16 bytes: for each j the dimensions 32 j + 4 g .. + 3 of two
+// tokens, whose scales are the halves of z's words; out(j, token 0's, token 1's).
+template <typename Out>
+__device__ __forceinline__ void convert_values(uint4 x, uint4 z, Out out) {
+  const uint32_t words[4] = {x.x, x.y, x.z, x.w}, zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t f[4];
+    q4_codes(words[j], f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = mul_f16x2(f[i], zw[j]);
+    out(j, make_uint2(__byte_perm(f[0], f[1], 0x5410), __byte_perm(f[2], f[3], 0x5410)),
+        make_uint2(__byte_perm(f[0], f[1], 0x7632), __byte_perm(f[2], f[3], 0x7632)));
+  }
+}
+
+// Warps 8-15 (kCodes): four warps for each half of a block.
 template <int P>
-__device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t kv, uint32_t raw) {
+__device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t ring, uint32_t raw) {
   using At = Q4Tile<P>;
-  const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+  const int hh = (threadIdx.x >> 7) & 1, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  auto wait_empty = [&](int i) {
+    return i < kSlots || wait_warp(&sh.empty[i % kSlots], (i / kSlots - 1) & 1, sh);
+  };
   for (int n = 0; n < w.j1 - w.j0; ++n) {
-    const int st = n % kKvStages;
-    const uint32_t kd = kv, vd = kv + kValues + st * kOperand;
-    if (n >= 1 && !wait_warp(&sh.k_empty[0], (n - 1) & 1, sh)) return;
-#pragma unroll 1
-    for (int hh = 0; hh < 2; ++hh) {
-      const int s = 2 * n + hh, rs = s % kRawSlots;
-      if (!wait_warp(&sh.raw_full[rs], (s / kRawSlots) & 1, sh)) return;
-      if (tid == 0) {
-        if (hh == 0) sh.skip[n % kSkipRing] = sh.raw_skip[rs];
-        else sh.skip[n % kSkipRing] |= sh.raw_skip[rs] << 4;
-      }
-      const uint32_t src = raw + rs * kQ4Slot;
+    const int s = 2 * n + hh, rs = s % kRawSlots, i = 3 * n;
+    const uint32_t src = raw + rs * kQ4Slot;
+    // both halves' codes: every warp sees every phase of every slot, in order, so that
+    // none can take an earlier phase for the one it waits for
+    for (int y = 2 * n; y < 2 * n + 2; ++y)
+      if (!wait_warp(&sh.raw_full[y % kRawSlots], (y / kRawSlots) & 1, sh)) return;
+    if (!wait_empty(i) || !wait_empty(i + 1)) return;
+    if (warp == 0 && lane == 0) sh.skip[hh][n % kSkipRing] = sh.raw_skip[rs];
+    {
       // a warp takes a 16-token tile, 8 tokens at a time; lane: 16 bytes of codes
       // (piece c) of one token, the eight lanes of a store phase on rows r and r + 4
+      const uint32_t kh = ring + i % kSlots * kOperand, kl = ring + (i + 1) % kSlots * kOperand;
       const int c = lane & 3;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 8 * i + ((lane >> 2) & 1) * 4 + (lane >> 3);
-        const uint4 x = lds128(src + At::key_codes(warp) + 64 * r + 16 * c);
-        const uint2 z = lds64(src + At::key_scales(warp) + 8 * r);
-        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-        const int row = 64 * hh + 16 * warp + r;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t zz = __byte_perm(j < 2 ? z.x : z.y, 0, j & 1 ? 0x3232 : 0x1010);
-          uint32_t f[4];
-          q4_codes(words[j], f);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            hi[e] = mul_f16x2(f[e], zz);
-            lo[e] = fma_f16x2(f[e], zz, hi[e] ^ 0x80008000u);  // s * code - hi, exact
-          }
-          const uint32_t at = kd + (j >> 1) * kHalf + swz(row, (j & 1) * 4 + c);
-          sts128(at, hi[0], hi[1], hi[2], hi[3]);
-          sts128(at + kOperand, lo[0], lo[1], lo[2], lo[3]);
-        }
+      for (int k = 0; k < 2; ++k) {
+        const int r = 8 * k + ((lane >> 2) & 1) * 4 + (lane >> 3), row = 64 * hh + 16 * warp + r;
+        convert_keys(lds128(src + At::key_codes(warp) + 64 * r + 16 * c), lds64(src + At::key_scales(warp) + 8 * r),
+                     [&](int j, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+                       const uint32_t at = (j >> 1) * kHalf + swz(row, (j & 1) * 4 + c);
+                       sts128(kh + at, hi[0], hi[1], hi[2], hi[3]);
+                       sts128(kl + at, lo[0], lo[1], lo[2], lo[3]);
+                     });
       }
     }
     fence_proxy_async();
-    mbar_arrive(&sh.k_full[0]);
-    if (n >= kKvStages && !wait_warp(&sh.v_empty[st], (n / kKvStages - 1) & 1, sh)) return;
-#pragma unroll 1
-    for (int hh = 0; hh < 2; ++hh) {
-      const int s = 2 * n + hh, rs = s % kRawSlots;
-      const uint32_t src = raw + rs * kQ4Slot;
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sh.full[i % kSlots]);
+      mbar_arrive(&sh.full[(i + 1) % kSlots]);
+    }
+    if (!wait_empty(i + 2)) return;
+    {
       // lane (g, c): dimensions 32 j + 4 g .. + 3 of tokens 2c, 2c + 1 (+ 8)
+      const uint32_t vd = ring + (i + 2) % kSlots * kOperand;
       const int g = lane >> 2, c = lane & 3;
 #pragma unroll
       for (int hi = 0; hi < 2; ++hi) {
-        const uint4 x = lds128(src + At::value_codes(warp) + 512 * hi + 16 * lane);
-        const uint4 z = lds128(src + At::value_scales(warp) + 32 * c + 16 * hi);
-        const uint32_t words[4] = {x.x, x.y, x.z, x.w}, zw[4] = {z.x, z.y, z.z, z.w};
         const int row = 64 * hh + 16 * warp + 8 * hi + 2 * c;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t f[4];
-          q4_codes(words[j], f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = mul_f16x2(f[i], zw[j]);
-          const uint32_t base = vd + (j >> 1) * kHalf + (g & 1) * 8;
-          const int cc = (j & 1) * 4 + (g >> 1);
-          sts64(base + swz(row, cc), __byte_perm(f[0], f[1], 0x5410), __byte_perm(f[2], f[3], 0x5410));
-          sts64(base + swz(row + 1, cc), __byte_perm(f[0], f[1], 0x7632), __byte_perm(f[2], f[3], 0x7632));
-        }
+        convert_values(lds128(src + At::value_codes(warp) + 512 * hi + 16 * lane),
+                       lds128(src + At::value_scales(warp) + 32 * c + 16 * hi), [&](int j, uint2 t0, uint2 t1) {
+                         const uint32_t base = vd + (j >> 1) * kHalf + (g & 1) * 8;
+                         const int cc = (j & 1) * 4 + (g >> 1);
+                         sts64(base + swz(row, cc), t0.x, t0.y);
+                         sts64(base + swz(row + 1, cc), t1.x, t1.y);
+                       });
       }
-      mbar_arrive(&sh.raw_empty[rs]);
     }
     fence_proxy_async();
-    mbar_arrive(&sh.v_full[st]);
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sh.raw_empty[rs]);
+      mbar_arrive(&sh.full[(i + 2) % kSlots]);
+    }
+  }
+}
+
+// The fp16 planes of every sequence and head: plane 0 the keys' nearest halves, 1 the
+// remainders, 2 the values, [3][batch][Hkv][plane_rows][128].  A CTA converts 64
+// tokens, a warp 16; pages outside the pool leave their rows as they are (the
+// attention leaves those tokens out).
+template <int P>
+__global__ void __launch_bounds__(128) planes_kernel(const PromptArgs a) {
+  using At = Q4Tile<P>;
+  pdl_wait();
+  const int hkv = blockIdx.y % a.num_kv_heads, b = blockIdx.y / a.num_kv_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = min(max(a.seq_lens[b], 0), a.max_pages * P), t0 = blockIdx.x * 64 + 16 * warp;
+  pdl_launch_dependents();
+  if (t0 >= len) return;
+  const int phys = a.block_table[(size_t)b * a.max_pages + t0 / P];
+  if (phys < 0 || phys >= a.pages_total) return;  // reported by the attention
+  const uint8_t* block = static_cast<const uint8_t*>(a.k_pool) +
+                         ((size_t)phys * a.num_kv_heads + hkv) * (size_t)LOCKS_KV_Q4_BLOCK_BYTES(P);
+  const int tile = P == 64 ? warp : 0;
+  const size_t plane = (size_t)a.batch * a.num_kv_heads * a.plane_rows * kHeadDim;
+  uint16_t* dst = a.planes + ((size_t)blockIdx.y * a.plane_rows + t0) * kHeadDim;
+  {
+    const int c = lane & 3;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = 8 * k + (lane >> 2);
+      convert_keys(__ldg(reinterpret_cast<const uint4*>(block + At::key_codes(tile) + 64 * r + 16 * c)),
+                   __ldg(reinterpret_cast<const uint2*>(block + At::key_scales(tile) + 8 * r)),
+                   [&](int j, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+                     uint16_t* at = dst + r * kHeadDim + 32 * j + 8 * c;
+                     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                     *reinterpret_cast<uint4*>(at + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                   });
+    }
+  }
+  const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int hi = 0; hi < 2; ++hi) {
+    uint16_t* row = dst + 2 * plane + (8 * hi + 2 * c) * kHeadDim + 4 * g;
+    convert_values(__ldg(reinterpret_cast<const uint4*>(block + At::value_codes(tile) + 512 * hi + 16 * lane)),
+                   __ldg(reinterpret_cast<const uint4*>(block + At::value_scales(tile) + 32 * c + 16 * hi)),
+                   [&](int j, uint2 x0, uint2 x1) {
+                     *reinterpret_cast<uint2*>(row + 32 * j) = x0;
+                     *reinterpret_cast<uint2*>(row + kHeadDim + 32 * j) = x1;
+                   });
   }
 }
 
 // ---- warp 0, one thread: the matrix instructions ------------------------------------
-template <bool Q4>
-__device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uint32_t kv, uint32_t tmem) {
-  constexpr uint32_t kIdS = umma_idesc(kRows, kBlock, !Q4, false), kIdO = umma_idesc(kRows, kHeadDim, !Q4, true);
-  constexpr int kKS = kKeyStages<Q4>;
-  const int n_blocks = w.j1 - w.j0;
-  auto scores = [&](int t, int n) {  // S_t = Q_t K^T (4-bit pages: both halves of K)
-    const uint32_t k = kv + (n % kKS) * kOperand, qt = q + t * kOperand;
+template <Source S>
+__device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uint32_t ring, uint32_t tmem) {
+  constexpr bool kBf16 = S == kBf16Pages;
+  constexpr uint32_t kIdS = umma_idesc(kRows, kBlock, kBf16, false), kIdO = umma_idesc(kRows, kHeadDim, kBf16, true);
+  constexpr int kU = kUnits<S>, kKeys = kU - 1;
+  const int n_blocks = w.j1 - w.j0, last = w.n_tiles - 1;
+  // the ring's operands arrive in order, one block's keys before its values
+  auto full = [&](int i) { return wait_bar(&sh.full[i % kSlots], (i / kSlots) & 1, sh); };
+  auto is_full = [&](int i) { return mbar_test(&sh.full[i % kSlots], (i / kSlots) & 1); };
+  auto scores = [&](int t, int n) {  // S = Q_t K^T (fp16: both halves of K)
+    const uint32_t d = tmem + (kTiles<S> == 1 ? n & 1 : t) * kBlock, qt = q + t * kOperand;
 #pragma unroll
-    for (int part = 0; part < (Q4 ? 2 : 1); ++part)
+    for (int part = 0; part < kKeys; ++part) {
+      const uint32_t k = ring + (kU * n + part) % kSlots * kOperand;
 #pragma unroll
       for (int s = 0; s < kHeadDim / 16; ++s) {
         const uint32_t off = (s / 4) * kHalf + (s % 4) * 32;
-        umma_ss(tmem + t * kBlock, umma_desc(qt + off, 16, 1024), umma_desc(k + part * kOperand + off, 16, 1024), kIdS,
-                part + s > 0);
+        umma_ss(d, umma_desc(qt + off, 16, 1024), umma_desc(k + off, 16, 1024), kIdS, part + s > 0);
       }
-    umma_commit(&sh.s_full[t]);
-    if (t == w.n_tiles - 1) umma_commit(&sh.k_empty[n % kKS]);
+    }
+    umma_commit(&sh.s_full[kTiles<S> == 1 ? n & 1 : t]);
+    if (t == last)
+#pragma unroll
+      for (int part = 0; part < kKeys; ++part) umma_commit(&sh.empty[(kU * n + part) % kSlots]);
   };
-  auto values = [&](int t, int n) {  // O_t (+)= P_t V
-    const uint32_t v = kv + kValues + (n % kKvStages) * kOperand;
+  auto values = [&](int t, int n) {  // O_t (+)= P V
+    const int i = kU * n + kKeys;
+    const uint32_t v = ring + i % kSlots * kOperand, p = tmem + (kTiles<S> == 1 ? n & 1 : t) * kBlock;
 #pragma unroll
     for (int s = 0; s < kBlock / 16; ++s)
-      umma_ts(tmem + kTmemO + t * kHeadDim, tmem + t * kBlock + s * 8, umma_desc(v + s * 16 * 128, kHalf, 1024), kIdO,
-              n > 0 || s > 0);
-    if (t == w.n_tiles - 1) umma_commit(&sh.v_empty[n % kKvStages]);
+      umma_ts(tmem + kTmemO + t * kHeadDim, p + s * 8, umma_desc(v + s * 16 * 128, kHalf, 1024), kIdO, n > 0 || s > 0);
+    if (t == last) umma_commit(&sh.empty[i % kSlots]);
+    if (kTiles<S> == 1) umma_commit(&sh.pv_done);
     if (n == n_blocks - 1) umma_commit(&sh.o_full[t]);
   };
-  bool ok = wait_bar(&sh.q_full, 0, sh) && wait_bar(&sh.k_full[0], 0, sh);
+  bool ok = wait_bar(&sh.q_full, 0, sh);
+  for (int part = 0; part < kKeys; ++part) ok = ok && full(part);
   if (ok) {
     tc_fence_after();
     for (int t = 0; t < w.n_tiles; ++t) scores(t, 0);
   }
   for (int n = 0; ok && n < n_blocks; ++n) {
-    if (!(ok = wait_bar(&sh.v_full[n % kKvStages], (n / kKvStages) & 1, sh) && wait_bar(&sh.p_ready[0], n & 1, sh))) break;
-    tc_fence_after();
-    values(0, n);
-    // the next scores of tile 0 and the values of tile 1, whichever can go first
+    // Two tiles: O_0, then S_0 of the next block and O_1 in the order in which they
+    // become possible, then S_1.  One tile: O and S of the next block, likewise.
+    bool first = true;                     // O_0 is to be issued
     bool next = n + 1 < n_blocks, second = w.n_tiles == 2;
     const bool more = next;
     uint32_t it = 0;
-    while (next || second) {
-      if (next && mbar_test(&sh.k_full[(n + 1) % kKS], ((n + 1) / kKS) & 1)) {
+    while (first || next || second) {
+      if (first && mbar_test(&sh.p_ready[kTiles<S> == 1 ? n & 1 : 0], kTiles<S> == 1 ? (n >> 1) & 1 : n & 1) &&
+          is_full(kU * n + kKeys)) {
+        tc_fence_after();
+        values(0, n);
+        first = false;
+      }
+      if (next && (kTiles<S> == 1 || !first) && is_full(kU * (n + 1)) && is_full(kU * (n + 1) + kKeys - 1)) {
         tc_fence_after();
         scores(0, n + 1);
         next = false;
       }
-      if (second && mbar_test(&sh.p_ready[1], n & 1)) {
+      if (second && !first && mbar_test(&sh.p_ready[1], n & 1)) {
         tc_fence_after();
         values(1, n);
         second = false;
@@ -391,13 +491,15 @@ __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uin
   }
 }
 
-// ---- warps 4-11: one softmax row per thread -------------------------------------------
-template <bool Q4, int P>
+// ---- warps 4 and up: one softmax row per thread -------------------------------------------
+template <Source S, int P>
 __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptShared& sh, uint8_t* smem, uint32_t tmem_base) {
+  constexpr bool Q4 = S != kBf16Pages;
+  constexpr bool kOne = kTiles<S> == 1;      // one tile, two S buffers
   constexpr float kOffset = Q4 ? 6.f : 0.f;  // weights are scaled by 2^kOffset
   const int warp = threadIdx.x >> 5, t = (warp - 4) / 4;
   if (t >= w.n_tiles) return;
-  const int row = threadIdx.x & 127;
+  const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
   const int G = a.group, tpt = kRows / G, Hq = a.num_kv_heads * G;
   const int ti = row / G, h = row - ti * G;
   const int i = t * tpt + ti;  // token of this CTA
@@ -441,22 +543,26 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
       sts128(dst + (k >> 3) * kHalf + swz(row, k & 7), v[0], v[1], v[2], v[3]);
     }
     fence_proxy_async();
-    mbar_arrive(&sh.q_full);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_full);
   }
 
-  float m = -INFINITY, l = 0.f;  // reference (base 2), sum of the weights
+  float m = -INFINITY, l0 = 0.f, l1 = 0.f;  // reference (base 2), sum of the weights (two halves)
   const int first_limit = max(0, w.start + w.tok0 + 1);  // keys that every row of the CTA sees
   const int n_blocks = w.j1 - w.j0;
   for (int n = 0; n < n_blocks; ++n) {
     const int kv0 = (w.j0 + n) * kBlock;
-    if (!wait_warp(&sh.s_full[t], n & 1, sh)) return;
+    const int buf = kOne ? n & 1 : t;
+    const uint32_t phase = kOne ? (n >> 1) & 1 : n & 1;
+    if (!wait_warp(&sh.s_full[buf], phase, sh)) return;
     tc_fence_after();
-    const int skip = *reinterpret_cast<volatile int*>(&sh.skip[n % kSkipRing]);
+    const int skip = *reinterpret_cast<volatile int*>(&sh.skip[0][n % kSkipRing]) |
+                     *reinterpret_cast<volatile int*>(&sh.skip[1][n % kSkipRing]) << 4;
     // values that some row must not see (tile 0's threads, one token each)
     if (t == 0 && (kv0 + kBlock > first_limit || kv0 + kBlock > w.len || skip)) {
-      const int st = n % kKvStages;
-      if (!wait_warp(&sh.v_full[st], (n / kKvStages) & 1, sh)) return;
-      uint8_t* v = smem + 2 * kOperand + kValues + st * kOperand + row * 128;
+      const int i = kUnits<S> * n + kUnits<S> - 1, slot = i % kSlots;
+      if (!wait_warp(&sh.full[slot], (i / kSlots) & 1, sh)) return;
+      uint8_t* v = smem + kTiles<S> * kOperand + slot * kOperand + row * 128;
       const int at = kv0 + row;
       bool zero = at >= w.kv_end || at >= w.len || ((skip >> (row / 16)) & 1);
       if (!zero && at >= first_limit) {
@@ -489,26 +595,49 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
       for (int k = 0; k < 32; ++k)
         if (c0 + k >= lim || ((skip >> ((c0 + k) / 16)) & 1)) s[k] = 0xff800000u;  // -infinity
     };
-    const uint32_t ts = tmem + t * kBlock, to = tmem + kTmemO + t * kHeadDim;
-    // the block's maximum
-    float mx = -INFINITY;
+    // two S buffers: the products of the block before are done (every block waits for
+    // that once, so that no phase is missed)
+    bool settled = !kOne || n == 0;
+    auto o_settled = [&] {
+      if (!settled && !wait_warp(&sh.pv_done, (n - 1) & 1, sh)) return false;
+      settled = true;
+      tc_fence_after();
+      return true;
+    };
+    const uint32_t ts = tmem + buf * kBlock, to = tmem + kTmemO + t * kHeadDim;
+    // the row's logits, all of them in registers, and their maximum
+    uint32_t s[4][32];
 #pragma unroll
-    for (int c0 = 0; c0 < kBlock; c0 += 32) {
-      uint32_t s[32];
-      tmem_ld32(s, ts + c0);
-      tmem_wait_ld32(s);
-      if (masked) hide(s, c0);
+    for (int k = 0; k < 4; ++k) tmem_ld32(s[k], ts + 32 * k);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
+    for (int k = 0; k < 4; ++k) tmem_wait_ld32(s[k]);
+    if (masked) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) hide(s[k], 32 * k);
     }
-    mx *= factor;  // positive
+    float mx;
+    {
+      float m4[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m4[k] = __uint_as_float(s[k][0]);
+#pragma unroll
+        for (int e = 1; e < 31; e += 2) m4[k] = max3(m4[k], __uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1]));
+        m4[k] = fmaxf(m4[k], __uint_as_float(s[k][31]));
+      }
+      mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * factor;  // the factor is positive
+    }
     if (__any_sync(0xffffffffu, mx > m + kLazy || (m == -INFINITY && mx > m))) {
       const float mn = fmaxf(m, mx);
       const float al = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
       m = mn;
-      l *= al;
-      if (n > 0) {  // O holds every block before this one
-#pragma unroll
+      l0 *= al;
+      l1 *= al;
+      if (n > 0) {
+        // O holds every block before this one: S of this block came behind them, or,
+        // with two S buffers, once they are done
+        if (kOne && !o_settled()) return;
+#pragma unroll 1
         for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
           uint32_t o[32];
           tmem_ld32(o, to + c0);
@@ -520,25 +649,30 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
       }
     }
     const float ref = m == -INFINITY ? 0.f : m - kOffset;
+    const uint64_t f2 = f32x2(factor, factor), r2 = f32x2(-ref, -ref);
+    uint64_t sum = f32x2(l0, l1);
 #pragma unroll
-    for (int c0 = 0; c0 < kBlock; c0 += 32) {
-      uint32_t s[32], p[16];
-      tmem_ld32(s, ts + c0);
-      tmem_wait_ld32(s);
-      if (masked) hide(s, c0);
+    for (int k = 0; k < 4; ++k) {
+      uint32_t p[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float x = fast_exp2(fmaf(__uint_as_float(s[2 * k]), factor, -ref));
-        const float y = fast_exp2(fmaf(__uint_as_float(s[2 * k + 1]), factor, -ref));
-        l += x + y;
-        p[k] = Q4 ? pack_f16(x, y) : pack_bf16(x, y);
+      for (int e = 0; e < 16; ++e) {
+        float x, y;
+        unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(s[k][2 * e]), __uint_as_float(s[k][2 * e + 1])), f2, r2), x, y);
+        x = fast_exp2(x);
+        y = fast_exp2(y);
+        sum = add_f32x2(sum, f32x2(x, y));
+        p[e] = Q4 ? pack_f16(x, y) : pack_bf16(x, y);
       }
-      tmem_st16(ts + c0 / 2, p);  // behind the columns of S that are still to be read
+      tmem_st16(ts + 16 * k, p);
     }
+    unpack_f32x2(sum, l0, l1);
+    if (kOne && !o_settled()) return;
     tmem_wait_st();
     tc_fence_before();
-    mbar_arrive(&sh.p_ready[t]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.p_ready[buf]);
   }
+  const float l = l0 + l1;
 
   // ---- the rows' results ----
   if (n_blocks > 0) {
@@ -591,14 +725,14 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
   }
 }
 
-template <bool Q4, int P>
-__global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
+template <Source S, int P>
+__global__ void __launch_bounds__(kThreadsOf<S>, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PromptArgs a) {
   extern __shared__ uint8_t dyn_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PromptShared sh;
-  uint8_t* kv = smem + 2 * kOperand;
-  uint8_t* raw = kv + kKvBytes;
+  uint8_t* ring = smem + kTiles<S> * kOperand;
+  uint8_t* raw = ring + kSlots * kOperand;
   const int tid = threadIdx.x, warp = tid >> 5;
 
   pdl_wait();
@@ -626,7 +760,7 @@ __global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
       n = 0;
     }
     if (says && (n > len || n > a.max_tokens)) set_error(a.err, LOCKS_DEVERR_LENGTHS);
-    const int mine = min(n, a.max_tokens), per_cta = 2 * (kRows / a.group);
+    const int mine = min(n, a.max_tokens), per_cta = kTiles<S> * (kRows / a.group);
     w.row0 = c0;
     w.len = len;
     w.start = len - n;
@@ -640,22 +774,21 @@ __global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
     w.j1 = (int)(nb * (w.split + 1) / a.n_splits);
   }
   if (tid == 0) {
-    mbar_init(&sh.q_full, kRows * w.n_tiles);
-    for (int s = 0; s < kKvStages; ++s) {
-      mbar_init(&sh.k_full[s], Q4 ? 128 : 1);
-      mbar_init(&sh.v_full[s], Q4 ? 128 : 1);
-      mbar_init(&sh.k_empty[s], 1);
-      mbar_init(&sh.v_empty[s], 1);
+    mbar_init(&sh.q_full, kRows / 32 * w.n_tiles);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&sh.full[s], S == kCodes ? 8 : 1);
+      mbar_init(&sh.empty[s], 1);
     }
+    mbar_init(&sh.pv_done, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_ready[t], kRows);
+      mbar_init(&sh.p_ready[t], kRows / 32);
       mbar_init(&sh.o_full[t], 1);
     }
     mbar_init(&sh.drain, 1);
     for (int s = 0; s < kRawSlots; ++s) {
       mbar_init(&sh.raw_full[s], 1);
-      mbar_init(&sh.raw_empty[s], 128);
+      mbar_init(&sh.raw_empty[s], 4);
     }
     fence_mbar_init();
     sh.abort = 0;
@@ -667,15 +800,21 @@ __global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (warp == 0) {
-    if ((tid & 31) == 0 && w.j1 > w.j0) mma_role<Q4>(w, sh, smem_u32(smem), smem_u32(kv), tmem);
-    __syncwarp();
-  } else if (warp == 1) {
-    load_role<Q4, P>(a, w, &tk, &tv, sh, kv, raw);
-  } else if (warp >= 12) {
-    if constexpr (Q4) convert_role<P>(w, sh, smem_u32(kv), smem_u32(raw));
-  } else if (warp >= 4) {
-    softmax_role<Q4, P>(a, w, sh, smem, tmem);
+  // registers per warpgroup: the launch's 504 (512) between them
+  if (warp < 4) {
+    set_registers_down<S == kCodes ? 72 : 88>();
+    if (warp == 0) {
+      if ((tid & 31) == 0 && w.j1 > w.j0) mma_role<S>(w, sh, smem_u32(smem), smem_u32(ring), tmem);
+      __syncwarp();
+    } else if (warp == 1) {
+      load_role<S, P>(a, w, &tk, &tv, sh, ring, raw);
+    }
+  } else if (warp < 4 + 4 * kTiles<S>) {
+    set_registers_up<208>();
+    softmax_role<S, P>(a, w, sh, smem, tmem);
+  } else {
+    set_registers_down<112>();
+    if constexpr (S == kCodes) convert_role<P>(w, sh, smem_u32(ring), smem_u32(raw));
   }
   __syncwarp();
   __threadfence();  // partial results, before the ticket
@@ -723,34 +862,40 @@ __global__ void __launch_bounds__(Q4 ? 512 : 384, 1)
   if (tid == 0) a.counters[prob] = 0;  // ready for the next call
 }
 
-size_t smem_bytes(bool q4) {
-  return 1024 + 2 * kOperand + (size_t)kKvBytes + (q4 ? kRawSlots * kQ4Slot : 0);
-}
-
-template <bool Q4, int P>
+template <Source S, int P>
 cudaError_t launch(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  auto kern = prompt_kernel<Q4, P>;
-  const size_t smem = smem_bytes(Q4);
+  auto kern = prompt_kernel<S, P>;
+  const size_t smem = 1024 + (size_t)(kTiles<S> + kSlots) * kOperand + (S == kCodes ? kRawSlots * kQ4Slot : 0);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.batch * a.num_kv_heads * a.n_splits, a.n_qtiles, 1);
-  cfg.blockDim = dim3(Q4 ? 512 : 384, 1, 1);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if constexpr (S == kPlanes) {
+    cfg.gridDim = dim3((a.max_pages * P + 63) / 64, a.batch * a.num_kv_heads, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    if ((e = cudaLaunchKernelEx(&cfg, planes_kernel<P>, a)) != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3(a.batch * a.num_kv_heads * a.n_splits, a.n_qtiles, 1);
+  cfg.blockDim = dim3(kThreadsOf<S>, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+}
+
+template <int P>
+cudaError_t launch_page(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  if (!a.q4) return launch<kBf16Pages, P>(a, tk, tv, s);
+  return a.planes ? launch<kPlanes, P>(a, tk, tv, s) : launch<kCodes, P>(a, tk, tv, s);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  if (a.q4) return a.page_size == 16 ? launch<true, 16>(a, tk, tv, s) : launch<true, 64>(a, tk, tv, s);
-  return a.page_size == 16 ? launch<false, 16>(a, tk, tv, s) : launch<false, 64>(a, tk, tv, s);
+  return a.page_size == 16 ? launch_page<16>(a, tk, tv, s) : launch_page<kPage>(a, tk, tv, s);
 }
 
 }  // namespace locks
