@@ -12,8 +12,8 @@
 // Layout.  Tensor memory (512 columns): two S buffers of 128 columns, whose first 64
 // columns P overwrites (16-bit pairs, the A operand of the second product), and one or
 // two O of 128 columns.  Keys and values come as 32 KiB operands (128 tokens in the
-// instructions' 128-byte swizzle) through a ring of five, so that copies run one to
-// two blocks ahead.  Warps: 0 issues the matrix instructions, 1 the copies, 4 and up
+// instructions' 128-byte swizzle) through a ring of five or six, so that copies run one
+// to two blocks ahead.  Warps: 0 issues the matrix instructions, 1 the copies, 4 and up
 // are the softmax of a tile, one thread per row, so neither maximum nor sum needs a
 // shuffle.  Matrix instructions of one CTA execute in the order of issue, so S of the
 // next block may be issued right behind the product that reads P from the same
@@ -28,7 +28,7 @@
 //    TMA copies fetch those; else as above.
 //  - 4-bit pages, few rows: eight warps turn the pages' codes into operands in shared
 //    memory.  A CTA takes one tile and both S buffers, so that S of the next block is
-//    made while the softmax of this one runs.
+//    made while the softmax of this one runs; its queries are in tensor memory.
 // fp16 operands: q is scaled by a power of two.  A key s * code has up to 14
 // significant bits: it is held as the nearest half and the remainder, both exact, and
 // S is the sum of the products with both (one half alone would put 2^-11 of
@@ -56,26 +56,34 @@ constexpr int kRows = 128;                   // rows of a tile
 constexpr int kBlock = 128;                  // keys of a block
 constexpr int kHalf = kBlock * 128;          // bytes of 64 columns of 128 16-bit rows
 constexpr int kOperand = 2 * kHalf;          // one tile of Q, K or V: 32 KiB
-constexpr int kSlots = 5;                    // operands in the ring of keys and values
 constexpr int kRawSlots = 3;                 // 4-bit pages: 64-token slots of codes
 constexpr int kSkipRing = 8;                 // the copies run at most five operands ahead of the products
 constexpr int kMaxBad = 2 * kRows;           // tokens near a diagonal: no more than a CTA has
 constexpr float kLazy = 8.f;                 // growth of a maximum (base 2) that O's reference tolerates
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;             // S: columns 0 and 128; O: 256 and 384
+constexpr uint32_t kTmemQ = 384;             // kCodes: the queries, in place of a second O
 
 // Where the operands come from.
 enum Source { kBf16Pages, kPlanes, kCodes };
 template <Source S>
 constexpr int kTiles = S == kCodes ? 1 : 2;   // tiles of a CTA
 template <Source S>
+constexpr int kQueryTiles = S == kCodes ? 0 : 2;  // of those, in shared memory (else in tensor memory)
+template <Source S>
 constexpr int kUnits = S == kBf16Pages ? 2 : 3;  // operands of a block: keys (two halves), values
+// Operands in the ring of keys and values: with 4-bit codes two whole blocks.
+template <Source S>
+constexpr int kSlots = S == kCodes ? 6 : 5;
+constexpr int kMaxSlots = 6;
 template <Source S>
 constexpr int kThreadsOf = S == kCodes ? 512 : 384;
 
 struct PromptShared {
-  uint64_t q_full, full[kSlots], empty[kSlots];
-  uint64_t s_full[2], p_ready[2], o_full[2], pv_done, drain;
+  uint64_t q_full, full[kMaxSlots];
+  // done[n % 2]: the products with the values of block n and the keys of block n + 1
+  // are complete (two barriers, so that no waiter can be a whole turn behind)
+  uint64_t s_full[2], p_ready[2], o_full[2], done[2], drain;
   uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
   uint32_t tmem;
   int skip[2][kSkipRing];   // per half of a block: 16-token groups whose page is outside the pool (bits)
@@ -103,9 +111,22 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, PromptS
   return false;
 }
 
-// The same by a whole warp, which goes on or gives up as one.
+// The same for a phase that is due soon: by testing, without being put to sleep.
+__device__ __forceinline__ bool spin_bar(uint64_t* bar, uint32_t parity, PromptShared& sh) {
+  for (uint32_t it = 0; it < kMbarSpinLimit; ++it) {
+    if (mbar_test(bar, parity)) return true;
+    if ((it & 63) == 63 && *reinterpret_cast<volatile int*>(&sh.abort)) return false;
+  }
+  *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+  return false;
+}
+// wait_bar by a whole warp, which goes on or gives up as one.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, PromptShared& sh) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, sh));
+}
+
+__device__ __forceinline__ bool block_done(int n, PromptShared& sh) {
+  return wait_warp(&sh.done[n & 1], (n >> 1) & 1, sh);
 }
 
 // Byte offset of 16-byte chunk `cc` (0..7) of row `row` in a 64-column half-tile
@@ -170,6 +191,7 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
   const int lane = threadIdx.x & 31;
   const int n_pages = (w.len + P - 1) / P;
   int asked = 0;  // operands (slots of codes) asked for
+  int seen = 0;   // blocks known to be done
   bool ok = true;
   for (int jb = w.j0; jb < w.j1 && ok; jb += kAtOnce) {
     // the pages of several blocks at a time, one per lane
@@ -194,10 +216,14 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
         const int copies = kPPB - __popc(skip) / (P / 16);
 #pragma unroll
         for (int u = 0; u < kUnits<S>; ++u, ++asked) {  // keys, then values
-          const int slot = asked % kSlots;
-          if (asked >= kSlots && !wait_warp(&sh.empty[slot], (asked / kSlots - 1) & 1, sh)) {
-            ok = false;
-            break;
+          const int slot = asked % kSlots<S>;
+          // the operand that was in the slot: values of block m are free after block m,
+          // keys after block m - 1 (the first block's after block 0, like the second's)
+          if (asked >= kSlots<S>) {
+            const int old = asked - kSlots<S>, m = old / kUnits<S>;
+            const int need = old % kUnits<S> == kUnits<S> - 1 ? m : max(0, m - 1);
+            for (; ok && seen <= need; ++seen) ok = block_done(seen, sh);
+            if (!ok) break;
           }
           if (lane == 0) {
             uint64_t* full = &sh.full[slot];
@@ -256,7 +282,7 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
   }
   if (!ok && lane == 0) {
     // let the copies in flight land before the memory is given back
-    constexpr int kRing = S == kCodes ? kRawSlots : kSlots;
+    constexpr int kRing = S == kCodes ? kRawSlots : kSlots<S>;
     for (int i = max(0, asked - kRing); i < asked; ++i)
       (void)mbar_wait(S == kCodes ? &sh.raw_full[i % kRing] : &sh.full[i % kRing], (i / kRing) & 1);
   }
@@ -303,8 +329,11 @@ template <int P>
 __device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t ring, uint32_t raw) {
   using At = Q4Tile<P>;
   const int hh = (threadIdx.x >> 7) & 1, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  auto wait_empty = [&](int i) {
-    return i < kSlots || wait_warp(&sh.empty[i % kSlots], (i / kSlots - 1) & 1, sh);
+  int seen = 0;  // blocks known to be done: each is waited for once, in order
+  auto done_until = [&](int m) {
+    for (; seen <= m; ++seen)
+      if (!block_done(seen, sh)) return false;
+    return true;
   };
   for (int n = 0; n < w.j1 - w.j0; ++n) {
     const int s = 2 * n + hh, rs = s % kRawSlots, i = 3 * n;
@@ -313,12 +342,14 @@ __device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t ri
     // none can take an earlier phase for the one it waits for
     for (int y = 2 * n; y < 2 * n + 2; ++y)
       if (!wait_warp(&sh.raw_full[y % kRawSlots], (y / kRawSlots) & 1, sh)) return;
-    if (!wait_empty(i) || !wait_empty(i + 1)) return;
+    // the ring holds two blocks: that of n - 2 makes room, its keys when block n - 3 is
+    // done (the first block's with the second's), its values when it is
+    if (n >= 2 && !done_until(max(0, n - 3))) return;
     if (warp == 0 && lane == 0) sh.skip[hh][n % kSkipRing] = sh.raw_skip[rs];
     {
       // a warp takes a 16-token tile, 8 tokens at a time; lane: 16 bytes of codes
       // (piece c) of one token, the eight lanes of a store phase on rows r and r + 4
-      const uint32_t kh = ring + i % kSlots * kOperand, kl = ring + (i + 1) % kSlots * kOperand;
+      const uint32_t kh = ring + i % kSlots<kCodes> * kOperand, kl = ring + (i + 1) % kSlots<kCodes> * kOperand;
       const int c = lane & 3;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -334,13 +365,13 @@ __device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t ri
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&sh.full[i % kSlots]);
-      mbar_arrive(&sh.full[(i + 1) % kSlots]);
+      mbar_arrive(&sh.full[i % kSlots<kCodes>]);
+      mbar_arrive(&sh.full[(i + 1) % kSlots<kCodes>]);
     }
-    if (!wait_empty(i + 2)) return;
+    if (n >= 2 && !done_until(n - 2)) return;
     {
       // lane (g, c): dimensions 32 j + 4 g .. + 3 of tokens 2c, 2c + 1 (+ 8)
-      const uint32_t vd = ring + (i + 2) % kSlots * kOperand;
+      const uint32_t vd = ring + (i + 2) % kSlots<kCodes> * kOperand;
       const int g = lane >> 2, c = lane & 3;
 #pragma unroll
       for (int hi = 0; hi < 2; ++hi) {
@@ -358,7 +389,7 @@ __device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t ri
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&sh.raw_empty[rs]);
-      mbar_arrive(&sh.full[(i + 2) % kSlots]);
+      mbar_arrive(&sh.full[(i + 2) % kSlots<kCodes>]);
     }
   }
 }
@@ -411,83 +442,104 @@ __global__ void __launch_bounds__(128) planes_kernel(const PromptArgs a) {
 }
 
 // ---- warp 0, one thread: the matrix instructions ------------------------------------
+// The thread's own steps (a test, a commit) cost some hundred clocks beside the busy
+// softmax warps, and the tensor core stands still meanwhile; so there are few of them:
+// with two tiles one test and one or two commits per tile and block.
 template <Source S>
 __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uint32_t ring, uint32_t tmem) {
-  constexpr bool kBf16 = S == kBf16Pages;
+  constexpr bool kBf16 = S == kBf16Pages, kOne = kTiles<S> == 1;
   constexpr uint32_t kIdS = umma_idesc(kRows, kBlock, kBf16, false), kIdO = umma_idesc(kRows, kHeadDim, kBf16, true);
-  constexpr int kU = kUnits<S>, kKeys = kU - 1;
-  const int n_blocks = w.j1 - w.j0, last = w.n_tiles - 1;
-  // the ring's operands arrive in order, one block's keys before its values
-  auto full = [&](int i) { return wait_bar(&sh.full[i % kSlots], (i / kSlots) & 1, sh); };
-  auto is_full = [&](int i) { return mbar_test(&sh.full[i % kSlots], (i / kSlots) & 1); };
-  auto scores = [&](int t, int n) {  // S = Q_t K^T (fp16: both halves of K)
-    const uint32_t d = tmem + (kTiles<S> == 1 ? n & 1 : t) * kBlock, qt = q + t * kOperand;
+  constexpr int kKeys = kUnits<S> - 1, kN = kSlots<S>;
+  const int n_blocks = w.j1 - w.j0;
+  // the next operand of the ring; they come in order, a block's keys before its values
+  int slot = 0, phase = 0;
+  auto next = [&](int& got, bool wait) {
+    got = slot;
+    const bool there = !wait || spin_bar(&sh.full[slot], phase, sh);
+    if (++slot == kN) slot = 0, phase ^= 1;
+    return there;
+  };
+  const uint32_t q_lo = umma_desc_lo(q, 16), k_lo = umma_desc_lo(ring, 16), v_lo = umma_desc_lo(ring, kHalf);
+  int key[kKeys], value = 0;
+  auto next_keys = [&](bool wait) {
+    bool there = true;
+#pragma unroll
+    for (int part = 0; part < kKeys; ++part) there = next(key[part], wait && there) && there;
+    return there;
+  };
+  auto scores = [&](int t, int buf) {  // S = Q_t K^T (fp16: both halves of K)
+    const uint32_t d = tmem + buf * kBlock, qd = q_lo + t * (kOperand / 16);
 #pragma unroll
     for (int part = 0; part < kKeys; ++part) {
-      const uint32_t k = ring + (kU * n + part) % kSlots * kOperand;
+      const uint32_t kd = k_lo + key[part] * (kOperand / 16);
 #pragma unroll
       for (int s = 0; s < kHeadDim / 16; ++s) {
-        const uint32_t off = (s / 4) * kHalf + (s % 4) * 32;
-        umma_ss(d, umma_desc(qt + off, 16, 1024), umma_desc(k + off, 16, 1024), kIdS, part + s > 0);
+        const uint32_t off = ((s / 4) * kHalf + (s % 4) * 32) / 16;
+        if (kOne) umma_ts(d, tmem + kTmemQ + s * 8, kd + off, kIdS, part + s > 0);
+        else umma_ss(d, qd + off, kd + off, kIdS, part + s > 0);
       }
     }
-    umma_commit(&sh.s_full[kTiles<S> == 1 ? n & 1 : t]);
-    if (t == last)
-#pragma unroll
-      for (int part = 0; part < kKeys; ++part) umma_commit(&sh.empty[(kU * n + part) % kSlots]);
+    umma_commit(&sh.s_full[buf]);
   };
-  auto values = [&](int t, int n) {  // O_t (+)= P V
-    const int i = kU * n + kKeys;
-    const uint32_t v = ring + i % kSlots * kOperand, p = tmem + (kTiles<S> == 1 ? n & 1 : t) * kBlock;
+  auto values = [&](int t, int buf, bool more) {  // O_t (+)= P V
+    const uint32_t p = tmem + buf * kBlock, vd = v_lo + value * (kOperand / 16), o = tmem + kTmemO + t * kHeadDim;
+    umma_ts(o, p, vd, kIdO, more);
 #pragma unroll
-    for (int s = 0; s < kBlock / 16; ++s)
-      umma_ts(tmem + kTmemO + t * kHeadDim, p + s * 8, umma_desc(v + s * 16 * 128, kHalf, 1024), kIdO, n > 0 || s > 0);
-    if (t == last) umma_commit(&sh.empty[i % kSlots]);
-    if (kTiles<S> == 1) umma_commit(&sh.pv_done);
-    if (n == n_blocks - 1) umma_commit(&sh.o_full[t]);
+    for (int s = 1; s < kBlock / 16; ++s) umma_ts(o, p + s * 8, vd + s * 16 * 128 / 16, kIdO, true);
   };
-  bool ok = wait_bar(&sh.q_full, 0, sh);
-  for (int part = 0; part < kKeys; ++part) ok = ok && full(part);
+  bool ok = wait_bar(&sh.q_full, 0, sh) && next_keys(true);
   if (ok) {
     tc_fence_after();
-    for (int t = 0; t < w.n_tiles; ++t) scores(t, 0);
+    for (int t = 0; t < w.n_tiles; ++t) scores(t, kOne ? 0 : t);
   }
   for (int n = 0; ok && n < n_blocks; ++n) {
-    // Two tiles: O_0, then S_0 of the next block and O_1 in the order in which they
-    // become possible, then S_1.  One tile: O and S of the next block, likewise.
-    bool first = true;                     // O_0 is to be issued
-    bool next = n + 1 < n_blocks, second = w.n_tiles == 2;
-    const bool more = next;
-    uint32_t it = 0;
-    while (first || next || second) {
-      if (first && mbar_test(&sh.p_ready[kTiles<S> == 1 ? n & 1 : 0], kTiles<S> == 1 ? (n >> 1) & 1 : n & 1) &&
-          is_full(kU * n + kKeys)) {
+    const bool last = n + 1 == n_blocks;
+    if constexpr (kOne) {
+      // S of the next block while the softmax of this one runs
+      if (!(ok = next(value, true))) break;
+      if (!last) {
+        if (!(ok = next_keys(true))) break;
         tc_fence_after();
-        values(0, n);
-        first = false;
+        scores(0, (n + 1) & 1);
       }
-      if (next && (kTiles<S> == 1 || !first) && is_full(kU * (n + 1)) && is_full(kU * (n + 1) + kKeys - 1)) {
+      if (!(ok = spin_bar(&sh.p_ready[n & 1], (n >> 1) & 1, sh))) break;
+      tc_fence_after();
+      values(0, n & 1, n > 0);
+    } else {
+      // each tile's O, then its S of the next block, while the other's softmax runs;
+      // tile 0's weights come with the news that the operands are there
+      (void)next(value, false);
+      if (!last) (void)next_keys(false);
+      for (int t = 0; t < w.n_tiles; ++t) {
+        if (!(ok = spin_bar(&sh.p_ready[t], n & 1, sh))) break;
         tc_fence_after();
-        scores(0, n + 1);
-        next = false;
-      }
-      if (second && !first && mbar_test(&sh.p_ready[1], n & 1)) {
-        tc_fence_after();
-        values(1, n);
-        second = false;
-      }
-      if (++it > kMbarSpinLimit || *reinterpret_cast<volatile int*>(&sh.abort)) {
-        *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-        ok = false;
-        break;
+        values(t, t, n > 0);
+        if (!last) scores(t, t);
+        else if (t + 1 < w.n_tiles) umma_commit(&sh.o_full[t]);
       }
     }
-    if (ok && more && w.n_tiles == 2) scores(1, n + 1);
+    if (ok) umma_commit(last ? &sh.o_full[w.n_tiles - 1] : &sh.done[n & 1]);
   }
   if (!ok) {
     // what was issued must end before its memory is given back
     umma_commit(&sh.drain);
     (void)mbar_wait(&sh.drain, 0);
+  }
+}
+
+// ---- warp 2 (two tiles): tells the issuing thread, with tile 0's weights of a block,
+// that the block's values and the next one's keys have landed ---------------------------
+template <Source S>
+__device__ void landed_role(const PromptPlace& w, PromptShared& sh) {
+  constexpr int kU = kUnits<S>;
+  const int n_blocks = w.j1 - w.j0;
+  for (int n = 0; n < n_blocks; ++n) {
+    // operands kU n + kU - 1 (values) to kU (n + 1) + kU - 2 (keys)
+    for (int i = kU * n + kU - 1; i < (n + 1 < n_blocks ? kU * (n + 2) - 1 : kU * (n + 1)); ++i)
+      if (!wait_warp(&sh.full[i % kSlots<S>], (i / kSlots<S>) & 1, sh)) return;
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.p_ready[0]);
+    // one arrival per phase
+    if (!wait_warp(&sh.p_ready[0], n & 1, sh)) return;
   }
 }
 
@@ -516,6 +568,7 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
     const uint16_t* src = a.q + qrow * a.q_stride + (size_t)(w.hkv * G + h) * kHeadDim;
     const uint32_t dst = smem_u32(smem) + t * kOperand;
     uint4 x[16];
+    uint32_t qt[2][32];  // one tile: the row in tensor memory
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + k) : make_uint4(0, 0, 0, 0);
     float down = 1.f;
@@ -540,9 +593,21 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
         for (int e = 0; e < 4; ++e)
           v[e] = pack_f16(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
       }
-      sts128(dst + (k >> 3) * kHalf + swz(row, k & 7), v[0], v[1], v[2], v[3]);
+      if (kOne) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qt[k >> 3][(k & 7) * 4 + e] = v[e];
+      } else {
+        sts128(dst + (k >> 3) * kHalf + swz(row, k & 7), v[0], v[1], v[2], v[3]);
+      }
     }
-    fence_proxy_async();
+    if (kOne) {
+      tmem_st32(tmem + kTmemQ, qt[0]);
+      tmem_st32(tmem + kTmemQ + 32, qt[1]);
+      tmem_wait_st();
+      tc_fence_before();
+    } else {
+      fence_proxy_async();
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_full);
   }
@@ -558,11 +623,13 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
     tc_fence_after();
     const int skip = *reinterpret_cast<volatile int*>(&sh.skip[0][n % kSkipRing]) |
                      *reinterpret_cast<volatile int*>(&sh.skip[1][n % kSkipRing]) << 4;
-    // values that some row must not see (tile 0's threads, one token each)
-    if (t == 0 && (kv0 + kBlock > first_limit || kv0 + kBlock > w.len || skip)) {
-      const int i = kUnits<S> * n + kUnits<S> - 1, slot = i % kSlots;
-      if (!wait_warp(&sh.full[slot], (i / kSlots) & 1, sh)) return;
-      uint8_t* v = smem + kTiles<S> * kOperand + slot * kOperand + row * 128;
+    // values that some row must not see are cleared by tile 0's threads, one token
+    // each, before its weights are handed over: the products of both tiles come later
+    const bool clear = kv0 + kBlock > first_limit || kv0 + kBlock > w.len || skip;
+    const int i = kUnits<S> * n + kUnits<S> - 1, slot = i % kSlots<S>;
+    if (t == 0 && clear) {
+      if (!wait_warp(&sh.full[slot], (i / kSlots<S>) & 1, sh)) return;
+      uint8_t* v = smem + kQueryTiles<S> * kOperand + slot * kOperand + row * 128;
       const int at = kv0 + row;
       bool zero = at >= w.kv_end || at >= w.len || ((skip >> (row / 16)) & 1);
       if (!zero && at >= first_limit) {
@@ -599,34 +666,32 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
     // that once, so that no phase is missed)
     bool settled = !kOne || n == 0;
     auto o_settled = [&] {
-      if (!settled && !wait_warp(&sh.pv_done, (n - 1) & 1, sh)) return false;
+      if (!settled && !block_done(n - 1, sh)) return false;
       settled = true;
       tc_fence_after();
       return true;
     };
     const uint32_t ts = tmem + buf * kBlock, to = tmem + kTmemO + t * kHeadDim;
-    // the row's logits, all of them in registers, and their maximum
+    // the row's logits, all of them in registers, and their maximum: that of the first
+    // half while the second is loaded
     uint32_t s[4][32];
+    float m4[4];
+    tmem_ld32(s[0], ts);
+    tmem_ld32(s[1], ts + 32);
+    tmem_wait_ld32(s[0]);
+    tmem_wait_ld32(s[1]);
+    tmem_ld32(s[2], ts + 64);
+    tmem_ld32(s[3], ts + 96);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) tmem_ld32(s[k], ts + 32 * k);
+    for (int k = 0; k < 4; ++k) {
+      if (k >= 2) tmem_wait_ld32(s[k]);
+      if (masked) hide(s[k], 32 * k);
+      m4[k] = __uint_as_float(s[k][0]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) tmem_wait_ld32(s[k]);
-    if (masked) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) hide(s[k], 32 * k);
+      for (int e = 1; e < 31; e += 2) m4[k] = max3(m4[k], __uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1]));
+      m4[k] = fmaxf(m4[k], __uint_as_float(s[k][31]));
     }
-    float mx;
-    {
-      float m4[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        m4[k] = __uint_as_float(s[k][0]);
-#pragma unroll
-        for (int e = 1; e < 31; e += 2) m4[k] = max3(m4[k], __uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1]));
-        m4[k] = fmaxf(m4[k], __uint_as_float(s[k][31]));
-      }
-      mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * factor;  // the factor is positive
-    }
+    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * factor;  // the factor is positive
     if (__any_sync(0xffffffffu, mx > m + kLazy || (m == -INFINITY && mx > m))) {
       const float mn = fmaxf(m, mx);
       const float al = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
@@ -665,12 +730,12 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
       }
       tmem_st16(ts + 16 * k, p);
     }
-    unpack_f32x2(sum, l0, l1);
     if (kOne && !o_settled()) return;
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.p_ready[buf]);
+    unpack_f32x2(sum, l0, l1);
   }
   const float l = l0 + l1;
 
@@ -731,8 +796,8 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
   extern __shared__ uint8_t dyn_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
   __shared__ PromptShared sh;
-  uint8_t* ring = smem + kTiles<S> * kOperand;
-  uint8_t* raw = ring + kSlots * kOperand;
+  uint8_t* ring = smem + kQueryTiles<S> * kOperand;
+  uint8_t* raw = ring + kSlots<S> * kOperand;
   const int tid = threadIdx.x, warp = tid >> 5;
 
   pdl_wait();
@@ -775,15 +840,12 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
   }
   if (tid == 0) {
     mbar_init(&sh.q_full, kRows / 32 * w.n_tiles);
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&sh.full[s], S == kCodes ? 8 : 1);
-      mbar_init(&sh.empty[s], 1);
-    }
-    mbar_init(&sh.pv_done, 1);
+    for (int s = 0; s < kSlots<S>; ++s) mbar_init(&sh.full[s], S == kCodes ? 8 : 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_ready[t], kRows / 32);
+      mbar_init(&sh.p_ready[t], kRows / 32 + (kTiles<S> == 2 && t == 0 ? 1 : 0));
       mbar_init(&sh.o_full[t], 1);
+      mbar_init(&sh.done[t], 1);
     }
     mbar_init(&sh.drain, 1);
     for (int s = 0; s < kRawSlots; ++s) {
@@ -808,6 +870,8 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
       __syncwarp();
     } else if (warp == 1) {
       load_role<S, P>(a, w, &tk, &tv, sh, ring, raw);
+    } else if (warp == 2 && kTiles<S> == 2) {
+      landed_role<S>(w, sh);
     }
   } else if (warp < 4 + 4 * kTiles<S>) {
     set_registers_up<208>();
@@ -865,7 +929,7 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
 template <Source S, int P>
 cudaError_t launch(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   auto kern = prompt_kernel<S, P>;
-  const size_t smem = 1024 + (size_t)(kTiles<S> + kSlots) * kOperand + (S == kCodes ? kRawSlots * kQ4Slot : 0);
+  const size_t smem = 1024 + (size_t)(kQueryTiles<S> + kSlots<S>) * kOperand + (S == kCodes ? kRawSlots * kQ4Slot : 0);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

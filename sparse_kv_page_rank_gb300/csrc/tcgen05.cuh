@@ -8,14 +8,14 @@
 namespace locks {
 
 // Shared-memory matrix descriptor, 128-byte swizzle (layout type 2), descriptor
-// version 1.  K-major operands (rows of 64 16-bit elements): `stride` is the byte
-// distance of 8-row groups, `lead` is unused.  MN-major operands (rows along K,
-// 64 contiguous elements along M or N): `stride` is the byte distance of groups of
-// 8 K rows, `lead` that of blocks of 64 elements.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// version 1, as two words: the low one holds the address / 16 and `lead` / 16, the high
+// one `stride` / 16 and constants, so stepping through an operand is one 32-bit
+// addition.  K-major operands (rows of 64 16-bit elements): `stride` is the byte
+// distance of 8-row groups, `lead` is unused.  MN-major operands (rows along K, 64
+// contiguous elements along M or N): `stride` is the byte distance of groups of 8 K
+// rows, `lead` that of blocks of 64 elements.
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t addr, uint32_t lead) { return addr >> 4 | (lead >> 4) << 16; }
+constexpr uint32_t kUmmaDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;  // stride 1024
 
 // Instruction descriptor of kind::f16 with fp32 accumulators: bf16 or fp16
 // operands, A K-major, B K-major or MN-major.
@@ -24,18 +24,20 @@ __host__ __device__ constexpr uint32_t umma_idesc(int m, int n, bool bf16, bool 
          (uint32_t)(m / 16) << 24;
 }
 
-// D[tmem] (+)= A[smem] B[smem]; one thread issues.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// D[tmem] (+)= A[smem] B[smem]; one thread issues.  a, b: low descriptor words.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kUmmaDescHi)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem].
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.u32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kUmmaDescHi)
       : "memory");
 }
 // Arrive on `bar` once every tcgen05 operation this thread issued before is complete.
