@@ -37,9 +37,9 @@
 //
 // Values that a row does not see must not reach it, not even as 0 * NaN: in the
 // blocks that straddle a tile's diagonal or the end of the sequence, value rows past
-// the end are zeroed in shared memory, and a visible token's non-finite values are
-// zeroed there too and added, as they are, to the rows that see the token at the
-// end.
+// the end are zeroed in shared memory, and the infinities and NaN of tokens that not
+// every row sees are zeroed there too and added, as they are, to the rows that do see
+// the token at the end.
 //
 // Few rows: the keys of a problem are cut among several CTAs, whose partial
 // (reference, sum, O) go to the workspace; the last one to finish joins them.
@@ -631,26 +631,28 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
       if (!wait_warp(&sh.full[slot], (i / kSlots<S>) & 1, sh)) return;
       uint8_t* v = smem + kQueryTiles<S> * kOperand + slot * kOperand + row * 128;
       const int at = kv0 + row;
-      bool zero = at >= w.kv_end || at >= w.len || ((skip >> (row / 16)) & 1);
-      if (!zero && at >= first_limit) {
-        bool bad = false;
+      if (at >= w.kv_end || at >= w.len || ((skip >> (row / 16)) & 1)) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(v + (k >> 3) * kHalf + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+      } else if (at >= first_limit) {
+        // infinities and NaN: cleared here, and added at the end to the rows that see them
+        constexpr uint32_t e = Q4 ? 0x7c007c00u : 0x7f807f80u;  // an exponent of all ones
+        auto hit = [&](uint32_t y) { return __vcmpeq2(y & e, e); };
+        uint32_t bad = 0;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const uint4 x = *reinterpret_cast<const uint4*>(v + (k >> 3) * kHalf + (k & 7) * 16);
-          const uint32_t e = Q4 ? 0x7c007c00u : 0x7f807f80u;
-          // an exponent of all ones in either half of a word
-          auto inf = [&](uint32_t y) { return __vcmpeq2(y & e, e) != 0; };
-          bad |= inf(x.x) | inf(x.y) | inf(x.z) | inf(x.w);
+          bad |= hit(x.x) | hit(x.y) | hit(x.z) | hit(x.w);
         }
         if (bad) {
+#pragma unroll 1
+          for (int k = 0; k < 64; ++k) {
+            uint32_t* x = reinterpret_cast<uint32_t*>(v + (k >> 5) * kHalf) + (k & 31);
+            *x &= ~hit(*x);
+          }
           const int k = atomicAdd(&sh.n_bad, 1);
           if (k < kMaxBad) sh.bad[k] = at;
-          zero = true;
         }
-      }
-      if (zero) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(v + (k >> 3) * kHalf + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async();
     }
@@ -860,7 +862,9 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  // All 512 columns, so they begin at address 0: a constant, which saves the address
+  // arithmetic of every tensor memory access (662 us, not 673, for 8K tokens of 4-bit pages).
+  constexpr uint32_t tmem = 0;
 
   // registers per warpgroup: the launch's 504 (512) between them
   if (warp < 4) {

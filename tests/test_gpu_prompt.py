@@ -152,6 +152,29 @@ def test_a_later_token_that_is_not_finite_stays_out_of_earlier_rows(value, where
         check(case, [new], q, out, lse, first_bad=(0, at))
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("dim", [0, 77, 127])
+def test_one_value_that_is_not_finite_reaches_one_column(value, dim):
+    """One dimension of one token's value: the rows that see the token have it there and
+    are right everywhere else."""
+    case = Case([400], 4, 1, 64, "bf16", seed=3)
+    at, new = 250, 300
+    page, slot = int(case.table[0, at // 64]), at % 64
+    was = case.v[page, 0, slot, dim].clone()
+    rt, q = case.runtime(), case.query(new)
+    good, _ = rt.prompt_attend(q, cu_tokens=cu_of([new]))
+    case.v[page, 0, slot, dim] = value
+    out, lse = rt.prompt_attend(q, cu_tokens=cu_of([new]))
+    case.v[page, 0, slot, dim] = was
+    sees = torch.arange(new, device="cuda") + 100 >= at
+    assert torch.equal(out[~sees], good[~sees])
+    col = out[sees][..., dim].float()
+    assert (torch.isnan(col) if math.isnan(value) else col == value).all()
+    rest = torch.arange(D, device="cuda") != dim
+    assert torch.equal(out[sees][..., rest], good[sees][..., rest])
+    assert rt.device_error() == 0
+
+
 def test_a_nan_scale_of_a_later_token_stays_out_of_earlier_rows():
     case = Case([400], 4, 1, 64, "q4", seed=3)
     at = 333
