@@ -101,23 +101,25 @@ float scale_of(const locks_params_t* p) {
 // pages still keep every warp busy.
 constexpr long long kQ4WholeSlots = 12;
 
+int q4_tiles_for(long long slots_per_cta) { return slots_per_cta >= kQ4WholeSlots ? 4 : 1; }
+// Every page: as many CTAs as are resident at once, but no more than slots.
+int q4_dense_ctas(long long slots, int sms) { return (int)std::min<long long>((long long)kQ4CtasPerSm * sms, slots); }
+
 void plan_q4(const locks_cache_t* c, Plan& pl, int sms, long long max_tiles, int ppt) {
   const int P = c->page_size;
   const long long BH = pl.BH;
-  auto tiles_for = [](long long slots_per_cta) { return slots_per_cta >= kQ4WholeSlots ? 4 : 1; };
   {
     // page list: one cluster per problem, the largest with which all are resident at once
     const long long slots = ((long long)pl.k_max + 2 + ppt - 1) / ppt;
     int cs = 16;
     while (cs > 1 && (cs > slots || BH > attend_q4_active_clusters(pl.G, P, 1, cs))) cs /= 2;
     pl.q4_sparse_cluster = cs;
-    pl.q4_sparse_tiles = tiles_for((slots + cs - 1) / cs);
+    pl.q4_sparse_tiles = q4_tiles_for((slots + cs - 1) / cs);
   }
   {
-    // every page: as many CTAs as are resident at once, but no more than slots
     const long long slots = BH * max_tiles;
-    pl.q4_dense_ctas = (int)std::min<long long>((long long)kQ4CtasPerSm * sms, slots);
-    pl.q4_dense_tiles = tiles_for(slots / pl.q4_dense_ctas);
+    pl.q4_dense_ctas = q4_dense_ctas(slots, sms);
+    pl.q4_dense_tiles = q4_tiles_for(slots / pl.q4_dense_ctas);
   }
 }
 
@@ -224,7 +226,7 @@ Plan make_plan(const locks_cache_t* c, const locks_params_t* p) {
   };
   // partial results of the dense decode, and its tickets
   const long long parts = is_q4(c) ? 2LL * pl.q4_dense_ctas : BH * pl.dense_nc;
-  const long long tickets = BH + 2LL * pl.q4_dense_ctas;
+  const long long tickets = std::max(BH, 3LL * pl.q4_dense_ctas);
   pl.off_err = take(sizeof(int));
   pl.off_cnt_tk = take(sizeof(unsigned) * BH);
   pl.off_cnt_att = take(sizeof(unsigned) * tickets);
@@ -460,6 +462,12 @@ locks_status_t check_err_ws(void* ws, size_t bytes) {
 
 // Launch shape and workspace of lockskv_prompt_attend.
 constexpr long long kPromptCounters = 1024;
+// 4-bit pages: up to this many (token, head) rows of a KV head take the kernel for one
+// query token, kQ4RowColumns at a time; a pass over the pages per eight rows, against
+// one of the tensor cores' kernel, whose softmax and conversion cost the same for 8
+// rows as for 128.  8 sequences of 12,000 tokens, 8 KV heads, in us: 4 rows 41 against
+// 155, 20 rows 79 and 159, 48 rows 137 and 161, 64 rows 174 and 164.
+constexpr int kFewRows = 48;
 // 4-bit pages: from this many row tiles of a head on, its keys and values are
 // converted once for all of them, where the planes take no more than this.
 constexpr int kPlaneTiles = 4;
@@ -467,6 +475,7 @@ constexpr long long kPlaneBytes = 4LL << 30;
 struct PromptPlan {
   int n_qtiles = 1, n_splits = 1, plane_rows = 0;
   bool planes = false;
+  int row_ctas = 0, row_tiles = 0;  // few rows of 4-bit pages, else 0
   size_t off_counters = 0, off_ml = 0, off_o = 0, off_planes = 0, total = 0;
 };
 
@@ -488,11 +497,20 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
   // The error word, then the counters (problems are split only while there are at
   // most half as many as SMs), in the same place for every shape: one workspace
   // serves calls of different lengths, whose partial results never lie on a counter.
-  size_t off = kAlign;
+  const long long counters = std::max(kPromptCounters, 3 * kQ4CtasPerSm * sms);
   if (ctas > kPromptCounters) pl->n_splits = 1;
-  const size_t parts = pl->n_splits > 1 ? (size_t)ctas * pl->n_splits * 256 : 0;
+  size_t parts = pl->n_splits > 1 ? (size_t)ctas * pl->n_splits * 256 : 0;
+  if (is_q4(c) && (long long)t->max_tokens * G <= kFewRows) {
+    const long long slots = BH * ((t->max_tokens * G + kQ4RowColumns - 1) / kQ4RowColumns) *
+                            (((long long)c->max_pages * c->page_size + kPage - 1) / kPage);
+    pl->row_ctas = std::max(1, q4_dense_ctas(slots, (int)sms));
+    pl->row_tiles = q4_tiles_for(slots / pl->row_ctas);
+    pl->planes = false;
+    parts = 2 * (size_t)pl->row_ctas * kQ4RowColumns;
+  }
+  size_t off = kAlign;
   pl->off_counters = off;
-  off = align_up(off + sizeof(unsigned) * kPromptCounters);
+  off = align_up(off + sizeof(unsigned) * counters);
   pl->off_ml = off;
   off = align_up(off + sizeof(float2) * parts);
   pl->off_o = off;
@@ -791,6 +809,33 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   if ((st = plan_prompt(cache, params, tokens, &pl)) != LOCKS_OK) return st;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) || ws_bytes < pl.total) return LOCKS_ERR_WORKSPACE;
   if (tokens->total == 0 || tokens->max_tokens == 0) return LOCKS_OK;
+  if (pl.row_ctas > 0) {
+    AttendArgs r = {};
+    r.q = static_cast<const uint16_t*>(q);
+    r.q_stride = q_stride;
+    r.k_pool16 = static_cast<const uint16_t*>(cache->k_pool);
+    r.cu_tokens = tokens->cu_tokens;
+    r.block_table = cache->block_table;
+    r.seq_lens = cache->seq_lens;
+    r.out = static_cast<uint16_t*>(out);
+    r.lse = lse;
+    r.part_o = at<float>(ws, pl.off_o);
+    r.part_ml = at<float2>(ws, pl.off_ml);
+    r.counters = at<unsigned>(ws, pl.off_counters);
+    r.err = at<int>(ws, 0);
+    r.batch = cache->batch;
+    r.num_kv_heads = cache->num_kv_heads;
+    r.group = params->num_q_heads / cache->num_kv_heads;
+    r.max_pages = cache->max_pages;
+    r.pages_total = cache->pages_total;
+    r.page_size = cache->page_size;
+    r.total = tokens->total;
+    r.max_tokens = tokens->max_tokens;
+    r.n_splits = pl.row_ctas;
+    r.cluster = 1;
+    r.scale_log2 = scale_of(params) * kLog2e;
+    return cuda_status(launch_attend_q4_rows(r, pl.row_tiles, static_cast<cudaStream_t>(stream)));
+  }
   CUtensorMap tk, tv;
   std::memset(&tk, 0, sizeof(tk));
   std::memset(&tv, 0, sizeof(tv));

@@ -105,8 +105,9 @@ __device__ __forceinline__ uint32_t pair_mask(int t, int len) {
 }
 
 // One warp's share of a problem.  TPU: 16-token tiles per turn (one buffer); NT:
-// blocks of 8 query heads.
-template <int P, int TPU, int NT, bool LSE>
+// blocks of 8 columns.  A column is a query head of the group, with ROWS one of one of
+// several query tokens, which do not all see the last keys.
+template <int P, int TPU, int NT, bool LSE, bool ROWS = false>
 struct Q4Warp {
   static constexpr int TP = P / 16;                        // tiles of a page
   static constexpr int kPages = TP >= TPU ? 1 : TPU / TP;  // pages a unit touches
@@ -119,7 +120,8 @@ struct Q4Warp {
   using At = Q4Tile<P, TPU>;
 
   Q4Shared& sh;
-  const int warp, lane, g, c, group;
+  const int warp, lane, g, c;
+  int group;             // columns in use
   const uint32_t wbase;  // this warp's buffers
   // q of head 8 nt + g, dimensions 32 j + 8 c .. + 7, scaled into fp16
   uint32_t qf[NT][4][4];
@@ -129,12 +131,14 @@ struct Q4Warp {
   float o[4][2][NT][4];  // their outputs: dimensions 32 j + 4 g + 2 half, + 1 (rows)
   int x;                 // exponent offset of the weights, lowered by large value scales
   int seq;               // units consumed so far: buffer seq % kBufs, phase seq / kBufs
+  // ROWS: keys at the end that heads 2c, 2c + 1 and head g, and the first column, do not see
+  int back[NT][2], back_g[NT], back_max;
   float* page_lse;       // LSE only
   size_t lse_stride;
 
   __device__ __forceinline__ Q4Warp(Q4Shared& s, uint32_t ring, int grp)
       : sh(s), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2), c(threadIdx.x & 3),
-        group(grp), wbase(ring + (threadIdx.x >> 5) * kWarpTiles * kTileBytes), x(15), seq(0), page_lse(nullptr),
+        group(grp), wbase(ring + (threadIdx.x >> 5) * kWarpTiles * kTileBytes), x(15), seq(0), back_max(0), page_lse(nullptr),
         lse_stride(0) {}
 
   __device__ __forceinline__ void reset() {
@@ -152,8 +156,9 @@ struct Q4Warp {
     }
   }
 
-  // The group's queries (rows q, bf16).
-  __device__ __forceinline__ void load_q(const uint16_t* q, float scale_log2) {
+  // The columns' queries (bf16), that of column h at row(h).
+  template <typename Row>
+  __device__ __forceinline__ void load_q(Row row, float scale_log2) {
     const int G = group;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -164,7 +169,7 @@ struct Q4Warp {
       for (int j = 0; j < 4; ++j) {
         raw[j] = make_uint4(0, 0, 0, 0);
         if (h < G)
-          raw[j] = __ldg(reinterpret_cast<const uint4*>(q + h * kHeadDim + 32 * j + 8 * c));
+          raw[j] = __ldg(reinterpret_cast<const uint4*>(row(h) + 32 * j + 8 * c));
         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
@@ -199,7 +204,19 @@ struct Q4Warp {
     }
   }
 
-  // One unit in buffer `buf`; WHOLE: all its tokens are inside the sequence, else
+  // behind(h): keys at the end that column h does not see (the first column the most).
+  template <typename Behind>
+  __device__ __forceinline__ void set_back(Behind behind) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) back[nt][k] = behind(8 * nt + 2 * c + k);
+      back_g[nt] = behind(8 * nt + g);
+    }
+    back_max = behind(0);
+  }
+
+  // One unit in buffer `buf`; WHOLE: every column sees all its tokens, else
   // left[t] counts those of tile t (two copies of the code, so that whole units
   // carry no masks).
   template <bool WHOLE>
@@ -253,10 +270,13 @@ struct Q4Warp {
       }
       if constexpr (!WHOLE) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (g >= left[t]) sc[t][nt][0] = sc[t][nt][1] = -INFINITY;
-          if (g + 8 >= left[t]) sc[t][nt][2] = sc[t][nt][3] = -INFINITY;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int n = ROWS ? left[t] - back[nt][k] : left[t];
+            if (g >= n) sc[t][nt][k] = -INFINITY;
+            if (g + 8 >= n) sc[t][nt][2 + k] = -INFINITY;
+          }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -348,7 +368,9 @@ struct Q4Warp {
           float p[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            p[k] = fast_exp2(fmaf(sc[t][nt][k], fac[nt][k & 1], -R[nt][k & 1]));
+            // a column that has seen no key yet has the reference -infinity
+            const float ref = ROWS && !WHOLE && R[nt][k & 1] == -INFINITY ? 0.f : R[nt][k & 1];
+            p[k] = fast_exp2(fmaf(sc[t][nt][k], fac[nt][k & 1], -ref));
             l[nt][k & 1] += p[k];
           }
           pb[nt][0] = transpose8x8(pack_f16(p[0], p[1]));  // tokens 2c, 2c + 1 of head g
@@ -373,7 +395,12 @@ struct Q4Warp {
           q4_codes01(vw1[j] >> 8, b2, b3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t p0 = mul_f16x2(pb[nt][0], zw0[j]), p1 = mul_f16x2(pb[nt][1], zw1[j]);
+            uint32_t p0 = mul_f16x2(pb[nt][0], zw0[j]), p1 = mul_f16x2(pb[nt][1], zw1[j]);
+            if constexpr (ROWS && !WHOLE) {
+              // 0 * NaN: a token that the column does not see
+              p0 &= pair_mask(2 * c, left[t] - back_g[nt]);
+              p1 &= pair_mask(8 + 2 * c, left[t] - back_g[nt]);
+            }
             mma_16816_f16(o[j][0][nt], a0, a1, a2, a3, p0, p1);
             mma_16816_f16(o[j][1][nt], b0, b1, b2, b3, p0, p1);
           }
@@ -463,7 +490,7 @@ struct Q4Warp {
 #pragma unroll
       for (int t = 0; t < TPU; ++t) {
         left[t] = P == 64 ? sh.len[warp][buf][0] - 16 * t : sh.len[warp][buf][t];
-        whole &= left[t] >= 16;
+        whole &= left[t] >= (ROWS ? 16 + back_max : 16);
         any |= left[t] > 0;
       }
       const uint32_t base = wbase + buf * kBufBytes;
@@ -566,18 +593,24 @@ __device__ __forceinline__ void store_result(const AttendArgs& a, size_t row, in
 }
 
 // ---- every page ------------------------------------------------------------------
+// A problem is a KV head of a sequence with, for the newest tokens of a sequence (ROWS),
+// up to 8 NT of their (token, head) rows as columns; its blocks of rows follow each other
+// in the line, so that they read the pages at about the same time.
 // Partial results a.part_ml, a.part_o: two per CTA (its first problem, which another
-// CTA began, and the one it begins itself), [2 CTA + begins][G].  Tickets a.counters:
-// [B*Hkv] per problem, then two per CTA for groups of partials.
+// CTA began, and the one it begins itself), [2 CTA + begins][G or 8 NT].  Tickets
+// a.counters: per CTA one for the problem that it begins and does not finish, then two
+// for groups of partials.
 constexpr int kJoinBytes = 80 * 1024;  // partials one CTA reads at a time
 
-// Joins n partials (the first in slot s0, the others in s1, s1 + step, ...) into the
-// result rows (row >= 0) or into the first slot.  The outputs come into shared memory
-// as bulk copies, all in flight at once, while the weights are made.
+// Joins n partials of G columns (the first in slot s0, the others in s1, s1 + step, ...;
+// slots of `pitch` columns) into the result rows row(column) or, if not `final`, into the
+// first slot.  The outputs come into shared memory as bulk copies, all in flight at
+// once, while the weights are made.
+template <typename Row>
 __device__ void join_partials(const AttendArgs& a, Q4Shared& sh, uint8_t* ring, int n, size_t s0, size_t s1, size_t step,
-                              long long row, int& phase) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.group;
-  auto slot = [&](int i) { return i == 0 ? s0 : s1 + step * (size_t)(i - 1); };
+                              int G, int pitch, bool final, Row row, int& phase) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto slot = [&](int i) { return (i == 0 ? s0 : s1 + step * (size_t)(i - 1)) * pitch; };
   const float* po = reinterpret_cast<const float*>(ring);  // [at_once][G][128]
   float* f = reinterpret_cast<float*>(ring + kJoinBytes);  // [n][G]: at most two per SM and 16 heads
   static_assert(kJoinBytes + 16 * 4 * 448 <= kRing, "weights of 448 partials");
@@ -587,7 +620,7 @@ __device__ void join_partials(const AttendArgs& a, Q4Shared& sh, uint8_t* ring, 
     if (lane == 0) mbar_arrive_expect_tx(&sh.join, (uint32_t)(m * G * kHeadDim * 4));
     __syncwarp();
     for (int i = lane; i < m; i += 32)
-      bulk_load(smem_u32(ring) + i * G * kHeadDim * 4, a.part_o + slot(i0 + i) * G * kHeadDim, G * kHeadDim * 4, &sh.join);
+      bulk_load(smem_u32(ring) + i * G * kHeadDim * 4, a.part_o + slot(i0 + i) * kHeadDim, G * kHeadDim * 4, &sh.join);
   };
   // the partials were written with ordinary stores (here: the ring too)
   asm volatile("fence.proxy.async;\n" ::: "memory");
@@ -595,10 +628,10 @@ __device__ void join_partials(const AttendArgs& a, Q4Shared& sh, uint8_t* ring, 
   if (warp == 0) ask(0);
   for (int h = warp; h < G; h += kW) {
     float M = -INFINITY, Ls = 0.f;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.part_ml + slot(i) * G + h).x);
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.part_ml + slot(i) + h).x);
     M = warp_max(M);
     for (int i = lane; i < n; i += 32) {
-      const float2 ml = __ldcg(a.part_ml + slot(i) * G + h);
+      const float2 ml = __ldcg(a.part_ml + slot(i) + h);
       const float e = M == -INFINITY ? 1.f : fast_exp2(ml.x - M);
       Ls = fmaf(ml.y, e, Ls);
       f[i * G + h] = e;
@@ -639,17 +672,48 @@ __device__ void join_partials(const AttendArgs& a, Q4Shared& sh, uint8_t* ring, 
     const int e = 2 * (tid + k * kThreads);
     if (e >= G * kHeadDim) break;
     const int h = e / kHeadDim, col = e % kHeadDim;
-    if (row >= 0) {
-      store_result(a, (size_t)row + h, col, O[k].x, sh.cta_m[h], sh.cta_l[h]);
-      store_result(a, (size_t)row + h, col + 1, O[k].y, sh.cta_m[h], sh.cta_l[h]);
+    if (final) {
+      store_result(a, row(h), col, O[k].x, sh.cta_m[h], sh.cta_l[h]);
+      store_result(a, row(h), col + 1, O[k].y, sh.cta_m[h], sh.cta_l[h]);
     } else {
-      *reinterpret_cast<float2*>(a.part_o + s0 * G * kHeadDim + e) = O[k];
-      if (col == 0) a.part_ml[s0 * G + h] = make_float2(sh.cta_m[h], sh.cta_l[h]);
+      *reinterpret_cast<float2*>(a.part_o + slot(0) * kHeadDim + e) = O[k];
+      if (col == 0) a.part_ml[slot(0) + h] = make_float2(sh.cta_m[h], sh.cta_l[h]);
     }
   }
 }
 
-template <int P, int TPU, int NT>
+struct Q4Seq {
+  int keys;             // that its newest token sees
+  int row0, n, start;   // its query tokens: first row, number, position of the first
+};
+template <int P, bool ROWS>
+__device__ __forceinline__ Q4Seq sequence(const AttendArgs& a, int b, bool says) {
+  Q4Seq s;
+  const int len = checked_length(a, b, P, says);
+  s.keys = len;
+  s.row0 = b;
+  s.n = 1;
+  s.start = len - 1;
+  if constexpr (ROWS) {
+    int n = len > 0 ? 1 : 0;
+    if (a.cu_tokens) {
+      s.row0 = a.cu_tokens[b];
+      const int end = a.cu_tokens[b + 1];
+      n = end - s.row0;
+      if (s.row0 < 0 || n < 0 || end > a.total) {
+        if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+        n = 0;
+      }
+    }
+    if (says && (n > len || n > a.max_tokens)) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+    s.n = min(n, a.max_tokens);
+    s.start = len - n;
+    s.keys = s.n > 0 ? max(0, min(len, s.start + s.n)) : 0;
+  }
+  return s;
+}
+
+template <int P, int TPU, int NT, bool ROWS>
 __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const AttendArgs a) {
   extern __shared__ __align__(128) uint8_t ring_raw[];
   __shared__ Q4Shared sh;
@@ -657,7 +721,10 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const Atte
   constexpr int kPPS = kPage / P;  // pages of a slot
   const int tid = threadIdx.x, lane = tid & 31;
   const int G = a.group, hkv_n = a.num_kv_heads;
-  Q4Warp<P, TPU, NT, false> w(sh, smem_u32(ring), G);
+  constexpr int kCols = 8 * NT;
+  static_assert(!ROWS || kCols == kQ4RowColumns, "the columns of a partial result");
+  const int pitch = ROWS ? kCols : G;  // columns of a partial result
+  Q4Warp<P, TPU, NT, false, ROWS> w(sh, smem_u32(ring), G);
   if (lane == 0) {
     for (int s = 0; s < kWarpTiles; ++s) mbar_init(&sh.full[w.warp][s], 1);
     if (w.warp == 0) mbar_init(&sh.join, 1);
@@ -667,8 +734,12 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const Atte
   __syncthreads();
   pdl_wait();
 
-  // all slots in one line: sequence by sequence, head by head
-  auto slots_of = [&](int b) { return (checked_length(a, b, P, blockIdx.x == 0 && tid < 32) + kPage - 1) / kPage; };
+  // all slots in one line: sequence by sequence, head by head, block of rows by block
+  auto blocks_of = [&](const Q4Seq& s) { return ROWS ? (s.n * G + kCols - 1) / kCols : 1; };
+  auto slots_of = [&](int b) {  // per head
+    const Q4Seq s = sequence<P, ROWS>(a, b, blockIdx.x == 0 && tid < 32);
+    return (s.keys + kPage - 1) / kPage * blocks_of(s);
+  };
   long long total = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     int n = b0 + lane < a.batch ? slots_of(b0 + lane) : 0;
@@ -685,21 +756,26 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const Atte
 
   if (cta == 0) {
     // sequences without a token have no slots and get their rows here
-    for (int b = 0; b < a.batch; ++b)
-      if (a.seq_lens[b] <= 0)
-        for (int e = tid; e < hkv_n * G * kHeadDim; e += kThreads)
-          store_result(a, (size_t)b * hkv_n * G + e / kHeadDim, e % kHeadDim, 0.f, 0.f, 0.f);
+    for (int b = 0; b < a.batch; ++b) {
+      const Q4Seq s = sequence<P, ROWS>(a, b, false);
+      if (s.keys > 0) continue;
+      for (int e = tid; e < s.n * hkv_n * G * kHeadDim; e += kThreads)
+        store_result(a, (size_t)s.row0 * hkv_n * G + e / kHeadDim, e % kHeadDim, 0.f, 0.f, 0.f);
+    }
   }
 
   // the sequence that holds slot `at`, and the line's position of its first slot
   int b = 0;
   long long first = 0;
-  int nb = 0;  // its slots per head
+  Q4Seq q = {};
+  int nb = 0, n_blocks = 1;  // its slots per problem, problems per head
   auto seek = [&](long long y) {
     while (b < a.batch) {
-      nb = slots_of(b);
-      if (y < first + (long long)nb * hkv_n) return;
-      first += (long long)nb * hkv_n;
+      q = sequence<P, ROWS>(a, b, false);
+      n_blocks = blocks_of(q);
+      nb = (q.keys + kPage - 1) / kPage;
+      if (y < first + (long long)nb * n_blocks * hkv_n) return;
+      first += (long long)nb * n_blocks * hkv_n;
       ++b;
     }
   };
@@ -716,60 +792,73 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const Atte
   }
   while (at < end) {
     seek(at);
-    const int h = (int)((at - first) / nb);
-    const long long p0 = first + (long long)h * nb, p1 = p0 + nb;  // the problem's slots in the line
-    const int s0 = (int)(at - p0), s1 = (int)(min(end, p1) - p0);  // this CTA's of them
-    const int L = checked_length(a, b, P, false);
-    const int pg0 = s0 * kPPS, pg1 = min(s1 * kPPS, (L + P - 1) / P);
-    const size_t row = ((size_t)b * hkv_n + h) * G;
+    const int prob = (int)((at - first) / nb), h = prob / n_blocks;
+    const int r0 = ROWS ? prob % n_blocks * kCols : 0;  // its first row of the head's
+    const long long p0 = first + (long long)prob * nb, p1 = p0 + nb;  // its slots in the line
+    const int s0 = (int)(at - p0), s1 = (int)(min(end, p1) - p0);     // this CTA's of them
+    const int L = q.keys, pg0 = s0 * kPPS, pg1 = min(s1 * kPPS, (L + P - 1) / P);
+    const int cols = ROWS ? min(kCols, q.n * G - r0) : G;
+    // the row in the outputs, and its query, of a column
+    auto row = [&](int x) {
+      const int i = ROWS ? (r0 + x) / G : 0, e = ROWS ? (r0 + x) % G : x;
+      return ((size_t)(q.row0 + i) * hkv_n + h) * G + e;
+    };
+    auto query = [&](int x) {
+      if constexpr (!ROWS) return a.q + row(x) * kHeadDim;
+      return a.q + (size_t)(q.row0 + (r0 + x) / G) * a.q_stride + (size_t)(h * G + (r0 + x) % G) * kHeadDim;
+    };
+    w.group = cols;
+    if constexpr (ROWS) w.set_back([&](int x) { return x < cols ? L - max(0, q.start + (r0 + x) / G + 1) : 0; });
     w.run(reinterpret_cast<const uint8_t*>(a.k_pool16), (size_t)hkv_n * LOCKS_KV_Q4_BLOCK_BYTES(P), h, pg1 - pg0, a.err,
           [&](int i, int& lp, int& phys, int& len) {
             lp = pg0 + i;
             phys = physical_page(a, b, lp);
-            len = phys >= 0 ? min(P, L - lp * P) : 0;
+            // with rows all that follow, against which a column's own end is counted
+            len = phys < 0 ? 0 : ROWS ? L - lp * P : min(P, L - lp * P);
           },
           [&] {
             w.reset();
-            w.load_q(a.q + row * kHeadDim, a.scale_log2);
+            w.load_q(query, a.scale_log2);
           });
     if (p0 + s1 >= end) pdl_launch_dependents();
     const float* octa = w.merge(ring);
     if (s0 == 0 && s1 == nb) {
-      for (int e = tid; e < G * kHeadDim; e += kThreads)
-        store_result(a, row + e / kHeadDim, e % kHeadDim, octa[e], sh.cta_m[e / kHeadDim], sh.cta_l[e / kHeadDim]);
+      for (int e = tid; e < cols * kHeadDim; e += kThreads)
+        store_result(a, row(e / kHeadDim), e % kHeadDim, octa[e], sh.cta_m[e / kHeadDim], sh.cta_l[e / kHeadDim]);
     } else {
       // the problem's CTAs c0 .. c1; c0 begins it
       const long long c0 = owner(p0), c1 = owner(p1 - 1);
-      const size_t mine = 2 * (size_t)cta + (s0 == 0 ? 1 : 0);
-      for (int e = tid; e < G * (kHeadDim / 4); e += kThreads)
-        reinterpret_cast<float4*>(a.part_o + mine * G * kHeadDim)[e] = reinterpret_cast<const float4*>(octa)[e];
-      if (tid < G) a.part_ml[mine * G + tid] = make_float2(sh.cta_m[tid], sh.cta_l[tid]);
+      const size_t mine = (2 * (size_t)cta + (s0 == 0 ? 1 : 0)) * pitch;
+      for (int e = tid; e < cols * (kHeadDim / 4); e += kThreads)
+        reinterpret_cast<float4*>(a.part_o + mine * kHeadDim)[e] = reinterpret_cast<const float4*>(octa)[e];
+      if (tid < cols) a.part_ml[mine + tid] = make_float2(sh.cta_m[tid], sh.cta_l[tid]);
       __threadfence();
       __syncthreads();
       const int n = (int)(c1 - c0) + 1;
       // partials of a group: all of them where they are two loads' worth, else 16
-      const int gs = n <= 2 * (kJoinBytes / (G * kHeadDim * 4)) ? n : 16;
+      const int gs = n <= 2 * (kJoinBytes / (cols * kHeadDim * 4)) ? n : 16;
       const int i = (int)(cta - c0), grp = i / gs, n_grp = (n + gs - 1) / gs;
       const size_t g0 = grp == 0 ? 2 * (size_t)c0 + 1 : 2 * ((size_t)c0 + (size_t)grp * gs);
       const int in_grp = min(gs, n - grp * gs);
-      unsigned* ticket = n_grp == 1 ? a.counters + (size_t)b * hkv_n + h : a.counters + (size_t)a.batch * hkv_n + g0;
+      unsigned* top = a.counters + c0;
+      unsigned* ticket = n_grp == 1 ? top : a.counters + gridDim.x + g0;
       if (tid == 0) sh.last = atomicAdd(ticket, 1u) == (unsigned)(in_grp - 1);
       __syncthreads();
       if (sh.last) {
         __threadfence();
         if (tid == 0) *ticket = 0;  // ready for the next call
-        join_partials(a, sh, ring, in_grp, g0, 2 * ((size_t)c0 + (size_t)grp * gs + 1), 2,
-                      n_grp == 1 ? (long long)row : -1, join_phase);
+        join_partials(a, sh, ring, in_grp, g0, 2 * ((size_t)c0 + (size_t)grp * gs + 1), 2, cols, pitch, n_grp == 1, row,
+                      join_phase);
         if (n_grp > 1) {
           __threadfence();
           __syncthreads();
-          unsigned* top = a.counters + (size_t)b * hkv_n + h;
           if (tid == 0) sh.last = atomicAdd(top, 1u) == (unsigned)(n_grp - 1);
           __syncthreads();
           if (sh.last) {
             __threadfence();
             if (tid == 0) *top = 0;
-            join_partials(a, sh, ring, n_grp, 2 * (size_t)c0 + 1, 2 * ((size_t)c0 + gs), 2 * (size_t)gs, (long long)row, join_phase);
+            join_partials(a, sh, ring, n_grp, 2 * (size_t)c0 + 1, 2 * ((size_t)c0 + gs), 2 * (size_t)gs, cols, pitch, true, row,
+                          join_phase);
           }
         }
       }
@@ -851,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_kernel(const AttendArgs
         },
         [&] {
           w.reset();
-          w.load_q(a.q + row * kHeadDim, a.scale_log2);
+          w.load_q([&](int h) { return a.q + (row + h) * kHeadDim; }, a.scale_log2);
         });
   pdl_launch_dependents();
   if constexpr (!LSE) {
@@ -904,8 +993,8 @@ Kern pick(int group, int tiles) {
     if (group <= 8) return tiles == 4 ? attend_q4_kernel<MODE, P, 4, 1> : attend_q4_kernel<MODE, P, 1, 1>;
     return tiles == 4 ? attend_q4_kernel<MODE, P, 2, 2> : attend_q4_kernel<MODE, P, 1, 2>;
   } else {
-    if (group <= 8) return tiles == 4 ? attend_q4_dense_kernel<P, 4, 1> : attend_q4_dense_kernel<P, 1, 1>;
-    return tiles == 4 ? attend_q4_dense_kernel<P, 2, 2> : attend_q4_dense_kernel<P, 1, 2>;
+    if (group <= 8) return tiles == 4 ? attend_q4_dense_kernel<P, 4, 1, false> : attend_q4_dense_kernel<P, 1, 1, false>;
+    return tiles == 4 ? attend_q4_dense_kernel<P, 2, 2, false> : attend_q4_dense_kernel<P, 1, 2, false>;
   }
 }
 
@@ -957,8 +1046,7 @@ int attend_q4_active_clusters(int group, int page_size, int tiles, int cs) {
   return slot > 0 ? slot : 0;
 }
 
-cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStream_t s) {
-  const Kern k = kernel_of(mode, a.group, a.page_size, tiles);
+static cudaError_t launch_kernel(Kern k, const AttendArgs& a, int mode, cudaStream_t s) {
   if (!prepare(k, a.cluster)) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_splits, mode == kAttendDense ? 1 : a.batch * a.num_kv_heads, 1);
@@ -975,6 +1063,19 @@ cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStream_t s) {
+  return launch_kernel(kernel_of(mode, a.group, a.page_size, tiles), a, mode, s);
+}
+
+template <int P>
+static Kern rows_kernel(int tiles) {
+  return tiles == 4 ? attend_q4_dense_kernel<P, 4, 1, true> : attend_q4_dense_kernel<P, 1, 1, true>;
+}
+
+cudaError_t launch_attend_q4_rows(const AttendArgs& a, int tiles, cudaStream_t s) {
+  return launch_kernel(a.page_size == 16 ? rows_kernel<16>(tiles) : rows_kernel<64>(tiles), a, kAttendDense, s);
 }
 
 }  // namespace locks

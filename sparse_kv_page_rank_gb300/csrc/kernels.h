@@ -83,6 +83,10 @@ struct AttendArgs {
   const uint16_t* v_pool16;
   int32_t* sel_pages_out;     // fused mode: the page list it selected, [B*Hkv][k_max] (as locks_select)
   int32_t* sel_count_out;     // fused mode: [B*Hkv]
+  // newest tokens of LOCKS_KV_Q4 pages only (launch_attend_q4_rows)
+  const int32_t* cu_tokens;   // [B+1], or null: one token each
+  int64_t q_stride;
+  int total, max_tokens;
   unsigned long long* trace_cta;  // tracing builds only: per-CTA timestamps [B*Hkv][n_splits][16], or null
 };
 
@@ -169,8 +173,12 @@ cudaError_t launch_read(const KvReadArgs& a, cudaStream_t s);
 // Attention over a LOCKS_KV_Q4 cache, one query token per sequence.  `tiles`:
 // 4 for many 16-token tiles per warp and turn, 1 where a CTA has few pages.
 // Page list: a.cluster = a.n_splits CTAs per problem.  Every page: a.n_splits CTAs in
-// all, a.part_* hold two partials per CTA, a.counters B*Hkv + two tickets per CTA.
+// all, a.part_* hold two partials per CTA, a.counters three tickets per CTA.
 cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStream_t s);
+// The newest tokens of each sequence over every page, for few of them: blocks of
+// kQ4RowColumns (token, head) rows; partials of that many columns.
+cudaError_t launch_attend_q4_rows(const AttendArgs& a, int tiles, cudaStream_t s);
+constexpr int kQ4RowColumns = 8;
 // Clusters of cs CTAs of the page-list kernel that the device holds at once.
 int attend_q4_active_clusters(int group, int page_size, int tiles, int cs);
 constexpr int kQ4CtasPerSm = 2;

@@ -260,3 +260,58 @@ def test_strided_queries():
     wide = torch.randn(300, 8, D, generator=case.gen).bfloat16().cuda()
     out, lse = rt.prompt_attend(wide[:, 2:6], cu_tokens=cu_of([300]))
     check(case, [300], wide[:, 2:6], out, lse)
+
+
+@pytest.mark.parametrize("P,hq,hkv,lens,new", [
+    # the last 64 tokens hold keys of the newest rows only: a part of the work in which
+    # the other rows see nothing
+    (64, 8, 2, [64 * 40 + 3], [5]),
+    (16, 8, 2, [64 * 3 + 1, 17, 5], [8, 2, 5]),
+    (64, 1, 1, [32], [32]),
+    (16, 1, 1, [31, 64, 0, 33], [31, 1, 0, 32]),
+    (64, 6, 2, [500] * 37, [1, 2, 3, 4, 5, 6, 7, 8, 9, 10] * 3 + [0, 10, 1, 9, 2, 8, 3]),
+    (16, 16, 1, [30000], [2]),
+    (64, 12, 1, [9000, 65], [1, 2]),
+])
+def test_few_rows_of_4_bit_pages(P, hq, hkv, lens, new):
+    """A few (token, head) rows of a KV head, in blocks of eight columns."""
+    case = Case(lens, hq, hkv, P, "q4", seed=P + sum(lens))
+    rt, total = case.runtime(), sum(new)
+    for _ in range(2):
+        q = case.query(total + 1, spread=1.5)
+        out = torch.full((total + 1, hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((total + 1, hq), 7.0, device="cuda")
+        rt.prompt_attend(q, cu_tokens=cu_of(new), max_tokens=max(new), out=out, lse=lse)
+        assert rt.device_error() == 0
+        check(case, new, q, out, lse)
+        assert (out[total:] == 7).all() and (lse[total:] == 7).all()
+
+
+@pytest.mark.parametrize("P,at", [(64, 397), (16, 399), (64, 395), (16, 384)])
+@pytest.mark.parametrize("part", ["k", "v"])
+def test_a_nan_scale_of_a_draft_token_stays_out_of_earlier_rows(P, at, part):
+    case = Case([400], 2, 1, P, "q4", seed=3)
+    block = case.k[int(case.table[0, at // P]), 0]
+    slot, u = at % P, at % 16
+    for j in range(4):
+        off = (64 * P + 128 * (slot // 16) + 8 * u + 2 * j if part == "k" else
+               136 * P + 128 * (slot // 16) + 32 * (u % 8 // 2) + 16 * (u // 8) + 4 * j + 2 * (u % 2))
+        block[off:off + 2] = torch.tensor([0xff, 0x7f], dtype=torch.uint8)
+    rt, q = case.runtime(), case.query(16)
+    out, lse = rt.prompt_attend(q, cu_tokens=cu_of([16]))
+    assert rt.device_error() == 0
+    check(case, [16], q, out, lse, first_bad=(0, at))
+
+
+@pytest.mark.parametrize("new", [3, 16])
+def test_strided_queries_of_few_rows(new):
+    """Query rows of a wider matrix, as a fused projection writes them."""
+    case = Case([777], 2, 1, 64, "q4", seed=new)
+    wide = torch.randn(new, 4 * D, device="cuda").bfloat16()
+    q = wide[:, D:3 * D].view(new, 2, D)
+    rt = case.runtime()
+    out, lse = rt.prompt_attend(q, cu_tokens=cu_of([new]))
+    assert rt.device_error() == 0
+    check(case, [new], q, out, lse)
+    same, _ = rt.prompt_attend(q.contiguous(), cu_tokens=cu_of([new]))
+    assert torch.equal(out, same)
