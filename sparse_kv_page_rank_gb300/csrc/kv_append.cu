@@ -6,9 +6,7 @@
 // depends on how a compiler contracts the sum; the result is rounded to bf16,
 // the precision of the queries and of a bf16 page), values pass unchanged, and
 // keys and values go to their page's slot.  A 4-bit page holds, for each 32
-// dimensions of those bf16 numbers, s = half(max|x| / 7) and rint(x / s): the
-// quotients are IEEE divisions of a bf16 by a half, whose distance from a tie is
-// either zero or far above their rounding, so the codes are the exact ones.
+// dimensions of those bf16 numbers, s = half(max|x| / 7) and rint(x / s), exactly.
 //
 // What bounds it: bytes (a token is read once and written once) for prompts, and
 // one round trip of dependent loads (lengths, block table, table row, data) plus
@@ -16,7 +14,7 @@
 //
 // Split: 16 threads take a row of 128 elements, 8 (16 bytes) each, so a thread's
 // dimensions, and with them its cosines and sines, are the same for every row of a
-// token.  The partner of a (d, d + rot/2) pair is read a second time, from L1.  A
+// token.  The partner of a (d, d + rot/2) pair is another thread's of the row.  A
 // 32-dimension group is 4 neighbouring threads, whose maximum takes two shuffles.  A
 // prompt's token is one warp's, which has four pairs of rows in flight while it finds
 // the token's place; a decode step's few tokens are a CTA's each, whose eight warps
@@ -88,38 +86,42 @@ __device__ __forceinline__ TokenPlace token_place(const KvTokenArgs& a, int t, b
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// This thread's 8 cosines and sines (dimensions 8 ch .. 8 ch + 7).
+// This thread's cosines and sines, for two dimensions at a time; the sines carry the
+// sign of their product: y = x c + mate s.
 struct Turn {
-  float c[8], s[8];
+  uint64_t c[4], s[4];
 };
 
-// 8 elements of a row, rotated.  half pairs: `mate` holds the partners and
-// `upper` says that these are the second ones (b' = b c + a s).
-__device__ __forceinline__ uint4 rotate8(uint4 x, uint4 mate, const Turn& tr, bool interleaved, bool upper) {
-  uint32_t in[4] = {x.x, x.y, x.z, x.w}, mt[4] = {mate.x, mate.y, mate.z, mate.w}, out[4];
+// 8 elements of a row, rotated.  PAIRS_NEXT: pairs are neighbours, else `mate` holds
+// the partners.
+template <bool PAIRS_NEXT>
+__device__ __forceinline__ uint4 rotate8(uint4 x, uint4 mate, const Turn& tr) {
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w}, mt[4] = {mate.x, mate.y, mate.z, mate.w};
+  uint32_t out[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float v0 = bf16_lo(in[k]), v1 = bf16_hi(in[k]);
-    float y0, y1;
-    if (interleaved) {
-      y0 = __fsub_rn(__fmul_rn(v0, tr.c[k]), __fmul_rn(v1, tr.s[k]));
-      y1 = __fadd_rn(__fmul_rn(v1, tr.c[k]), __fmul_rn(v0, tr.s[k]));
-    } else {
-      const float m0 = bf16_lo(mt[k]), m1 = bf16_hi(mt[k]);
-      const float p0 = __fmul_rn(v0, tr.c[2 * k]), r0 = __fmul_rn(m0, tr.s[2 * k]);
-      const float p1 = __fmul_rn(v1, tr.c[2 * k + 1]), r1 = __fmul_rn(m1, tr.s[2 * k + 1]);
-      y0 = upper ? __fadd_rn(p0, r0) : __fsub_rn(p0, r0);
-      y1 = upper ? __fadd_rn(p1, r1) : __fsub_rn(p1, r1);
-    }
-    out[k] = pack_bf16(y0, y1);
+    const uint64_t m = PAIRS_NEXT ? f32x2(v1, v0) : f32x2(bf16_lo(mt[k]), bf16_hi(mt[k]));
+    // the sums one by one: of packed products and a packed sum the compiler makes one
+    // operation with one rounding less
+    float a0, a1, b0, b1;
+    unpack_f32x2(mul_f32x2(f32x2(v0, v1), tr.c[k]), a0, a1);
+    unpack_f32x2(mul_f32x2(m, tr.s[k]), b0, b1);
+    out[k] = pack_bf16(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // The 4-bit form of 8 elements of a row: code + 8 of each, and the group's scale
 // (the same in the 4 threads of a 32-dimension group).
-__device__ __forceinline__ __half quantise8(uint4 x, int (&u)[8]) {
-  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+//
+// rint(x / s) without a division per element: 200 + x fl(1/s), rounded once to a
+// multiple of 2^-16, is off by less than 2^-16.  A bf16 x and a half s have x / s either
+// exactly at a tie k + 1/2 or at least 2^-12 away from it (2x - (2k+1) s is a multiple of
+// the lowest bit of s, and s has 11), so this neither crosses a tie nor leaves one, and
+// 200 is even: rounding the sum to an integer, ties to even, gives 200 + rint(x / s).
+__device__ __forceinline__ __half quantise8(uint4 x, uint32_t (&u)[8]) {
+  uint32_t in[4] = {x.x, x.y, x.z, x.w};
   uint32_t m = 0;  // max |x| as bf16 bits, whose order is the numbers'
 #pragma unroll
   for (int k = 0; k < 4; ++k) m = max(m, max(in[k] & 0x7fffu, (in[k] >> 16) & 0x7fffu));
@@ -131,26 +133,26 @@ __device__ __forceinline__ __half quantise8(uint4 x, int (&u)[8]) {
   const __half s = finite ? __float2half_rn(fminf(__fdiv_rn(__uint_as_float(m << 16), 7.f), 9352.f))
                           : __ushort_as_half((unsigned short)0x7fff);
   const float sf = __half2float(s);
+  const float r = finite && sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float v = k & 1 ? bf16_hi(in[k / 2]) : bf16_lo(in[k / 2]);
-    int c = 0;
-    if (finite && sf > 0.f) c = (int)rintf(fminf(fmaxf(__fdiv_rn(v, sf), -7.f), 7.f));
-    u[k] = c + 8;
+    const float v = finite ? (k & 1 ? bf16_hi(in[k / 2]) : bf16_lo(in[k / 2])) : 0.f;
+    const float y = fminf(fmaxf(__fmaf_rn(v, r, 200.f), 193.f), 207.f);
+    u[k] = __float_as_uint(__fadd_rn(y, 12582912.f)) & 15u;  // 1.5 2^23: the low bits are the integer
   }
   return s;
 }
 
 // Stores of dimensions 8 ch .. 8 ch + 7 of a token in its 4-bit block (u: code + 8).
-__device__ __forceinline__ void put_k_q4(uint8_t* block, int P, int slot, int ch, const int (&u)[8], __half s) {
+__device__ __forceinline__ void put_k_q4(uint8_t* block, int P, int slot, int ch, const uint32_t (&u)[8], __half s) {
   uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w |= (uint32_t)u[e] << (4 * (e / 2) + 16 * (e % 2));
+  for (int e = 0; e < 8; ++e) w |= u[e] << (4 * (e / 2) + 16 * (e % 2));
   const int j = ch >> 2, c = ch & 3;
   *reinterpret_cast<uint32_t*>(block + 64 * slot + 16 * c + 4 * j) = w;
   if (c == 0) *reinterpret_cast<__half*>(block + 64 * P + 8 * slot + 2 * j) = s;
 }
-__device__ __forceinline__ void put_v_q4(uint8_t* block, int P, int slot, int ch, const int (&u)[8], __half s) {
+__device__ __forceinline__ void put_v_q4(uint8_t* block, int P, int slot, int ch, const uint32_t (&u)[8], __half s) {
   const int j = ch >> 2, tile = slot >> 4, t = slot & 15;
   uint8_t* base = block + 72 * P + 1024 * tile + 512 * (t >> 3) + 16 * ((t & 7) >> 1) + 4 * j + 2 * (t & 1);
 #pragma unroll
@@ -162,36 +164,38 @@ __device__ __forceinline__ void put_v_q4(uint8_t* block, int P, int slot, int ch
                                2 * (t & 1)) = s;
 }
 
-// WPT: warps of a token (1 or 8).
-template <bool Q4, int WPT>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppendArgs a) {
+// WPT: warps of a token (1 or 8).  A step is two rows, either of keys and values (an
+// even number together) or of queries.
+template <bool Q4, int WPT, bool PAIRS_NEXT>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvAppendArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kAppendWarps / WPT) + warp / WPT;
-  const int ch = lane % kRowThreads, r0 = warp % WPT * 2 + lane / kRowThreads;
+  const int ch = lane % kRowThreads, sub = lane / kRowThreads;
   pdl_wait();
   pdl_launch_dependents();
   if (t >= a.tok.total) return;
   const int hkv = a.tok.num_kv_heads, P = a.tok.page_size;
   const int half = a.rotary_dim / 2, d0 = 8 * ch;
   const bool turns = d0 < a.rotary_dim;
-  const bool upper = !a.interleaved && d0 >= half;
+  const bool upper = !PAIRS_NEXT && d0 >= half;
   // rows of the token: keys, values, then queries
-  const int rows = 2 * hkv + (a.q ? a.num_q_heads : 0);
+  const int rows = 2 * hkv + (a.q ? a.num_q_heads : 0), steps = (rows + 1) / 2;
   const uint16_t* kr = a.k + (size_t)t * a.k_stride + d0;
   const uint16_t* vr = a.v + (size_t)t * a.v_stride + d0 - hkv * kHeadDim;
   const uint16_t* qr = a.q + (size_t)t * a.q_stride + d0 - 2 * hkv * kHeadDim;
-  const int to_mate = upper ? -half : half;
-  uint4 x[kInFlight], mate[kInFlight];
-  auto load = [&](int r) {
+  // the lane with the partners of this one's elements (rotary_dim / 2 is a multiple of 8)
+  const int mate_lane = !turns ? lane : upper ? lane - half / 8 : lane + half / 8;
+  uint4 x[kInFlight];
+  auto load = [&](int i) {
 #pragma unroll
-    for (int k = 0; k < kInFlight; ++k, r += 2 * WPT) {
-      if (r >= rows) continue;
-      const uint16_t* src = (r < hkv ? kr : (r < 2 * hkv ? vr : qr)) + r * kHeadDim;
-      x[k] = *reinterpret_cast<const uint4*>(src);
-      if (turns && !a.interleaved && (r < hkv || r >= 2 * hkv)) mate[k] = *reinterpret_cast<const uint4*>(src + to_mate);
+    for (int k = 0; k < kInFlight; ++k, i += WPT) {
+      const int r = 2 * i + sub;
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (r < rows) x[k] = *reinterpret_cast<const uint4*>((i >= hkv ? qr : r < hkv ? kr : vr) + r * kHeadDim);
     }
   };
-  load(r0);  // under way while the token's place is looked up
+  const int i0 = warp % WPT;
+  load(i0);  // under way while the token's place is looked up
   const bool says = lane == 0 && warp % WPT == 0;
   const TokenPlace tp = token_place(a.tok, t, says);
   if (!tp.ok) return;
@@ -203,47 +207,63 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvAppendAr
       return;
     }
     if (turns) {
-      const float* cs = a.rope + (size_t)row * a.rotary_dim + (a.interleaved ? d0 / 2 : (upper ? d0 - half : d0));
+      const float* cs = a.rope + (size_t)row * a.rotary_dim + (PAIRS_NEXT ? d0 / 2 : (upper ? d0 - half : d0));
 #pragma unroll
-      for (int k = 0; k < 8; k += 4) {
-        if (k == 0 || !a.interleaved) {
-          const float4 c = __ldg(reinterpret_cast<const float4*>(cs + k));
-          const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + k));
-          tr.c[k] = c.x, tr.c[k + 1] = c.y, tr.c[k + 2] = c.z, tr.c[k + 3] = c.w;
-          tr.s[k] = s.x, tr.s[k + 1] = s.y, tr.s[k + 2] = s.z, tr.s[k + 3] = s.w;
+      for (int k = 0; k < (PAIRS_NEXT ? 1 : 2); ++k) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(cs) + k);
+        const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half) + k);
+        if constexpr (PAIRS_NEXT) {
+          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            tr.c[e] = f32x2(cc[e], cc[e]);
+            tr.s[e] = f32x2(-ss[e], ss[e]);
+          }
+        } else {
+          const float sign = upper ? 1.f : -1.f;
+          tr.c[2 * k] = f32x2(c.x, c.y);
+          tr.c[2 * k + 1] = f32x2(c.z, c.w);
+          tr.s[2 * k] = f32x2(sign * s.x, sign * s.y);
+          tr.s[2 * k + 1] = f32x2(sign * s.z, sign * s.w);
         }
       }
     }
   }
   const size_t page = (size_t)tp.phys * hkv;
   uint16_t* q_out = a.q_out + (size_t)t * a.q_out_stride + d0 - 2 * hkv * kHeadDim;
-  // both rows of a warp's step exist or end together but for the last one
-  for (int rb = r0; rb - lane / kRowThreads < rows; rb += 2 * WPT * kInFlight) {
-    if (rb != r0) load(rb);
-    // queries may be rotated in place: a row's partners are read before either is written
-    __syncwarp();
+  for (int ib = i0; ib < steps; ib += WPT * kInFlight) {
+    if (ib != i0) load(ib);
 #pragma unroll
     for (int k = 0; k < kInFlight; ++k) {
-      const int r = rb + 2 * WPT * k;
-      const bool in = r < rows, is_kv = r < 2 * hkv, is_v = is_kv && r >= hkv;
-      uint4 y = in ? x[k] : make_uint4(0, 0, 0, 0);
-      if (in && turns && !is_v) y = rotate8(y, mate[k], tr, a.interleaved, upper);
+      const int i = ib + WPT * k;  // the same for the whole warp
+      if (i >= steps) break;
+      const int r = 2 * i + sub;
+      const bool is_v = i < hkv && r >= hkv;
+      uint4 y = x[k], mate = make_uint4(0, 0, 0, 0);
+      if (a.rotary_dim) {
+        if constexpr (!PAIRS_NEXT) {
+          mate.x = __shfl_sync(0xffffffffu, y.x, mate_lane);
+          mate.y = __shfl_sync(0xffffffffu, y.y, mate_lane);
+          mate.z = __shfl_sync(0xffffffffu, y.z, mate_lane);
+          mate.w = __shfl_sync(0xffffffffu, y.w, mate_lane);
+        }
+        if (turns && !is_v) y = rotate8<PAIRS_NEXT>(y, mate, tr);
+      }
+      if (i >= hkv) {
+        if (r < rows) *reinterpret_cast<uint4*>(q_out + (size_t)r * kHeadDim) = y;
+        continue;
+      }
       const size_t ph = page + (is_v ? r - hkv : r);
       if (Q4) {
-        // the shuffles of the quantiser are a whole warp's, whose two rows may be of
-        // different kinds
-        if (__any_sync(0xffffffffu, in && is_kv)) {
-          uint8_t* block = reinterpret_cast<uint8_t*>(a.k_pool) + ph * (size_t)LOCKS_KV_Q4_BLOCK_BYTES(P);
-          int u[8];
-          const __half s = quantise8(y, u);
-          if (in && is_kv && !is_v) put_k_q4(block, P, tp.slot, ch, u, s);
-          if (in && is_v) put_v_q4(block, P, tp.slot, ch, u, s);
-        }
-      } else if (in && is_kv) {
+        uint8_t* block = reinterpret_cast<uint8_t*>(a.k_pool) + ph * (size_t)LOCKS_KV_Q4_BLOCK_BYTES(P);
+        uint32_t u[8];
+        const __half s = quantise8(y, u);
+        if (is_v) put_v_q4(block, P, tp.slot, ch, u, s);
+        else put_k_q4(block, P, tp.slot, ch, u, s);
+      } else {
         uint16_t* pool = reinterpret_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool);
         *reinterpret_cast<uint4*>(pool + (ph * P + tp.slot) * kHeadDim + d0) = y;
       }
-      if (in && !is_kv) *reinterpret_cast<uint4*>(q_out + (size_t)r * kHeadDim) = y;
     }
   }
 }
@@ -299,8 +319,11 @@ __global__ void __launch_bounds__(kAppendThreads) read_kernel(const KvReadArgs a
   }
 }
 
-// A CTA per token while that many CTAs are resident at once (eight per SM), so that a
-// decode step takes one round of loads; beyond that a warp per token.
+// A CTA per token for so few that they take one or two rounds of resident CTAs (four
+// per SM), so that a decode step takes one round of loads; beyond that a warp per token,
+// which has one wait for its place per token and not eight.  32 + 8 heads, bf16, in us
+// (CTA, warp): 8 tokens 2.7, 7.2; 608 tokens 4.0, 7.4; 1216 tokens 6.8, 7.5; 2432 tokens
+// 12.1, 9.1.
 constexpr int kWideTokens = 8 * 152;
 
 template <typename K, typename A>
@@ -322,8 +345,11 @@ cudaError_t launch_tokens(K wide, K narrow, const A& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t s) {
-  return a.tok.q4 ? launch_tokens(append_kernel<true, 8>, append_kernel<true, 1>, a, s)
-                  : launch_tokens(append_kernel<false, 8>, append_kernel<false, 1>, a, s);
+  if (a.interleaved)
+    return a.tok.q4 ? launch_tokens(append_kernel<true, 8, true>, append_kernel<true, 1, true>, a, s)
+                    : launch_tokens(append_kernel<false, 8, true>, append_kernel<false, 1, true>, a, s);
+  return a.tok.q4 ? launch_tokens(append_kernel<true, 8, false>, append_kernel<true, 1, false>, a, s)
+                  : launch_tokens(append_kernel<false, 8, false>, append_kernel<false, 1, false>, a, s);
 }
 
 cudaError_t launch_read(const KvReadArgs& a, cudaStream_t s) {
