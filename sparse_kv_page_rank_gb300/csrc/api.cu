@@ -224,12 +224,11 @@ Plan make_plan(const locks_cache_t* c, const locks_params_t* p) {
     off = align_up(off + std::max<size_t>(bytes, 1));
     return o;
   };
-  // partial results of the dense decode, and its tickets
+  // partial results of the dense decode
   const long long parts = is_q4(c) ? 2LL * pl.q4_dense_ctas : BH * pl.dense_nc;
-  const long long tickets = std::max(BH, 3LL * pl.q4_dense_ctas);
   pl.off_err = take(sizeof(int));
   pl.off_cnt_tk = take(sizeof(unsigned) * BH);
-  pl.off_cnt_att = take(sizeof(unsigned) * tickets);
+  pl.off_cnt_att = take(sizeof(unsigned) * BH);
   pl.off_shat = take(sizeof(float) * BH * c->max_pages * pl.G);
   pl.off_part = take(sizeof(float2) * BH * pl.n_scan * pl.G);
   pl.off_ckey = take(sizeof(uint32_t) * BH * pl.n_tk * std::max(pl.k_max, 1));
@@ -497,7 +496,6 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
   // The error word, then the counters (problems are split only while there are at
   // most half as many as SMs), in the same place for every shape: one workspace
   // serves calls of different lengths, whose partial results never lie on a counter.
-  const long long counters = std::max(kPromptCounters, 3 * kQ4CtasPerSm * sms);
   if (ctas > kPromptCounters) pl->n_splits = 1;
   size_t parts = pl->n_splits > 1 ? (size_t)ctas * pl->n_splits * 256 : 0;
   if (is_q4(c) && (long long)t->max_tokens * G <= kFewRows) {
@@ -510,7 +508,7 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
   }
   size_t off = kAlign;
   pl->off_counters = off;
-  off = align_up(off + sizeof(unsigned) * counters);
+  off = align_up(off + sizeof(unsigned) * kPromptCounters);
   pl->off_ml = off;
   off = align_up(off + sizeof(float2) * parts);
   pl->off_o = off;
@@ -821,7 +819,6 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
     r.lse = lse;
     r.part_o = at<float>(ws, pl.off_o);
     r.part_ml = at<float2>(ws, pl.off_ml);
-    r.counters = at<unsigned>(ws, pl.off_counters);
     r.err = at<int>(ws, 0);
     r.batch = cache->batch;
     r.num_kv_heads = cache->num_kv_heads;

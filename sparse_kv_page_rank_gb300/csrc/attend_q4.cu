@@ -46,10 +46,10 @@
 // Work split.  Over every page: the 64-token slots of all sequences and heads in one
 // line, cut into equal parts, one per CTA (two CTAs per SM), so that ragged lengths and
 // any number of problems fill every SM.  A CTA whose part ends inside a problem writes
-// its partial (R, sum, O) to the workspace; the last CTA of a problem to finish joins
-// them (in two levels where they would be many).  Over a page list, a few pages of
-// each problem: one thread-block cluster per problem, whose CTAs push their partial
-// states to each other through distributed shared memory.
+// its partial (R, sum, O) to the workspace, and a second, dependent kernel joins them.
+// Over a page list, a few pages of each problem: one thread-block cluster per problem,
+// whose CTAs push their partial states to each other through distributed shared memory.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -70,11 +70,10 @@ constexpr int kRecvMl = 16 * 16 * 8;                     // (R, sum) received fr
 constexpr int kSmem = kRing + 128;
 
 struct Q4Shared {
-  uint64_t full[kW][kWarpTiles], recv, join;
+  uint64_t full[kW][kWarpTiles], recv;
   int len[kW][kWarpTiles][4], lp[kW][kWarpTiles];
   float m[kW][16], l[kW][16], f[kW][16];
   float cta_m[16], cta_l[16];
-  int last;
 };
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -597,89 +596,14 @@ __device__ __forceinline__ void store_result(const AttendArgs& a, size_t row, in
 // up to 8 NT of their (token, head) rows as columns; its blocks of rows follow each other
 // in the line, so that they read the pages at about the same time.
 // Partial results a.part_ml, a.part_o: two per CTA (its first problem, which another
-// CTA began, and the one it begins itself), [2 CTA + begins][G or 8 NT].  Tickets
-// a.counters: per CTA one for the problem that it begins and does not finish, then two
-// for groups of partials.
-constexpr int kJoinBytes = 80 * 1024;  // partials one CTA reads at a time
-
-// Joins n partials of G columns (the first in slot s0, the others in s1, s1 + step, ...;
-// slots of `pitch` columns) into the result rows row(column) or, if not `final`, into the
-// first slot.  The outputs come into shared memory as bulk copies, all in flight at
-// once, while the weights are made.
-template <typename Row>
-__device__ void join_partials(const AttendArgs& a, Q4Shared& sh, uint8_t* ring, int n, size_t s0, size_t s1, size_t step,
-                              int G, int pitch, bool final, Row row, int& phase) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto slot = [&](int i) { return (i == 0 ? s0 : s1 + step * (size_t)(i - 1)) * pitch; };
-  const float* po = reinterpret_cast<const float*>(ring);  // [at_once][G][128]
-  float* f = reinterpret_cast<float*>(ring + kJoinBytes);  // [n][G]: at most two per SM and 16 heads
-  static_assert(kJoinBytes + 16 * 4 * 448 <= kRing, "weights of 448 partials");
-  const int at_once = kJoinBytes / (G * kHeadDim * 4);
-  auto ask = [&](int i0) {  // warp 0: partials i0 .. i0 + at_once - 1
-    const int m = min(at_once, n - i0);
-    if (lane == 0) mbar_arrive_expect_tx(&sh.join, (uint32_t)(m * G * kHeadDim * 4));
-    __syncwarp();
-    for (int i = lane; i < m; i += 32)
-      bulk_load(smem_u32(ring) + i * G * kHeadDim * 4, a.part_o + slot(i0 + i) * kHeadDim, G * kHeadDim * 4, &sh.join);
-  };
-  // the partials were written with ordinary stores (here: the ring too)
-  asm volatile("fence.proxy.async;\n" ::: "memory");
-  __syncthreads();
-  if (warp == 0) ask(0);
-  for (int h = warp; h < G; h += kW) {
-    float M = -INFINITY, Ls = 0.f;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.part_ml + slot(i) + h).x);
-    M = warp_max(M);
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = __ldcg(a.part_ml + slot(i) + h);
-      const float e = M == -INFINITY ? 1.f : fast_exp2(ml.x - M);
-      Ls = fmaf(ml.y, e, Ls);
-      f[i * G + h] = e;
-    }
-    Ls = warp_sum(Ls);
-    if (lane == 0) {
-      sh.cta_m[h] = M;
-      sh.cta_l[h] = Ls;
-    }
-  }
-  constexpr int kPairs = 16 * kHeadDim / 2 / kThreads + 1;
-  float2 O[kPairs];
+// CTA began, and the one it begins itself), [2 CTA + begins][G or 8 NT].  A second kernel
+// joins those of a problem, each column on its own.  (The last CTA of a problem to finish
+// did it before, alone, in two levels: 17 of 110 us for 16 heads and 152 CTAs per
+// problem, which now take 95; one head over 4096 tokens took 10.3 us, now 6.4.)
+__device__ __forceinline__ int warp_sum_int(int v) {
 #pragma unroll
-  for (int k = 0; k < kPairs; ++k) O[k] = make_float2(0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += at_once) {
-    const bool ok = mbar_wait(&sh.join, phase);
-    phase ^= 1;
-    if (!ok && tid == 0) set_error(a.err, kDevErrTimeout);
-    __syncthreads();  // and the weights are there
-    const int m = min(at_once, n - i0);
-#pragma unroll
-    for (int k = 0; k < kPairs; ++k) {
-      const int e = 2 * (tid + k * kThreads);
-      if (e >= G * kHeadDim) break;
-#pragma unroll 4
-      for (int i = 0; i < m; ++i) {
-        const float2 y = *reinterpret_cast<const float2*>(po + (size_t)i * G * kHeadDim + e);
-        const float x = f[(i0 + i) * G + e / kHeadDim];
-        O[k].x = fmaf(y.x, x, O[k].x);
-        O[k].y = fmaf(y.y, x, O[k].y);
-      }
-    }
-    __syncthreads();  // read, before it is overwritten
-    if (warp == 0 && i0 + at_once < n) ask(i0 + at_once);
-  }
-#pragma unroll
-  for (int k = 0; k < kPairs; ++k) {
-    const int e = 2 * (tid + k * kThreads);
-    if (e >= G * kHeadDim) break;
-    const int h = e / kHeadDim, col = e % kHeadDim;
-    if (final) {
-      store_result(a, row(h), col, O[k].x, sh.cta_m[h], sh.cta_l[h]);
-      store_result(a, row(h), col + 1, O[k].y, sh.cta_m[h], sh.cta_l[h]);
-    } else {
-      *reinterpret_cast<float2*>(a.part_o + slot(0) * kHeadDim + e) = O[k];
-      if (col == 0) a.part_ml[slot(0) + h] = make_float2(sh.cta_m[h], sh.cta_l[h]);
-    }
-  }
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
 }
 
 struct Q4Seq {
@@ -713,6 +637,77 @@ __device__ __forceinline__ Q4Seq sequence(const AttendArgs& a, int b, bool says)
   return s;
 }
 
+// The line of all slots: sequence by sequence, head by head, block of COLS rows by block.
+template <int P, bool ROWS, int COLS>
+struct Q4Line {
+  const AttendArgs& a;
+  long long total = 0, C = 1;  // slots, and the CTAs that have a part of them
+  // the sequence at hand: its first slot, slots per problem, problems per head
+  int b = 0, nb = 0, n_blocks = 1;
+  long long first = 0;
+  Q4Seq q = {};
+
+  __device__ __forceinline__ explicit Q4Line(const AttendArgs& args) : a(args) {}
+  __device__ __forceinline__ int blocks_of(const Q4Seq& s) const { return ROWS ? (s.n * a.group + COLS - 1) / COLS : 1; }
+  __device__ __forceinline__ int slots_of(int i, bool says) const {  // per head
+    const Q4Seq s = sequence<P, ROWS>(a, i, says);
+    return (s.keys + kPage - 1) / kPage * blocks_of(s);
+  }
+  // Whole warps: all slots, and those before sequence `until`.
+  __device__ __forceinline__ long long measure(int ctas, int until, bool says) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int i = b0 + lane;
+      const int n = i < a.batch ? slots_of(i, says) : 0;
+      total += warp_sum_int(n);
+      before += warp_sum_int(i < until ? n : 0);
+    }
+    total *= a.num_kv_heads;
+    // with fewer slots than CTAs the last CTAs get none, so that no part is empty
+    C = min((long long)ctas, max(total, 1LL));
+    return before * a.num_kv_heads;
+  }
+  __device__ __forceinline__ long long begin(long long cta) const { return cta < C ? total * cta / C : total; }
+  // the CTA whose part holds slot y
+  __device__ __forceinline__ long long owner(long long y) const { return ((y + 1) * C - 1) / total; }
+  __device__ __forceinline__ void load() {
+    q = sequence<P, ROWS>(a, b, false);
+    n_blocks = blocks_of(q);
+    nb = (q.keys + kPage - 1) / kPage;
+  }
+  // Whole warps: past whole blocks of 32 sequences that end before slot y.
+  __device__ __forceinline__ void skip(long long y) {
+    while (b + 32 <= a.batch) {
+      const long long n = (long long)warp_sum_int(slots_of(b + (threadIdx.x & 31), false)) * a.num_kv_heads;
+      if (y < first + n) break;
+      first += n;
+      b += 32;
+    }
+  }
+  // The sequence that holds slot y (from the current one on).
+  __device__ __forceinline__ void seek(long long y) {
+    while (b < a.batch) {
+      load();
+      const long long n = (long long)nb * n_blocks * a.num_kv_heads;
+      if (y < first + n) return;
+      first += n;
+      ++b;
+    }
+  }
+  // Problem `prob` of the sequence at hand: its head, first row of the head's, columns.
+  __device__ __forceinline__ int head(int prob) const { return prob / n_blocks; }
+  __device__ __forceinline__ int row0(int prob) const { return ROWS ? prob % n_blocks * COLS : 0; }
+  __device__ __forceinline__ int columns(int prob) const {
+    return ROWS ? min(COLS, q.n * a.group - row0(prob)) : a.group;
+  }
+  // Column x of it: the row in the outputs.
+  __device__ __forceinline__ size_t out_row(int prob, int x) const {
+    const int r = row0(prob) + x, i = ROWS ? r / a.group : 0, e = ROWS ? r % a.group : x;
+    return ((size_t)(q.row0 + i) * a.num_kv_heads + head(prob)) * a.group + e;
+  }
+};
+
 template <int P, int TPU, int NT, bool ROWS>
 __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const AttendArgs a) {
   extern __shared__ __align__(128) uint8_t ring_raw[];
@@ -727,33 +722,16 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const Atte
   Q4Warp<P, TPU, NT, false, ROWS> w(sh, smem_u32(ring), G);
   if (lane == 0) {
     for (int s = 0; s < kWarpTiles; ++s) mbar_init(&sh.full[w.warp][s], 1);
-    if (w.warp == 0) mbar_init(&sh.join, 1);
     fence_mbar_init();
   }
-  int join_phase = 0;
   __syncthreads();
   pdl_wait();
 
-  // all slots in one line: sequence by sequence, head by head, block of rows by block
-  auto blocks_of = [&](const Q4Seq& s) { return ROWS ? (s.n * G + kCols - 1) / kCols : 1; };
-  auto slots_of = [&](int b) {  // per head
-    const Q4Seq s = sequence<P, ROWS>(a, b, blockIdx.x == 0 && tid < 32);
-    return (s.keys + kPage - 1) / kPage * blocks_of(s);
-  };
-  long long total = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    int n = b0 + lane < a.batch ? slots_of(b0 + lane) : 0;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-    total += n;
-  }
-  total *= hkv_n;
-  // with fewer slots than CTAs the last CTAs get none, so that no part is empty
-  const long long C = min((long long)gridDim.x, max(total, 1LL)), cta = blockIdx.x;
-  long long at = cta < C ? total * cta / C : total;
-  const long long end = cta < C ? total * (cta + 1) / C : total;
-  auto owner = [&](long long y) { return ((y + 1) * C - 1) / total; };  // the CTA whose part holds slot y
-
+  Q4Line<P, ROWS, kCols> line(a);
+  const long long cta = blockIdx.x;
+  line.measure(gridDim.x, 0, cta == 0 && tid < 32);
+  long long at = line.begin(cta);
+  const long long end = line.begin(cta + 1);
   if (cta == 0) {
     // sequences without a token have no slots and get their rows here
     for (int b = 0; b < a.batch; ++b) {
@@ -763,56 +741,24 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const Atte
         store_result(a, (size_t)s.row0 * hkv_n * G + e / kHeadDim, e % kHeadDim, 0.f, 0.f, 0.f);
     }
   }
-
-  // the sequence that holds slot `at`, and the line's position of its first slot
-  int b = 0;
-  long long first = 0;
-  Q4Seq q = {};
-  int nb = 0, n_blocks = 1;  // its slots per problem, problems per head
-  auto seek = [&](long long y) {
-    while (b < a.batch) {
-      q = sequence<P, ROWS>(a, b, false);
-      n_blocks = blocks_of(q);
-      nb = (q.keys + kPage - 1) / kPage;
-      if (y < first + (long long)nb * n_blocks * hkv_n) return;
-      first += (long long)nb * n_blocks * hkv_n;
-      ++b;
-    }
-  };
-  {
-    // whole blocks of 32 sequences at a time
-    while (b + 32 <= a.batch) {
-      int n = slots_of(b + lane);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-      if (at < first + (long long)n * hkv_n) break;
-      first += (long long)n * hkv_n;
-      b += 32;
-    }
-  }
+  line.skip(at);
   while (at < end) {
-    seek(at);
-    const int prob = (int)((at - first) / nb), h = prob / n_blocks;
-    const int r0 = ROWS ? prob % n_blocks * kCols : 0;  // its first row of the head's
-    const long long p0 = first + (long long)prob * nb, p1 = p0 + nb;  // its slots in the line
-    const int s0 = (int)(at - p0), s1 = (int)(min(end, p1) - p0);     // this CTA's of them
-    const int L = q.keys, pg0 = s0 * kPPS, pg1 = min(s1 * kPPS, (L + P - 1) / P);
-    const int cols = ROWS ? min(kCols, q.n * G - r0) : G;
-    // the row in the outputs, and its query, of a column
-    auto row = [&](int x) {
-      const int i = ROWS ? (r0 + x) / G : 0, e = ROWS ? (r0 + x) % G : x;
-      return ((size_t)(q.row0 + i) * hkv_n + h) * G + e;
-    };
+    line.seek(at);
+    const int nb = line.nb, prob = (int)((at - line.first) / nb), h = line.head(prob);
+    const long long p0 = line.first + (long long)prob * nb, p1 = p0 + nb;  // its slots in the line
+    const int s0 = (int)(at - p0), s1 = (int)(min(end, p1) - p0);          // this CTA's of them
+    const int L = line.q.keys, pg0 = s0 * kPPS, pg1 = min(s1 * kPPS, (L + P - 1) / P);
+    const int cols = line.columns(prob), r0 = line.row0(prob);
     auto query = [&](int x) {
-      if constexpr (!ROWS) return a.q + row(x) * kHeadDim;
-      return a.q + (size_t)(q.row0 + (r0 + x) / G) * a.q_stride + (size_t)(h * G + (r0 + x) % G) * kHeadDim;
+      if constexpr (!ROWS) return a.q + line.out_row(prob, x) * kHeadDim;
+      return a.q + (size_t)(line.q.row0 + (r0 + x) / G) * a.q_stride + (size_t)(h * G + (r0 + x) % G) * kHeadDim;
     };
     w.group = cols;
-    if constexpr (ROWS) w.set_back([&](int x) { return x < cols ? L - max(0, q.start + (r0 + x) / G + 1) : 0; });
+    if constexpr (ROWS) w.set_back([&](int x) { return x < cols ? L - max(0, line.q.start + (r0 + x) / G + 1) : 0; });
     w.run(reinterpret_cast<const uint8_t*>(a.k_pool16), (size_t)hkv_n * LOCKS_KV_Q4_BLOCK_BYTES(P), h, pg1 - pg0, a.err,
           [&](int i, int& lp, int& phys, int& len) {
             lp = pg0 + i;
-            phys = physical_page(a, b, lp);
+            phys = physical_page(a, line.b, lp);
             // with rows all that follow, against which a column's own end is counted
             len = phys < 0 ? 0 : ROWS ? L - lp * P : min(P, L - lp * P);
           },
@@ -824,50 +770,106 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const Atte
     const float* octa = w.merge(ring);
     if (s0 == 0 && s1 == nb) {
       for (int e = tid; e < cols * kHeadDim; e += kThreads)
-        store_result(a, row(e / kHeadDim), e % kHeadDim, octa[e], sh.cta_m[e / kHeadDim], sh.cta_l[e / kHeadDim]);
+        store_result(a, line.out_row(prob, e / kHeadDim), e % kHeadDim, octa[e], sh.cta_m[e / kHeadDim],
+                     sh.cta_l[e / kHeadDim]);
     } else {
-      // the problem's CTAs c0 .. c1; c0 begins it
-      const long long c0 = owner(p0), c1 = owner(p1 - 1);
       const size_t mine = (2 * (size_t)cta + (s0 == 0 ? 1 : 0)) * pitch;
       for (int e = tid; e < cols * (kHeadDim / 4); e += kThreads)
         reinterpret_cast<float4*>(a.part_o + mine * kHeadDim)[e] = reinterpret_cast<const float4*>(octa)[e];
       if (tid < cols) a.part_ml[mine + tid] = make_float2(sh.cta_m[tid], sh.cta_l[tid]);
-      __threadfence();
-      __syncthreads();
-      const int n = (int)(c1 - c0) + 1;
-      // partials of a group: all of them where they are two loads' worth, else 16
-      const int gs = n <= 2 * (kJoinBytes / (cols * kHeadDim * 4)) ? n : 16;
-      const int i = (int)(cta - c0), grp = i / gs, n_grp = (n + gs - 1) / gs;
-      const size_t g0 = grp == 0 ? 2 * (size_t)c0 + 1 : 2 * ((size_t)c0 + (size_t)grp * gs);
-      const int in_grp = min(gs, n - grp * gs);
-      unsigned* top = a.counters + c0;
-      unsigned* ticket = n_grp == 1 ? top : a.counters + gridDim.x + g0;
-      if (tid == 0) sh.last = atomicAdd(ticket, 1u) == (unsigned)(in_grp - 1);
-      __syncthreads();
-      if (sh.last) {
-        __threadfence();
-        if (tid == 0) *ticket = 0;  // ready for the next call
-        join_partials(a, sh, ring, in_grp, g0, 2 * ((size_t)c0 + (size_t)grp * gs + 1), 2, cols, pitch, n_grp == 1, row,
-                      join_phase);
-        if (n_grp > 1) {
-          __threadfence();
-          __syncthreads();
-          if (tid == 0) sh.last = atomicAdd(top, 1u) == (unsigned)(n_grp - 1);
-          __syncthreads();
-          if (sh.last) {
-            __threadfence();
-            if (tid == 0) *top = 0;
-            join_partials(a, sh, ring, n_grp, 2 * (size_t)c0 + 1, 2 * ((size_t)c0 + gs), 2 * (size_t)gs, cols, pitch, true, row,
-                          join_phase);
-          }
-        }
-      }
     }
     at = p0 + s1;
     // the buffers were written with ordinary stores: before the next copies into them
     fence_proxy_async();
     __syncthreads();
   }
+}
+
+// Joins the partial results of the problems that were cut.  Grid (a.n_joins, columns):
+// problem by problem where there are fewer than CTAs of the other kernel (a.join_blocks
+// blocks of rows per head at most), else the problem that CTA blockIdx.x begins and
+// does not finish.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinFlight = 8;  // partials that a warp loads at once
+
+template <int P, bool ROWS, int COLS>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs a) {
+  __shared__ float so[kJoinWarps][kHeadDim];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
+  // the other kernel's inputs were complete before it let this one begin
+  Q4Line<P, ROWS, COLS> line(a);
+  int prob = 0;
+  long long p0 = 0;
+  bool cut = false;
+  if (a.join_blocks > 0) {
+    const int per_seq = a.num_kv_heads * a.join_blocks;
+    line.b = blockIdx.x / per_seq;
+    prob = blockIdx.x % per_seq;
+    line.first = line.measure(a.n_splits, line.b, false);
+    line.load();
+    if (line.nb > 0 && prob < line.n_blocks * a.num_kv_heads) {
+      p0 = line.first + (long long)prob * line.nb;
+      cut = line.owner(p0) != line.owner(p0 + line.nb - 1);
+    }
+  } else {
+    line.measure(a.n_splits, 0, false);
+    const long long at = line.begin(blockIdx.x), end = line.begin((long long)blockIdx.x + 1);
+    if (at < end) {
+      line.skip(end - 1);
+      line.seek(end - 1);
+      prob = (int)((end - 1 - line.first) / line.nb);
+      p0 = line.first + (long long)prob * line.nb;
+      cut = p0 >= at && p0 + line.nb > end;
+    }
+  }
+  cut = cut && h < line.columns(prob);
+  // also where there is nothing to join: whatever follows may rely on this kernel's end
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!cut) return;
+  const int pitch = ROWS ? COLS : a.group;
+  const int c0 = (int)line.owner(p0), n = (int)line.owner(p0 + line.nb - 1) - c0 + 1;
+  auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * pitch + h; };
+  // a warp takes partials warp, warp + 8, ...; each warp finds the reference of all
+  float M = -INFINITY, L = 0.f;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(a.part_ml + slot(i)).x);
+  M = warp_max(M);
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = warp; i0 < n; i0 += kJoinWarps * kJoinFlight) {
+    float4 v[kJoinFlight];
+    float2 ml[kJoinFlight];
+#pragma unroll
+    for (int k = 0; k < kJoinFlight; ++k) {
+      const int i = i0 + kJoinWarps * k;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ml[k] = make_float2(M, 0.f);
+      if (i >= n) continue;
+      v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * kHeadDim) + lane);
+      ml[k] = __ldcg(a.part_ml + slot(i));
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinFlight; ++k) {
+      const float f = M == -INFINITY ? 1.f : fast_exp2(ml[k].x - M);
+      L = fmaf(ml[k].y, f, L);
+      O.x = fmaf(v[k].x, f, O.x);
+      O.y = fmaf(v[k].y, f, O.y);
+      O.z = fmaf(v[k].z, f, O.z);
+      O.w = fmaf(v[k].w, f, O.w);
+    }
+  }
+  __shared__ float sl[kJoinWarps];
+  *reinterpret_cast<float4*>(&so[warp][4 * lane]) = O;
+  if (lane == 0) sl[warp] = L;
+  __syncthreads();
+  if (threadIdx.x >= kHeadDim) return;
+  float Os = 0.f, Ls = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinWarps; ++k) {
+    Os += so[k][threadIdx.x];
+    Ls += sl[k];
+  }
+  store_result(a, line.out_row(prob, h), threadIdx.x, Os, M, Ls);
 }
 
 // ---- a page list, or the exact page log-sum-exp ------------------------------------
@@ -1065,8 +1067,28 @@ static cudaError_t launch_kernel(Kern k, const AttendArgs& a, int mode, cudaStre
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 
+// After the kernel over every page: `columns` of a problem, `blocks` of rows per head.
+template <bool ROWS, int COLS>
+static cudaError_t launch_join(AttendArgs a, int columns, int blocks, cudaStream_t s) {
+  const long long problems = (long long)a.batch * a.num_kv_heads * blocks;
+  a.join_blocks = problems <= a.n_splits ? blocks : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.join_blocks ? problems : a.n_splits), columns, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return a.page_size == 16 ? cudaLaunchKernelEx(&cfg, join_kernel<16, ROWS, COLS>, a)
+                           : cudaLaunchKernelEx(&cfg, join_kernel<64, ROWS, COLS>, a);
+}
+
 cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStream_t s) {
-  return launch_kernel(kernel_of(mode, a.group, a.page_size, tiles), a, mode, s);
+  const cudaError_t e = launch_kernel(kernel_of(mode, a.group, a.page_size, tiles), a, mode, s);
+  if (e != cudaSuccess || mode != kAttendDense || a.n_splits == 1) return e;
+  return launch_join<false, 8>(a, a.group, 1, s);
 }
 
 template <int P>
@@ -1075,7 +1097,11 @@ static Kern rows_kernel(int tiles) {
 }
 
 cudaError_t launch_attend_q4_rows(const AttendArgs& a, int tiles, cudaStream_t s) {
-  return launch_kernel(a.page_size == 16 ? rows_kernel<16>(tiles) : rows_kernel<64>(tiles), a, kAttendDense, s);
+  const cudaError_t e =
+      launch_kernel(a.page_size == 16 ? rows_kernel<16>(tiles) : rows_kernel<64>(tiles), a, kAttendDense, s);
+  if (e != cudaSuccess || a.n_splits == 1) return e;
+  const int rows = a.max_tokens * a.group;
+  return launch_join<true, kQ4RowColumns>(a, std::min(rows, kQ4RowColumns), (rows + kQ4RowColumns - 1) / kQ4RowColumns, s);
 }
 
 }  // namespace locks

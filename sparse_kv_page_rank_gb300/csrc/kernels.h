@@ -87,6 +87,7 @@ struct AttendArgs {
   const int32_t* cu_tokens;   // [B+1], or null: one token each
   int64_t q_stride;
   int total, max_tokens;
+  int join_blocks;            // set by the launch
   unsigned long long* trace_cta;  // tracing builds only: per-CTA timestamps [B*Hkv][n_splits][16], or null
 };
 
@@ -173,7 +174,7 @@ cudaError_t launch_read(const KvReadArgs& a, cudaStream_t s);
 // Attention over a LOCKS_KV_Q4 cache, one query token per sequence.  `tiles`:
 // 4 for many 16-token tiles per warp and turn, 1 where a CTA has few pages.
 // Page list: a.cluster = a.n_splits CTAs per problem.  Every page: a.n_splits CTAs in
-// all, a.part_* hold two partials per CTA, a.counters three tickets per CTA.
+// all, a.part_* hold two partials per CTA, which a second kernel joins.
 cudaError_t launch_attend_q4(const AttendArgs& a, int mode, int tiles, cudaStream_t s);
 // The newest tokens of each sequence over every page, for few of them: blocks of
 // kQ4RowColumns (token, head) rows; partials of that many columns.
