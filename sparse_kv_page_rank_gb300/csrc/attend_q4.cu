@@ -40,7 +40,9 @@
 // into the warp's own two 64-token buffers (9216 or 4 x 2304 contiguous bytes; with
 // few pages per CTA eight 16-token buffers, so that a page occupies four warps).  A
 // warp waits for its own copies in order and refills a buffer only when it is done
-// with it, so no warp waits for another.  Two CTAs of six warps per SM hold 221 KB of
+// with it, so no warp waits for another.  With 9 to 16 heads a warp works on half a
+// buffer at a time, which is what its registers hold; copies of half pages, in four
+// pieces each, took 95 us for 1M tokens, whole ones 88.  Two CTAs of six warps per SM hold 221 KB of
 // buffers, half of them in flight at any time.
 //
 // Work split.  Over every page: the 64-token slots of all sequences and heads in one
@@ -112,6 +114,9 @@ struct Q4Warp {
   static constexpr int kPages = TP >= TPU ? 1 : TPU / TP;  // pages a unit touches
   static constexpr int kUPP = TP >= TPU ? TP / TPU : 1;    // units of a page
   static constexpr int kBufs = kWarpTiles / TPU;
+  // tiles worked on together: with two blocks of columns the registers hold two tiles' logits
+  static constexpr int kTiles = NT == 2 && !LSE && TPU == 4 ? 2 : TPU;
+  static_assert(kTiles == TPU || 2 * kTiles == TPU, "one or two turns");
   static constexpr int kBufBytes = TPU * kTileBytes;
   // one block of heads has the registers to start its products at the codes' offset
   static constexpr bool kBiased = NT == 1;
@@ -217,18 +222,18 @@ struct Q4Warp {
 
   // One unit in buffer `buf`; WHOLE: every column sees all its tokens, else
   // left[t] counts those of tile t (two copies of the code, so that whole units
-  // carry no masks).
+  // carry no masks).  Tiles t0 .. t0 + kTiles - 1 of the buffer.
   template <bool WHOLE>
-  __device__ __forceinline__ void unit(uint32_t base, int buf, const int (&left)[TPU]) {
-    float sc[TPU][NT][4];
+  __device__ __forceinline__ void unit(uint32_t base, int buf, int t0, const int (&left)[kTiles]) {
+    float sc[kTiles][NT][4];
     float mx[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
     // ---- logits of the unit's tokens (rows g, g + 8 of each tile) ----
 #pragma unroll
-    for (int t = 0; t < TPU; ++t) {
-      const uint4 k0 = lds128(base + At::key_codes(t) + lane * 16), k1 = lds128(base + At::key_codes(t) + 512 + lane * 16);
-      const uint2 s0 = lds64(base + At::key_scales(t) + g * 8), s1 = lds64(base + At::key_scales(t) + 64 + g * 8);
+    for (int t = 0; t < kTiles; ++t) {
+      const uint4 k0 = lds128(base + At::key_codes(t0 + t) + lane * 16), k1 = lds128(base + At::key_codes(t0 + t) + 512 + lane * 16);
+      const uint2 s0 = lds64(base + At::key_scales(t0 + t) + g * 8), s1 = lds64(base + At::key_scales(t0 + t) + 64 + g * 8);
       const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
       const float z0[4] = {f16_lo(s0.x), f16_hi(s0.x), f16_lo(s0.y), f16_hi(s0.y)};
       const float z1[4] = {f16_lo(s1.x), f16_hi(s1.x), f16_lo(s1.y), f16_hi(s1.y)};
@@ -303,7 +308,7 @@ struct Q4Warp {
         for (int k = 0; k < 2; ++k) {
           float ps = 0.f;
 #pragma unroll
-          for (int t = 0; t < TPU; ++t)
+          for (int t = 0; t < kTiles; ++t)
             ps += fast_exp2(fmaf(sc[t][nt][k], fac[nt][k], -mx[nt][k])) +
                   fast_exp2(fmaf(sc[t][nt][2 + k], fac[nt][k], -mx[nt][k]));
           ps += __shfl_xor_sync(0xffffffffu, ps, 4);
@@ -319,8 +324,8 @@ struct Q4Warp {
       // scale below 2^15.  R is moved, and x lowered, only when a token or a scale of
       // the unit breaks that; then the largest weight becomes 2^(x - 4).
       uint32_t top = 0;  // largest scale of this lane's 16 bytes, as half bits
-      if (lane < 8 * TPU) {
-        const int t = lane >> 3;
+      if (lane < 8 * kTiles) {
+        const int t = t0 + (lane >> 3);
         uint4 w = lds128(base + At::value_scales(t) + (lane & 7) * 16);
         if constexpr (!WHOLE) {
           // each word: tokens 8 (lane%2) + (lane%8)/2 2, + 1 of tile t
@@ -360,7 +365,7 @@ struct Q4Warp {
       }
       // ---- weights and the values they weight ----
 #pragma unroll
-      for (int t = 0; t < TPU; ++t) {
+      for (int t = 0; t < kTiles; ++t) {
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -375,8 +380,8 @@ struct Q4Warp {
           pb[nt][0] = transpose8x8(pack_f16(p[0], p[1]));  // tokens 2c, 2c + 1 of head g
           pb[nt][1] = transpose8x8(pack_f16(p[2], p[3]));  // tokens 8 + 2c, + 1
         }
-        const uint4 v0 = lds128(base + At::value_codes(t) + lane * 16), v1 = lds128(base + At::value_codes(t) + 512 + lane * 16);
-        uint4 z0 = lds128(base + At::value_scales(t) + c * 32), z1 = lds128(base + At::value_scales(t) + c * 32 + 16);
+        const uint4 v0 = lds128(base + At::value_codes(t0 + t) + lane * 16), v1 = lds128(base + At::value_codes(t0 + t) + 512 + lane * 16);
+        uint4 z0 = lds128(base + At::value_scales(t0 + t) + c * 32), z1 = lds128(base + At::value_scales(t0 + t) + c * 32 + 16);
         if constexpr (!WHOLE) {
           // scales past the end may be anything, a NaN too
           const uint32_t m0 = pair_mask(2 * c, left[t]), m1 = pair_mask(8 + 2 * c, left[t]);
@@ -483,18 +488,21 @@ struct Q4Warp {
         if (lane == 0) set_error(err, kDevErrTimeout);
         break;
       }
-      // tokens from each tile's first on (one page's, or a page per tile)
-      int left[TPU];
-      bool whole = true, any = false;
-#pragma unroll
-      for (int t = 0; t < TPU; ++t) {
-        left[t] = P == 64 ? sh.len[warp][buf][0] - 16 * t : sh.len[warp][buf][t];
-        whole &= left[t] >= (ROWS ? 16 + back_max : 16);
-        any |= left[t] > 0;
-      }
       const uint32_t base = wbase + buf * kBufBytes;
-      if (whole) unit<true>(base, buf, left);
-      else if (any) unit<false>(base, buf, left);
+#pragma unroll 1
+      for (int t0 = 0; t0 < TPU; t0 += kTiles) {
+        // tokens from each tile's first on (one page's, or a page per tile)
+        int left[kTiles];
+        bool whole = true, any = false;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          left[t] = P == 64 ? sh.len[warp][buf][0] - 16 * (t0 + t) : sh.len[warp][buf][t0 + t];
+          whole &= left[t] >= (ROWS ? 16 + back_max : 16);
+          any |= left[t] > 0;
+        }
+        if (whole) unit<true>(base, buf, t0, left);
+        else if (any) unit<false>(base, buf, t0, left);
+      }
       __syncwarp();  // every lane is done with the buffer
       if (issued < n_mine) {
         if ((issued & 31) == 0) resolve(issued);
@@ -993,10 +1001,10 @@ Kern pick(int group, int tiles) {
     return group <= 8 ? attend_q4_kernel<MODE, P, P / 16, 1> : attend_q4_kernel<MODE, P, P / 16, 2>;
   } else if constexpr (MODE == kAttendSparse) {
     if (group <= 8) return tiles == 4 ? attend_q4_kernel<MODE, P, 4, 1> : attend_q4_kernel<MODE, P, 1, 1>;
-    return tiles == 4 ? attend_q4_kernel<MODE, P, 2, 2> : attend_q4_kernel<MODE, P, 1, 2>;
+    return tiles == 4 ? attend_q4_kernel<MODE, P, 4, 2> : attend_q4_kernel<MODE, P, 1, 2>;
   } else {
     if (group <= 8) return tiles == 4 ? attend_q4_dense_kernel<P, 4, 1, false> : attend_q4_dense_kernel<P, 1, 1, false>;
-    return tiles == 4 ? attend_q4_dense_kernel<P, 2, 2, false> : attend_q4_dense_kernel<P, 1, 2, false>;
+    return tiles == 4 ? attend_q4_dense_kernel<P, 4, 2, false> : attend_q4_dense_kernel<P, 1, 2, false>;
   }
 }
 
