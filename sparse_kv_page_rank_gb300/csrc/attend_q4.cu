@@ -663,13 +663,17 @@ struct Q4Line {
   }
   // Whole warps: all slots, and those before sequence `until`.
   __device__ __forceinline__ long long measure(int ctas, int until, bool says) {
-    const int lane = threadIdx.x & 31;
     long long before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int i = b0 + lane;
-      const int n = i < a.batch ? slots_of(i, says) : 0;
-      total += warp_sum_int(n);
-      before += warp_sum_int(i < until ? n : 0);
+#pragma unroll 4
+    for (int i = threadIdx.x & 31; i < a.batch; i += 32) {
+      const int n = slots_of(i, says);
+      total += n;
+      before += i < until ? n : 0;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, d);
+      before += __shfl_xor_sync(0xffffffffu, before, d);
     }
     total *= a.num_kv_heads;
     // with fewer slots than CTAs the last CTAs get none, so that no part is empty
@@ -740,13 +744,15 @@ __global__ void __launch_bounds__(kThreads, 2) attend_q4_dense_kernel(const Atte
   line.measure(gridDim.x, 0, cta == 0 && tid < 32);
   long long at = line.begin(cta);
   const long long end = line.begin(cta + 1);
-  if (cta == 0) {
-    // sequences without a token have no slots and get their rows here
-    for (int b = 0; b < a.batch; ++b) {
-      const Q4Seq s = sequence<P, ROWS>(a, b, false);
-      if (s.keys > 0) continue;
-      for (int e = tid; e < s.n * hkv_n * G * kHeadDim; e += kThreads)
-        store_result(a, (size_t)s.row0 * hkv_n * G + e / kHeadDim, e % kHeadDim, 0.f, 0.f, 0.f);
+  // sequences without a token have no slots and get their rows here
+  for (int b0 = 32 * blockIdx.x; b0 < a.batch; b0 += 32 * gridDim.x) {
+    Q4Seq s = {};
+    if (b0 + lane < a.batch) s = sequence<P, ROWS>(a, b0 + lane, false);
+    for (uint32_t none = __ballot_sync(0xffffffffu, s.keys == 0 && s.n > 0); none; none &= none - 1) {
+      const int src = __ffs(none) - 1;
+      const int row0 = __shfl_sync(0xffffffffu, s.row0, src), n = __shfl_sync(0xffffffffu, s.n, src);
+      for (int e = tid; e < n * hkv_n * G * kHeadDim; e += kThreads)
+        store_result(a, (size_t)row0 * hkv_n * G + e / kHeadDim, e % kHeadDim, 0.f, 0.f, 0.f);
     }
   }
   line.skip(at);
