@@ -36,7 +36,8 @@ extern "C" {
  *   max_tokens  at least every n_b (host knowledge that shapes the launch; 1
  *               when cu_tokens is NULL).  A sequence with more sets
  *               LOCKS_DEVERR_LENGTHS and its rows past max_tokens are skipped.
- * total = 0 or max_tokens = 0 is a call that does nothing. */
+ * total = 0 (whose arrays may be NULL) or max_tokens = 0 is a call that does
+ * nothing. */
 typedef struct lockskv_tokens {
   const int32_t* cu_tokens;
   int32_t total;
@@ -99,7 +100,10 @@ LOCKS_API locks_status_t lockskv_read(const locks_cache_t* cache, const lockskv_
                                       void* v_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace lockskv_prompt_attend needs for these shapes (at least
- * 256).  Zero it once (locks_workspace_init) before its first use. */
+ * 256).  Zero it once (locks_workspace_init) before its first use; calls of any
+ * shapes that it is large enough for may then share it, one after another.  Two
+ * calls, or replays of two captured graphs, that may run at the same time need
+ * a workspace each. */
 LOCKS_API locks_status_t lockskv_prompt_workspace_size(const locks_cache_t* cache, const locks_params_t* params,
                                                        const lockskv_tokens_t* tokens, size_t* bytes);
 

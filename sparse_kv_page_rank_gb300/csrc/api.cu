@@ -725,6 +725,7 @@ locks_status_t lockskv_append(const locks_cache_t* cache, const lockskv_tokens_t
   if (st != LOCKS_OK) return st;
   if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
   if ((st = check_err_ws(ws, ws_bytes)) != LOCKS_OK) return st;
+  if (tokens->total == 0) return LOCKS_OK;  // an empty array may have no address
   if (!ap || !ap->k || !ap->v || (ap->q == nullptr) != (ap->q_out == nullptr)) return LOCKS_ERR_INVALID_ARG;
   const int64_t kv_row = (int64_t)cache->num_kv_heads * kHeadDim;
   if ((st = check_rows(ap->k, ap->k_stride, kv_row)) != LOCKS_OK) return st;
@@ -741,7 +742,7 @@ locks_status_t lockskv_append(const locks_cache_t* cache, const lockskv_tokens_t
   if ((ap->rotary_dim > 0) != (ap->rope != nullptr)) return LOCKS_ERR_INVALID_ARG;
   if (ap->rope && (ap->rope_rows <= 0 || (reinterpret_cast<uintptr_t>(ap->rope) & 15))) return LOCKS_ERR_INVALID_ARG;
   if ((ap->interleaved & ~1) != 0) return LOCKS_ERR_INVALID_ARG;
-  if (tokens->total == 0 || tokens->max_tokens == 0) return LOCKS_OK;
+  if (tokens->max_tokens == 0) return LOCKS_OK;
   KvAppendArgs a;
   a.tok = token_args(cache, tokens, ws);
   a.k_pool = const_cast<void*>(cache->k_pool);
@@ -769,9 +770,10 @@ locks_status_t lockskv_read(const locks_cache_t* cache, const lockskv_tokens_t* 
   if (st != LOCKS_OK) return st;
   if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
   if ((st = check_err_ws(ws, ws_bytes)) != LOCKS_OK) return st;
+  if (tokens->total == 0) return LOCKS_OK;
   if (!k_out && !v_out) return LOCKS_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15) return LOCKS_ERR_INVALID_ARG;
-  if (tokens->total == 0 || tokens->max_tokens == 0) return LOCKS_OK;
+  if (tokens->max_tokens == 0) return LOCKS_OK;
   KvReadArgs a;
   a.tok = token_args(cache, tokens, ws);
   a.k_pool = cache->k_pool;
@@ -801,12 +803,13 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   if (st != LOCKS_OK) return st;
   if ((st = check_params(cache, params)) != LOCKS_OK) return st;
   if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
+  if (tokens->total == 0) return LOCKS_OK;
   if (!q || !out || (reinterpret_cast<uintptr_t>(out) & 15)) return LOCKS_ERR_INVALID_ARG;
   if ((st = check_rows(q, q_stride, (int64_t)params->num_q_heads * kHeadDim)) != LOCKS_OK) return st;
   PromptPlan pl;
   if ((st = plan_prompt(cache, params, tokens, &pl)) != LOCKS_OK) return st;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) || ws_bytes < pl.total) return LOCKS_ERR_WORKSPACE;
-  if (tokens->total == 0 || tokens->max_tokens == 0) return LOCKS_OK;
+  if (tokens->max_tokens == 0) return LOCKS_OK;
   if (pl.row_ctas > 0) {
     AttendArgs r = {};
     r.q = static_cast<const uint16_t*>(q);

@@ -83,7 +83,9 @@ class LocksRuntime:
         off = (-self.kv_ws.data_ptr()) % 256
         self.kv_ws = self.kv_ws[off:off + 256]
         self.prompt_ws = None
-        self._prompt_need = {}
+        self._prompt_need = {}     # bytes by max_tokens
+        self._prompt_captured = False
+        self._prompt_held = []     # outgrown workspaces that a captured graph may still use
         B = self.batch
         self.sel_pages = torch.zeros((B, hkv, max(self.k_max, 1)), dtype=torch.int32, device=self.device)
         self.sel_count = torch.zeros((B, hkv), dtype=torch.int32, device=self.device)
@@ -142,8 +144,9 @@ class LocksRuntime:
     def _tokens(self, total: int, cu_tokens: torch.Tensor | None, max_tokens: int | None):
         if cu_tokens is None:
             return L.make_tokens(None, total, 1)
-        if cu_tokens.dtype != torch.int32 or cu_tokens.numel() != self.batch + 1 or not cu_tokens.is_contiguous():
-            raise ValueError("cu_tokens must be contiguous int32 [batch + 1]")
+        if (cu_tokens.dtype is not torch.int32 or cu_tokens.numel() != self.batch + 1 or not cu_tokens.is_cuda
+                or not cu_tokens.is_contiguous()):
+            raise ValueError("cu_tokens must be contiguous int32 [batch + 1] on the device")
         return L.make_tokens(cu_tokens, total, total if max_tokens is None else max_tokens)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None, *,
@@ -162,31 +165,31 @@ class LocksRuntime:
         rotates in place), or None without q."""
         shape = k.shape
         total = shape[0]
-        if shape[1] != self.num_kv_heads or v.shape != shape:
-            raise ValueError(f"k and v must be [tokens][{self.num_kv_heads}][128]")
+        if len(shape) != 3 or shape[1] != self.num_kv_heads or v.shape != shape or not (k.is_cuda and v.is_cuda):
+            raise ValueError(f"k and v must be [tokens][{self.num_kv_heads}][128] on the device")
         if q is not None:
             shape = q.shape
-            if shape[0] != total or shape[1] != self.num_q_heads:
-                raise ValueError(f"q must be [{total}][{self.num_q_heads}][128]")
+            if len(shape) != 3 or shape[0] != total or shape[1] != self.num_q_heads or not q.is_cuda:
+                raise ValueError(f"q must be [{total}][{self.num_q_heads}][128] on the device")
             if q_out is None:
                 q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            elif q_out.shape != shape:
-                raise ValueError("q_out must have q's shape")
+            elif q_out.shape != shape or not q_out.is_cuda:
+                raise ValueError("q_out must have q's shape, on the device")
         elif q_out is not None:
             raise ValueError("q_out without q")
         if rope is None:
             rotary_dim = rotary_dim or 0
         else:
-            if rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
-                raise ValueError("rope must be contiguous float32 [positions][rotary_dim]")
+            if rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_cuda or not rope.is_contiguous():
+                raise ValueError("rope must be contiguous float32 [positions][rotary_dim] on the device")
             cols = rope.shape[1]
             if rotary_dim is None:
                 rotary_dim = cols
             elif rotary_dim != cols:
                 raise ValueError("rope must have rotary_dim columns")
-        if positions is not None and (positions.dtype != torch.int32 or positions.numel() != total
-                                      or not positions.is_contiguous()):
-            raise ValueError("positions must be contiguous int32 [tokens]")
+        if positions is not None and (positions.dtype is not torch.int32 or positions.numel() != total
+                                      or not positions.is_cuda or not positions.is_contiguous()):
+            raise ValueError("positions must be contiguous int32 [tokens] on the device")
         L.lockskv_append(self.cache, self._tokens(total, cu_tokens, max_tokens),
                          L.make_append(k, v, q, q_out, rope, rotary_dim, positions, interleaved),
                          self.kv_ws, 256, stream)
@@ -205,27 +208,52 @@ class LocksRuntime:
                       max_tokens: int | None = None, out=None, lse=None, stream=None):
         """Causal attention of the newest tokens, already in the cache, over it:
         q bf16 [total][Hq][128] -> out bf16 [total][Hq][128], lse float32
-        [total][Hq] (new tensors by default)."""
+        [total][Hq] (new tensors by default).
+
+        The workspace grows with the calls and is shared by all of them, so
+        they run one after another; a call is captured into a graph after one
+        of the same max_tokens has run."""
         total = q.shape[0]
-        if q.shape[1] != self.num_q_heads:
-            raise ValueError(f"q must be [tokens][{self.num_q_heads}][128]")
+        if q.dim() != 3 or q.shape[1] != self.num_q_heads or not q.is_cuda:
+            raise ValueError(f"q must be [tokens][{self.num_q_heads}][128] on the device")
         stride = L._row_stride(q, "q")
         tokens = self._tokens(total, cu_tokens, max_tokens)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        elif out.shape != q.shape or out.dtype is not torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
+            raise ValueError("out must be contiguous bf16 of q's shape on the device")
         if lse is None:
             lse = torch.empty((total, self.num_q_heads), dtype=torch.float32, device=self.device)
-        need = self._prompt_need.get((total, tokens.max_tokens))
+        elif (lse.shape != (total, self.num_q_heads) or lse.dtype is not torch.float32 or not lse.is_cuda
+              or not lse.is_contiguous()):
+            raise ValueError(f"lse must be contiguous float32 [{total}][{self.num_q_heads}] on the device")
+        need = self._prompt_need.get(tokens.max_tokens)
         if need is None:
             need = L.lockskv_prompt_workspace_size(self.cache, self.params, tokens)
-            self._prompt_need[(total, tokens.max_tokens)] = need
+            self._prompt_need[tokens.max_tokens] = need
+        capturing = torch.cuda.is_current_stream_capturing()
         if self.prompt_ws is None or self.prompt_ws.numel() < need:
-            ws = torch.zeros(need + 256, dtype=torch.uint8, device=self.device)
-            off = (-ws.data_ptr()) % 256
-            self.prompt_ws = ws[off:off + need]
+            self._grow_prompt_ws(need, capturing)
+        self._prompt_captured |= capturing
         L.lockskv_prompt_attend(self.cache, self.params, tokens, q, stride, out, lse, self.prompt_ws,
                                 self.prompt_ws.numel(), stream)
         return out, lse
+
+    def _grow_prompt_ws(self, need: int, capturing: bool):
+        if capturing:
+            raise RuntimeError("prompt_attend needs a larger workspace: run a call of these sizes before the capture")
+        # calls on any stream may still use the old one, and a captured graph keeps its address
+        torch.cuda.synchronize(self.device)
+        if self._prompt_captured:
+            self._prompt_held.append(self.prompt_ws)
+            self._prompt_captured = False
+        err = 0 if self.prompt_ws is None else L.locks_get_device_error(self.prompt_ws)
+        ws = torch.zeros(need + 256, dtype=torch.uint8, device=self.device)
+        off = (-ws.data_ptr()) % 256
+        self.prompt_ws = ws[off:off + need]
+        if err:
+            self.prompt_ws[:4].view(torch.int32).fill_(err)
+        torch.cuda.synchronize(self.device)
 
     def device_error(self, stream=None) -> int:
         """LOCKS_DEVERR_* bits set since the last read, by the calls on the
@@ -233,4 +261,7 @@ class LocksRuntime:
         (all words are cleared)."""
         err = L.locks_get_device_error(self.ws, stream) | L.locks_get_device_error(self.build_ws, stream)
         err |= L.locks_get_device_error(self.kv_ws, stream)
-        return err | (L.locks_get_device_error(self.prompt_ws, stream) if self.prompt_ws is not None else 0)
+        for ws in [self.prompt_ws, *self._prompt_held]:
+            if ws is not None:
+                err |= L.locks_get_device_error(ws, stream)
+        return err
