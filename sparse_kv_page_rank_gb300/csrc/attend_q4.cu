@@ -608,12 +608,6 @@ __device__ __forceinline__ void store_result(const AttendArgs& a, size_t row, in
 // joins those of a problem, each column on its own.  (The last CTA of a problem to finish
 // did it before, alone, in two levels: 17 of 110 us for 16 heads and 152 CTAs per
 // problem, which now take 95; one head over 4096 tokens took 10.3 us, now 6.4.)
-__device__ __forceinline__ int warp_sum_int(int v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
-}
-
 struct Q4Seq {
   int keys;             // that its newest token sees
   int row0, n, start;   // its query tokens: first row, number, position of the first
@@ -688,12 +682,26 @@ struct Q4Line {
     n_blocks = blocks_of(q);
     nb = (q.keys + kPage - 1) / kPage;
   }
-  // Whole warps: past whole blocks of 32 sequences that end before slot y.
+  // Whole warps: to the sequence that holds slot y, 32 at a time.
   __device__ __forceinline__ void skip(long long y) {
-    while (b + 32 <= a.batch) {
-      const long long n = (long long)warp_sum_int(slots_of(b + (threadIdx.x & 31), false)) * a.num_kv_heads;
-      if (y < first + n) break;
-      first += n;
+    const int lane = threadIdx.x & 31;
+    while (b < a.batch) {
+      // slots of this lane's sequence and those of the 32 before it
+      long long upto = b + lane < a.batch ? (long long)slots_of(b + lane, false) * a.num_kv_heads : 0;
+      const long long own = upto;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const long long other = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += other;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, y < first + upto);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        b += at;
+        first += __shfl_sync(0xffffffffu, upto - own, at);
+        return;
+      }
+      first += __shfl_sync(0xffffffffu, upto, 31);
       b += 32;
     }
   }
