@@ -460,7 +460,6 @@ locks_status_t check_err_ws(void* ws, size_t bytes) {
 }
 
 // Launch shape and workspace of lockskv_prompt_attend.
-constexpr long long kPromptCounters = 1024;
 // 4-bit pages: up to this many (token, head) rows of a KV head take the kernel for one
 // query token, kQ4RowColumns at a time; a pass over the pages per eight rows, against
 // one of the tensor cores' kernel, whose softmax and conversion cost the same for 8
@@ -475,7 +474,7 @@ struct PromptPlan {
   int n_qtiles = 1, n_splits = 1, plane_rows = 0;
   bool planes = false;
   int row_ctas = 0, row_tiles = 0;  // few rows of 4-bit pages, else 0
-  size_t off_counters = 0, off_ml = 0, off_o = 0, off_planes = 0, total = 0;
+  size_t off_ml = 0, off_o = 0, off_planes = 0, total = 0;
 };
 
 // Where there are fewer row tiles than SMs, the keys are cut as well, down to about
@@ -493,10 +492,6 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
   const long long ctas = BH * pl->n_qtiles, sms = device_sm_count();
   pl->n_splits = (int)std::max<long long>(1, std::min<long long>(sms / ctas, (blocks + 1) / 2));
   if (BH * pl->n_splits > 0x7fffffffLL) return LOCKS_ERR_UNSUPPORTED;
-  // The error word, then the counters (problems are split only while there are at
-  // most half as many as SMs), in the same place for every shape: one workspace
-  // serves calls of different lengths, whose partial results never lie on a counter.
-  if (ctas > kPromptCounters) pl->n_splits = 1;
   size_t parts = pl->n_splits > 1 ? (size_t)ctas * pl->n_splits * 256 : 0;
   if (is_q4(c) && (long long)t->max_tokens * G <= kFewRows) {
     const long long slots = BH * ((t->max_tokens * G + kQ4RowColumns - 1) / kQ4RowColumns) *
@@ -506,9 +501,7 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
     pl->planes = false;
     parts = 2 * (size_t)pl->row_ctas * kQ4RowColumns;
   }
-  size_t off = kAlign;
-  pl->off_counters = off;
-  off = align_up(off + sizeof(unsigned) * kPromptCounters);
+  size_t off = kAlign;  // the error word
   pl->off_ml = off;
   off = align_up(off + sizeof(float2) * parts);
   pl->off_o = off;
@@ -858,7 +851,6 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   a.lse = lse;
   a.part_o = at<float>(ws, pl.off_o);
   a.part_ml = at<float2>(ws, pl.off_ml);
-  a.counters = at<unsigned>(ws, pl.off_counters);
   a.err = at<int>(ws, 0);
   a.batch = cache->batch;
   a.num_kv_heads = cache->num_kv_heads;

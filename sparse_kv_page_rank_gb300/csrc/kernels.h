@@ -155,7 +155,6 @@ struct PromptArgs {
   float* lse;                // or null
   float* part_o;             // ws: [B*Hkv*n_qtiles][n_splits][256][d]
   float2* part_ml;           // ws: the same without d: (reference, sum), base 2
-  unsigned* counters;        // ws: [B*Hkv*n_qtiles]
   int* err;
   int batch, num_kv_heads, group, max_pages, pages_total, page_size;
   int total, max_tokens;

@@ -42,7 +42,9 @@
 // the token at the end.
 //
 // Few rows: the keys of a problem are cut among several CTAs, whose partial
-// (reference, sum, O) go to the workspace; the last one to finish joins them.
+// (reference, sum, O) go to the workspace; a second, dependent kernel joins them, a warp
+// per row.  (The last CTA to finish did it before, alone: 64 tokens over 131,000, 8 KV
+// heads, 260 us, now 154.)
 #include "common.cuh"
 #include "kernels.h"
 #include "kv_q4.cuh"
@@ -90,7 +92,6 @@ struct PromptShared {
   int raw_skip[kRawSlots];  // the same of a slot of codes
   int abort;                // a bounded wait gave up
   int n_bad, bad[kMaxBad];
-  int last;
 };
 
 // Waits for phase `parity`; gives up after the iteration limit, or once another
@@ -157,6 +158,42 @@ struct PromptPlace {
   int kv_end;        // keys that its last token sees
   int j0, j1;        // its blocks of keys
 };
+
+// The sequence's part: false where there is nothing to do.  y: the CTA's row tiles, those
+// with the most keys first.
+template <int TILES>
+__device__ __forceinline__ bool find_place(const PromptArgs& a, PromptPlace& w, int x, int y, bool says) {
+  w.hkv = x % a.num_kv_heads;
+  w.b = x / a.num_kv_heads;
+  const int qt = a.n_qtiles - 1 - y;
+  const int cap = a.max_pages * a.page_size;
+  int len = a.seq_lens[w.b];
+  if (len < 0 || len > cap) {
+    if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+    len = len < 0 ? 0 : cap;
+  }
+  int c0 = w.b, c1 = w.b + (len > 0 ? 1 : 0);
+  if (a.cu_tokens) {
+    c0 = a.cu_tokens[w.b];
+    c1 = a.cu_tokens[w.b + 1];
+  }
+  int n = c1 - c0;
+  if (c0 < 0 || n < 0 || c1 > a.total) {
+    if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+    n = 0;
+  }
+  if (says && (n > len || n > a.max_tokens)) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+  const int mine = min(n, a.max_tokens), per_tile = kRows / a.group, per_cta = TILES * per_tile;
+  w.row0 = c0;
+  w.len = len;
+  w.start = len - n;
+  w.tok0 = qt * per_cta;
+  if (w.tok0 >= mine) return false;
+  w.n_tok = min(per_cta, mine - w.tok0);
+  w.n_tiles = w.n_tok > per_tile ? 2 : 1;
+  w.kv_end = max(0, min(len, w.start + w.tok0 + w.n_tok));
+  return true;
+}
 
 // Index of a CTA's partial results (of 256 rows each): its sequence, head, tiles and split.
 __device__ __forceinline__ size_t part_row(const PromptArgs& a, const PromptPlace& w, int y) {
@@ -805,37 +842,9 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
   pdl_wait();
   PromptPlace w;
   {
-    const int x = blockIdx.x / a.n_splits;
     w.split = blockIdx.x % a.n_splits;
-    w.hkv = x % a.num_kv_heads;
-    w.b = x / a.num_kv_heads;
-    const int qt = gridDim.y - 1 - blockIdx.y;  // the tiles with the most keys first
     const bool says = tid == 0 && blockIdx.y == 0 && w.split == 0;
-    int len = a.seq_lens[w.b];
-    if (len < 0 || len > a.max_pages * P) {
-      if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
-      len = len < 0 ? 0 : a.max_pages * P;
-    }
-    int c0 = w.b, c1 = w.b + (len > 0 ? 1 : 0);
-    if (a.cu_tokens) {
-      c0 = a.cu_tokens[w.b];
-      c1 = a.cu_tokens[w.b + 1];
-    }
-    int n = c1 - c0;
-    if (c0 < 0 || n < 0 || c1 > a.total) {
-      if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
-      n = 0;
-    }
-    if (says && (n > len || n > a.max_tokens)) set_error(a.err, LOCKS_DEVERR_LENGTHS);
-    const int mine = min(n, a.max_tokens), per_cta = kTiles<S> * (kRows / a.group);
-    w.row0 = c0;
-    w.len = len;
-    w.start = len - n;
-    w.tok0 = qt * per_cta;
-    if (w.tok0 >= mine) return;  // the whole CTA
-    w.n_tok = min(per_cta, mine - w.tok0);
-    w.n_tiles = w.n_tok > kRows / a.group ? 2 : 1;
-    w.kv_end = max(0, min(len, w.start + w.tok0 + w.n_tok));
+    if (!find_place<kTiles<S>>(a, w, blockIdx.x / a.n_splits, blockIdx.y, says)) return;  // the whole CTA
     const long long nb = (w.kv_end + kBlock - 1) / kBlock;
     w.j0 = (int)(nb * w.split / a.n_splits);
     w.j1 = (int)(nb * (w.split + 1) / a.n_splits);
@@ -885,49 +894,63 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
     if constexpr (S == kCodes) convert_role<P>(w, sh, smem_u32(ring), smem_u32(raw));
   }
   __syncwarp();
-  __threadfence();  // partial results, before the ticket
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
   pdl_launch_dependents();
   if (tid == 0 && sh.abort) set_error(a.err, kDevErrTimeout);
-  if (a.n_splits == 1) return;
+}
 
-  // ---- the last CTA of the tiles joins the partial results ----
-  const size_t prob = part_row(a, w, blockIdx.y) / a.n_splits;
-  if (tid == 0) sh.last = atomicAdd(a.counters + prob, 1u) == (unsigned)(a.n_splits - 1);
-  __syncthreads();
-  if (!sh.last) return;
-  __threadfence();
-  const int G = a.group, tpt = kRows / G, lane = tid & 31;
-  for (int r = warp; r < w.n_tiles * kRows; r += blockDim.x / 32) {
-    const int ti = (r % kRows) / G, h = (r % kRows) % G, i = (r / kRows) * tpt + ti;
-    if (ti >= tpt || i >= w.n_tok) continue;
-    float M = -INFINITY;
-    for (int s = 0; s < a.n_splits; ++s)
-      M = fmaxf(M, __ldcg(a.part_ml + (prob * a.n_splits + s) * (2 * kRows) + r).x);
-    float L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < a.n_splits; ++s) {
-      const size_t pi = (prob * a.n_splits + s) * (2 * kRows) + r;
-      const float2 ml = __ldcg(a.part_ml + pi);
-      if (ml.y == 0.f) continue;  // saw no key
-      const float f = fast_exp2(ml.x - M);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + pi * kHeadDim) + lane);
-      L = fmaf(ml.y, f, L);
-      O.x = fmaf(v.x, f, O.x);
-      O.y = fmaf(v.y, f, O.y);
-      O.z = fmaf(v.z, f, O.z);
-      O.w = fmaf(v.w, f, O.w);
+// ---- joins the partial results: grid (B * Hkv, row tiles, blocks of eight rows) ------------
+constexpr int kJoinWarps = 8;
+constexpr int kJoinFlight = 8;  // partials that a warp loads at once
+
+template <int TILES>
+__global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const PromptArgs a) {
+  const int lane = threadIdx.x & 31, r = blockIdx.z * kJoinWarps + (threadIdx.x >> 5);
+  PromptPlace w;
+  // the other kernel's inputs were complete before it let this one begin
+  const bool some = find_place<TILES>(a, w, blockIdx.x, blockIdx.y, false);
+  const int G = a.group, tpt = kRows / G, n = a.n_splits;
+  const int ti = (r % kRows) / G, h = (r % kRows) % G, i = (r / kRows) * tpt + ti;
+  // also where there is nothing to join: whatever follows may rely on this kernel's end
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!some || ti >= tpt || i >= w.n_tok) return;
+  w.split = 0;
+  const size_t p0 = part_row(a, w, blockIdx.y) * (2 * kRows) + r;
+  auto part = [&](int s) { return p0 + (size_t)s * (2 * kRows); };
+  float M = -INFINITY, L = 0.f;
+  for (int s = lane; s < n; s += 32) M = fmaxf(M, __ldcg(a.part_ml + part(s)).x);
+  M = warp_max(M);
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += kJoinFlight) {
+    float4 v[kJoinFlight];
+    float2 ml[kJoinFlight];
+#pragma unroll
+    for (int k = 0; k < kJoinFlight; ++k) {
+      ml[k] = make_float2(0.f, 0.f);
+      if (s0 + k >= n) continue;
+      v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + part(s0 + k) * kHeadDim) + lane);
+      ml[k] = __ldcg(a.part_ml + part(s0 + k));
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const size_t oi = ((size_t)w.row0 + w.tok0 + i) * ((size_t)a.num_kv_heads * G) + (size_t)w.hkv * G + h;
-    *reinterpret_cast<uint2*>(a.out + oi * kHeadDim + 4 * lane) =
-        make_uint2(pack_bf16(O.x * inv, O.y * inv), pack_bf16(O.z * inv, O.w * inv));
-    if (a.lse && lane == 0) a.lse[oi] = L == 0.f ? -INFINITY : (M + fast_log2(L)) * kLn2;
+#pragma unroll
+    for (int k = 0; k < kJoinFlight; ++k) {
+      if (ml[k].y == 0.f) continue;  // saw no key
+      const float f = fast_exp2(ml[k].x - M);
+      L = fmaf(ml[k].y, f, L);
+      O.x = fmaf(v[k].x, f, O.x);
+      O.y = fmaf(v[k].y, f, O.y);
+      O.z = fmaf(v[k].z, f, O.z);
+      O.w = fmaf(v[k].w, f, O.w);
+    }
   }
-  if (tid == 0) a.counters[prob] = 0;  // ready for the next call
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const size_t oi = ((size_t)w.row0 + w.tok0 + i) * ((size_t)a.num_kv_heads * G) + (size_t)w.hkv * G + h;
+  *reinterpret_cast<uint2*>(a.out + oi * kHeadDim + 4 * lane) =
+      make_uint2(pack_bf16(O.x * inv, O.y * inv), pack_bf16(O.z * inv, O.w * inv));
+  if (a.lse && lane == 0) a.lse[oi] = L == 0.f ? -INFINITY : (M + fast_log2(L)) * kLn2;
 }
 
 template <Source S, int P>
@@ -951,7 +974,11 @@ cudaError_t launch(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap
   cfg.gridDim = dim3(a.batch * a.num_kv_heads * a.n_splits, a.n_qtiles, 1);
   cfg.blockDim = dim3(kThreadsOf<S>, 1, 1);
   cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a)) != cudaSuccess || a.n_splits == 1) return e;
+  cfg.gridDim = dim3(a.batch * a.num_kv_heads, a.n_qtiles, kTiles<S> * kRows / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<kTiles<S>>, a);
 }
 
 template <int P>
