@@ -469,6 +469,10 @@ constexpr int kFewRows = 48;
 // 4-bit pages: from this many row tiles of a head on, its keys and values are
 // converted once for all of them, where the planes take no more than this.
 constexpr int kPlaneTiles = 4;
+// bf16 pages of 16 tokens: the same, against their many small copies.  One sequence of
+// 131,000 tokens, 8 KV heads of 4 heads, in us (planes, pages): 200 new tokens (7 tiles)
+// 607, 606; 300 (10 tiles) 752, 803; 1000 tokens 1868, 2347.
+constexpr int kBf16PlaneTiles = 8;
 constexpr long long kPlaneBytes = 4LL << 30;
 struct PromptPlan {
   int n_qtiles = 1, n_splits = 1, plane_rows = 0;
@@ -484,8 +488,9 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
   const long long BH = (long long)c->batch * c->num_kv_heads;
   const long long blocks = ((long long)c->max_pages * c->page_size + 127) / 128;
   const long long tiles = std::max(1, (t->max_tokens + per_tile - 1) / per_tile);
-  const long long plane_bytes = 3 * BH * blocks * 128 * kHeadDim * 2;
-  pl->planes = is_q4(c) && tiles >= kPlaneTiles && plane_bytes <= kPlaneBytes;
+  const long long plane_bytes = (is_q4(c) ? 3 : 2) * BH * blocks * 128 * kHeadDim * 2;
+  pl->planes = plane_bytes <= kPlaneBytes &&
+               (is_q4(c) ? tiles >= kPlaneTiles : c->page_size == 16 && tiles >= kBf16PlaneTiles);
   pl->plane_rows = (int)(blocks * 128);
   pl->n_qtiles = (int)(is_q4(c) && !pl->planes ? tiles : (tiles + 1) / 2);
   if (pl->n_qtiles > 65535) return LOCKS_ERR_UNSUPPORTED;
@@ -835,7 +840,7 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   if (!is_q4(cache) && (!encode_pool(&tk, cache->k_pool, cache) || !encode_pool(&tv, cache->v_pool, cache)))
     return LOCKS_ERR_CUDA;
   if (pl.planes && !encode_matrix(&tk, at<uint16_t>(ws, pl.off_planes),
-                                  3 * (size_t)cache->batch * cache->num_kv_heads * pl.plane_rows, 128))
+                                  (is_q4(cache) ? 3 : 2) * (size_t)cache->batch * cache->num_kv_heads * pl.plane_rows, 128))
     return LOCKS_ERR_CUDA;
   PromptArgs a;
   a.planes = pl.planes ? at<uint16_t>(ws, pl.off_planes) : nullptr;

@@ -162,7 +162,7 @@ struct PromptArgs {
   int n_splits;              // CTAs along the keys
   float scale_log2;
   int q4;
-  uint16_t* planes;          // 4-bit pages, many rows: ws [3][B][Hkv][plane_rows][d] fp16; else null
+  uint16_t* planes;          // many rows: ws [3 (4-bit pages, fp16) or 2 (bf16)][B][Hkv][plane_rows][d]; else null
   int plane_rows;            // tokens of a plane, whole blocks of 128
 };
 

@@ -22,7 +22,10 @@
 //
 // Three sources of the operands:
 //  - bf16 pages: TMA copies of the pages (64-column boxes).  A CTA takes two tiles
-//    (256 rows), so that one tile's softmax runs while the other's products do.
+//    (256 rows), so that one tile's softmax runs while the other's products do.  Pages of
+//    16 tokens make 64 copies of 2 KiB per block, which at some 37 ns each take twice as
+//    long as its products: with many rows one kernel first gathers keys and values into
+//    planes, of which a block is eight copies.
 //  - 4-bit pages, many rows: each key is needed by many CTAs, so one kernel first
 //    writes the sequence's keys and values as fp16 planes into the workspace, and
 //    TMA copies fetch those; else as above.
@@ -67,13 +70,15 @@ constexpr uint32_t kTmemO = 256;             // S: columns 0 and 128; O: 256 and
 constexpr uint32_t kTmemQ = 384;             // kCodes: the queries, in place of a second O
 
 // Where the operands come from.
-enum Source { kBf16Pages, kPlanes, kCodes };
+enum Source { kBf16Pages, kBf16Planes, kPlanes, kCodes };
+template <Source S>
+constexpr bool kIsBf16 = S == kBf16Pages || S == kBf16Planes;  // else fp16
 template <Source S>
 constexpr int kTiles = S == kCodes ? 1 : 2;   // tiles of a CTA
 template <Source S>
 constexpr int kQueryTiles = S == kCodes ? 0 : 2;  // of those, in shared memory (else in tensor memory)
 template <Source S>
-constexpr int kUnits = S == kBf16Pages ? 2 : 3;  // operands of a block: keys (two halves), values
+constexpr int kUnits = kIsBf16<S> ? 2 : 3;  // operands of a block: keys (two halves), values
 // Operands in the ring of keys and values: with 4-bit codes two whole blocks.
 template <Source S>
 constexpr int kSlots = S == kCodes ? 6 : 5;
@@ -269,7 +274,7 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
               sh.skip[0][n % kSkipRing] = skip & 15;
               sh.skip[1][n % kSkipRing] = skip >> 4;
             }
-            if constexpr (S == kPlanes) {
+            if constexpr (S == kPlanes || S == kBf16Planes) {
               // plane u of this sequence and head
               const int y = (int)(((long long)u * a.batch + w.b) * a.num_kv_heads + w.hkv) * a.plane_rows + j * kBlock;
               mbar_arrive_expect_tx(full, kOperand);
@@ -478,13 +483,42 @@ __global__ void __launch_bounds__(128) planes_kernel(const PromptArgs a) {
   }
 }
 
+// The same of bf16 pages of 16 tokens: keys and values, [2][batch][Hkv][plane_rows][128].
+__global__ void __launch_bounds__(128) bf16_planes_kernel(const PromptArgs a) {
+  constexpr int P = 16;
+  pdl_wait();
+  const int hkv = blockIdx.y % a.num_kv_heads, b = blockIdx.y / a.num_kv_heads, lane = threadIdx.x & 31;
+  const int len = min(max(a.seq_lens[b], 0), a.max_pages * P), t0 = blockIdx.x * 64 + P * (threadIdx.x >> 5);
+  pdl_launch_dependents();
+  if (t0 >= len) return;
+  const int phys = a.block_table[(size_t)b * a.max_pages + t0 / P];
+  if (phys < 0 || phys >= a.pages_total) return;  // reported by the attention
+  const size_t from = ((size_t)phys * a.num_kv_heads + hkv) * P * kHeadDim;
+  const size_t plane = (size_t)a.batch * a.num_kv_heads * a.plane_rows * kHeadDim;
+  uint4* dst = reinterpret_cast<uint4*>(a.planes + ((size_t)blockIdx.y * a.plane_rows + t0) * kHeadDim) + lane;
+  const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k_pool) + from) + lane;
+  const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_pool) + from) + lane;
+  constexpr int kSteps = P * kHeadDim / 8 / 32;
+  uint4 x[2 * kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    x[i] = __ldg(k + 32 * i);
+    x[kSteps + i] = __ldg(v + 32 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    dst[32 * i] = x[i];
+    dst[plane / 8 + 32 * i] = x[kSteps + i];
+  }
+}
+
 // ---- warp 0, one thread: the matrix instructions ------------------------------------
 // The thread's own steps (a test, a commit) cost some hundred clocks beside the busy
 // softmax warps, and the tensor core stands still meanwhile; so there are few of them:
 // with two tiles one test and one or two commits per tile and block.
 template <Source S>
 __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uint32_t ring, uint32_t tmem) {
-  constexpr bool kBf16 = S == kBf16Pages, kOne = kTiles<S> == 1;
+  constexpr bool kBf16 = kIsBf16<S>, kOne = kTiles<S> == 1;
   constexpr uint32_t kIdS = umma_idesc(kRows, kBlock, kBf16, false), kIdO = umma_idesc(kRows, kHeadDim, kBf16, true);
   constexpr int kKeys = kUnits<S> - 1, kN = kSlots<S>;
   const int n_blocks = w.j1 - w.j0;
@@ -583,7 +617,7 @@ __device__ void landed_role(const PromptPlace& w, PromptShared& sh) {
 // ---- warps 4 and up: one softmax row per thread -------------------------------------------
 template <Source S, int P>
 __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptShared& sh, uint8_t* smem, uint32_t tmem_base) {
-  constexpr bool Q4 = S != kBf16Pages;
+  constexpr bool Q4 = !kIsBf16<S>;
   constexpr bool kOne = kTiles<S> == 1;      // one tile, two S buffers
   constexpr float kOffset = Q4 ? 6.f : 0.f;  // weights are scaled by 2^kOffset
   const int warp = threadIdx.x >> 5, t = (warp - 4) / 4;
@@ -966,10 +1000,10 @@ cudaError_t launch(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if constexpr (S == kPlanes) {
+  if constexpr (S == kPlanes || S == kBf16Planes) {
     cfg.gridDim = dim3((a.max_pages * P + 63) / 64, a.batch * a.num_kv_heads, 1);
     cfg.blockDim = dim3(128, 1, 1);
-    if ((e = cudaLaunchKernelEx(&cfg, planes_kernel<P>, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, S == kPlanes ? planes_kernel<P> : bf16_planes_kernel, a)) != cudaSuccess) return e;
   }
   cfg.gridDim = dim3(a.batch * a.num_kv_heads * a.n_splits, a.n_qtiles, 1);
   cfg.blockDim = dim3(kThreadsOf<S>, 1, 1);
@@ -983,6 +1017,8 @@ cudaError_t launch(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap
 
 template <int P>
 cudaError_t launch_page(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  if constexpr (P == 16)
+    if (!a.q4 && a.planes) return launch<kBf16Planes, P>(a, tk, tv, s);
   if (!a.q4) return launch<kBf16Pages, P>(a, tk, tv, s);
   return a.planes ? launch<kPlanes, P>(a, tk, tv, s) : launch<kCodes, P>(a, tk, tv, s);
 }

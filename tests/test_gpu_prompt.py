@@ -315,3 +315,30 @@ def test_strided_queries_of_few_rows(new):
     check(case, [new], q, out, lse)
     same, _ = rt.prompt_attend(q.contiguous(), cu_tokens=cu_of([new]))
     assert torch.equal(out, same)
+
+
+@pytest.mark.parametrize("fmt,P,hq,hkv,new", [("bf16", 16, 4, 1, 300), ("bf16", 16, 16, 1, 100), ("bf16", 16, 8, 2, 20),
+                                              ("q4", 16, 8, 2, 5), ("q4", 64, 4, 1, 40)])
+def test_a_page_outside_the_pool_is_left_out(fmt, P, hq, hkv, new):
+    """Its tokens are reported and take no part; the rest is as if they were not there,
+    whatever the path: pages, planes, few rows."""
+    from sparse_kv_page_rank_gb300 import locks as L
+    case = Case([400], hq, hkv, P, fmt, seed=21)
+    rt, q = case.runtime(), case.query(new)
+    lp = 48 // P
+    case.table[0, lp] = case.k.shape[0] + 3
+    out, lse = rt.prompt_attend(q, cu_tokens=cu_of([new]), max_tokens=new)
+    assert rt.device_error() == L.LOCKS_DEVERR_BLOCK_TABLE
+    case.table[0, lp] = case.table[0, lp + 1]  # for the reference: any page that holds numbers
+    gone = torch.zeros(400, dtype=torch.bool, device="cuda")
+    gone[lp * P:(lp + 1) * P] = True
+    at = torch.arange(400, device="cuda")
+    hidden = gone[None, :] | (at[None, :] > (400 - new + torch.arange(new, device="cuda"))[:, None])
+    k, v = case.kv64(0)
+    for g in range(hq):
+        h = g * hkv // hq
+        ro, rl, av, mag, _ = attend64(q[:, g], k[h], v[h], hidden, ksc=case.scale64(0)[h])
+        e = 2.0 ** -15 * mag + 2.0 ** -22 * (mag + 16)
+        to = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2 * e + 400 * 2.0 ** -23)[:, None] * av + 400 * 2.0 ** -31 * v.abs().max()
+        assert ((out[:, g].double() - ro).abs() <= to).all(), g
+        assert ((lse[:, g].double() - rl).abs() <= e + 400 * 2.0 ** -24 + 2.0 ** -22 * (rl.abs() + 16)).all(), g

@@ -230,3 +230,20 @@ def test_wrong_places_and_shapes_are_refused():
         with pytest.raises(ValueError, match="on the device"):
             rt.append(*args, cu_tokens=cu, max_tokens=2, **kw)
     assert rt.device_error() == 0
+
+
+@pytest.mark.parametrize("P", [64, 16])
+def test_the_growing_loop_over_4_bit_pages(P):
+    """Captured segments of decode steps, filled pages summarised beside them."""
+    from sparse_kv_page_rank_gb300.growing import GrowingLoop
+    segments = 3
+    case = Case([P * (4 + segments), P * (2 + segments)], 8, 2, P, "q4", seed=P, nsum=[4, 2])
+    case.seq.copy_(torch.tensor([4 * P, 2 * P], dtype=torch.int32))
+    rt, q = case.runtime(budget=1024), case.query(2)
+    for b in range(2):
+        rt.build_summaries(case.table[b, :case.nsum[b]])
+    loop = GrowingLoop(rt, q)
+    loop.run(segments)
+    torch.cuda.synchronize()
+    assert case.seq.tolist() == case.lens and rt.device_error() == 0
+    check_decode_q4(case, q, rt.out, rt.lse)  # the budget holds every page
