@@ -475,14 +475,20 @@ constexpr int kPlaneTiles = 4;
 constexpr int kBf16PlaneTiles = 8;
 constexpr long long kPlaneBytes = 4LL << 30;
 struct PromptPlan {
-  int n_qtiles = 1, n_splits = 1, plane_rows = 0;
+  int n_qtiles = 1, n_whole = 0, n_splits = 1, plane_rows = 0;
   bool planes = false;
   int row_ctas = 0, row_tiles = 0;  // few rows of 4-bit pages, else 0
   size_t off_ml = 0, off_o = 0, off_planes = 0, total = 0;
 };
 
-// Where there are fewer row tiles than SMs, the keys are cut as well, down to about
-// two blocks of 128 per CTA.
+// Row tiles that do not fill a wave of CTAs (all of them, or what is left over after
+// whole waves) have their keys cut as well, down to about two blocks of 128 per CTA: into
+// the number of parts whose waves take least, in blocks' times, a part costing some eight
+// blocks of its own and a partial result's way through memory a fiftieth.  30,000 keys, 8
+// KV heads, 4-bit pages, in us (cut, whole): 400 new tokens 311, 354; 700 448, 630; 2048
+// 1094, 1175.  With many waves the gain is small.
+constexpr int kCutWaves = 8;
+constexpr double kPartBlocks = 8.0, kPartialBlocks = 0.02;
 locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, const lockskv_tokens_t* t, PromptPlan* pl) {
   const int G = p->num_q_heads / c->num_kv_heads, per_tile = 128 / G;  // tokens of a 128-row tile
   const long long BH = (long long)c->batch * c->num_kv_heads;
@@ -493,11 +499,22 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
                (is_q4(c) ? tiles >= kPlaneTiles : c->page_size == 16 && tiles >= kBf16PlaneTiles);
   pl->plane_rows = (int)(blocks * 128);
   pl->n_qtiles = (int)(is_q4(c) && !pl->planes ? tiles : (tiles + 1) / 2);
-  if (pl->n_qtiles > 65535) return LOCKS_ERR_UNSUPPORTED;
   const long long ctas = BH * pl->n_qtiles, sms = device_sm_count();
-  pl->n_splits = (int)std::max<long long>(1, std::min<long long>(sms / ctas, (blocks + 1) / 2));
-  if (BH * pl->n_splits > 0x7fffffffLL) return LOCKS_ERR_UNSUPPORTED;
-  size_t parts = pl->n_splits > 1 ? (size_t)ctas * pl->n_splits * 256 : 0;
+  if (ctas > 0x3fffffffLL) return LOCKS_ERR_UNSUPPORTED;
+  // what is left over after whole waves of CTAs; where the tiles' keys differ much, the
+  // last ones have few and fill the gaps
+  long long cut = ctas % sms;
+  if (ctas > sms && (ctas > kCutWaves * sms || 2LL * t->max_tokens > (long long)c->max_pages * c->page_size)) cut = 0;
+  // their time in blocks: waves of parts, each with a fixed cost, and the partial results
+  double best = (double)blocks + kPartBlocks;
+  pl->n_splits = 1;
+  for (long long n = 2; cut && n <= std::min<long long>(sms, (blocks + 1) / 2); ++n) {
+    const double time = (double)((cut * n + sms - 1) / sms) * ((double)blocks / n + kPartBlocks) + kPartialBlocks * cut * n;
+    if (time < best) best = time, pl->n_splits = (int)n;
+  }
+  if (pl->n_splits == 1) cut = 0;
+  pl->n_whole = (int)(ctas - cut);
+  size_t parts = (size_t)cut * pl->n_splits * 256;
   if (is_q4(c) && (long long)t->max_tokens * G <= kFewRows) {
     const long long slots = BH * ((t->max_tokens * G + kQ4RowColumns - 1) / kQ4RowColumns) *
                             (((long long)c->max_pages * c->page_size + kPage - 1) / kPage);
@@ -866,6 +883,7 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   a.total = tokens->total;
   a.max_tokens = tokens->max_tokens;
   a.n_qtiles = pl.n_qtiles;
+  a.n_whole = pl.n_whole;
   a.n_splits = pl.n_splits;
   a.scale_log2 = scale_of(params) * kLog2e;
   a.q4 = is_q4(cache) ? 1 : 0;

@@ -153,13 +153,13 @@ struct PromptArgs {
   const int32_t* seq_lens;
   uint16_t* out;
   float* lse;                // or null
-  float* part_o;             // ws: [B*Hkv*n_qtiles][n_splits][256][d]
+  float* part_o;             // ws: [tiles that are cut][n_splits][256][d]
   float2* part_ml;           // ws: the same without d: (reference, sum), base 2
   int* err;
   int batch, num_kv_heads, group, max_pages, pages_total, page_size;
   int total, max_tokens;
   int n_qtiles;              // CTAs along a sequence's new tokens (256 rows each; 128 for 4-bit codes)
-  int n_splits;              // CTAs along the keys
+  int n_whole, n_splits;     // row tiles of one CTA each; CTAs along the keys of each of the others
   float scale_log2;
   int q4;
   uint16_t* planes;          // many rows: ws [3 (4-bit pages, fp16) or 2 (bf16)][B][Hkv][plane_rows][d]; else null

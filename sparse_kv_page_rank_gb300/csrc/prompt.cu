@@ -44,7 +44,8 @@
 // every row sees are zeroed there too and added, as they are, to the rows that do see
 // the token at the end.
 //
-// Few rows: the keys of a problem are cut among several CTAs, whose partial
+// Few row tiles, or some left over after whole waves of CTAs: the keys of a tile are cut
+// among several CTAs, whose partial
 // (reference, sum, O) go to the workspace; a second, dependent kernel joins them, a warp
 // per row.  (The last CTA to finish did it before, alone: 64 tokens over 131,000, 8 KV
 // heads, 260 us, now 154.)
@@ -79,6 +80,11 @@ template <Source S>
 constexpr int kQueryTiles = S == kCodes ? 0 : 2;  // of those, in shared memory (else in tensor memory)
 template <Source S>
 constexpr int kUnits = kIsBf16<S> ? 2 : 3;  // operands of a block: keys (two halves), values
+// With three operands of a block the ring of five is short of one: the second half of the
+// next keys lands in the place of this block's values.  It is asked for as soon as those
+// are used, and waited for only when it is needed.
+template <Source S>
+constexpr bool kLateKeys = kTiles<S> == 2 && kUnits<S> == 3;
 // Operands in the ring of keys and values: with 4-bit codes two whole blocks.
 template <Source S>
 constexpr int kSlots = S == kCodes ? 6 : 5;
@@ -91,6 +97,7 @@ struct PromptShared {
   // done[n % 2]: the products with the values of block n and the keys of block n + 1
   // are complete (two barriers, so that no waiter can be a whole turn behind)
   uint64_t s_full[2], p_ready[2], o_full[2], done[2], drain;
+  uint64_t v_free[2];  // kLateKeys: the products with the values of block n are complete
   uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
   uint32_t tmem;
   int skip[2][kSkipRing];   // per half of a block: 16-token groups whose page is outside the pool (bits)
@@ -154,7 +161,7 @@ __device__ __forceinline__ void q4_codes(uint32_t w, uint32_t (&f)[4]) {
 
 // What one CTA works on.
 struct PromptPlace {
-  int b, hkv, split;
+  int b, hkv, tile, split, n_splits;
   int row0;          // first token row of the sequence in the token arrays
   int len;           // tokens in the cache
   int start;         // position of the sequence's first new token
@@ -164,13 +171,14 @@ struct PromptPlace {
   int j0, j1;        // its blocks of keys
 };
 
-// The sequence's part: false where there is nothing to do.  y: the CTA's row tiles, those
-// with the most keys first.
+// A row tile's place (all but split, j0, j1); false where there is nothing to do.
 template <int TILES>
-__device__ __forceinline__ bool find_place(const PromptArgs& a, PromptPlace& w, int x, int y, bool says) {
+__device__ __forceinline__ bool find_place(const PromptArgs& a, PromptPlace& w, int tile, bool says) {
+  const int problems = a.batch * a.num_kv_heads, x = tile % problems;
   w.hkv = x % a.num_kv_heads;
   w.b = x / a.num_kv_heads;
-  const int qt = a.n_qtiles - 1 - y;
+  const int qt = a.n_qtiles - 1 - tile / problems;
+  says = says && tile < problems;
   const int cap = a.max_pages * a.page_size;
   int len = a.seq_lens[w.b];
   if (len < 0 || len > cap) {
@@ -200,9 +208,11 @@ __device__ __forceinline__ bool find_place(const PromptArgs& a, PromptPlace& w, 
   return true;
 }
 
-// Index of a CTA's partial results (of 256 rows each): its sequence, head, tiles and split.
-__device__ __forceinline__ size_t part_row(const PromptArgs& a, const PromptPlace& w, int y) {
-  return (((size_t)w.b * a.num_kv_heads + w.hkv) * a.n_qtiles + y) * a.n_splits + w.split;
+// Row tiles are numbered tile by tile, those with the most keys first, sequence by
+// sequence and head by head within; from a.n_whole on the keys of each are cut in
+// a.n_splits parts, whose partial results (of 256 rows each) are numbered likewise.
+__device__ __forceinline__ size_t part_of(const PromptArgs& a, int tile, int split) {
+  return (size_t)(tile - a.n_whole) * a.n_splits + split;
 }
 
 // One value of the cache (bf16 pages: any; 4-bit pages: with its scale).
@@ -234,6 +244,7 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
   const int n_pages = (w.len + P - 1) / P;
   int asked = 0;  // operands (slots of codes) asked for
   int seen = 0;   // blocks known to be done
+  int seen_v = 0; // blocks whose values are known to be free
   bool ok = true;
   for (int jb = w.j0; jb < w.j1 && ok; jb += kAtOnce) {
     // the pages of several blocks at a time, one per lane
@@ -263,8 +274,13 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
           // keys after block m - 1 (the first block's after block 0, like the second's)
           if (asked >= kSlots<S>) {
             const int old = asked - kSlots<S>, m = old / kUnits<S>;
-            const int need = old % kUnits<S> == kUnits<S> - 1 ? m : max(0, m - 1);
-            for (; ok && seen <= need; ++seen) ok = block_done(seen, sh);
+            const bool values = old % kUnits<S> == kUnits<S> - 1;
+            if (kLateKeys<S> && values) {
+              for (; ok && seen_v <= m; ++seen_v) ok = wait_warp(&sh.v_free[seen_v & 1], (seen_v >> 1) & 1, sh);
+            } else {
+              const int need = values ? m : max(0, m - 1);
+              for (; ok && seen <= need; ++seen) ok = block_done(seen, sh);
+            }
             if (!ok) break;
           }
           if (lane == 0) {
@@ -531,11 +547,14 @@ __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uin
     return there;
   };
   const uint32_t q_lo = umma_desc_lo(q, 16), k_lo = umma_desc_lo(ring, 16), v_lo = umma_desc_lo(ring, kHalf);
-  int key[kKeys], value = 0;
+  int key[kKeys], value = 0, late_phase = 0;
   auto next_keys = [&](bool wait) {
     bool there = true;
 #pragma unroll
-    for (int part = 0; part < kKeys; ++part) there = next(key[part], wait && there) && there;
+    for (int part = 0; part < kKeys; ++part) {
+      late_phase = phase;
+      there = next(key[part], wait && there) && there;
+    }
     return there;
   };
   auto scores = [&](int t, int buf) {  // S = Q_t K^T (fp16: both halves of K)
@@ -543,6 +562,10 @@ __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uin
 #pragma unroll
     for (int part = 0; part < kKeys; ++part) {
       const uint32_t kd = k_lo + key[part] * (kOperand / 16);
+      if (kLateKeys<S> && part == 1 && t == 0) {
+        if (!spin_bar(&sh.full[key[1]], late_phase, sh)) return false;
+        tc_fence_after();
+      }
 #pragma unroll
       for (int s = 0; s < kHeadDim / 16; ++s) {
         const uint32_t off = ((s / 4) * kHalf + (s % 4) * 32) / 16;
@@ -551,6 +574,7 @@ __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uin
       }
     }
     umma_commit(&sh.s_full[buf]);
+    return true;
   };
   auto values = [&](int t, int buf, bool more) {  // O_t (+)= P V
     const uint32_t p = tmem + buf * kBlock, vd = v_lo + value * (kOperand / 16), o = tmem + kTmemO + t * kHeadDim;
@@ -561,7 +585,7 @@ __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uin
   bool ok = wait_bar(&sh.q_full, 0, sh) && next_keys(true);
   if (ok) {
     tc_fence_after();
-    for (int t = 0; t < w.n_tiles; ++t) scores(t, kOne ? 0 : t);
+    for (int t = 0; ok && t < w.n_tiles; ++t) ok = scores(t, kOne ? 0 : t);
   }
   for (int n = 0; ok && n < n_blocks; ++n) {
     const bool last = n + 1 == n_blocks;
@@ -571,7 +595,7 @@ __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uin
       if (!last) {
         if (!(ok = next_keys(true))) break;
         tc_fence_after();
-        scores(0, (n + 1) & 1);
+        (void)scores(0, (n + 1) & 1);
       }
       if (!(ok = spin_bar(&sh.p_ready[n & 1], (n >> 1) & 1, sh))) break;
       tc_fence_after();
@@ -585,8 +609,10 @@ __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uin
         if (!(ok = spin_bar(&sh.p_ready[t], n & 1, sh))) break;
         tc_fence_after();
         values(t, t, n > 0);
-        if (!last) scores(t, t);
+        if (kLateKeys<S> && !last && t + 1 == w.n_tiles) umma_commit(&sh.v_free[n & 1]);
+        if (!last) ok = scores(t, t);
         else if (t + 1 < w.n_tiles) umma_commit(&sh.o_full[t]);
+        if (!ok) break;
       }
     }
     if (ok) umma_commit(last ? &sh.o_full[w.n_tiles - 1] : &sh.done[n & 1]);
@@ -605,8 +631,8 @@ __device__ void landed_role(const PromptPlace& w, PromptShared& sh) {
   constexpr int kU = kUnits<S>;
   const int n_blocks = w.j1 - w.j0;
   for (int n = 0; n < n_blocks; ++n) {
-    // operands kU n + kU - 1 (values) to kU (n + 1) + kU - 2 (keys)
-    for (int i = kU * n + kU - 1; i < (n + 1 < n_blocks ? kU * (n + 2) - 1 : kU * (n + 1)); ++i)
+    // operands kU n + kU - 1 (values) and kU (n + 1) (keys; their second half: see kLateKeys)
+    for (int i = kU * n + kU - 1; i <= (n + 1 < n_blocks ? kU * (n + 1) : kU * n + kU - 1); ++i)
       if (!wait_warp(&sh.full[i % kSlots<S>], (i / kSlots<S>) & 1, sh)) return;
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.p_ready[0]);
     // one arrival per phase
@@ -820,7 +846,7 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
   const int n_bad = min(*reinterpret_cast<volatile int*>(&sh.n_bad), kMaxBad);
   const float lse2 = (m == -INFINITY ? 0.f : m - kOffset) + fast_log2(l);
   const size_t oi = qrow * Hq + (size_t)w.hkv * G + h;
-  const size_t pi = a.n_splits > 1 ? part_row(a, w, blockIdx.y) * (2 * kRows) + t * kRows + row : 0;
+  const size_t pi = w.n_splits > 1 ? part_of(a, w.tile, w.split) * (2 * kRows) + t * kRows + row : 0;
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
@@ -842,7 +868,7 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
       }
     }
     if (!valid) continue;
-    if (a.n_splits > 1) {
+    if (w.n_splits > 1) {
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
         *reinterpret_cast<uint4*>(a.part_o + pi * kHeadDim + c0 + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
@@ -858,7 +884,7 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
     }
   }
   if (valid) {
-    if (a.n_splits > 1) a.part_ml[pi] = make_float2(l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m - kOffset), l);
+    if (w.n_splits > 1) a.part_ml[pi] = make_float2(l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m - kOffset), l);
     else if (a.lse) a.lse[oi] = l == 0.f ? -INFINITY : lse2 * kLn2;
   }
 }
@@ -876,12 +902,14 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
   pdl_wait();
   PromptPlace w;
   {
-    w.split = blockIdx.x % a.n_splits;
-    const bool says = tid == 0 && blockIdx.y == 0 && w.split == 0;
-    if (!find_place<kTiles<S>>(a, w, blockIdx.x / a.n_splits, blockIdx.y, says)) return;  // the whole CTA
+    const int cut = (int)blockIdx.x - a.n_whole;  // CTAs of whole tiles first
+    w.tile = cut < 0 ? blockIdx.x : a.n_whole + cut / a.n_splits;
+    w.split = cut < 0 ? 0 : cut % a.n_splits;
+    w.n_splits = cut < 0 ? 1 : a.n_splits;
+    if (!find_place<kTiles<S>>(a, w, w.tile, tid == 0 && w.split == 0)) return;  // the whole CTA
     const long long nb = (w.kv_end + kBlock - 1) / kBlock;
-    w.j0 = (int)(nb * w.split / a.n_splits);
-    w.j1 = (int)(nb * (w.split + 1) / a.n_splits);
+    w.j0 = (int)(nb * w.split / w.n_splits);
+    w.j1 = (int)(nb * (w.split + 1) / w.n_splits);
   }
   if (tid == 0) {
     mbar_init(&sh.q_full, kRows / 32 * w.n_tiles);
@@ -891,6 +919,7 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
       mbar_init(&sh.p_ready[t], kRows / 32 + (kTiles<S> == 2 && t == 0 ? 1 : 0));
       mbar_init(&sh.o_full[t], 1);
       mbar_init(&sh.done[t], 1);
+      mbar_init(&sh.v_free[t], 1);
     }
     mbar_init(&sh.drain, 1);
     for (int s = 0; s < kRawSlots; ++s) {
@@ -936,24 +965,23 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
   if (tid == 0 && sh.abort) set_error(a.err, kDevErrTimeout);
 }
 
-// ---- joins the partial results: grid (B * Hkv, row tiles, blocks of eight rows) ------------
+// ---- joins the partial results: grid (tiles that were cut, blocks of eight rows) ------------
 constexpr int kJoinWarps = 8;
 constexpr int kJoinFlight = 8;  // partials that a warp loads at once
 
 template <int TILES>
 __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const PromptArgs a) {
-  const int lane = threadIdx.x & 31, r = blockIdx.z * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), tile = a.n_whole + blockIdx.x;
   PromptPlace w;
   // the other kernel's inputs were complete before it let this one begin
-  const bool some = find_place<TILES>(a, w, blockIdx.x, blockIdx.y, false);
+  const bool some = find_place<TILES>(a, w, tile, false);
   const int G = a.group, tpt = kRows / G, n = a.n_splits;
   const int ti = (r % kRows) / G, h = (r % kRows) % G, i = (r / kRows) * tpt + ti;
   // also where there is nothing to join: whatever follows may rely on this kernel's end
   pdl_wait();
   pdl_launch_dependents();
   if (!some || ti >= tpt || i >= w.n_tok) return;
-  w.split = 0;
-  const size_t p0 = part_row(a, w, blockIdx.y) * (2 * kRows) + r;
+  const size_t p0 = part_of(a, tile, 0) * (2 * kRows) + r;
   auto part = [&](int s) { return p0 + (size_t)s * (2 * kRows); };
   float M = -INFINITY, L = 0.f;
   for (int s = lane; s < n; s += 32) M = fmaxf(M, __ldcg(a.part_ml + part(s)).x);
@@ -1005,11 +1033,12 @@ cudaError_t launch(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap
     cfg.blockDim = dim3(128, 1, 1);
     if ((e = cudaLaunchKernelEx(&cfg, S == kPlanes ? planes_kernel<P> : bf16_planes_kernel, a)) != cudaSuccess) return e;
   }
-  cfg.gridDim = dim3(a.batch * a.num_kv_heads * a.n_splits, a.n_qtiles, 1);
+  const int tiles = a.batch * a.num_kv_heads * a.n_qtiles, cut = tiles - a.n_whole;
+  cfg.gridDim = dim3(a.n_whole + cut * a.n_splits, 1, 1);
   cfg.blockDim = dim3(kThreadsOf<S>, 1, 1);
   cfg.dynamicSmemBytes = smem;
-  if ((e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a)) != cudaSuccess || a.n_splits == 1) return e;
-  cfg.gridDim = dim3(a.batch * a.num_kv_heads, a.n_qtiles, kTiles<S> * kRows / kJoinWarps);
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tk, tv, a)) != cudaSuccess || cut == 0) return e;
+  cfg.gridDim = dim3(cut, kTiles<S> * kRows / kJoinWarps, 1);
   cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, prompt_join_kernel<kTiles<S>>, a);

@@ -248,9 +248,12 @@ class LocksRuntime:
             self._prompt_held.append(self.prompt_ws)
             self._prompt_captured = False
         err = 0 if self.prompt_ws is None else L.locks_get_device_error(self.prompt_ws)
-        ws = torch.zeros(need + 256, dtype=torch.uint8, device=self.device)
+        if self.prompt_ws is not None:  # in large steps, while they are cheap
+            need = max(need, min(2 * self.prompt_ws.numel(), 256 << 20))
+        ws = torch.empty(need + 256, dtype=torch.uint8, device=self.device)
         off = (-ws.data_ptr()) % 256
         self.prompt_ws = ws[off:off + need]
+        L.locks_workspace_init(self.prompt_ws, need)
         if err:
             self.prompt_ws[:4].view(torch.int32).fill_(err)
         torch.cuda.synchronize(self.device)

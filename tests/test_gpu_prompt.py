@@ -342,3 +342,21 @@ def test_a_page_outside_the_pool_is_left_out(fmt, P, hq, hkv, new):
         to = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2 * e + 400 * 2.0 ** -23)[:, None] * av + 400 * 2.0 ** -31 * v.abs().max()
         assert ((out[:, g].double() - ro).abs() <= to).all(), g
         assert ((lse[:, g].double() - rl).abs() <= e + 400 * 2.0 ** -24 + 2.0 ** -22 * (rl.abs() + 16)).all(), g
+
+
+@pytest.mark.parametrize("fmt,P,hq,hkv,lens,new", [
+    # whole waves of tiles, and some left over whose keys are cut
+    ("bf16", 64, 32, 8, [3000], [1300]), ("q4", 64, 32, 8, [3000], [1300]),
+    # fewer tiles than SMs, more than half as many
+    ("bf16", 64, 16, 8, [5000, 2000], [700, 1000]), ("q4", 16, 16, 8, [5000, 300], [900, 300]),
+])
+def test_left_over_tiles(fmt, P, hq, hkv, lens, new):
+    case = Case(lens, hq, hkv, P, fmt, seed=sum(lens), extra_cols=5)
+    rt, q = case.runtime(), case.query(sum(new))
+    first = None
+    for _ in range(2):
+        out, lse = rt.prompt_attend(q, cu_tokens=cu_of(new), max_tokens=max(new))
+        assert rt.device_error() == 0
+        assert first is None or torch.equal(out, first)
+        first = out
+    check(case, new, q, out, lse)
