@@ -141,6 +141,13 @@ class LocksRuntime:
         L.locks_exact_page_lse(self.cache, self.params, q, pl, stream)
         return pl
 
+    def _new(self, shape, dtype, stream):
+        """An output of a call on `stream`, whose memory belongs to that stream."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
     def _tokens(self, total: int, cu_tokens: torch.Tensor | None, max_tokens: int | None):
         if cu_tokens is None:
             return L.make_tokens(None, total, 1)
@@ -172,7 +179,7 @@ class LocksRuntime:
             if len(shape) != 3 or shape[0] != total or shape[1] != self.num_q_heads or not q.is_cuda:
                 raise ValueError(f"q must be [{total}][{self.num_q_heads}][128] on the device")
             if q_out is None:
-                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+                q_out = self._new(shape, torch.bfloat16, stream)
             elif q_out.shape != shape or not q_out.is_cuda:
                 raise ValueError("q_out must have q's shape, on the device")
         elif q_out is not None:
@@ -199,8 +206,7 @@ class LocksRuntime:
                     stream=None):
         """The newest tokens' keys and values as the cache holds them: two new
         bf16 tensors [total][Hkv][128] (rows of nobody are left unwritten)."""
-        k, v = (torch.empty((total, self.num_kv_heads, 128), dtype=torch.bfloat16, device=self.device)
-                for _ in range(2))
+        k, v = (self._new((total, self.num_kv_heads, 128), torch.bfloat16, stream) for _ in range(2))
         L.lockskv_read(self.cache, self._tokens(total, cu_tokens, max_tokens), k, v, self.kv_ws, 256, stream)
         return k, v
 
@@ -219,11 +225,11 @@ class LocksRuntime:
         stride = L._row_stride(q, "q")
         tokens = self._tokens(total, cu_tokens, max_tokens)
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = self._new(q.shape, torch.bfloat16, stream)
         elif out.shape != q.shape or out.dtype is not torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
             raise ValueError("out must be contiguous bf16 of q's shape on the device")
         if lse is None:
-            lse = torch.empty((total, self.num_q_heads), dtype=torch.float32, device=self.device)
+            lse = self._new((total, self.num_q_heads), torch.float32, stream)
         elif (lse.shape != (total, self.num_q_heads) or lse.dtype is not torch.float32 or not lse.is_cuda
               or not lse.is_contiguous()):
             raise ValueError(f"lse must be contiguous float32 [{total}][{self.num_q_heads}] on the device")

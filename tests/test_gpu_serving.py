@@ -247,3 +247,40 @@ def test_the_growing_loop_over_4_bit_pages(P):
     torch.cuda.synchronize()
     assert case.seq.tolist() == case.lens and rt.device_error() == 0
     check_decode_q4(case, q, rt.out, rt.lse)  # the budget holds every page
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_on_another_stream(raw):
+    """Outputs that a call makes belong to the stream it is given."""
+    s = Served("q4", 64, [300, 100], 8, 2, budget=0)
+    other = torch.cuda.Stream()
+    qkv, at = s.tokens([300, 100])
+    q, k, v = qkv.split([8, 2, 2], dim=1)
+    s.record([300, 100], qkv, at)
+    s.case.seq.copy_(torch.tensor(s.case.lens, dtype=torch.int32))
+    cu = cu_of([300, 100])
+    torch.cuda.synchronize()
+    on = other.cuda_stream if raw else other
+    rows = s.rt.append(k, v, q, rope=s.rope, cu_tokens=cu, max_tokens=300, stream=on)
+    out, lse = s.rt.prompt_attend(rows, cu_tokens=cu, max_tokens=300, stream=on)
+    kr, vr = s.rt.read_tokens(400, cu_tokens=cu, max_tokens=300, stream=on)
+    other.synchronize()
+    assert s.rt.device_error() == 0
+    assert torch.equal(rows, rotated(q, s.rope, at, D, False).bfloat16())
+    check_rows(s.case, [300, 100], rows, out, lse)
+    want = [torch.cat([x.transpose(0, 1) for x in pair]) for pair in zip(s.case.kv64(0), s.case.kv64(1))]
+    for got, x in zip((kr, vr), want):
+        assert torch.equal(got, x.float().bfloat16())
+
+
+def test_the_step_without_a_workspace_over_4_bit_pages():
+    from sparse_kv_page_rank_gb300 import locks as L
+    case = Case([1000, 130], 8, 2, 64, "q4", seed=9, nsum=[14, 1])
+    rt, q = case.runtime(budget=256), case.query(2)
+    for b in range(2):
+        rt.build_summaries(case.table[b, :case.nsum[b]])
+    out, lse = (x.clone() for x in rt.decode_step(q))
+    got, glse = torch.zeros_like(out), torch.zeros_like(lse)
+    err = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+    L.locks_decode_step_static(rt.cache, rt.summary, rt.params, q, got, glse, None, None, err)
+    assert int(err) == 0 and torch.equal(got, out) and torch.equal(glse, lse)
