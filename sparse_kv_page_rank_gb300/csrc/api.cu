@@ -883,6 +883,7 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   a.total = tokens->total;
   a.max_tokens = tokens->max_tokens;
   a.n_qtiles = pl.n_qtiles;
+  a.one_tile = tokens->max_tokens <= 128 / a.group ? 1 : 0;
   a.n_whole = pl.n_whole;
   a.n_splits = pl.n_splits;
   a.scale_log2 = scale_of(params) * kLog2e;

@@ -159,6 +159,7 @@ struct PromptArgs {
   int batch, num_kv_heads, group, max_pages, pages_total, page_size;
   int total, max_tokens;
   int n_qtiles;              // CTAs along a sequence's new tokens (256 rows each; 128 for 4-bit codes)
+  int one_tile;              // bf16 pages: a sequence's new rows fit one tile of 128
   int n_whole, n_splits;     // row tiles of one CTA each; CTAs along the keys of each of the others
   float scale_log2;
   int q4;

@@ -25,13 +25,14 @@
 //    (256 rows), so that one tile's softmax runs while the other's products do.  Pages of
 //    16 tokens make 64 copies of 2 KiB per block, which at some 37 ns each take twice as
 //    long as its products: with many rows one kernel first gathers keys and values into
-//    planes, of which a block is eight copies.
+//    planes, of which a block is eight copies.  Up to 128 rows: a CTA takes one tile and
+//    both S buffers, so that S of the next block is made while the softmax of this one
+//    runs; its queries are in tensor memory.
 //  - 4-bit pages, many rows: each key is needed by many CTAs, so one kernel first
 //    writes the sequence's keys and values as fp16 planes into the workspace, and
 //    TMA copies fetch those; else as above.
 //  - 4-bit pages, few rows: eight warps turn the pages' codes into operands in shared
-//    memory.  A CTA takes one tile and both S buffers, so that S of the next block is
-//    made while the softmax of this one runs; its queries are in tensor memory.
+//    memory, for one tile per CTA in the same way.
 // fp16 operands: q is scaled by a power of two.  A key s * code has up to 14
 // significant bits: it is held as the nearest half and the remainder, both exact, and
 // S is the sum of the products with both (one half alone would put 2^-11 of
@@ -78,13 +79,13 @@ constexpr uint32_t kTmemO = 256;             // S: columns 0 and 128; O: 256 and
 constexpr uint32_t kTmemQ = 384;             // kCodes: the queries, in place of a second O
 
 // Where the operands come from.
-enum Source { kBf16Pages, kBf16Planes, kPlanes, kCodes };
+enum Source { kBf16Pages, kBf16Few, kBf16Planes, kPlanes, kCodes };
 template <Source S>
-constexpr bool kIsBf16 = S == kBf16Pages || S == kBf16Planes;  // else fp16
+constexpr bool kIsBf16 = S == kBf16Pages || S == kBf16Few || S == kBf16Planes;  // else fp16
 template <Source S>
-constexpr int kTiles = S == kCodes ? 1 : 2;   // tiles of a CTA
+constexpr int kTiles = S == kCodes || S == kBf16Few ? 1 : 2;  // tiles of a CTA
 template <Source S>
-constexpr int kQueryTiles = S == kCodes ? 0 : 2;  // of those, in shared memory (else in tensor memory)
+constexpr int kQueryTiles = kTiles<S> == 1 ? 0 : 2;  // of those, in shared memory (else in tensor memory)
 template <Source S>
 constexpr int kUnits = kIsBf16<S> ? 2 : 3;  // operands of a block: keys (two halves), values
 // With three operands of a block the ring of five is short of one: the second half of the
@@ -92,18 +93,19 @@ constexpr int kUnits = kIsBf16<S> ? 2 : 3;  // operands of a block: keys (two ha
 // are used, and waited for only when it is needed.
 template <Source S>
 constexpr bool kLateKeys = kTiles<S> == 2 && kUnits<S> == 3;
-// Operands in the ring of keys and values: with 4-bit codes two whole blocks.
+// Operands in the ring of keys and values.
 template <Source S>
-constexpr int kSlots = S == kCodes ? 6 : 5;
+constexpr int kSlots = kTiles<S> == 1 ? 6 : 5;
 constexpr int kMaxSlots = 6;
 template <Source S>
-constexpr int kThreadsOf = S == kCodes ? 512 : 384;
+constexpr int kThreadsOf = S == kCodes ? 512 : S == kBf16Few ? 256 : 384;
 
 struct PromptShared {
   uint64_t q_full, full[kMaxSlots];
-  // done[n % 2]: the products with the values of block n and the keys of block n + 1
-  // are complete (two barriers, so that no waiter can be a whole turn behind)
-  uint64_t s_full[2], p_ready[2], o_full[2], done[2], drain;
+  // done[n % 4]: the products with the values of block n and the keys of block n + 1
+  // are complete (the ring holds fewer than four blocks, so no waiter can be a whole turn
+  // behind)
+  uint64_t s_full[2], p_ready[2], o_full[2], done[4], drain;
   uint64_t v_free[2];  // kLateKeys: the products with the values of block n are complete
   uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
   uint32_t tmem;
@@ -146,7 +148,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Prompt
 }
 
 __device__ __forceinline__ bool block_done(int n, PromptShared& sh) {
-  return wait_warp(&sh.done[n & 1], (n >> 1) & 1, sh);
+  return wait_warp(&sh.done[n & 3], (n >> 2) & 1, sh);
 }
 
 // Byte offset of 16-byte chunk `cc` (0..7) of row `row` in a 64-column half-tile
@@ -622,7 +624,7 @@ __device__ void mma_role(const PromptPlace& w, PromptShared& sh, uint32_t q, uin
         if (!ok) break;
       }
     }
-    if (ok) umma_commit(last ? &sh.o_full[w.n_tiles - 1] : &sh.done[n & 1]);
+    if (ok) umma_commit(last ? &sh.o_full[w.n_tiles - 1] : &sh.done[n & 3]);
   }
   if (!ok) {
     // what was issued must end before its memory is given back
@@ -926,6 +928,7 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
       mbar_init(&sh.p_ready[t], kRows / 32 + (kTiles<S> == 2 && t == 0 ? 1 : 0));
       mbar_init(&sh.o_full[t], 1);
       mbar_init(&sh.done[t], 1);
+      mbar_init(&sh.done[2 + t], 1);
       mbar_init(&sh.v_free[t], 1);
     }
     mbar_init(&sh.drain, 1);
@@ -945,9 +948,10 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
   // arithmetic of every tensor memory access (662 us, not 673, for 8K tokens of 4-bit pages).
   constexpr uint32_t tmem = 0;
 
-  // registers per warpgroup: the launch's 504 (512) between them
+  // registers per warpgroup: the launch's 504 (512) between them; 256 threads have
+  // enough each
   if (warp < 4) {
-    set_registers_down<S == kCodes ? 72 : 88>();
+    if constexpr (S != kBf16Few) set_registers_down<S == kCodes ? 72 : 88>();
     if (warp == 0) {
       if ((tid & 31) == 0 && w.j1 > w.j0) mma_role<S>(w, sh, smem_u32(smem), smem_u32(ring), tmem);
       __syncwarp();
@@ -957,11 +961,11 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
       landed_role<S>(w, sh);
     }
   } else if (warp < 4 + 4 * kTiles<S>) {
-    set_registers_up<208>();
+    if constexpr (S != kBf16Few) set_registers_up<208>();
     softmax_role<S, P>(a, w, sh, smem, tmem);
-  } else {
+  } else if constexpr (S == kCodes) {
     set_registers_down<112>();
-    if constexpr (S == kCodes) convert_role<P>(w, sh, smem_u32(ring), smem_u32(raw));
+    convert_role<P>(w, sh, smem_u32(ring), smem_u32(raw));
   }
   __syncwarp();
   tc_fence_before();
@@ -1055,7 +1059,7 @@ template <int P>
 cudaError_t launch_page(const PromptArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   if constexpr (P == 16)
     if (!a.q4 && a.planes) return launch<kBf16Planes, P>(a, tk, tv, s);
-  if (!a.q4) return launch<kBf16Pages, P>(a, tk, tv, s);
+  if (!a.q4) return a.one_tile ? launch<kBf16Few, P>(a, tk, tv, s) : launch<kBf16Pages, P>(a, tk, tv, s);
   return a.planes ? launch<kPlanes, P>(a, tk, tv, s) : launch<kCodes, P>(a, tk, tv, s);
 }
 
