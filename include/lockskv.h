@@ -18,7 +18,8 @@
  * counts the new tokens, as in locks.h).  With cu_tokens NULL row b is the one
  * newest token of sequence b, `total` is the batch, and a sequence of length 0
  * (an idle slot of a padded batch) has none.  Rows from cu_tokens[batch] on
- * belong to nobody: they are neither read nor written.
+ * belong to nobody: what they hold has no effect, and nothing is written to
+ * them or for them.
  */
 #ifndef LOCKSKV_H_
 #define LOCKSKV_H_
