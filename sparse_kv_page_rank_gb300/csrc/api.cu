@@ -463,11 +463,13 @@ locks_status_t check_err_ws(void* ws, size_t bytes) {
 // 4-bit pages: up to this many (token, head) rows of a KV head take the kernel for one
 // query token, kQ4RowColumns at a time; a pass over the pages per eight rows, against
 // one of the tensor cores' kernel, whose softmax and conversion cost the same for 8
-// rows as for 128.  8 sequences of 12,000 tokens, 8 KV heads, in us: 4 rows 41 against
-// 155, 20 rows 79 and 159, 48 rows 137 and 161, 64 rows 174 and 164.
-constexpr int kFewRows = 48;
+// rows as for 128.  8 sequences of 12,000 tokens, 8 KV heads, in us: 4 rows 35 against
+// 150, 20 rows 79 and 155, 40 rows 121 and 132, 48 rows 143 and 132.
+constexpr int kFewRows = 40;
 // 4-bit pages: from this many row tiles of a head on, its keys and values are
-// converted once for all of them, where the planes take no more than this.
+// converted once for all of them, where the planes take no more than this.  8 KV heads,
+// in us (planes, codes): 131,000 keys, 3 tiles 456, 434; 4 tiles 457, 578; 12 tiles 1024,
+// 1623; 16 sequences of 3000, 3 tiles 195, 190; 4 tiles 205, 238.
 constexpr int kPlaneTiles = 4;
 // bf16 pages of 16 tokens: the same, against their many small copies.  One sequence of
 // 131,000 tokens, 8 KV heads of 4 heads, in us (planes, pages): 200 new tokens (7 tiles)
