@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t pair_mask(int t, int len) {
 }
 
 // One warp's share of a problem.  TPU: 16-token tiles per turn (one buffer); NT:
-// blocks of 8 columns.  A column is a query head of the group, with ROWS one of one of
+// blocks of 8 columns.  A column is a query head of the group; with ROWS that of one of
 // several query tokens, which do not all see the last keys.
 template <int P, int TPU, int NT, bool LSE, bool ROWS = false>
 struct Q4Warp {

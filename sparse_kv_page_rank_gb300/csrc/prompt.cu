@@ -46,9 +46,8 @@
 // the token at the end.
 //
 // Few row tiles, or some left over after whole waves of CTAs: the keys of a tile are cut
-// among several CTAs, whose partial
-// (reference, sum, O) go to the workspace; a second, dependent kernel joins them, a warp
-// per row.  (The last CTA to finish did it before, alone: 64 tokens over 131,000, 8 KV
+// among several CTAs, whose partial (reference, sum, O) go to the workspace; a second,
+// dependent kernel joins them, a warp per row.  (The last CTA to finish did it before, alone: 64 tokens over 131,000, 8 KV
 // heads, 260 us, now 154.)
 //
 // Measured, 32 heads over 8 KV heads: 2048 new tokens of two sequences over caches of up
@@ -76,7 +75,7 @@ constexpr int kMaxBad = 2 * kRows;           // tokens near a diagonal: no more 
 constexpr float kLazy = 8.f;                 // growth of a maximum (base 2) that O's reference tolerates
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;             // S: columns 0 and 128; O: 256 and 384
-constexpr uint32_t kTmemQ = 384;             // kCodes: the queries, in place of a second O
+constexpr uint32_t kTmemQ = 384;             // one tile: the queries, in place of a second O
 
 // Where the operands come from.
 enum Source { kBf16Pages, kBf16Few, kBf16Planes, kPlanes, kCodes };
