@@ -284,3 +284,36 @@ def test_the_step_without_a_workspace_over_4_bit_pages():
     err = torch.full((1,), 77, dtype=torch.int32, device="cuda")
     L.locks_decode_step_static(rt.cache, rt.summary, rt.params, q, got, glse, None, None, err)
     assert int(err) == 0 and torch.equal(got, out) and torch.equal(glse, lse)
+
+
+@pytest.mark.parametrize("fmt,P", [("bf16", 64), ("bf16", 16), ("q4", 64), ("q4", 16)])
+def test_pages_beyond_4_gib_of_a_pool(fmt, P):
+    """The same pages in a small pool and at the end of a large one give the same bits."""
+    from sparse_kv_page_rank_gb300.runtime import LocksRuntime
+    small = Case([700, 90], 16, 8, P, fmt, seed=P)
+    page_bytes = small.k[0].numel() * small.k.element_size()
+    pages = (9 << 30) // 2 // page_bytes
+    shift = pages - small.k.shape[0]
+    pools = []
+    for x in (small.k, small.v):
+        if x is not None:
+            big = torch.empty((pages,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda")
+            big[shift:] = x
+            pools.append(big)
+    high_table = small.table + shift
+    rt = small.runtime()
+    high = LocksRuntime(pools[0], pools[1] if len(pools) == 2 else None, high_table, small.seq, small.nsum, 16, 2, 0)
+    rope, gen = table(800, D), torch.Generator().manual_seed(1)
+    for new in ([3, 1], [400, 80]):
+        cu = cu_of(new)
+        qkv = torch.randn(sum(new), 32, D, generator=gen).bfloat16().cuda()
+        got = []
+        for r in (rt, high):
+            q = r.append(qkv[:, 16:24], qkv[:, 24:], qkv[:, :16], rope=rope, cu_tokens=cu, max_tokens=max(new))
+            k, v = r.read_tokens(sum(new), cu_tokens=cu, max_tokens=max(new))
+            out, lse = r.prompt_attend(q, cu_tokens=cu, max_tokens=max(new))
+            dec, dlse = r.dense_decode(q[:2].contiguous())
+            got.append([q, k, v, out, lse, dec.clone(), dlse.clone()])
+            assert r.device_error() == 0
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
