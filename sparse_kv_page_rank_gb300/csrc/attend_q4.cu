@@ -30,11 +30,17 @@
 //
 // Precision.  q is scaled by a power of two to fit fp16 (bf16's 8 bits are exact
 // there); logits, maxima, sums and outputs are fp32.  Weights are rounded to fp16
-// twice (2^-11 each, before and after their scale).  They are kept in fp16's range
-// by the reference R of the softmax, from which weights grow up to 2^x, x chosen from
-// the largest value scale seen, so that weight * scale stays below 2^15 and weights
-// 2^-30 below the largest still count.  R moves only when a token outgrows it, so the
-// usual unit needs no maximum across lanes, only a vote.
+// twice (2^-11 each, before and after their scale).  Two things keep both in fp16's
+// range.  The reference R of the softmax lets a warp's largest weight lie between 2^11
+// and 2^15.  And value scales are multiplied by the power of two that brings the largest
+// that the warp has seen to between 1/2 and 1 (or between 1/4 and 1 as it is), which its
+// outputs give back in fp32 at the end; so weight * scale stays below 2^15, and how small
+// a cache's values are takes no bits from the weights.  Below 2^-14 fp16 is no finer than
+// 2^-24: each rounding is off by 2^-25 at most, 2^-36 of the largest weight for the first
+// and, for the second, 2^-34 of the largest weight times the largest scale.  R and the
+// power of two move only when a token outgrows them, so the usual unit needs no maximum
+// across lanes, only a vote.  (32 sequences of 9K take 64.8 us, and 1.8 us more where the
+// scales are multiplied.)
 //
 // Buffers.  Every warp copies for itself: its lane 0 issues bulk copies of whole pages
 // into the warp's own two 64-token buffers (9216 or 4 x 2304 contiguous bytes; with
@@ -52,11 +58,11 @@
 // Over a page list, a few pages of each problem: one thread-block cluster per problem,
 // whose CTAs push their partial states to each other through distributed shared memory.
 //
-// Measured (floor by bytes): 131,001 tokens of 8 KV heads, 4 heads each, 31.9 us (22.3),
-// streaming at 6.97 TB/s; 32 sequences of up to 9216 tokens in 16-token pages 63.8 us
-// (40.0); 1M tokens of 2 KV heads, 16 heads each, 87.4 us (44.5); 4096 tokens of one
+// Measured (floor by bytes): 131,001 tokens of 8 KV heads, 4 heads each, 32.8 us (22.3),
+// streaming at 6.97 TB/s; 32 sequences of up to 9216 tokens in 16-token pages 64.8 us
+// (40.0); 1M tokens of 2 KV heads, 16 heads each, 87.7 us (44.5); 4096 tokens of one
 // head 6.4 us; a list of 32 pages of 8 KV heads 7.7 us.  Five rows over eight sequences
-// of up to 16,411 tokens 58 us (14.2).
+// of up to 16,411 tokens 60 us (14.2).
 #include <algorithm>
 #include <type_traits>
 
@@ -97,6 +103,20 @@ __device__ __forceinline__ void fields64(uint32_t w, uint32_t (&f)[4]) {
   f[2] = sub_f16x2(field_under<0x000f000fu, 0x64006400u>(v), 0x63806380u);
   f[3] = field_under<0x00f000f0u, 0x54005400u>(v);
 }
+// The lowest power of two above the finite half with bits `h`, as half bits: 0x7c00
+// stands for 2^16, which is where it lies in order.
+__device__ __forceinline__ uint32_t half_limit(uint32_t h) {
+  return h < 0x400u ? 1u << (32 - __clz(h)) : (h >> 10) + 1 << 10;
+}
+// Its number, and half bits of its inverse; below 2^-14 of 2^-9 times the inverse, which a half can hold.
+__device__ __forceinline__ float limit_value(uint32_t lim) {
+  return __uint_as_float((lim < 0x400u ? 134 - __clz(lim) : (lim >> 10) + 112) << 23);
+}
+__device__ __forceinline__ uint32_t limit_inverse(uint32_t lim) {
+  if (lim < 0x400u) return (__clz(lim) - 1) << 10;
+  const int e = lim >> 10;
+  return e < 30 ? (30 - e) << 10 : 0x400u >> (e - 29);
+}
 // D = A B + C with an accumulator that is not overwritten.
 __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1, const float (&c)[4]) {
@@ -127,6 +147,7 @@ struct Q4Warp {
   // one block of heads has the registers to start its products at the codes' offset
   static constexpr bool kBiased = NT == 1;
   static_assert(!LSE || (kPages == 1 && kUPP == 1), "a unit of the page LSE is one page");
+  static constexpr uint32_t kOne = 0x3c003c00u;  // two halves 1
   using At = Q4Tile<P, TPU>;
 
   Q4Shared& sh;
@@ -139,7 +160,7 @@ struct Q4Warp {
   float fac[NT][2];      // logit factor of heads 2c, 2c + 1
   float R[NT][2], l[NT][2];  // their softmax reference (base 2) and sum
   float o[4][2][NT][4];  // their outputs: dimensions 32 j + 4 g + 2 half, + 1 (rows)
-  int x;                 // exponent offset of the weights, lowered by large value scales
+  uint32_t zlim, zup;    // the power of two above every value scale so far, and its inverse (twice), as halves
   int seq;               // units consumed so far: buffer seq % kBufs, phase seq / kBufs
   // ROWS: keys at the end that heads 2c, 2c + 1 and head g, and the first column, do not see
   int back[NT][2], back_g[NT], back_max;
@@ -148,11 +169,21 @@ struct Q4Warp {
 
   __device__ __forceinline__ Q4Warp(Q4Shared& s, uint32_t ring, int grp)
       : sh(s), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2), c(threadIdx.x & 3),
-        group(grp), wbase(ring + (threadIdx.x >> 5) * kWarpTiles * kTileBytes), x(15), seq(0), back_max(0), page_lse(nullptr),
+        group(grp), wbase(ring + (threadIdx.x >> 5) * kWarpTiles * kTileBytes), seq(0), back_max(0), page_lse(nullptr),
         lse_stride(0) {}
 
+  __device__ __forceinline__ void set_limit(uint32_t lim) {
+    zlim = lim == 0x3800u ? 0x3c00u : lim;  // 1/2 counts as 1, which costs no multiplication
+    zup = limit_inverse(zlim) * 0x10001u;
+  }
+  // Two scales times the power of two under which the largest so far is below 1.
+  __device__ __forceinline__ uint32_t scaled_up(uint32_t z) const {
+    if (zlim < 0x400u) z = mul_f16x2(z, 0x60006000u);  // 2^9
+    return mul_f16x2(z, zup);
+  }
+
   __device__ __forceinline__ void reset() {
-    x = 15;
+    set_limit(2);  // 2^-23: only zeros and the smallest half lie below
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       R[nt][0] = R[nt][1] = -INFINITY;
@@ -326,9 +357,9 @@ struct Q4Warp {
           }
         }
     } else {
-      // The weights 2^(s - R) have to stay below 2^x, and 2^x times the largest value
-      // scale below 2^15.  R is moved, and x lowered, only when a token or a scale of
-      // the unit breaks that; then the largest weight becomes 2^(x - 4).
+      // The weights 2^(s - R) have to stay below 2^15, and the value scales below the
+      // limit.  R or the limit is moved only when a token or a scale of the unit breaks
+      // that; then the largest weight becomes 2^11.
       uint32_t top = 0;  // largest scale of this lane's 16 bytes, as half bits
       if (lane < 8 * kTiles) {
         const int t = t0 + (lane >> 3);
@@ -342,24 +373,42 @@ struct Q4Warp {
         const uint32_t v = __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w));
         top = max(v & 0xffffu, v >> 16);
       }
-      const float fx = (float)x;
-      bool moved = (int)(top >> 10) > 29 - x;
+      bool moved = top >= zlim;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) moved |= fmaf(mx[nt][k], fac[nt][k], -R[nt][k]) > fx;
+        for (int k = 0; k < 2; ++k) moved |= fmaf(mx[nt][k], fac[nt][k], -R[nt][k]) > 15.f;
       if (__any_sync(0xffffffffu, moved)) {
         whole_max();
-        // half bits -> exponent; a NaN scale (its product is NaN anyway) counts as the largest
-        x = min(x, 29 - min((int)(__reduce_max_sync(0xffffffffu, top) >> 10), 29));
+        float down = 1.f;
+        uint32_t largest = __reduce_max_sync(0xffffffffu, top);
+        if (largest >= 0x7c00u) {
+          // a NaN stays one under any power of two, and must not take the others' bits
+          top = 0;
+          const int t = lane >> 3, u = 8 * (lane & 1) + 2 * ((lane & 7) >> 1);  // tile, first of two tokens
+          const int ln = lane >= 8 * kTiles ? 0 : P == 64 ? sh.len[warp][buf][0] - 16 * (t0 + t) : sh.len[warp][buf][t0 + t];
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e) {
+            if (u + (e & 1) >= ln) continue;
+            const uint32_t h = lds16(base + At::value_scales(t0 + t) + (lane & 7) * 16 + 2 * e);
+            if (h < 0x7c00u) top = max(top, h);
+          }
+          largest = __reduce_max_sync(0xffffffffu, top);
+        }
+        if (largest >= zlim) {
+          const float was = limit_value(zlim);
+          set_limit(half_limit(largest));
+          down = was * __uint_as_float((254u << 23) - __float_as_uint(limit_value(zlim)));  // powers of two
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float Rn = fmaxf(R[nt][k], mx[nt][k] - (float)(x - 4));
-            const float al = Rn == -INFINITY ? 1.f : fast_exp2(R[nt][k] - Rn);
+            const float Rn = fmaxf(R[nt][k], mx[nt][k] - 11.f);
+            float al = Rn == -INFINITY ? 1.f : fast_exp2(R[nt][k] - Rn);
             R[nt][k] = Rn;
             l[nt][k] *= al;
+            al *= down;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -369,53 +418,62 @@ struct Q4Warp {
               }
           }
       }
-      // ---- weights and the values they weight ----
+      // ---- weights and the values they weight ---- (two copies of the code: a branch per
+      // tile would keep the tiles' loads apart, 65.1 us for 63.9 on 32 sequences of 9K)
+      auto weigh = [&](auto scaled) {
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // a column that has seen no key yet has the reference -infinity
-            const float ref = ROWS && !WHOLE && R[nt][k & 1] == -INFINITY ? 0.f : R[nt][k & 1];
-            p[k] = fast_exp2(fmaf(sc[t][nt][k], fac[nt][k & 1], -ref));
-            l[nt][k & 1] += p[k];
-          }
-          pb[nt][0] = transpose8x8(pack_f16(p[0], p[1]));  // tokens 2c, 2c + 1 of head g
-          pb[nt][1] = transpose8x8(pack_f16(p[2], p[3]));  // tokens 8 + 2c, + 1
-        }
-        const uint4 v0 = lds128(base + At::value_codes(t0 + t) + lane * 16), v1 = lds128(base + At::value_codes(t0 + t) + 512 + lane * 16);
-        uint4 z0 = lds128(base + At::value_scales(t0 + t) + c * 32), z1 = lds128(base + At::value_scales(t0 + t) + c * 32 + 16);
-        if constexpr (!WHOLE) {
-          // scales past the end may be anything, a NaN too
-          const uint32_t m0 = pair_mask(2 * c, left[t]), m1 = pair_mask(8 + 2 * c, left[t]);
-          z0.x &= m0; z0.y &= m0; z0.z &= m0; z0.w &= m0;
-          z1.x &= m1; z1.y &= m1; z1.z &= m1; z1.w &= m1;
-        }
-        const uint32_t vw0[4] = {v0.x, v0.y, v0.z, v0.w}, vw1[4] = {v1.x, v1.y, v1.z, v1.w};
-        const uint32_t zw0[4] = {z0.x, z0.y, z0.z, z0.w}, zw1[4] = {z1.x, z1.y, z1.z, z1.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-          q4_codes01(vw0[j], a0, a1);
-          q4_codes01(vw1[j], a2, a3);
-          q4_codes01(vw0[j] >> 8, b0, b1);
-          q4_codes01(vw1[j] >> 8, b2, b3);
+        for (int t = 0; t < kTiles; ++t) {
+          uint32_t pb[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            uint32_t p0 = mul_f16x2(pb[nt][0], zw0[j]), p1 = mul_f16x2(pb[nt][1], zw1[j]);
-            if constexpr (ROWS && !WHOLE) {
-              // 0 * NaN: a token that the column does not see
-              p0 &= pair_mask(2 * c, left[t] - back_g[nt]);
-              p1 &= pair_mask(8 + 2 * c, left[t] - back_g[nt]);
+            float p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // a column that has seen no key yet has the reference -infinity
+              const float ref = ROWS && !WHOLE && R[nt][k & 1] == -INFINITY ? 0.f : R[nt][k & 1];
+              p[k] = fast_exp2(fmaf(sc[t][nt][k], fac[nt][k & 1], -ref));
+              l[nt][k & 1] += p[k];
             }
-            mma_16816_f16(o[j][0][nt], a0, a1, a2, a3, p0, p1);
-            mma_16816_f16(o[j][1][nt], b0, b1, b2, b3, p0, p1);
+            pb[nt][0] = transpose8x8(pack_f16(p[0], p[1]));  // tokens 2c, 2c + 1 of head g
+            pb[nt][1] = transpose8x8(pack_f16(p[2], p[3]));  // tokens 8 + 2c, + 1
+          }
+          const uint4 v0 = lds128(base + At::value_codes(t0 + t) + lane * 16), v1 = lds128(base + At::value_codes(t0 + t) + 512 + lane * 16);
+          uint4 z0 = lds128(base + At::value_scales(t0 + t) + c * 32), z1 = lds128(base + At::value_scales(t0 + t) + c * 32 + 16);
+          if constexpr (!WHOLE) {
+            // scales past the end may be anything, a NaN too
+            const uint32_t m0 = pair_mask(2 * c, left[t]), m1 = pair_mask(8 + 2 * c, left[t]);
+            z0.x &= m0; z0.y &= m0; z0.z &= m0; z0.w &= m0;
+            z1.x &= m1; z1.y &= m1; z1.z &= m1; z1.w &= m1;
+          }
+          if constexpr (scaled) {
+            z0 = make_uint4(scaled_up(z0.x), scaled_up(z0.y), scaled_up(z0.z), scaled_up(z0.w));
+            z1 = make_uint4(scaled_up(z1.x), scaled_up(z1.y), scaled_up(z1.z), scaled_up(z1.w));
+          }
+          const uint32_t vw0[4] = {v0.x, v0.y, v0.z, v0.w}, vw1[4] = {v1.x, v1.y, v1.z, v1.w};
+          const uint32_t zw0[4] = {z0.x, z0.y, z0.z, z0.w}, zw1[4] = {z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+            q4_codes01(vw0[j], a0, a1);
+            q4_codes01(vw1[j], a2, a3);
+            q4_codes01(vw0[j] >> 8, b0, b1);
+            q4_codes01(vw1[j] >> 8, b2, b3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t p0 = mul_f16x2(pb[nt][0], zw0[j]), p1 = mul_f16x2(pb[nt][1], zw1[j]);
+              if constexpr (ROWS && !WHOLE) {
+                // 0 * NaN: a token that the column does not see
+                p0 &= pair_mask(2 * c, left[t] - back_g[nt]);
+                p1 &= pair_mask(8 + 2 * c, left[t] - back_g[nt]);
+              }
+              mma_16816_f16(o[j][0][nt], a0, a1, a2, a3, p0, p1);
+              mma_16816_f16(o[j][1][nt], b0, b1, b2, b3, p0, p1);
+            }
           }
         }
-      }
+      };
+      if (zup == kOne) weigh(std::false_type{});
+      else weigh(std::true_type{});
     }
   }
 
@@ -529,6 +587,7 @@ struct Q4Warp {
     float* so = reinterpret_cast<float*>(ring);  // [kW][8 NT][kOStride]
     float* octa = so + kW * 8 * NT * kOStride;   // [16][128]
     const int tid = threadIdx.x, G = group;
+    const float back = limit_value(zlim);  // the power of two that the scales were held under
     __syncthreads();  // the buffers are no longer read, nor written by copies
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -547,7 +606,8 @@ struct Q4Warp {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<float4*>(so + (warp * 8 * NT + h) * kOStride + 32 * j + 4 * g) =
-                make_float4(o[j][0][nt][k], o[j][0][nt][2 + k], o[j][1][nt][k], o[j][1][nt][2 + k]);
+                make_float4(o[j][0][nt][k] * back, o[j][0][nt][2 + k] * back, o[j][1][nt][k] * back,
+                            o[j][1][nt][2 + k] * back);
       }
     __syncthreads();
     if (tid < G) {
