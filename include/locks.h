@@ -105,6 +105,8 @@ typedef enum {
 /* Bytes of one page-head of a LOCKS_KV_Q4 cache (keys and values together,
  * head_dim 128): 144 per token, 28% of the 512 of a bf16 token. */
 #define LOCKS_KV_Q4_BLOCK_BYTES(P) (144 * (P))
+/* Largest scale of such a page. */
+#define LOCKS_KV_Q4_MAX_SCALE 9352
 
 /* Paged KV cache.  K and V pools hold whole pages for all KV heads:
  *   k_pool, v_pool  bf16 [pages_total][num_kv_heads][page_size][head_dim]
@@ -124,9 +126,13 @@ typedef enum {
  *                   [pages_total][num_kv_heads][bytes], base 16-byte aligned,
  *                   with the page's keys and values; v_pool is unused.  Each
  *                   32 consecutive dimensions (32j .. 32j+31) of a token's key
- *                   and of its value have a half-precision scale s >= 0 and 32
+ *                   and of its value have a half-precision scale s and 32
  *                   codes in [-7, 7], stored as code + 8; the element is
- *                   s * code.  Token t of the page, dimension d, j = d/32:
+ *                   s * code.  0 <= s <= 9352 (LOCKS_KV_Q4_MAX_SCALE, the
+ *                   largest whose 7-fold is finite in half precision, where
+ *                   prompt attention holds s * code; beyond it the element
+ *                   is infinite there).  Token t of the page, dimension d,
+ *                   j = d/32:
  *                     byte 0      key codes, 64 bytes per token: element d in
  *                                 the little-endian 32-bit word at 64 t +
  *                                 16 ((d%32)/8) + 4 j, bits

@@ -133,9 +133,7 @@ __device__ __forceinline__ __half quantise8(uint4 x, uint32_t (&u)[8]) {
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const bool finite = m < 0x7f80u;
-  // 9352 = the largest half whose 7-fold is finite in half precision, where
-  // attention over prompts holds s * code
-  const __half s = finite ? __float2half_rn(fminf(__fdiv_rn(__uint_as_float(m << 16), 7.f), 9352.f))
+  const __half s = finite ? __float2half_rn(fminf(__fdiv_rn(__uint_as_float(m << 16), 7.f), (float)LOCKS_KV_Q4_MAX_SCALE))
                           : __ushort_as_half((unsigned short)0x7fff);
   const float sf = __half2float(s);
   const float r = finite && sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;
