@@ -405,9 +405,11 @@ __device__ void convert_role(const PromptPlace& w, PromptShared& sh, uint32_t ri
     const int s = 2 * n + hh, rs = s % kRawSlots, i = 3 * n;
     const uint32_t src = raw + rs * kQ4Slot;
     // both halves' codes: every warp sees every phase of every slot, in order, so that
-    // none can take an earlier phase for the one it waits for
+    // none can take an earlier phase for the one it waits for; and the other half's slot is
+    // filled anew only when this warp has seen it full, so that no phase passes it by
     for (int y = 2 * n; y < 2 * n + 2; ++y)
       if (!wait_warp(&sh.raw_full[y % kRawSlots], (y / kRawSlots) & 1, sh)) return;
+    if (lane == 0) mbar_arrive(&sh.raw_empty[(2 * n + 1 - hh) % kRawSlots]);
     // the ring holds two blocks: that of n - 2 makes room, its keys when block n - 3 is
     // done (the first block's with the second's), its values when it is
     if (n >= 2 && !done_until(max(0, n - 3))) return;
@@ -933,7 +935,7 @@ __global__ void __launch_bounds__(kThreadsOf<S>, 1)
     mbar_init(&sh.drain, 1);
     for (int s = 0; s < kRawSlots; ++s) {
       mbar_init(&sh.raw_full[s], 1);
-      mbar_init(&sh.raw_empty[s], 4);
+      mbar_init(&sh.raw_empty[s], 8);
     }
     fence_mbar_init();
     sh.abort = 0;
