@@ -28,6 +28,11 @@ class LocksRuntime:
     ``form``: "auto" (the library's choice: three kernels), or "unfused" /
     "fused" for LOCKS_FLAG_UNFUSED / LOCKS_FLAG_FUSED (the decode step as three
     kernels, or as two wherever the size limits allow).
+
+    One workspace serves all decode calls and one all prompt attention: the
+    caller orders calls of a kind that are on different streams, and replays of
+    graphs that hold them (an event between them, or a LocksRuntime over the
+    same tensors for each).
     """
 
     def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor | None, block_table: torch.Tensor,
@@ -145,8 +150,20 @@ class LocksRuntime:
         """An output of a call on `stream`, whose memory belongs to that stream."""
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream):
+        with self._on(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _on(self, stream):
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream)
+
+    def _capturing(self, stream) -> bool:
+        """Whether the current stream, or the one that a call is given, is being captured."""
+        if torch.cuda.is_current_stream_capturing():
+            return True
+        if stream is None:
+            return False
+        with self._on(stream):
+            return torch.cuda.is_current_stream_capturing()
 
     def _tokens(self, total: int, cu_tokens: torch.Tensor | None, max_tokens: int | None):
         if cu_tokens is None:
@@ -216,9 +233,9 @@ class LocksRuntime:
         q bf16 [total][Hq][128] -> out bf16 [total][Hq][128], lse float32
         [total][Hq] (new tensors by default).
 
-        The workspace grows with the calls and is shared by all of them, so
-        they run one after another; a call is captured into a graph after one
-        of the same max_tokens has run."""
+        The workspace grows with the calls and is shared by all of them (see
+        the class on calls that could overlap); a call is captured into a graph
+        after one of the same max_tokens has run."""
         total = q.shape[0]
         if q.dim() != 3 or q.shape[1] != self.num_q_heads or not q.is_cuda:
             raise ValueError(f"q must be [tokens][{self.num_q_heads}][128] on the device")
@@ -237,7 +254,7 @@ class LocksRuntime:
         if need is None:
             need = L.lockskv_prompt_workspace_size(self.cache, self.params, tokens)
             self._prompt_need[tokens.max_tokens] = need
-        capturing = torch.cuda.is_current_stream_capturing()
+        capturing = self._capturing(stream)
         if self.prompt_ws is None or self.prompt_ws.numel() < need:
             self._grow_prompt_ws(need, capturing)
         self._prompt_captured |= capturing
