@@ -483,6 +483,12 @@ struct PromptPlan {
   size_t off_ml = 0, off_o = 0, off_planes = 0, total = 0;
 };
 
+// The most new tokens that a sequence can have: what the caller says, but no more than its
+// table holds (the bound may be any number, where the caller knows none).
+int most_tokens(const locks_cache_t* c, const lockskv_tokens_t* t) {
+  return std::min(t->max_tokens, c->max_pages * c->page_size);
+}
+
 // Row tiles that do not fill a wave of CTAs (all of them, or what is left over after
 // whole waves) have their keys cut as well, down to about two blocks of 128 per CTA: into
 // the number of parts whose waves take least, in blocks' times, a part costing some eight
@@ -491,11 +497,11 @@ struct PromptPlan {
 // 1094, 1175.  With many waves the gain is small.
 constexpr int kCutWaves = 8;
 constexpr double kPartBlocks = 8.0, kPartialBlocks = 0.02;
-locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, const lockskv_tokens_t* t, PromptPlan* pl) {
+locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, int max_tokens, PromptPlan* pl) {
   const int G = p->num_q_heads / c->num_kv_heads, per_tile = 128 / G;  // tokens of a 128-row tile
   const long long BH = (long long)c->batch * c->num_kv_heads;
   const long long blocks = ((long long)c->max_pages * c->page_size + 127) / 128;
-  const long long tiles = std::max(1, (t->max_tokens + per_tile - 1) / per_tile);
+  const long long tiles = std::max(1LL, ((long long)max_tokens + per_tile - 1) / per_tile);
   const long long plane_bytes = (is_q4(c) ? 3 : 2) * BH * blocks * 128 * kHeadDim * 2;
   pl->planes = plane_bytes <= kPlaneBytes &&
                (is_q4(c) ? tiles >= kPlaneTiles : c->page_size == 16 && tiles >= kBf16PlaneTiles);
@@ -506,7 +512,7 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
   // what is left over after whole waves of CTAs; where the tiles' keys differ much, the
   // last ones have few and fill the gaps
   long long cut = ctas % sms;
-  if (ctas > sms && (ctas > kCutWaves * sms || 2LL * t->max_tokens > (long long)c->max_pages * c->page_size)) cut = 0;
+  if (ctas > sms && (ctas > kCutWaves * sms || 2LL * max_tokens > (long long)c->max_pages * c->page_size)) cut = 0;
   // their time in blocks: waves of parts, each with a fixed cost, and the partial results
   double best = (double)blocks + kPartBlocks;
   pl->n_splits = 1;
@@ -517,8 +523,8 @@ locks_status_t plan_prompt(const locks_cache_t* c, const locks_params_t* p, cons
   if (pl->n_splits == 1) cut = 0;
   pl->n_whole = (int)(ctas - cut);
   size_t parts = (size_t)cut * pl->n_splits * 256;
-  if (is_q4(c) && (long long)t->max_tokens * G <= kFewRows) {
-    const long long slots = BH * ((t->max_tokens * G + kQ4RowColumns - 1) / kQ4RowColumns) *
+  if (is_q4(c) && (long long)max_tokens * G <= kFewRows) {
+    const long long slots = BH * ((max_tokens * G + kQ4RowColumns - 1) / kQ4RowColumns) *
                             (((long long)c->max_pages * c->page_size + kPage - 1) / kPage);
     pl->row_ctas = std::max(1, q4_dense_ctas(slots, (int)sms));
     pl->row_tiles = q4_tiles_for(slots / pl->row_ctas);
@@ -808,7 +814,7 @@ locks_status_t lockskv_prompt_workspace_size(const locks_cache_t* cache, const l
   if ((st = check_params(cache, params)) != LOCKS_OK) return st;
   if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
   PromptPlan pl;
-  if ((st = plan_prompt(cache, params, tokens, &pl)) != LOCKS_OK) return st;
+  if ((st = plan_prompt(cache, params, most_tokens(cache, tokens), &pl)) != LOCKS_OK) return st;
   *bytes = pl.total;
   return LOCKS_OK;
 }
@@ -824,7 +830,7 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   if (!q || !out || (reinterpret_cast<uintptr_t>(out) & 15)) return LOCKS_ERR_INVALID_ARG;
   if ((st = check_rows(q, q_stride, (int64_t)params->num_q_heads * kHeadDim)) != LOCKS_OK) return st;
   PromptPlan pl;
-  if ((st = plan_prompt(cache, params, tokens, &pl)) != LOCKS_OK) return st;
+  if ((st = plan_prompt(cache, params, most_tokens(cache, tokens), &pl)) != LOCKS_OK) return st;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) || ws_bytes < pl.total) return LOCKS_ERR_WORKSPACE;
   if (tokens->max_tokens == 0) return LOCKS_OK;
   if (pl.row_ctas > 0) {
@@ -847,7 +853,7 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
     r.pages_total = cache->pages_total;
     r.page_size = cache->page_size;
     r.total = tokens->total;
-    r.max_tokens = tokens->max_tokens;
+    r.max_tokens = most_tokens(cache, tokens);
     r.n_splits = pl.row_ctas;
     r.cluster = 1;
     r.scale_log2 = scale_of(params) * kLog2e;
@@ -883,9 +889,9 @@ locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_par
   a.pages_total = cache->pages_total;
   a.page_size = cache->page_size;
   a.total = tokens->total;
-  a.max_tokens = tokens->max_tokens;
+  a.max_tokens = most_tokens(cache, tokens);
   a.n_qtiles = pl.n_qtiles;
-  a.one_tile = tokens->max_tokens <= 128 / a.group ? 1 : 0;
+  a.one_tile = a.max_tokens <= 128 / a.group ? 1 : 0;
   a.n_whole = pl.n_whole;
   a.n_splits = pl.n_splits;
   a.scale_log2 = scale_of(params) * kLog2e;
