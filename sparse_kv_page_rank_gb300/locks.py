@@ -66,7 +66,7 @@ class locks_cache_t(ctypes.Structure):
                 ("n_summarized", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("pages_total", ctypes.c_int32),
-                ("max_pages", ctypes.c_int32), ("kv_format", ctypes.c_int32)]
+                ("max_pages", ctypes.c_int32, 28), ("kv_format", ctypes.c_int32, 4)]
 
 
 class locks_summary_t(ctypes.Structure):
