@@ -152,11 +152,11 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device: int | None = None) -> int | None:
     if stream is None:
         import torch
         # the current stream's handle without building a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -45,6 +45,7 @@ class LocksRuntime:
             assert k_pool.dtype == torch.bfloat16 and v_pool.dtype == torch.bfloat16
         assert block_table.dtype == torch.int32 and seq_lens.dtype == torch.int32
         self.device = k_pool.device
+        self._index = k_pool.get_device()
         self.k_pool, self.v_pool = k_pool, v_pool
         self.block_table, self.seq_lens = block_table, seq_lens
         self.n_summarized = n_summarized.to(torch.int32)
@@ -165,10 +166,16 @@ class LocksRuntime:
         with self._on(stream):
             return torch.cuda.is_current_stream_capturing()
 
+    def _launch_on(self, stream) -> int:
+        """Handle of the stream of a call on tokens, which launches where the cache is or not at all."""
+        if torch.cuda.current_device() != self._index:
+            raise ValueError(f"the cache is on {self.device}, which is not the current device")
+        return L._stream(stream, self._index)
+
     def _tokens(self, total: int, cu_tokens: torch.Tensor | None, max_tokens: int | None):
         if cu_tokens is None:
             return L.make_tokens(None, total, 1)
-        if (cu_tokens.dtype is not torch.int32 or cu_tokens.numel() != self.batch + 1 or not cu_tokens.is_cuda
+        if (cu_tokens.dtype is not torch.int32 or cu_tokens.numel() != self.batch + 1 or cu_tokens.get_device() != self._index
                 or not cu_tokens.is_contiguous()):
             raise ValueError("cu_tokens must be contiguous int32 [batch + 1] on the device")
         return L.make_tokens(cu_tokens, total, total if max_tokens is None else max_tokens)
@@ -189,22 +196,25 @@ class LocksRuntime:
         rotates in place), or None without q."""
         shape = k.shape
         total = shape[0]
-        if len(shape) != 3 or shape[1] != self.num_kv_heads or v.shape != shape or not (k.is_cuda and v.is_cuda):
+        index, handle = self._index, self._launch_on(stream)
+        if (len(shape) != 3 or shape[1] != self.num_kv_heads or v.shape != shape or k.get_device() != index
+                or v.get_device() != index):
             raise ValueError(f"k and v must be [tokens][{self.num_kv_heads}][128] on the device")
         if q is not None:
             shape = q.shape
-            if len(shape) != 3 or shape[0] != total or shape[1] != self.num_q_heads or not q.is_cuda:
+            if len(shape) != 3 or shape[0] != total or shape[1] != self.num_q_heads or q.get_device() != index:
                 raise ValueError(f"q must be [{total}][{self.num_q_heads}][128] on the device")
             if q_out is None:
                 q_out = self._new(shape, torch.bfloat16, stream)
-            elif q_out.shape != shape or not q_out.is_cuda:
+            elif q_out.shape != shape or q_out.get_device() != index:
                 raise ValueError("q_out must have q's shape, on the device")
         elif q_out is not None:
             raise ValueError("q_out without q")
         if rope is None:
             rotary_dim = rotary_dim or 0
         else:
-            if rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_cuda or not rope.is_contiguous():
+            if (rope.dtype is not torch.float32 or rope.dim() != 2 or rope.get_device() != index
+                    or not rope.is_contiguous()):
                 raise ValueError("rope must be contiguous float32 [positions][rotary_dim] on the device")
             cols = rope.shape[1]
             if rotary_dim is None:
@@ -212,19 +222,20 @@ class LocksRuntime:
             elif rotary_dim != cols:
                 raise ValueError("rope must have rotary_dim columns")
         if positions is not None and (positions.dtype is not torch.int32 or positions.numel() != total
-                                      or not positions.is_cuda or not positions.is_contiguous()):
+                                      or positions.get_device() != index or not positions.is_contiguous()):
             raise ValueError("positions must be contiguous int32 [tokens] on the device")
         L.lockskv_append(self.cache, self._tokens(total, cu_tokens, max_tokens),
                          L.make_append(k, v, q, q_out, rope, rotary_dim, positions, interleaved),
-                         self.kv_ws, 256, stream)
+                         self.kv_ws, 256, handle)
         return q_out
 
     def read_tokens(self, total: int, *, cu_tokens: torch.Tensor | None = None, max_tokens: int | None = None,
                     stream=None):
         """The newest tokens' keys and values as the cache holds them: two new
         bf16 tensors [total][Hkv][128] (rows of nobody are left unwritten)."""
+        handle = self._launch_on(stream)
         k, v = (self._new((total, self.num_kv_heads, 128), torch.bfloat16, stream) for _ in range(2))
-        L.lockskv_read(self.cache, self._tokens(total, cu_tokens, max_tokens), k, v, self.kv_ws, 256, stream)
+        L.lockskv_read(self.cache, self._tokens(total, cu_tokens, max_tokens), k, v, self.kv_ws, 256, handle)
         return k, v
 
     def prompt_attend(self, q: torch.Tensor, *, cu_tokens: torch.Tensor | None = None,
@@ -237,17 +248,19 @@ class LocksRuntime:
         the class on calls that could overlap); a call is captured into a graph
         after one of the same max_tokens has run."""
         total = q.shape[0]
-        if q.dim() != 3 or q.shape[1] != self.num_q_heads or not q.is_cuda:
+        index, handle = self._index, self._launch_on(stream)
+        if q.dim() != 3 or q.shape[1] != self.num_q_heads or q.get_device() != index:
             raise ValueError(f"q must be [tokens][{self.num_q_heads}][128] on the device")
         stride = L._row_stride(q, "q")
         tokens = self._tokens(total, cu_tokens, max_tokens)
         if out is None:
             out = self._new(q.shape, torch.bfloat16, stream)
-        elif out.shape != q.shape or out.dtype is not torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
+        elif (out.shape != q.shape or out.dtype is not torch.bfloat16 or out.get_device() != index
+              or not out.is_contiguous()):
             raise ValueError("out must be contiguous bf16 of q's shape on the device")
         if lse is None:
             lse = self._new((total, self.num_q_heads), torch.float32, stream)
-        elif (lse.shape != (total, self.num_q_heads) or lse.dtype is not torch.float32 or not lse.is_cuda
+        elif (lse.shape != (total, self.num_q_heads) or lse.dtype is not torch.float32 or lse.get_device() != index
               or not lse.is_contiguous()):
             raise ValueError(f"lse must be contiguous float32 [{total}][{self.num_q_heads}] on the device")
         need = self._prompt_need.get(tokens.max_tokens)
@@ -259,7 +272,7 @@ class LocksRuntime:
             self._grow_prompt_ws(need, capturing)
         self._prompt_captured |= capturing
         L.lockskv_prompt_attend(self.cache, self.params, tokens, q, stride, out, lse, self.prompt_ws,
-                                self.prompt_ws.numel(), stream)
+                                self.prompt_ws.numel(), handle)
         return out, lse
 
     def _grow_prompt_ws(self, need: int, capturing: bool):
