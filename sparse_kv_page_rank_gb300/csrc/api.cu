@@ -98,7 +98,10 @@ float scale_of(const locks_params_t* p) {
 
 // Launch shapes of attend_q4.cu.  A warp takes 64 tokens at a time where a CTA has
 // at least two turns of them for its six warps, else 16 tokens, so that a few
-// pages still keep every warp busy.
+// pages still keep every warp busy.  Every page of one sequence, 64-token pages, in us
+// (64 tokens, 16) by 64-token slots per CTA: 4 heads per KV head, 1 slot 9.4, 8.4; 4 slots
+// 10.7, 11.1; 8 slots 13.4, 15.1; 12 slots 15.5, 18.5; 16 heads, 1 slot 17.3, 11.9; 8 slots
+// 22.1, 20.6; 12 slots 24.3, 24.7; 24 slots 32.6, 36.2.
 constexpr long long kQ4WholeSlots = 12;
 
 int q4_tiles_for(long long slots_per_cta) { return slots_per_cta >= kQ4WholeSlots ? 4 : 1; }
@@ -112,9 +115,10 @@ void plan_q4(const locks_cache_t* c, Plan& pl, int sms, long long max_tiles, int
     // page list: one cluster per problem, the largest with which all are resident at once
     const long long slots = ((long long)pl.k_max + 2 + ppt - 1) / ppt;
     int cs = 16;
-    while (cs > 1 && (cs > slots || BH > attend_q4_active_clusters(pl.G, P, 1, cs))) cs /= 2;
+    auto tiles = [&] { return q4_tiles_for((slots + cs - 1) / cs); };
+    while (cs > 1 && (cs > slots || BH > attend_q4_active_clusters(pl.G, P, tiles(), cs))) cs /= 2;
     pl.q4_sparse_cluster = cs;
-    pl.q4_sparse_tiles = q4_tiles_for((slots + cs - 1) / cs);
+    pl.q4_sparse_tiles = tiles();
   }
   {
     const long long slots = BH * max_tiles;
