@@ -35,7 +35,8 @@ extern "C" {
  *               total; or NULL (one token per sequence)
  *   total       rows of the token arrays
  *   max_tokens  at least every n_b (host knowledge that shapes the launch; 1
- *               when cu_tokens is NULL).  A sequence with more sets
+ *               when cu_tokens is NULL); any larger number is right too, but
+ *               makes a larger launch.  A sequence with more sets
  *               LOCKS_DEVERR_LENGTHS and its rows past max_tokens are skipped.
  * total = 0 (whose arrays may be NULL) or max_tokens = 0 is a call that does
  * nothing. */
@@ -84,7 +85,7 @@ typedef struct lockskv_append {
  * bf16; values are stored as they are.  A bf16 cache holds those bf16 numbers.
  * A LOCKS_KV_Q4 cache holds, for each 32 dimensions of them, s = half(max|x| / 7)
  * and the codes rint(x / s) clamped to [-7, 7] (ties to even; zeros where s is
- * zero).  s is at most 9352, so larger numbers saturate at +-65464; a group with
+ * zero).  s is at most LOCKS_KV_Q4_MAX_SCALE, so larger numbers saturate at +-65464; a group with
  * an infinity or a NaN gets a NaN scale.  `ws` may be NULL, or any 256-byte
  * aligned memory whose first word is the device error word
  * (locks_get_device_error).  Two sequences must not share a page that either of
@@ -101,7 +102,11 @@ LOCKS_API locks_status_t lockskv_read(const locks_cache_t* cache, const lockskv_
                                       void* v_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace lockskv_prompt_attend needs for these shapes (at least
- * 256).  Zero it once (locks_workspace_init) before its first use; calls of any
+ * 256).  It is planned for sequences as long as the block table is wide, not
+ * for their lengths: from 385 (token, head) rows of a KV head on, 4-bit pages
+ * are turned into fp16 planes of 768 bytes per KV head and token of the table (16-token
+ * bf16 pages: 512 bytes, from 897 rows on), unless those exceed 4 GiB.
+ * A narrower table (fewer max_pages, the same pages) needs less.  Zero it once (locks_workspace_init) before its first use; calls of any
  * shapes that it is large enough for may then share it, one after another.  Two
  * calls, or replays of two captured graphs, that may run at the same time need
  * a workspace each. */
@@ -115,7 +120,10 @@ LOCKS_API locks_status_t lockskv_prompt_workspace_size(const locks_cache_t* cach
  * q: bf16 [total][num_q_heads][128], rows q_stride elements apart (a multiple
  * of 8, at least num_q_heads * 128; base 16-byte aligned); out bf16
  * [total][num_q_heads][128] and lse float32 [total][num_q_heads], contiguous.
- * params->budget_tokens and flags are not used. */
+ * params->budget_tokens and flags are not used.  Logits, sums and the output's
+ * accumulation are float32; softmax weights are rounded to bf16 for bf16 pages
+ * (2^-8 of each) and to half precision for 4-bit ones (2^-11, and 2^-31 of the
+ * row's largest), whose values s * code are rounded to half precision too. */
 LOCKS_API locks_status_t lockskv_prompt_attend(const locks_cache_t* cache, const locks_params_t* params,
                                                const lockskv_tokens_t* tokens, const void* q, int64_t q_stride,
                                                void* out, float* lse, void* ws, size_t ws_bytes, void* stream);

@@ -58,10 +58,10 @@
 // Over a page list, a few pages of each problem: one thread-block cluster per problem,
 // whose CTAs push their partial states to each other through distributed shared memory.
 //
-// Measured (floor by bytes): 131,001 tokens of 8 KV heads, 4 heads each, 32.8 us (22.3),
-// streaming at 6.97 TB/s; 32 sequences of up to 9216 tokens in 16-token pages 64.8 us
+// Measured (floor by bytes): 131,001 tokens of 8 KV heads, 4 heads each, 32.7 us (22.3),
+// streaming at 7.08 TB/s; 32 sequences of up to 9216 tokens in 16-token pages 64.8 us
 // (40.0); 1M tokens of 2 KV heads, 16 heads each, 87.7 us (44.5); 4096 tokens of one
-// head 6.4 us; a list of 32 pages of 8 KV heads 7.7 us.  Five rows over eight sequences
+// head 6.7 us; a list of 32 pages of 8 KV heads 8.0 us.  Five rows over eight sequences
 // of up to 16,411 tokens 60 us (14.2).
 #include <algorithm>
 #include <type_traits>
@@ -673,7 +673,7 @@ __device__ __forceinline__ void store_result(const AttendArgs& a, size_t row, in
 // CTA began, and the one it begins itself), [2 CTA + begins][G or 8 NT].  A second kernel
 // joins those of a problem, each column on its own.  (The last CTA of a problem to finish
 // did it before, alone, in two levels: 17 of 110 us for 16 heads and 152 CTAs per
-// problem, which now take 95; one head over 4096 tokens took 10.3 us, now 6.4.)
+// problem, which took 95 then; one head over 4096 tokens 10.3 us, 6.4 with the join.)
 struct Q4Seq {
   int keys;             // that its newest token sees
   int row0, n, start;   // its query tokens: first row, number, position of the first
