@@ -160,9 +160,9 @@ typedef struct locks_cache {
   int32_t head_dim;
   int32_t page_size;
   int32_t pages_total;
-  /* One 32-bit word for both (max_pages in the low 28 bits, which hold every
-   * supported table), so that the struct keeps the size and the layout that it
-   * had without formats: a caller built then passes kv_format 0. */
+  /* One 32-bit word for both (max_pages below 2^27 in the low 28 bits, which
+   * hold every supported table), so that the struct keeps the size and the
+   * layout that it had without formats: a caller built then passes kv_format 0. */
   int32_t max_pages : 28;
   int32_t kv_format : 4;
 } locks_cache_t;

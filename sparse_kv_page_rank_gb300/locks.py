@@ -182,6 +182,8 @@ def make_cache(k_pool, v_pool, block_table, seq_lens, n_summarized=None, *, page
             pt, hkv, P, d = k_pool.shape
     else:
         pt, hkv, P, d = pages_total, num_kv_heads, 64, 128
+    if block_table.shape[1] >= 1 << 27:  # beyond every limit, and more than the field holds
+        raise LocksError(LOCKS_ERR_UNSUPPORTED, "make_cache")
     return locks_cache_t(_ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(seq_lens),
                          _ptr(n_summarized), int(block_table.shape[0]), int(hkv), int(d), int(P),
                          int(pt), int(block_table.shape[1]), fmt)

@@ -67,3 +67,20 @@ def test_an_earlier_callers_struct_is_read_to_its_end_only(behind):
     status = L.lib().locks_workspace_size(ctypes.cast(ctypes.byref(old), ctypes.POINTER(L.locks_cache_t)), None,
                                           ctypes.byref(p), ctypes.byref(n))
     assert status == L.LOCKS_OK and n.value == L.locks_workspace_size(new, None, p)
+
+
+def test_a_table_wider_than_the_field_is_refused():
+    import torch
+    build()
+    k, lens = torch.zeros(2, 1, 64, 128, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    one = torch.zeros(1, 1, dtype=torch.int32)
+    for cols in (1 << 27, (1 << 28) + 5, 1 << 31):
+        with pytest.raises(L.LocksError) as e:
+            L.make_cache(k, k, one.expand(1, cols), lens)
+        assert e.value.status == L.LOCKS_ERR_UNSUPPORTED
+    c = L.make_cache(k, k, one.expand(1, (1 << 27) - 1), lens)
+    assert c.max_pages == (1 << 27) - 1
+    # what the field holds but the limits on tokens do not allow
+    with pytest.raises(L.LocksError) as e:
+        L.locks_workspace_size(c, None, L.make_params(4, 0))
+    assert e.value.status == L.LOCKS_ERR_UNSUPPORTED
