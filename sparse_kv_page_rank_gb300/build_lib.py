@@ -25,7 +25,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "--expt-relaxed-constexpr"]
 SOURCES = ["api.cu", "scan.cu", "topk.cu", "attend.cu", "build.cu", "static_ws.cu", "attend_q4.cu",
-           "kv_append.cu", "prompt.cu"]
+           "kv_append.cu", "prompt.cu", "gen_api.cu", "gen_select.cu", "gen_reorder.cu", "gen_attend.cu"]
 
 
 def nvcc() -> str:

@@ -4,6 +4,7 @@
 // locks_get_device_error).
 #include <cstring>
 
+#include "../../include/locksgen.h"
 #include "host.h"
 
 namespace {
@@ -440,6 +441,68 @@ KvTokenArgs token_args(const locks_cache_t* c, const lockskv_tokens_t* t, void* 
   return a;
 }
 
+// lockskv_append, or with axes locksgen_append_axes.
+locks_status_t run_append(const locks_cache_t* cache, const lockskv_tokens_t* tokens, const lockskv_append_t* ap,
+                          const locksgen_axes_t* axes, void* ws, size_t ws_bytes, void* stream) {
+  locks_status_t st = check_cache(cache, true);
+  if (st != LOCKS_OK) return st;
+  if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
+  if ((st = check_err_ws(ws, ws_bytes)) != LOCKS_OK) return st;
+  if (tokens->total == 0) return LOCKS_OK;  // an empty array may have no address
+  if (!ap || !ap->k || !ap->v || (ap->q == nullptr) != (ap->q_out == nullptr)) return LOCKS_ERR_INVALID_ARG;
+  const int64_t kv_row = (int64_t)cache->num_kv_heads * kHeadDim;
+  if ((st = check_rows(ap->k, ap->k_stride, kv_row)) != LOCKS_OK) return st;
+  if ((st = check_rows(ap->v, ap->v_stride, kv_row)) != LOCKS_OK) return st;
+  if (ap->q) {
+    if (ap->num_q_heads <= 0) return LOCKS_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)ap->num_q_heads * kHeadDim;
+    if ((st = check_rows(ap->q, ap->q_stride, q_row)) != LOCKS_OK) return st;
+    if ((st = check_rows(ap->q_out, ap->q_out_stride, q_row)) != LOCKS_OK) return st;
+    if (ap->q == ap->q_out && ap->q_stride != ap->q_out_stride) return LOCKS_ERR_INVALID_ARG;
+  }
+  if (ap->rotary_dim < 0) return LOCKS_ERR_INVALID_ARG;
+  if (ap->rotary_dim % 16 || ap->rotary_dim > kHeadDim) return LOCKS_ERR_UNSUPPORTED;
+  if ((ap->rotary_dim > 0) != (ap->rope != nullptr)) return LOCKS_ERR_INVALID_ARG;
+  if (ap->rope && (ap->rope_rows <= 0 || (reinterpret_cast<uintptr_t>(ap->rope) & 15))) return LOCKS_ERR_INVALID_ARG;
+  if ((ap->interleaved & ~1) != 0) return LOCKS_ERR_INVALID_ARG;
+  if (axes) {
+    if (!ap->rope || ap->positions || !axes->positions) return LOCKS_ERR_INVALID_ARG;
+    if (axes->num_axes < 1 || axes->axis_stride < tokens->total) return LOCKS_ERR_INVALID_ARG;
+    if (axes->num_axes > LOCKSGEN_MAX_AXES) return LOCKS_ERR_UNSUPPORTED;
+    for (int i = 0; i < ap->rotary_dim / 2; ++i)
+      if (axes->axis_of_pair[i] >= axes->num_axes) return LOCKS_ERR_INVALID_ARG;
+  }
+  if (tokens->max_tokens == 0) return LOCKS_OK;
+  KvAppendArgs a;
+  a.tok = token_args(cache, tokens, ws);
+  a.k_pool = const_cast<void*>(cache->k_pool);
+  a.v_pool = const_cast<void*>(cache->v_pool);
+  a.k = static_cast<const uint16_t*>(ap->k);
+  a.v = static_cast<const uint16_t*>(ap->v);
+  a.q = static_cast<const uint16_t*>(ap->q);
+  a.q_out = static_cast<uint16_t*>(ap->q_out);
+  a.rope = ap->rope;
+  a.positions = ap->positions;
+  a.k_stride = ap->k_stride;
+  a.v_stride = ap->v_stride;
+  a.q_stride = ap->q_stride;
+  a.q_out_stride = ap->q_out_stride;
+  a.num_q_heads = ap->num_q_heads;
+  a.rope_rows = ap->rope_rows;
+  a.rotary_dim = ap->rotary_dim;
+  a.interleaved = ap->interleaved;
+  a.num_axes = 0;
+  a.axis_stride = 0;
+  for (uint32_t& w : a.pair_axes) w = 0;
+  if (axes) {
+    a.positions = axes->positions;
+    a.num_axes = axes->num_axes;
+    a.axis_stride = axes->axis_stride;
+    for (int i = 0; i < ap->rotary_dim / 2; ++i) a.pair_axes[i / 16] |= (uint32_t)axes->axis_of_pair[i] << (2 * (i % 16));
+  }
+  return cuda_status(launch_append(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -625,48 +688,15 @@ locks_status_t locks_get_device_error(void* ws, int32_t* code, void* stream) {
 }
 
 locks_status_t lockskv_append(const locks_cache_t* cache, const lockskv_tokens_t* tokens,
-                              const lockskv_append_t* ap, void* ws, size_t ws_bytes, void* stream) {
-  locks_status_t st = check_cache(cache, true);
-  if (st != LOCKS_OK) return st;
-  if ((st = check_tokens(cache, tokens)) != LOCKS_OK) return st;
-  if ((st = check_err_ws(ws, ws_bytes)) != LOCKS_OK) return st;
-  if (tokens->total == 0) return LOCKS_OK;  // an empty array may have no address
-  if (!ap || !ap->k || !ap->v || (ap->q == nullptr) != (ap->q_out == nullptr)) return LOCKS_ERR_INVALID_ARG;
-  const int64_t kv_row = (int64_t)cache->num_kv_heads * kHeadDim;
-  if ((st = check_rows(ap->k, ap->k_stride, kv_row)) != LOCKS_OK) return st;
-  if ((st = check_rows(ap->v, ap->v_stride, kv_row)) != LOCKS_OK) return st;
-  if (ap->q) {
-    if (ap->num_q_heads <= 0) return LOCKS_ERR_INVALID_ARG;
-    const int64_t q_row = (int64_t)ap->num_q_heads * kHeadDim;
-    if ((st = check_rows(ap->q, ap->q_stride, q_row)) != LOCKS_OK) return st;
-    if ((st = check_rows(ap->q_out, ap->q_out_stride, q_row)) != LOCKS_OK) return st;
-    if (ap->q == ap->q_out && ap->q_stride != ap->q_out_stride) return LOCKS_ERR_INVALID_ARG;
-  }
-  if (ap->rotary_dim < 0) return LOCKS_ERR_INVALID_ARG;
-  if (ap->rotary_dim % 16 || ap->rotary_dim > kHeadDim) return LOCKS_ERR_UNSUPPORTED;
-  if ((ap->rotary_dim > 0) != (ap->rope != nullptr)) return LOCKS_ERR_INVALID_ARG;
-  if (ap->rope && (ap->rope_rows <= 0 || (reinterpret_cast<uintptr_t>(ap->rope) & 15))) return LOCKS_ERR_INVALID_ARG;
-  if ((ap->interleaved & ~1) != 0) return LOCKS_ERR_INVALID_ARG;
-  if (tokens->max_tokens == 0) return LOCKS_OK;
-  KvAppendArgs a;
-  a.tok = token_args(cache, tokens, ws);
-  a.k_pool = const_cast<void*>(cache->k_pool);
-  a.v_pool = const_cast<void*>(cache->v_pool);
-  a.k = static_cast<const uint16_t*>(ap->k);
-  a.v = static_cast<const uint16_t*>(ap->v);
-  a.q = static_cast<const uint16_t*>(ap->q);
-  a.q_out = static_cast<uint16_t*>(ap->q_out);
-  a.rope = ap->rope;
-  a.positions = ap->positions;
-  a.k_stride = ap->k_stride;
-  a.v_stride = ap->v_stride;
-  a.q_stride = ap->q_stride;
-  a.q_out_stride = ap->q_out_stride;
-  a.num_q_heads = ap->num_q_heads;
-  a.rope_rows = ap->rope_rows;
-  a.rotary_dim = ap->rotary_dim;
-  a.interleaved = ap->interleaved;
-  return cuda_status(launch_append(a, static_cast<cudaStream_t>(stream)));
+                              const lockskv_append_t* append, void* ws, size_t ws_bytes, void* stream) {
+  return run_append(cache, tokens, append, nullptr, ws, ws_bytes, stream);
+}
+
+locks_status_t locksgen_append_axes(const locks_cache_t* cache, const lockskv_tokens_t* tokens,
+                                    const lockskv_append_t* append, const locksgen_axes_t* axes, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  if (!axes) return LOCKS_ERR_INVALID_ARG;
+  return run_append(cache, tokens, append, axes, ws, ws_bytes, stream);
 }
 
 locks_status_t lockskv_read(const locks_cache_t* cache, const lockskv_tokens_t* tokens, void* k_out, void* v_out,

@@ -1,0 +1,788 @@
+// Attention of one query token per row of the cache, where the W rows of a request share
+// their first pages (beams of one prompt): the shared pages are read once for
+// all of the request's rows, the rest once per row.
+//
+// Mathematics.  The softmax over a row's keys is that over two parts, joined by their
+// maxima and sums.  For the shared part the rows of the products are (beam, query head of
+// the group), up to 32 at a time; for a row's own part the group's heads.
+//
+// What bounds it: the bytes of the shared pages once and of the rows' own pages.
+//
+// Layout.  mma.sync m16n8k16 with one or two tiles of 16 rows: a CTA of four warps takes
+// 64 tokens at a time from a ring that bulk and tensor copies fill, warp w tokens 16 w ..
+// 16 w + 15, with the softmax and the outputs of its tokens in registers; the warps' states
+// meet in shared memory at the end of a piece.  The queries stay in shared memory (their
+// fragments would take 64 more registers than there are).  bf16 pages: ldmatrix.
+// 4-bit pages: the codes are bf16 numbers (exact), keys get their scale on the four
+// partial sums of a logit, values theirs on the weights, in fp32 before those are
+// rounded to bf16, whose range needs no care.
+//
+// Work split.  All 64-token tiles of all problems lie in one line: request by request, KV
+// head by head, first the shared pages (once per block of 32 rows), then each row's own.  Every
+// CTA gets an equal part of it, two CTAs per SM; a segment counts kSegment tiles more
+// than it has, which is what its queries, its first copies and its merge cost.  A piece
+// (the part of a segment that a CTA has) leaves its state in the workspace at place
+// CTA + segment, which no two pieces share; a second, dependent kernel joins them.
+#include <algorithm>
+#include <climits>
+
+#include "gen.h"
+#include "kv_q4.cuh"
+
+namespace locks {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSegment = 2;
+constexpr int kHalfTile = 64 * 128;   // bytes of a 64-row x 64-column bf16 box
+constexpr int kTile = 2 * kHalfTile;  // 64 tokens of K (or V)
+constexpr int kQueryBytes = kSharedRows * kHeadDim * 2;
+constexpr int kOStride = 132;  // padded row of a warp's outputs (floats)
+template <bool Q4>
+constexpr int kStageBytes = Q4 ? kQ4Slot : 2 * kTile;
+template <bool Q4>
+constexpr int kStages = Q4 ? 8 : 3;
+template <bool Q4>
+constexpr int kSmem = kStages<Q4> * kStageBytes<Q4> + kQueryBytes + 1024;
+static_assert(kWarps * kSharedRows * kOStride * 4 <= kStages<true> * kStageBytes<true> &&
+                  kWarps * kSharedRows * kOStride * 4 <= kStages<false> * kStageBytes<false>,
+              "the merge fits the ring");
+
+// ---- lengths, and what follows from them ----------------------------------------------
+
+__device__ __forceinline__ int row_length(const GroupArgs& a, int row, bool says) {
+  int len = __ldg(a.seq_lens + row);
+  if (len < 0 || len > a.max_pages * a.page_size) {
+    if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
+    len = len < 0 ? 0 : a.max_pages * a.page_size;
+  }
+  return len;
+}
+// Shared pages of a request whose `live` rows have at least `full` whole pages: a row
+// alone shares with nobody.
+__device__ __forceinline__ int shared_of(int given, int full, int live) { return live > 1 ? max(0, min(given, full)) : 0; }
+__device__ __forceinline__ int tiles_of(int tokens) { return (tokens + kPage - 1) / kPage; }
+__device__ __forceinline__ int line_of(int tiles) { return tiles > 0 ? tiles + kSegment : 0; }
+
+// One thread: the places in the line of one KV head of request g.
+__device__ __forceinline__ int head_line(const GroupArgs& a, int g) {
+  int full = INT_MAX, live = 0;
+  const int base = g * a.beams;
+#pragma unroll 8
+  for (int w = 0; w < a.beams; ++w) {
+    const int len = row_length(a, base + w, false);
+    if (len > 0) full = min(full, len / a.page_size), ++live;
+  }
+  const int sp = shared_of(__ldg(a.shared_pages + g), full, live);
+  int n = a.n_blocks * line_of(tiles_of(sp * a.page_size));
+  for (int w = 0; w < a.beams; ++w) n += line_of(tiles_of(row_length(a, base + w, false) - sp * a.page_size));
+  return n;
+}
+
+// A request, for the CTA at hand.
+struct Group {
+  int g, sp, first, shared_tiles, line;  // line: places of one head
+  int len[LOCKSGEN_MAX_BEAMS];
+  int upto[LOCKSGEN_MAX_BEAMS];          // places of the rows' own parts, up to and with row w
+};
+// One warp.
+__device__ void load_group(const GroupArgs& a, int g, Group& s, bool says) {
+  const int lane = threadIdx.x & 31;
+  const int len = lane < a.beams ? row_length(a, g * a.beams + lane, says) : 0;
+  const uint32_t live = __ballot_sync(0xffffffffu, len > 0);
+  const int full = __reduce_min_sync(0xffffffffu, len > 0 ? len / a.page_size : INT_MAX);
+  const int sp = shared_of(__ldg(a.shared_pages + g), full, __popc(live));
+  int upto = line_of(tiles_of(len > 0 ? len - sp * a.page_size : 0));
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int other = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += other;
+  }
+  s.len[lane] = len;
+  s.upto[lane] = upto;
+  if (lane == 31) {
+    s.g = g;
+    s.sp = sp;
+    s.first = live ? __ffs(live) - 1 : 0;
+    s.shared_tiles = tiles_of(sp * a.page_size);
+    s.line = upto + a.n_blocks * line_of(s.shared_tiles);
+  }
+}
+static_assert(LOCKSGEN_MAX_BEAMS == 32, "a lane per row");
+
+// The part of the line that CTA c of C has.
+__device__ __forceinline__ long long part_begin(long long total, long long C, long long c) { return c < C ? total * c / C : total; }
+__device__ __forceinline__ long long part_owner(long long total, long long C, long long y) { return ((y + 1) * C - 1) / total; }
+__device__ __forceinline__ long long ctas_used(long long total, int n) { return min((long long)n, max(total, 1LL)); }
+
+// ---- a piece of a segment ---------------------------------------------------------------
+
+struct Piece {
+  bool shared;
+  int h, w, block;     // KV head; row (own part); block of rows (shared part)
+  int rows;            // of the products
+  int t0, t1;          // tiles of the segment
+  int page0, pages;    // first logical page, pages
+  int limit;           // tokens that may be seen
+  const int32_t* table;
+};
+
+struct Shared {
+  uint64_t full[8], empty[8];
+  int left[8][4];  // per stage (and page of it): tokens of the tile to be seen
+  float m[kWarps][kSharedRows], l[kWarps][kSharedRows];
+  Group grp;
+  long long offset, total;
+  int group, abort;
+  long long scan[kWarps];
+};
+
+// The query of row r of a piece.
+__device__ __forceinline__ size_t query_row(const GroupArgs& a, const Piece& p, int g, int r) {
+  int w = p.w, e = r;
+  if (p.shared) {
+    const int i = p.block * kSharedRows + r;
+    w = i / a.group;
+    e = i % a.group;
+  }
+  return ((size_t)(g * a.beams + w) * a.num_kv_heads + p.h) * a.group + e;
+}
+
+// Address of 16 bytes (chunk) of a query: bf16 pages read them by ldmatrix, 8 rows of one
+// chunk together; 4-bit pages as 16 bytes per lane, two rows of four chunks.
+template <bool Q4>
+__device__ __forceinline__ uint32_t query_addr(uint32_t base, int row, int chunk) {
+  return base + row * 256 + ((chunk ^ (Q4 ? (row & 1) * 4 : row & 7)) << 4);
+}
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int row, int chunk) {
+  return base + (chunk >> 3) * kHalfTile + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+// Mask of a packed pair of tokens (t, t + 1) that keeps those before `len`.
+__device__ __forceinline__ uint32_t pair_mask(int t, int len) {
+  return (t < len ? 0x0000ffffu : 0u) | (t + 1 < len ? 0xffff0000u : 0u);
+}
+
+// A warp's softmax state and outputs for its tokens: rows 16 i + g, 16 i + g + 8.
+template <int MT>
+struct State {
+  float m[MT][2], l[MT][2];
+  float o[MT][16][4];
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+    }
+  }
+  // Logits (unscaled) to weights.  The reference of a row moves only when a logit exceeds it
+  // by more than 2^8, so the usual tile needs no maximum across lanes, only a vote.
+  __device__ __forceinline__ void weigh(float (&s)[MT][2][4], float scale_log2) {
+    bool moved = false;
+    float top[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        top[i][k] = fmaxf(fmaxf(s[i][0][2 * k], s[i][0][2 * k + 1]), fmaxf(s[i][1][2 * k], s[i][1][2 * k + 1])) * scale_log2;
+        moved |= top[i][k] > m[i][k] + 8.f;
+      }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float t = fmaxf(top[i][k], __shfl_xor_sync(0xffffffffu, top[i][k], 1));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+          t = fmaxf(t, m[i][k]);
+          const float al = t == -INFINITY ? 1.f : fast_exp2(m[i][k] - t);
+          m[i][k] = t;
+          l[i][k] *= al;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            o[i][n][2 * k] *= al;
+            o[i][n][2 * k + 1] *= al;
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float ref = m[i][k] == -INFINITY ? 0.f : m[i][k];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = s[i][n][2 * k + e];
+            x = fast_exp2(fmaf(x, scale_log2, -ref));
+            l[i][k] += x;
+          }
+      }
+  }
+};
+
+// Tokens 16 warp .. + 15 of a tile of bf16 pages at `base` (keys, then values), of which the
+// first `left` are seen.
+template <int MT, bool WHOLE>
+__device__ __forceinline__ void tile_bf16(State<MT>& st, uint32_t base, uint32_t queries, int left, float scale_log2) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, mi = lane >> 3;
+  float s[MT][2][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[i][0][e] = s[i][1][e] = 0.f;
+  const int krow = 16 * warp + (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    uint32_t b0, b1, b2, b3;
+    ldmatrix_x4(b0, b1, b2, b3, tile_addr(base, krow, 2 * kk + (mi & 1)));
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      uint32_t a0, a1, a2, a3;
+      ldmatrix_x4(a0, a1, a2, a3, query_addr<false>(queries, 16 * i + (mi & 1) * 8 + (lane & 7), 2 * kk + (mi >> 1)));
+      mma_16816(s[i][0], a0, a1, a2, a3, b0, b1);
+      mma_16816(s[i][1], a0, a1, a2, a3, b2, b3);
+    }
+  }
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * n + 2 * c + (e & 1) >= left) s[i][n][e] = -INFINITY;
+  }
+  st.weigh(s, scale_log2);
+  uint32_t p[MT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    p[i][0] = pack_bf16(s[i][0][0], s[i][0][1]);
+    p[i][1] = pack_bf16(s[i][0][2], s[i][0][3]);
+    p[i][2] = pack_bf16(s[i][1][0], s[i][1][1]);
+    p[i][3] = pack_bf16(s[i][1][2], s[i][1][3]);
+  }
+  const int vrow = 16 * warp + (mi & 1) * 8 + (lane & 7);
+  const uint32_t k0 = WHOLE ? ~0u : pair_mask(2 * c, left), k1 = WHOLE ? ~0u : pair_mask(8 + 2 * c, left);
+#pragma unroll
+  for (int dn = 0; dn < 8; ++dn) {
+    uint32_t v0, v1, v2, v3;
+    ldmatrix_x4_trans(v0, v1, v2, v3, tile_addr(base + kTile, vrow, 2 * dn + (mi >> 1)));
+    if constexpr (!WHOLE) v0 &= k0, v1 &= k1, v2 &= k0, v3 &= k1;  // what lies past the end may be anything
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      mma_16816(st.o[i][2 * dn], p[i][0], p[i][1], p[i][2], p[i][3], v0, v1);
+      mma_16816(st.o[i][2 * dn + 1], p[i][0], p[i][1], p[i][2], p[i][3], v2, v3);
+    }
+  }
+}
+
+// The same of 4-bit pages.  A key word holds dimensions 32 j + 8 c .. + 7 of one token, field
+// i the pair 8 c + 2 i, + 1, so fields 0 and 1 are one step of a product, 2 and 3 the next; the
+// queries are read in that order.  A value word holds four dimensions of two tokens, field
+// i dimension 32 j + 4 n + i of column n: output block 4 j + i, whose columns 2c and 2c + 1 are
+// dimensions 32 j + 8 c + i and 32 j + 8 c + 4 + i.
+template <int P, int MT, bool WHOLE>
+__device__ __forceinline__ void tile_q4(State<MT>& st, uint32_t base, uint32_t queries, int left, float scale_log2) {
+  using At = Q4Tile<P>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  float s[MT][2][4];
+  {
+    // keys: tokens g and 8 + g for the products, their scales for columns 2c, 2c + 1
+    const uint32_t kb = base + At::key_codes(warp), sb = base + At::key_scales(warp);
+    const uint4 w0 = lds128(kb + lane * 16), w1 = lds128(kb + 512 + lane * 16);
+    const uint4 z0 = lds128(sb + c * 16), z1 = lds128(sb + 64 + c * 16);
+    const uint32_t kw0[4] = {w0.x, w0.y, w0.z, w0.w}, kw1[4] = {w1.x, w1.y, w1.z, w1.w};
+    // halves j of tokens 2c (x, y) and 2c + 1 (z, w)
+    const uint32_t za[2][2] = {{z0.x, z0.y}, {z1.x, z1.y}}, zb[2][2] = {{z0.z, z0.w}, {z1.z, z1.w}};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t f[2][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[0][k] = u4pair_bf16(kw0[j], 4 * k);
+        f[1][k] = u4pair_bf16(kw1[j], 4 * k);
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint4 qa = lds128(query_addr<true>(queries, 16 * i + g, 4 * j + c));
+        const uint4 qb = lds128(query_addr<true>(queries, 16 * i + g + 8, 4 * j + c));
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_16816(acc, qa.x, qb.x, qa.y, qb.y, f[n][0], f[n][1]);
+          mma_16816(acc, qa.z, qb.z, qa.w, qb.w, f[n][2], f[n][3]);
+          const float s0 = j & 1 ? f16_hi(za[n][j >> 1]) : f16_lo(za[n][j >> 1]);
+          const float s1 = j & 1 ? f16_hi(zb[n][j >> 1]) : f16_lo(zb[n][j >> 1]);
+          s[i][n][0] = j == 0 ? s0 * acc[0] : fmaf(s0, acc[0], s[i][n][0]);
+          s[i][n][1] = j == 0 ? s1 * acc[1] : fmaf(s1, acc[1], s[i][n][1]);
+          s[i][n][2] = j == 0 ? s0 * acc[2] : fmaf(s0, acc[2], s[i][n][2]);
+          s[i][n][3] = j == 0 ? s1 * acc[3] : fmaf(s1, acc[3], s[i][n][3]);
+        }
+      }
+    }
+  }
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * n + 2 * c + (e & 1) >= left) s[i][n][e] = -INFINITY;
+  }
+  st.weigh(s, scale_log2);
+  const uint32_t vb = base + At::value_codes(warp), zb = base + At::value_scales(warp);
+  const uint4 v0 = lds128(vb + lane * 16), v1 = lds128(vb + 512 + lane * 16);
+  uint4 z0 = lds128(zb + c * 32), z1 = lds128(zb + c * 32 + 16);
+  if constexpr (!WHOLE) {
+    // scales past the end may be anything, a NaN too
+    const uint32_t m0 = pair_mask(2 * c, left), m1 = pair_mask(8 + 2 * c, left);
+    z0.x &= m0; z0.y &= m0; z0.z &= m0; z0.w &= m0;
+    z1.x &= m1; z1.y &= m1; z1.z &= m1; z1.w &= m1;
+  }
+  const uint32_t vw0[4] = {v0.x, v0.y, v0.z, v0.w}, vw1[4] = {v1.x, v1.y, v1.z, v1.w};
+  const uint32_t zw0[4] = {z0.x, z0.y, z0.z, z0.w}, zw1[4] = {z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t p[MT][4];
+    const float a0 = f16_lo(zw0[j]), a1 = f16_hi(zw0[j]), b0 = f16_lo(zw1[j]), b1 = f16_hi(zw1[j]);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      p[i][0] = pack_bf16(s[i][0][0] * a0, s[i][0][1] * a1);
+      p[i][1] = pack_bf16(s[i][0][2] * a0, s[i][0][3] * a1);
+      p[i][2] = pack_bf16(s[i][1][0] * b0, s[i][1][1] * b1);
+      p[i][3] = pack_bf16(s[i][1][2] * b0, s[i][1][3] * b1);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t f0 = u4pair_bf16(vw0[j], 4 * k), f1 = u4pair_bf16(vw1[j], 4 * k);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) mma_16816(st.o[i][4 * j + k], p[i][0], p[i][1], p[i][2], p[i][3], f0, f1);
+    }
+  }
+}
+
+// False where a wait gave up.
+template <int P, bool Q4, int MT>
+__device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const Piece& p, Shared& sh,
+                                          uint8_t* ring, uint8_t* queries, uint32_t& seq, float* part_o, float2* part_ml) {
+  constexpr int kPPT = kPage / P, S = kStages<Q4>, kBatch = 32;  // pages of a tile; page entries a warp looks up at once
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int nt = p.t1 - p.t0, G = sh.grp.g;
+  const uint32_t rbase = smem_u32(ring), qbase = smem_u32(queries);
+
+  // warp 0 asks for the copies; its lanes hold 32 pages' entries, and the next 32
+  int cur = 0, nxt = 0;
+  const bool checks = p.shared && p.h == 0 && p.block == 0;
+  auto entry = [&](int k) {  // of page k of the piece
+    if (k >= p.pages) return 0;
+    const int lp = p.page0 + k;
+    int phys = __ldg(p.table + lp);
+    if (phys < 0 || phys >= a.pages_total) {
+      set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
+      phys = -1;
+    }
+    if (checks)
+      for (int w = 0; w < a.beams; ++w)
+        if (sh.grp.len[w] > 0 && __ldg(a.block_table + (size_t)(G * a.beams + w) * a.max_pages + lp) != phys)
+          set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
+    return phys;
+  };
+  auto issue = [&](int t) {  // warp 0: tile t of the piece
+    const int k0 = t * kPPT;
+    if (k0 % kBatch == 0) {
+      cur = k0 == 0 ? entry(lane) : nxt;
+      nxt = entry(k0 + kBatch + lane);
+    }
+    const int stage = (seq + t) % S;
+    const int np = min(kPPT, p.pages - k0);
+    uint8_t* dst = ring + stage * kStageBytes<Q4>;
+    const int mine = __shfl_sync(0xffffffffu, cur, (k0 + lane % kPPT) % kBatch);  // lane w: page w of the tile
+    if (lane < kPPT) sh.left[stage][lane] = lane < np && mine >= 0 ? min(P, p.limit - (p.page0 + k0 + lane) * P) : 0;
+    __syncwarp();  // before the arrival, which releases it
+    if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], (uint32_t)np * (Q4 ? LOCKS_KV_Q4_BLOCK_BYTES(P) : 2 * P * kHeadDim * 2));
+#pragma unroll
+    for (int w = 0; w < kPPT; ++w) {
+      const int phys = __shfl_sync(0xffffffffu, mine, w);
+      if (lane == 0 && w < np) {
+        const size_t ph = (size_t)max(phys, 0) * a.num_kv_heads + p.h;  // (a page outside the pool: any, unseen)
+        if constexpr (Q4) {
+          bulk_load(smem_u32(dst + w * LOCKS_KV_Q4_BLOCK_BYTES(P)), a.blocks + ph * LOCKS_KV_Q4_BLOCK_BYTES(P),
+                    LOCKS_KV_Q4_BLOCK_BYTES(P), &sh.full[stage]);
+        } else {
+          const int y = (int)(ph * P);
+          uint8_t* d = dst + w * (P * 128);
+          tma_load_2d(d, &tk, &sh.full[stage], 0, y);
+          tma_load_2d(d + kHalfTile, &tk, &sh.full[stage], 64, y);
+          tma_load_2d(d + kTile, &tv, &sh.full[stage], 0, y);
+          tma_load_2d(d + kTile + kHalfTile, &tv, &sh.full[stage], 64, y);
+        }
+      }
+    }
+  };
+  int issued = 0;
+  if (warp == 0)
+    for (; issued < min(S, nt); ++issued) issue(issued);
+  // the queries; rows past the last are zero
+  for (int e = tid; e < MT * 16 * 16; e += kThreads) {
+    const int r = e / 16, chunk = e % 16;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < p.rows) v = __ldg(reinterpret_cast<const uint4*>(a.q + query_row(a, p, G, r) * kHeadDim) + chunk);
+    const uint32_t at = query_addr<Q4>(qbase, r, chunk);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  }
+  __syncthreads();
+
+  State<MT> st;
+  st.reset();
+  bool ok = true;
+  for (int t = 0; t < nt; ++t) {
+    if (warp == 0 && t > 0 && issued < nt) {
+      // the stage of the tile before this one, when all warps are done with it
+      ok = mbar_wait(&sh.empty[(seq + t - 1) % S], ((seq + t - 1) / S) & 1);
+      if (!ok) break;
+      issue(issued++);
+    }
+    const int stage = (seq + t) % S;
+    ok = mbar_wait(&sh.full[stage], ((seq + t) / S) & 1);
+    if (!ok) break;
+    const int left = P == kPage ? min(16, sh.left[stage][0] - 16 * warp) : sh.left[stage][P == kPage ? 0 : warp];
+    const uint32_t base = rbase + stage * kStageBytes<Q4>;
+    if constexpr (Q4) {
+      if (left >= 16) tile_q4<P, MT, true>(st, base, qbase, 16, a.scale_log2);
+      else if (left > 0) tile_q4<P, MT, false>(st, base, qbase, left, a.scale_log2);
+    } else {
+      if (left >= 16) tile_bf16<MT, true>(st, base, qbase, 16, a.scale_log2);
+      else if (left > 0) tile_bf16<MT, false>(st, base, qbase, left, a.scale_log2);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[stage]);
+  }
+  if (!ok) {
+    // the copies asked for get a bounded time to land
+    if (lane == 0) {
+      atomicExch(&sh.abort, 1);
+      set_error(a.err, kDevErrTimeout);
+    }
+    if (warp == 0 && lane == 0)
+      for (int t = max(0, issued - S); t < issued; ++t) (void)mbar_wait(&sh.full[(seq + t) % S], ((seq + t) / S) & 1);
+  }
+  seq += nt;
+  // ---- the warps' states, merged ----
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      st.l[i][k] += __shfl_xor_sync(0xffffffffu, st.l[i][k], 1);
+      st.l[i][k] += __shfl_xor_sync(0xffffffffu, st.l[i][k], 2);
+      if (c == 0) {
+        sh.m[warp][16 * i + 8 * k + g] = st.m[i][k];
+        sh.l[warp][16 * i + 8 * k + g] = st.l[i][k];
+      }
+    }
+  __syncthreads();  // every warp is done with the ring
+  float* so = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float* row = so + (warp * kSharedRows + 16 * i + 8 * k + g) * kOStride;
+      if constexpr (Q4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4*>(row + 32 * j + 8 * c + 4 * e) =
+                make_float4(st.o[i][4 * j][2 * k + e], st.o[i][4 * j + 1][2 * k + e], st.o[i][4 * j + 2][2 * k + e],
+                            st.o[i][4 * j + 3][2 * k + e]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+          *reinterpret_cast<float2*>(row + 8 * n + 2 * c) = make_float2(st.o[i][n][2 * k], st.o[i][n][2 * k + 1]);
+      }
+    }
+  __syncthreads();
+  for (int e = tid; e < p.rows * (kHeadDim / 4); e += kThreads) {
+    const int r = e / (kHeadDim / 4), c4 = e % (kHeadDim / 4);
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][r]);
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = M == -INFINITY ? 1.f : fast_exp2(sh.m[w][r] - M);
+      const float4 v = *reinterpret_cast<const float4*>(so + (w * kSharedRows + r) * kOStride + 4 * c4);
+      L = fmaf(sh.l[w][r], f, L);
+      O.x = fmaf(v.x, f, O.x);
+      O.y = fmaf(v.y, f, O.y);
+      O.z = fmaf(v.z, f, O.z);
+      O.w = fmaf(v.w, f, O.w);
+    }
+    reinterpret_cast<float4*>(part_o)[e] = O;
+    if (c4 == 0) part_ml[r] = make_float2(M, L);
+  }
+  // the ring was written with ordinary stores: before the next copies into it
+  fence_proxy_async();
+  __syncthreads();
+  return !sh.abort;
+}
+
+template <int P, bool Q4>
+__global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_constant__ CUtensorMap tk,
+                                                                   const __grid_constant__ CUtensorMap tv,
+                                                                   const GroupArgs a) {
+  constexpr int kPPT = kPage / P;
+  extern __shared__ uint8_t dyn_raw[];
+  __shared__ Shared sh;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* queries = ring + kStages<Q4> * kStageBytes<Q4>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  const int groups = a.batch / a.beams;
+  if (tid == 0) {
+    if constexpr (!Q4) {
+      prefetch_tmap(&tk);
+      prefetch_tmap(&tv);
+    }
+    for (int s = 0; s < kStages<Q4>; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], kWarps);
+    }
+    fence_mbar_init();
+    sh.abort = 0;
+  }
+  pdl_wait();
+
+  // the whole line
+  long long mine = 0;
+  for (int g = tid; g < groups; g += kThreads) mine += head_line(a, g);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sh.scan[warp] = mine;
+  __syncthreads();
+  const long long total = (sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3]) * a.num_kv_heads;
+  const long long C = ctas_used(total, a.n_ctas);
+  const long long lo = part_begin(total, C, cta), hi = part_begin(total, C, (long long)cta + 1);
+  // the request that holds place lo; CTA 0 leaves every request's first place for the join
+  long long before = 0;
+  for (int g0 = 0; g0 < groups; g0 += kThreads) {
+    const int g = g0 + tid;
+    const long long own = g < groups ? (long long)head_line(a, g) * a.num_kv_heads : 0;
+    long long upto = own;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long other = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += other;
+    }
+    __syncthreads();
+    if (lane == 31) sh.scan[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) upto += w < warp ? sh.scan[w] : 0;
+    const long long first = before + upto - own;
+    if (lo >= first && lo < first + own) {
+      sh.group = g;
+      sh.offset = first;
+    }
+    if (cta == 0 && g < groups) a.offsets[g] = first;
+    before += sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3];
+    if (cta != 0 && before > lo) break;
+  }
+  if (cta == 0 && tid == 0) a.offsets[groups] = total;
+  __syncthreads();
+  if (lo >= hi) return;
+  int g = sh.group;
+  long long offset = sh.offset, pos = lo;
+  uint32_t seq = 0;
+  auto load = [&] {
+    if (warp == 0) load_group(a, g, sh.grp, true);
+    __syncthreads();
+  };
+  load();
+  const int problems_per_group = a.num_kv_heads;
+  const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;  // records of shared parts
+  while (pos < hi) {
+    while (pos >= offset + (long long)sh.grp.line * a.num_kv_heads) {
+      offset += (long long)sh.grp.line * a.num_kv_heads;
+      ++g;
+      __syncthreads();  // all have read the last request's
+      load();
+    }
+    const Group& s = sh.grp;
+    Piece p;
+    const long long in = pos - offset;
+    p.h = (int)(in / s.line);
+    int x = (int)(in % s.line);
+    const int shared_line = line_of(s.shared_tiles), shared_all = a.n_blocks * shared_line;
+    long long start = offset + (long long)p.h * s.line;
+    int tiles, end_page;
+    p.shared = x < shared_all;
+    p.w = p.block = 0;
+    if (p.shared) {
+      p.block = x / shared_line;
+      start += p.block * shared_line;
+      tiles = s.shared_tiles;
+      p.rows = min(kSharedRows, a.beams * a.group - p.block * kSharedRows);
+      p.limit = s.sp * P;
+      end_page = s.sp;
+      p.table = a.block_table + (size_t)(g * a.beams + s.first) * a.max_pages;
+    } else {
+      x -= shared_all;
+      while (x >= s.upto[p.w]) ++p.w;
+      start += shared_all + (p.w ? s.upto[p.w - 1] : 0);
+      p.limit = s.len[p.w];
+      tiles = tiles_of(p.limit - s.sp * P);
+      p.rows = a.group;
+      end_page = (p.limit + P - 1) / P;
+      p.table = a.block_table + (size_t)(g * a.beams + p.w) * a.max_pages;
+    }
+    p.t0 = (int)max(0LL, pos - start - kSegment);
+    p.t1 = (int)min((long long)tiles, max(0LL, hi - start - kSegment));
+    if (p.t1 > p.t0) {
+      p.page0 = (p.shared ? 0 : s.sp) + p.t0 * kPPT;
+      p.pages = min(end_page - p.page0, (p.t1 - p.t0) * kPPT);
+      const size_t problem = (size_t)g * problems_per_group + p.h;
+      size_t row;  // of the partial results
+      if (p.shared) row = (cta + problem * a.n_blocks + p.block) * kSharedRows;
+      else row = own_base * kSharedRows + (cta + problem * a.beams + p.w) * a.group;
+      float* part_o = a.part_o + row * kHeadDim;
+      float2* part_ml = a.part_ml + row;
+      const bool done = p.rows > 16 ? run_piece<P, Q4, 2>(a, tk, tv, p, sh, ring, queries, seq, part_o, part_ml)
+                                    : run_piece<P, Q4, 1>(a, tk, tv, p, sh, ring, queries, seq, part_o, part_ml);
+      if (!done) return;
+    }
+    pos = start + kSegment + tiles;
+  }
+  pdl_launch_dependents();
+}
+
+// Joins the pieces of one (row, query head).  Grid (batch * Hkv, group).
+constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinFlight = 8;  // pieces that a warp loads at once
+
+__global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArgs a) {
+  __shared__ __align__(16) float so[kJoinWarps][kHeadDim];  // (read and written 16 bytes at a time)
+  __shared__ float sl[kJoinWarps];
+  __shared__ Group s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads, e = blockIdx.y;
+  const int g = b / a.beams, w = b % a.beams, groups = a.batch / a.beams;
+  // (the lengths were complete before the other kernel let this one begin)
+  if (warp == 0) load_group(a, g, s, false);
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long total = a.offsets[groups], C = ctas_used(total, a.n_ctas);
+  const int len = s.len[w];
+  const size_t out_row = ((size_t)b * a.num_kv_heads + h) * a.group + e;
+  if (len == 0) {
+    a.out[out_row * kHeadDim + tid] = 0;
+    if (a.lse && tid == 0) a.lse[out_row] = -INFINITY;
+    return;
+  }
+  // the CTAs that have pieces of the two segments
+  const int i = w * a.group + e, block = i / kSharedRows;
+  const int shared_line = line_of(s.shared_tiles), own_tiles = tiles_of(len - s.sp * a.page_size);
+  const long long head = a.offsets[g] + (long long)h * s.line;
+  const size_t problem = (size_t)g * a.num_kv_heads + h;
+  const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;
+  long long c0[2] = {0, 0}, slot[2];
+  int n[2] = {0, 0};
+  auto segment = [&](int k, long long start, int tiles) {
+    if (tiles == 0) return;
+    c0[k] = part_owner(total, C, start);
+    n[k] = (int)(part_owner(total, C, start + kSegment + tiles - 1) - c0[k]) + 1;
+    // the first of them may end before the first tile
+    while (part_begin(total, C, c0[k] + 1) <= start + kSegment) ++c0[k], --n[k];
+  };
+  segment(0, head + (long long)block * shared_line, s.shared_tiles);
+  segment(1, head + (long long)a.n_blocks * shared_line + (w ? s.upto[w - 1] : 0), own_tiles);
+  slot[0] = (long long)(c0[0] + problem * a.n_blocks + block) * kSharedRows + i % kSharedRows;
+  slot[1] = (long long)own_base * kSharedRows + (long long)(c0[1] + problem * a.beams + w) * a.group + e;
+  const int all = n[0] + n[1];
+  auto row = [&](int k) { return (size_t)(k < n[0] ? slot[0] + (long long)k * kSharedRows : slot[1] + (long long)(k - n[0]) * a.group); };
+  float M = -INFINITY, L = 0.f;
+  for (int k = lane; k < all; k += 32) M = fmaxf(M, __ldcg(a.part_ml + row(k)).x);
+  M = warp_max(M);
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = warp; k0 < all; k0 += kJoinWarps * kJoinFlight) {
+    float4 v[kJoinFlight];
+    float2 ml[kJoinFlight];
+#pragma unroll
+    for (int k = 0; k < kJoinFlight; ++k) {
+      const int at = k0 + kJoinWarps * k;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ml[k] = make_float2(M, 0.f);
+      if (at >= all) continue;
+      v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row(at) * kHeadDim) + lane);
+      ml[k] = __ldcg(a.part_ml + row(at));
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinFlight; ++k) {
+      const float f = M == -INFINITY ? 1.f : fast_exp2(ml[k].x - M);
+      L = fmaf(ml[k].y, f, L);
+      O.x = fmaf(v[k].x, f, O.x);
+      O.y = fmaf(v[k].y, f, O.y);
+      O.z = fmaf(v[k].z, f, O.z);
+      O.w = fmaf(v[k].w, f, O.w);
+    }
+  }
+  *reinterpret_cast<float4*>(&so[warp][4 * lane]) = O;
+  if (lane == 0) sl[warp] = L;
+  __syncthreads();
+  float Os = 0.f, Ls = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinWarps; ++k) {
+    Os += so[k][tid];
+    Ls += sl[k];
+  }
+  const float val = Ls == 0.f ? 0.f : Os / Ls;  // a NaN stays one
+  a.out[out_row * kHeadDim + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(val));
+  if (a.lse && tid == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
+}
+static_assert(kJoinThreads == kHeadDim, "a thread per dimension");
+
+template <int P, bool Q4>
+cudaError_t launch(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  auto kern = group_attend_kernel<P, Q4>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<Q4>);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.n_ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem<Q4>;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+}
+
+}  // namespace
+
+int group_attend_ctas_per_sm() { return 2; }
+
+cudaError_t launch_group_attend(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  const cudaError_t e = a.q4 ? (a.page_size == 16 ? launch<16, true>(a, tk, tv, s) : launch<64, true>(a, tk, tv, s))
+                             : (a.page_size == 16 ? launch<16, false>(a, tk, tv, s) : launch<64, false>(a, tk, tv, s));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.batch * a.num_kv_heads, a.group, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, group_join_kernel, a);
+}
+
+}  // namespace locks

@@ -133,6 +133,11 @@ struct KvAppendArgs {
   const int32_t* positions;  // or null: the position in the sequence
   long long k_stride, v_stride, q_stride, q_out_stride;  // elements
   int num_q_heads, rope_rows, rotary_dim, interleaved;
+  // positions of several axes (num_axes > 0): positions is [num_axes][axis_stride], and
+  // pair i is of axis pair_axes[i / 16] >> 2 (i % 16) & 3
+  int num_axes;
+  long long axis_stride;
+  uint32_t pair_axes[4];
 };
 struct KvReadArgs {
   KvTokenArgs tok;

@@ -167,9 +167,31 @@ __device__ __forceinline__ void put_v_q4(uint8_t* block, int P, int slot, int ch
                                2 * (t & 1)) = s;
 }
 
+// Cosines and sines of pairs p .. p + 3 (p a multiple of 4), whose table rows are those of
+// their own axes (`row`: lane x holds that of axis x).  Whole warps.  Four pairs of one
+// axis, the usual case where an axis has a range of pairs, are one load of each.
+__device__ __forceinline__ void axis_pairs(const KvAppendArgs& a, int row, int p, bool turns, float4& c, float4& s) {
+  const uint32_t axes = a.pair_axes[p >> 4] >> (2 * (p & 15));
+  const int r0 = __shfl_sync(0xffffffffu, row, axes & 3), r1 = __shfl_sync(0xffffffffu, row, axes >> 2 & 3);
+  const int r2 = __shfl_sync(0xffffffffu, row, axes >> 4 & 3), r3 = __shfl_sync(0xffffffffu, row, axes >> 6 & 3);
+  if (!turns) return;
+  const int half = a.rotary_dim / 2;
+  const float* t0 = a.rope + (size_t)r0 * a.rotary_dim + p;
+  if (r0 == r1 && r0 == r2 && r0 == r3) {
+    c = __ldg(reinterpret_cast<const float4*>(t0));
+    s = __ldg(reinterpret_cast<const float4*>(t0 + half));
+  } else {
+    const float* t1 = a.rope + (size_t)r1 * a.rotary_dim + p + 1;
+    const float* t2 = a.rope + (size_t)r2 * a.rotary_dim + p + 2;
+    const float* t3 = a.rope + (size_t)r3 * a.rotary_dim + p + 3;
+    c = make_float4(__ldg(t0), __ldg(t1), __ldg(t2), __ldg(t3));
+    s = make_float4(__ldg(t0 + half), __ldg(t1 + half), __ldg(t2 + half), __ldg(t3 + half));
+  }
+}
+
 // WPT: warps of a token (1 or 8).  A step is two rows, either of keys and values (an
-// even number together) or of queries.
-template <bool Q4, int WPT, bool PAIRS_NEXT>
+// even number together) or of queries.  AXES: a pair's table row is that of its axis.
+template <bool Q4, int WPT, bool PAIRS_NEXT, bool AXES>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvAppendArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kAppendWarps / WPT) + warp / WPT;
@@ -204,17 +226,27 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvAppen
   if (!tp.ok) return;
   Turn tr;
   if (a.rotary_dim) {
-    const int row = a.positions ? __ldg(a.positions + t) : tp.pos;
-    if (row < 0 || row >= a.rope_rows) {
+    // AXES: each lane the row of one axis
+    const int row = AXES ? __ldg(a.positions + (lane < a.num_axes ? lane : 0) * a.axis_stride + t)
+                         : a.positions ? __ldg(a.positions + t) : tp.pos;
+    bool outside = row < 0 || row >= a.rope_rows;
+    if (AXES) outside = __any_sync(0xffffffffu, outside);
+    if (outside) {
       if (says) set_error(a.tok.err, LOCKS_DEVERR_POSITION);
       return;
     }
-    if (turns) {
-      const float* cs = a.rope + (size_t)row * a.rotary_dim + (PAIRS_NEXT ? d0 / 2 : (upper ? d0 - half : d0));
+    if (AXES || turns) {
+      const int p0 = !turns ? 0 : PAIRS_NEXT ? d0 / 2 : (upper ? d0 - half : d0);
+      const float* cs = a.rope + (size_t)row * a.rotary_dim + p0;
 #pragma unroll
       for (int k = 0; k < (PAIRS_NEXT ? 1 : 2); ++k) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(cs) + k);
-        const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half) + k);
+        float4 c, s;
+        if constexpr (AXES) {
+          axis_pairs(a, row, p0 + 4 * k, turns, c, s);
+        } else {
+          c = __ldg(reinterpret_cast<const float4*>(cs) + k);
+          s = __ldg(reinterpret_cast<const float4*>(cs + half) + k);
+        }
         if constexpr (PAIRS_NEXT) {
           const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
@@ -347,12 +379,19 @@ cudaError_t launch_tokens(K wide, K narrow, const A& a, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+
+template <bool PAIRS_NEXT, bool AXES>
+cudaError_t launch_append_as(const KvAppendArgs& a, cudaStream_t s) {
+  return a.tok.q4 ? launch_tokens(append_kernel<true, 8, PAIRS_NEXT, AXES>, append_kernel<true, 1, PAIRS_NEXT, AXES>, a, s)
+                  : launch_tokens(append_kernel<false, 8, PAIRS_NEXT, AXES>, append_kernel<false, 1, PAIRS_NEXT, AXES>, a, s);
+}
+
+}  // namespace
+
 cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t s) {
-  if (a.interleaved)
-    return a.tok.q4 ? launch_tokens(append_kernel<true, 8, true>, append_kernel<true, 1, true>, a, s)
-                    : launch_tokens(append_kernel<false, 8, true>, append_kernel<false, 1, true>, a, s);
-  return a.tok.q4 ? launch_tokens(append_kernel<true, 8, false>, append_kernel<true, 1, false>, a, s)
-                  : launch_tokens(append_kernel<false, 8, false>, append_kernel<false, 1, false>, a, s);
+  if (a.num_axes) return a.interleaved ? launch_append_as<true, true>(a, s) : launch_append_as<false, true>(a, s);
+  return a.interleaved ? launch_append_as<true, false>(a, s) : launch_append_as<false, false>(a, s);
 }
 
 cudaError_t launch_read(const KvReadArgs& a, cudaStream_t s) {

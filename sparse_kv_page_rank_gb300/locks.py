@@ -52,6 +52,11 @@ LOCKS_DEVERR_LENGTHS = 0x4
 LOCKS_DEVERR_PAGE_ID = 0x8
 LOCKS_DEVERR_TIMEOUT = 0x10
 LOCKS_DEVERR_POSITION = 0x20
+LOCKSGEN_DEVERR_LOGITS = 0x40
+LOCKSGEN_DEVERR_PARENT = 0x80
+LOCKSGEN_MAX_BEAMS = 32
+LOCKSGEN_MAX_KEEP = 64
+LOCKSGEN_MAX_AXES = 4
 
 
 class LocksError(RuntimeError):
@@ -91,6 +96,19 @@ class lockskv_append_t(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
+class locksgen_axes_t(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64), ("num_axes", ctypes.c_int32),
+                ("axis_of_pair", ctypes.c_uint8 * 64)]
+
+
+class locksgen_choice_t(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("scores", ctypes.c_void_p), ("ended", ctypes.c_void_p),
+                ("out_scores", ctypes.c_void_p), ("out_parents", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p),
+                ("out_ended", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("beams", ctypes.c_int32), ("vocab", ctypes.c_int32), ("keep", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("end_token", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -124,6 +142,13 @@ def lib() -> ctypes.CDLL:
             "lockskv_read": (ctypes.c_int, [C, T, vp, vp, vp, sz, vp]),
             "lockskv_prompt_workspace_size": (ctypes.c_int, [C, R, T, P(sz)]),
             "lockskv_prompt_attend": (ctypes.c_int, [C, R, T, vp, i64, vp, vp, vp, sz, vp]),
+            "locksgen_append_axes": (ctypes.c_int, [C, T, A, P(locksgen_axes_t), vp, sz, vp]),
+            "locksgen_select_workspace_size": (ctypes.c_int, [P(locksgen_choice_t), P(sz)]),
+            "locksgen_select": (ctypes.c_int, [P(locksgen_choice_t), vp, sz, vp]),
+            "locksgen_reorder_workspace_size": (ctypes.c_int, [C, i32, P(sz)]),
+            "locksgen_reorder": (ctypes.c_int, [C, i32, i32, vp, vp, sz, vp]),
+            "locksgen_attend_workspace_size": (ctypes.c_int, [C, R, i32, P(sz)]),
+            "locksgen_attend": (ctypes.c_int, [C, R, i32, vp, vp, vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -224,6 +249,35 @@ def make_append(k, v, q=None, q_out=None, rope=None, rotary_dim: int = 0, positi
         rows = rope.shape[0]
     return lockskv_append_t(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), _ptr(rope), _ptr(positions),
                             _row_stride(k, "k"), _row_stride(v, "v"), qs, qos, heads, rows, rotary_dim, interleaved)
+
+
+def rope_axes(parts, cyclic: bool = False) -> list[int]:
+    """The axis of each rotated pair when axis a has parts[a] of them.  The axes follow one
+    another; or, ``cyclic``, they take turns: axis a > 0 has the pairs a, a + n, a + 2 n, ...
+    (n axes) and axis 0 all others."""
+    parts = [int(n) for n in parts]
+    if not parts or min(parts) < 0:
+        raise ValueError("an axis has a number of pairs")
+    if not cyclic:
+        return [a for a, n in enumerate(parts) for _ in range(n)]
+    axes = [0] * sum(parts)
+    for a in range(1, len(parts)):
+        for i in range(parts[a]):
+            if a + i * len(parts) >= len(axes):
+                raise ValueError(f"axis {a} cannot take turns for {parts[a]} of {len(axes)} pairs")
+            axes[a + i * len(parts)] = a
+    return axes
+
+
+def make_axes(axis_of_pair) -> locksgen_axes_t:
+    """What ``LocksRuntime.append`` takes as ``axes``: the axis of each rotated pair
+    (``rope_axes`` gives the usual ones).  The positions are set by the call."""
+    axis_of_pair = [int(a) for a in axis_of_pair]
+    if not 0 < len(axis_of_pair) <= 64 or min(axis_of_pair) < 0 or max(axis_of_pair) >= LOCKSGEN_MAX_AXES:
+        raise ValueError(f"the axes of 1 to 64 pairs, each below {LOCKSGEN_MAX_AXES}")
+    axes = locksgen_axes_t(None, 0, max(axis_of_pair) + 1, (ctypes.c_uint8 * 64)(*axis_of_pair))
+    axes.pairs = len(axis_of_pair)
+    return axes
 
 
 def make_summary(basis_t, coeffs, rank: int, dtype: int = LOCKS_DTYPE_BF16) -> locks_summary_t:
@@ -331,3 +385,43 @@ def lockskv_prompt_attend(cache, params, tokens, q, q_stride: int, out, lse, ws,
     _check(lib().lockskv_prompt_attend(ctypes.byref(cache), ctypes.byref(params), ctypes.byref(tokens), _ptr(q),
                                        int(q_stride), _ptr(out), _ptr(lse), _ptr(ws), int(ws_bytes),
                                        _stream(stream)), "lockskv_prompt_attend")
+
+
+def locksgen_append_axes(cache, tokens, append, axes, ws=None, ws_bytes: int = 0, stream=None):
+    _check(lib().locksgen_append_axes(ctypes.byref(cache), ctypes.byref(tokens), ctypes.byref(append), ctypes.byref(axes),
+                                      _ptr(ws), int(ws_bytes), _stream(stream)), "locksgen_append_axes")
+
+
+def locksgen_select_workspace_size(choice) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().locksgen_select_workspace_size(ctypes.byref(choice), ctypes.byref(n)), "locksgen_select_workspace_size")
+    return int(n.value)
+
+
+def locksgen_select(choice, ws, ws_bytes: int, stream=None):
+    _check(lib().locksgen_select(ctypes.byref(choice), _ptr(ws), int(ws_bytes), _stream(stream)), "locksgen_select")
+
+
+def locksgen_reorder_workspace_size(cache, beams: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().locksgen_reorder_workspace_size(ctypes.byref(cache), int(beams), ctypes.byref(n)),
+           "locksgen_reorder_workspace_size")
+    return int(n.value)
+
+
+def locksgen_reorder(caches, num_caches: int, beams: int, parents, ws, ws_bytes: int, stream=None):
+    """caches: a ctypes array of num_caches locks_cache_t."""
+    _check(lib().locksgen_reorder(caches, int(num_caches), int(beams), _ptr(parents), _ptr(ws), int(ws_bytes),
+                                  _stream(stream)), "locksgen_reorder")
+
+
+def locksgen_attend_workspace_size(cache, params, beams: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().locksgen_attend_workspace_size(ctypes.byref(cache), ctypes.byref(params), int(beams), ctypes.byref(n)),
+           "locksgen_attend_workspace_size")
+    return int(n.value)
+
+
+def locksgen_attend(cache, params, beams: int, shared_pages, q, out, lse, ws, ws_bytes: int, stream=None):
+    _check(lib().locksgen_attend(ctypes.byref(cache), ctypes.byref(params), int(beams), _ptr(shared_pages), _ptr(q),
+                                 _ptr(out), _ptr(lse), _ptr(ws), int(ws_bytes), _stream(stream)), "locksgen_attend")

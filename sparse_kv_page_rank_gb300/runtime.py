@@ -182,7 +182,7 @@ class LocksRuntime:
 
     def append(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None, *,
                rope: torch.Tensor | None = None, rotary_dim: int | None = None, interleaved: bool = False,
-               positions: torch.Tensor | None = None, cu_tokens: torch.Tensor | None = None,
+               positions: torch.Tensor | None = None, axes=None, cu_tokens: torch.Tensor | None = None,
                max_tokens: int | None = None, q_out: torch.Tensor | None = None, stream=None):
         """Writes the newest tokens of every sequence into the cache (seq_lens
         already counts them) and rotates their keys and queries.
@@ -191,7 +191,10 @@ class LocksRuntime:
         fused projection are fine); rope: float32 [positions][rotary_dim], the
         cosines, then the sines; cu_tokens int32 [batch + 1] gives each
         sequence's rows and max_tokens the most that one has (default: total);
-        without cu_tokens there is one token per sequence.  Returns the
+        without cu_tokens there is one token per sequence.  positions: int32
+        [total], the table rows of the tokens (default: their positions in the
+        sequences); or, with ``axes`` (``locks.make_axes``: the axis of each
+        rotated pair), int32 [axes][total], a row per axis.  Returns the
         rotated queries (``q_out``, by default a new tensor; ``q`` itself
         rotates in place), or None without q."""
         shape = k.shape
@@ -221,12 +224,31 @@ class LocksRuntime:
                 rotary_dim = cols
             elif rotary_dim != cols:
                 raise ValueError("rope must have rotary_dim columns")
+        if axes is not None:
+            return self._append_axes(k, v, q, q_out, rope, rotary_dim, interleaved, positions, axes,
+                                     self._tokens(total, cu_tokens, max_tokens), handle)
         if positions is not None and (positions.dtype is not torch.int32 or positions.numel() != total
                                       or positions.get_device() != index or not positions.is_contiguous()):
             raise ValueError("positions must be contiguous int32 [tokens] on the device")
         L.lockskv_append(self.cache, self._tokens(total, cu_tokens, max_tokens),
                          L.make_append(k, v, q, q_out, rope, rotary_dim, positions, interleaved),
                          self.kv_ws, 256, handle)
+        return q_out
+
+    def _append_axes(self, k, v, q, q_out, rope, rotary_dim, interleaved, positions, axes, tokens, handle):
+        if rope is None or axes.pairs != rotary_dim // 2:
+            raise ValueError("axes need a rope, of whose pairs each has its axis")
+        if (positions is None or positions.dtype is not torch.int32 or positions.dim() != 2
+                or positions.shape[1] != tokens.total or positions.get_device() != self._index
+                or (tokens.total > 1 and positions.stride(1) != 1)):
+            raise ValueError("positions must be int32 [axes][tokens] on the device, an axis' tokens contiguous")
+        n, total = positions.shape
+        stride = positions.stride(0) if n > 1 else total
+        if not axes.num_axes <= n <= L.LOCKSGEN_MAX_AXES or stride < total:
+            raise ValueError(f"positions of {axes.num_axes} to {L.LOCKSGEN_MAX_AXES} axes are needed, that do not overlap")
+        call = L.locksgen_axes_t(positions.data_ptr(), stride, n, axes.axis_of_pair)
+        L.locksgen_append_axes(self.cache, tokens, L.make_append(k, v, q, q_out, rope, rotary_dim, None, interleaved),
+                               call, self.kv_ws, 256, handle)
         return q_out
 
     def read_tokens(self, total: int, *, cu_tokens: torch.Tensor | None = None, max_tokens: int | None = None,
