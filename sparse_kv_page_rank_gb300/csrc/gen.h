@@ -10,7 +10,8 @@
 namespace locks {
 
 // Choice of continuations (gen_select.cu).
-constexpr int kSelectPart = 8192;  // logits that a CTA takes into its registers
+constexpr int kSelectChunk = 8192, kSelectSmall = 2048;  // logits that a CTA takes into its registers
+constexpr int kSelectCtas = 3;  // of them per SM
 struct SelectArgs {
   const void* logits;
   const float* scores;
@@ -23,7 +24,9 @@ struct SelectArgs {
   uint2* lists;        // ws: [rows][n_parts][keep] (ordered logit, token), best first
   int* err;
   long long row_stride;
-  int batch, beams, vocab, keep, end_token, n_parts;
+  int batch, beams, vocab, keep, end_token;
+  int n_parts, chunks;  // parts of a row, chunks of a part
+  int small;            // 1: chunks of kSelectSmall
 };
 cudaError_t launch_select(const SelectArgs& a, bool f32, cudaStream_t s);
 

@@ -15,8 +15,11 @@ locks_status_t check_ws(void* ws, size_t bytes, size_t need) {
   return LOCKS_OK;
 }
 
+// Parts of the rows of a choice: small chunks while chunks are few, and as many parts as take
+// least, in chunks' times: waves of CTAs, each of its chunks and some two more.
+constexpr double kPartChunks = 2.0;
 struct SelectPlan {
-  int n_parts = 0;
+  int n_parts = 0, chunks = 1, small = 0;
   size_t off_parts = 0, off_lists = 0, total = 0;
 };
 
@@ -31,7 +34,20 @@ locks_status_t plan_select(const locksgen_choice_t* c, SelectPlan* pl) {
   if (rows > 65535) return LOCKS_ERR_UNSUPPORTED;  // the launch's second dimension
   // a row may begin inside its first 16 bytes
   const int vec = c->dtype == LOCKS_DTYPE_BF16 ? 8 : 4;
-  pl->n_parts = (c->vocab + vec - 1 + kSelectPart - 1) / kSelectPart;
+  const long long span = c->vocab + vec - 1, sms = device_sm_count();
+  auto count = [&](int size) { return (span + size - 1) / size; };
+  pl->small = rows * count(kSelectChunk) <= sms / 2 ? 1 : 0;
+  const long long chunks = count(pl->small ? kSelectSmall : kSelectChunk);
+  const long long slots = kSelectCtas * sms;
+  double best = 1e30;
+  for (long long n = 1; n <= chunks; ++n) {
+    const long long each = (chunks + n - 1) / n, waves = (rows * n + slots - 1) / slots;
+    const double time = (double)waves * ((double)each + kPartChunks);
+    if (time >= best) continue;
+    best = time;
+    pl->n_parts = (int)((chunks + each - 1) / each);
+    pl->chunks = (int)each;
+  }
   size_t off = kAlign;  // the error word
   pl->off_parts = off;
   off = align_up(off + sizeof(float4) * rows * pl->n_parts);
@@ -112,6 +128,8 @@ locks_status_t locksgen_select(const locksgen_choice_t* c, void* ws, size_t ws_b
   a.keep = c->keep;
   a.end_token = c->end_token;
   a.n_parts = pl.n_parts;
+  a.chunks = pl.chunks;
+  a.small = pl.small;
   return cuda_status(launch_select(a, c->dtype == LOCKS_DTYPE_F32, static_cast<cudaStream_t>(stream)));
 }
 
