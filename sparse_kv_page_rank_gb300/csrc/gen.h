@@ -10,8 +10,8 @@
 namespace locks {
 
 // Choice of continuations (gen_select.cu).
-constexpr int kSelectChunk = 8192, kSelectSmall = 2048;  // logits that a CTA takes into its registers
-constexpr int kSelectCtas = 3;  // of them per SM
+constexpr int kSelectChunk = 4096, kSelectSmall = 2048;  // logits that a CTA takes into its registers
+constexpr int kSelectCtas = 4;  // of them per SM
 struct SelectArgs {
   const void* logits;
   const float* scores;
@@ -64,7 +64,7 @@ struct GroupArgs {
   const int32_t* shared_pages;  // [batch / beams]
   uint16_t* out;
   float* lse;         // or null
-  long long* offsets; // ws: [requests + 1] first place of each in the line, and their number
+  uint32_t* offsets;  // ws: [requests + 1] first place of each in the line, and their number
   // ws, partial results: [ctas + problems * blocks][kSharedRows] of the shared parts, then
   // [ctas + batch * Hkv][group] of the rows' own
   float* part_o;

@@ -75,11 +75,12 @@ locks_status_t plan_group(const locks_cache_t* c, const locks_params_t* p, int b
   pl->n_blocks = (beams * G + kSharedRows - 1) / kSharedRows;
   const long long segments = groups * hkv * pl->n_blocks + rows;
   const long long tiles = ((long long)c->max_pages * c->page_size + kPage - 1) / kPage;
+  if (segments * (tiles + 2) > 0x7fffffffLL) return LOCKS_ERR_UNSUPPORTED;  // places of the line are 32-bit numbers
   pl->n_ctas = (int)std::min<long long>((long long)group_attend_ctas_per_sm() * device_sm_count(), segments * tiles);
   const size_t parts = (size_t)(pl->n_ctas + groups * hkv * pl->n_blocks) * kSharedRows + (size_t)(pl->n_ctas + rows) * G;
   size_t off = kAlign;  // the error word
   pl->off_line = off;
-  off = align_up(off + sizeof(long long) * (groups + 1));
+  off = align_up(off + sizeof(uint32_t) * (groups + 1));
   pl->off_ml = off;
   off = align_up(off + sizeof(float2) * parts);
   pl->off_o = off;
@@ -217,7 +218,7 @@ locks_status_t locksgen_attend(const locks_cache_t* cache, const locks_params_t*
   a.shared_pages = shared_pages;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  a.offsets = at<long long>(ws, pl.off_line);
+  a.offsets = at<uint32_t>(ws, pl.off_line);
   a.part_o = at<float>(ws, pl.off_o);
   a.part_ml = at<float2>(ws, pl.off_ml);
   a.err = at<int>(ws, 0);

@@ -39,15 +39,16 @@ constexpr int kSegment = 2;
 constexpr int kHalfTile = 64 * 128;   // bytes of a 64-row x 64-column bf16 box
 constexpr int kTile = 2 * kHalfTile;  // 64 tokens of K (or V)
 constexpr int kQueryBytes = kSharedRows * kHeadDim * 2;
-constexpr int kOStride = 132;  // padded row of a warp's outputs (floats)
+template <bool Q4>
+constexpr int kOStride = Q4 ? 132 : 136;  // padded row of a warp's outputs (floats): no two lanes' stores meet in a bank
 template <bool Q4>
 constexpr int kStageBytes = Q4 ? kQ4Slot : 2 * kTile;
 template <bool Q4>
 constexpr int kStages = Q4 ? 8 : 3;
 template <bool Q4>
 constexpr int kSmem = kStages<Q4> * kStageBytes<Q4> + kQueryBytes + 1024;
-static_assert(kWarps * kSharedRows * kOStride * 4 <= kStages<true> * kStageBytes<true> &&
-                  kWarps * kSharedRows * kOStride * 4 <= kStages<false> * kStageBytes<false>,
+static_assert(kWarps * kSharedRows * kOStride<true> * 4 <= kStages<true> * kStageBytes<true> &&
+                  kWarps * kSharedRows * kOStride<false> * 4 <= kStages<false> * kStageBytes<false>,
               "the merge fits the ring");
 
 // ---- lengths, and what follows from them ----------------------------------------------
@@ -112,10 +113,24 @@ __device__ void load_group(const GroupArgs& a, int g, Group& s, bool says) {
 }
 static_assert(LOCKSGEN_MAX_BEAMS == 32, "a lane per row");
 
-// The part of the line that CTA c of C has.
-__device__ __forceinline__ long long part_begin(long long total, long long C, long long c) { return c < C ? total * c / C : total; }
-__device__ __forceinline__ long long part_owner(long long total, long long C, long long y) { return ((y + 1) * C - 1) / total; }
-__device__ __forceinline__ long long ctas_used(long long total, int n) { return min((long long)n, max(total, 1LL)); }
+// The line in equal parts: the first `more` CTAs have one place more than the others.
+struct Parts {
+  uint32_t ctas, each, more;
+  __device__ __forceinline__ Parts(uint32_t total, int n) {
+    ctas = max(min((uint32_t)n, total), 1u);
+    each = total / ctas;
+    more = total - each * ctas;
+  }
+  __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
+    const uint32_t c = min(cta, ctas);
+    return c * each + min(c, more);
+  }
+  // the CTA that has place y
+  __device__ __forceinline__ uint32_t owner(uint32_t y) const {
+    const uint32_t big = more * (each + 1);
+    return y < big ? y / (each + 1) : more + (y - big) / each;
+  }
+};
 
 // ---- a piece of a segment ---------------------------------------------------------------
 
@@ -134,9 +149,8 @@ struct Shared {
   int left[8][4];  // per stage (and page of it): tokens of the tile to be seen
   float m[kWarps][kSharedRows], l[kWarps][kSharedRows];
   Group grp;
-  long long offset, total;
+  uint32_t offset, scan[kWarps];
   int group, abort;
-  long long scan[kWarps];
 };
 
 // The query of row r of a piece.
@@ -378,7 +392,6 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
 
   // warp 0 asks for the copies; its lanes hold 32 pages' entries, and the next 32
   int cur = 0, nxt = 0;
-  const bool checks = p.shared && p.h == 0 && p.block == 0;
   auto entry = [&](int k) {  // of page k of the piece
     if (k >= p.pages) return 0;
     const int lp = p.page0 + k;
@@ -387,10 +400,6 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
       set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
       phys = -1;
     }
-    if (checks)
-      for (int w = 0; w < a.beams; ++w)
-        if (sh.grp.len[w] > 0 && __ldg(a.block_table + (size_t)(G * a.beams + w) * a.max_pages + lp) != phys)
-          set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
     return phys;
   };
   auto issue = [&](int t) {  // warp 0: tile t of the piece
@@ -435,6 +444,17 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
     if (r < p.rows) v = __ldg(reinterpret_cast<const uint4*>(a.q + query_row(a, p, G, r) * kHeadDim) + chunk);
     const uint32_t at = query_addr<Q4>(qbase, r, chunk);
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  }
+  // one head's last warp sees, while the first copies are under way, whether the rows do share
+  if (p.shared && p.h == 0 && p.block == 0 && warp == kWarps - 1) {
+    bool differs = false;
+    for (int k = lane; k < p.pages; k += 32) {
+      const int32_t* column = a.block_table + (size_t)G * a.beams * a.max_pages + p.page0 + k;
+      const int phys = __ldg(p.table + p.page0 + k);
+#pragma unroll 8
+      for (int w = 0; w < a.beams; ++w) differs |= __ldg(column + (size_t)w * a.max_pages) != phys && sh.grp.len[w] > 0;
+    }
+    if (differs) set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
   }
   __syncthreads();
 
@@ -491,41 +511,44 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      float* row = so + (warp * kSharedRows + 16 * i + 8 * k + g) * kOStride;
+      const int r = 16 * i + 8 * k + g;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][r]);
+      const float f = M == -INFINITY ? 1.f : fast_exp2(st.m[i][k] - M);
+      float* row = so + (warp * kSharedRows + r) * kOStride<Q4>;
       if constexpr (Q4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float4*>(row + 32 * j + 8 * c + 4 * e) =
-                make_float4(st.o[i][4 * j][2 * k + e], st.o[i][4 * j + 1][2 * k + e], st.o[i][4 * j + 2][2 * k + e],
-                            st.o[i][4 * j + 3][2 * k + e]);
+                make_float4(f * st.o[i][4 * j][2 * k + e], f * st.o[i][4 * j + 1][2 * k + e],
+                            f * st.o[i][4 * j + 2][2 * k + e], f * st.o[i][4 * j + 3][2 * k + e]);
       } else {
 #pragma unroll
         for (int n = 0; n < 16; ++n)
-          *reinterpret_cast<float2*>(row + 8 * n + 2 * c) = make_float2(st.o[i][n][2 * k], st.o[i][n][2 * k + 1]);
+          *reinterpret_cast<float2*>(row + 8 * n + 2 * c) = make_float2(f * st.o[i][n][2 * k], f * st.o[i][n][2 * k + 1]);
       }
     }
+  if (tid < p.rows) {
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][tid]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) L = fmaf(sh.l[w][tid], M == -INFINITY ? 1.f : fast_exp2(sh.m[w][tid] - M), L);
+    part_ml[tid] = make_float2(M, L);
+  }
   __syncthreads();
   for (int e = tid; e < p.rows * (kHeadDim / 4); e += kThreads) {
-    const int r = e / (kHeadDim / 4), c4 = e % (kHeadDim / 4);
-    float M = -INFINITY;
+    const float* at = so + e / (kHeadDim / 4) * kOStride<Q4> + e % (kHeadDim / 4) * 4;
+    float4 O = *reinterpret_cast<const float4*>(at);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][r]);
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = M == -INFINITY ? 1.f : fast_exp2(sh.m[w][r] - M);
-      const float4 v = *reinterpret_cast<const float4*>(so + (w * kSharedRows + r) * kOStride + 4 * c4);
-      L = fmaf(sh.l[w][r], f, L);
-      O.x = fmaf(v.x, f, O.x);
-      O.y = fmaf(v.y, f, O.y);
-      O.z = fmaf(v.z, f, O.z);
-      O.w = fmaf(v.w, f, O.w);
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 v = *reinterpret_cast<const float4*>(at + w * kSharedRows * kOStride<Q4>);
+      O = make_float4(O.x + v.x, O.y + v.y, O.z + v.z, O.w + v.w);
     }
     reinterpret_cast<float4*>(part_o)[e] = O;
-    if (c4 == 0) part_ml[r] = make_float2(M, L);
   }
   // the ring was written with ordinary stores: before the next copies into it
   fence_proxy_async();
@@ -558,67 +581,75 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
   }
   pdl_wait();
 
-  // the whole line
-  long long mine = 0;
-  for (int g = tid; g < groups; g += kThreads) mine += head_line(a, g);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh.scan[warp] = mine;
-  __syncthreads();
-  const long long total = (sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3]) * a.num_kv_heads;
-  const long long C = ctas_used(total, a.n_ctas);
-  const long long lo = part_begin(total, C, cta), hi = part_begin(total, C, (long long)cta + 1);
-  // the request that holds place lo; CTA 0 leaves every request's first place for the join
-  long long before = 0;
-  for (int g0 = 0; g0 < groups; g0 += kThreads) {
-    const int g = g0 + tid;
-    const long long own = g < groups ? (long long)head_line(a, g) * a.num_kv_heads : 0;
-    long long upto = own;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const long long other = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += other;
-    }
+  uint32_t lo, hi;
+  if (groups == 1) {
+    if (warp == 0) load_group(a, 0, sh.grp, cta == 0);
+    if (tid == 0) sh.group = 0, sh.offset = 0;
     __syncthreads();
-    if (lane == 31) sh.scan[warp] = upto;
+    const Parts parts((uint32_t)sh.grp.line * a.num_kv_heads, a.n_ctas);
+    lo = parts.begin(cta);
+    hi = parts.begin(cta + 1);
+  } else {
+    // the whole line; with no more requests than threads, each thread's own for good
+    uint32_t own = tid < groups ? (uint32_t)head_line(a, tid) * a.num_kv_heads : 0, mine = own;
+    for (int g = tid + kThreads; g < groups; g += kThreads) mine += (uint32_t)head_line(a, g) * a.num_kv_heads;
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) sh.scan[warp] = sum;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) upto += w < warp ? sh.scan[w] : 0;
-    const long long first = before + upto - own;
-    if (lo >= first && lo < first + own) {
-      sh.group = g;
-      sh.offset = first;
+    const uint32_t total = sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3];
+    const Parts parts(total, a.n_ctas);
+    lo = parts.begin(cta);
+    hi = parts.begin(cta + 1);
+    // the request that holds place lo; CTA 0 leaves every request's first place for the join
+    uint32_t before = 0;
+    for (int g0 = 0; g0 < groups; g0 += kThreads) {
+      const int g = g0 + tid;
+      if (g0 > 0) own = g < groups ? (uint32_t)head_line(a, g) * a.num_kv_heads : 0;
+      uint32_t upto = own;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const uint32_t other = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += other;
+      }
+      __syncthreads();
+      if (lane == 31) sh.scan[warp] = upto;
+      __syncthreads();
+      for (int w = 0; w < kWarps; ++w) upto += w < warp ? sh.scan[w] : 0;
+      const uint32_t first = before + upto - own;
+      if (lo >= first && lo < first + own) {
+        sh.group = g;
+        sh.offset = first;
+      }
+      if (cta == 0 && g < groups) a.offsets[g] = first;
+      before += sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3];
+      if (cta != 0 && before > lo) break;
     }
-    if (cta == 0 && g < groups) a.offsets[g] = first;
-    before += sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3];
-    if (cta != 0 && before > lo) break;
+    if (cta == 0 && tid == 0) a.offsets[groups] = total;
+    __syncthreads();
   }
-  if (cta == 0 && tid == 0) a.offsets[groups] = total;
-  __syncthreads();
   if (lo >= hi) return;
   int g = sh.group;
-  long long offset = sh.offset, pos = lo;
-  uint32_t seq = 0;
+  uint32_t offset = sh.offset, pos = lo, seq = 0;
   auto load = [&] {
     if (warp == 0) load_group(a, g, sh.grp, true);
     __syncthreads();
   };
-  load();
-  const int problems_per_group = a.num_kv_heads;
+  if (groups > 1) load();
   const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;  // records of shared parts
   while (pos < hi) {
-    while (pos >= offset + (long long)sh.grp.line * a.num_kv_heads) {
-      offset += (long long)sh.grp.line * a.num_kv_heads;
+    while (pos >= offset + (uint32_t)sh.grp.line * a.num_kv_heads) {
+      offset += (uint32_t)sh.grp.line * a.num_kv_heads;
       ++g;
       __syncthreads();  // all have read the last request's
       load();
     }
     const Group& s = sh.grp;
     Piece p;
-    const long long in = pos - offset;
-    p.h = (int)(in / s.line);
-    int x = (int)(in % s.line);
+    const uint32_t in = pos - offset;
+    p.h = (int)(in / (uint32_t)s.line);
+    int x = (int)(in - (uint32_t)p.h * s.line);
     const int shared_line = line_of(s.shared_tiles), shared_all = a.n_blocks * shared_line;
-    long long start = offset + (long long)p.h * s.line;
+    uint32_t start = offset + (uint32_t)p.h * s.line;
     int tiles, end_page;
     p.shared = x < shared_all;
     p.w = p.block = 0;
@@ -640,12 +671,12 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
       end_page = (p.limit + P - 1) / P;
       p.table = a.block_table + (size_t)(g * a.beams + p.w) * a.max_pages;
     }
-    p.t0 = (int)max(0LL, pos - start - kSegment);
-    p.t1 = (int)min((long long)tiles, max(0LL, hi - start - kSegment));
+    p.t0 = max(0, (int)(pos - start) - kSegment);
+    p.t1 = min(tiles, max(0, (int)(hi - start) - kSegment));
     if (p.t1 > p.t0) {
       p.page0 = (p.shared ? 0 : s.sp) + p.t0 * kPPT;
       p.pages = min(end_page - p.page0, (p.t1 - p.t0) * kPPT);
-      const size_t problem = (size_t)g * problems_per_group + p.h;
+      const size_t problem = (size_t)g * a.num_kv_heads + p.h;
       size_t row;  // of the partial results
       if (p.shared) row = (cta + problem * a.n_blocks + p.block) * kSharedRows;
       else row = own_base * kSharedRows + (cta + problem * a.beams + p.w) * a.group;
@@ -661,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
 }
 
 // Joins the pieces of one (row, query head).  Grid (batch * Hkv, group).
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinFlight = 8;  // pieces that a warp loads at once
 
@@ -677,54 +708,62 @@ __global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArg
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  const long long total = a.offsets[groups], C = ctas_used(total, a.n_ctas);
+  const uint32_t total = groups == 1 ? (uint32_t)s.line * a.num_kv_heads : a.offsets[groups];
+  const Parts parts(total, a.n_ctas);
   const int len = s.len[w];
   const size_t out_row = ((size_t)b * a.num_kv_heads + h) * a.group + e;
   if (len == 0) {
-    a.out[out_row * kHeadDim + tid] = 0;
+    if (tid < kHeadDim) a.out[out_row * kHeadDim + tid] = 0;
     if (a.lse && tid == 0) a.lse[out_row] = -INFINITY;
     return;
   }
   // the CTAs that have pieces of the two segments
   const int i = w * a.group + e, block = i / kSharedRows;
   const int shared_line = line_of(s.shared_tiles), own_tiles = tiles_of(len - s.sp * a.page_size);
-  const long long head = a.offsets[g] + (long long)h * s.line;
+  const uint32_t head = (groups == 1 ? 0u : a.offsets[g]) + (uint32_t)h * s.line;
   const size_t problem = (size_t)g * a.num_kv_heads + h;
   const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;
-  long long c0[2] = {0, 0}, slot[2];
+  uint32_t c0[2] = {0, 0};
   int n[2] = {0, 0};
-  auto segment = [&](int k, long long start, int tiles) {
+  auto segment = [&](int k, uint32_t start, int tiles) {
     if (tiles == 0) return;
-    c0[k] = part_owner(total, C, start);
-    n[k] = (int)(part_owner(total, C, start + kSegment + tiles - 1) - c0[k]) + 1;
+    c0[k] = parts.owner(start);
+    n[k] = (int)(parts.owner(start + kSegment + tiles - 1) - c0[k]) + 1;
     // the first of them may end before the first tile
-    while (part_begin(total, C, c0[k] + 1) <= start + kSegment) ++c0[k], --n[k];
+    while (parts.begin(c0[k] + 1) <= start + kSegment) ++c0[k], --n[k];
   };
-  segment(0, head + (long long)block * shared_line, s.shared_tiles);
-  segment(1, head + (long long)a.n_blocks * shared_line + (w ? s.upto[w - 1] : 0), own_tiles);
-  slot[0] = (long long)(c0[0] + problem * a.n_blocks + block) * kSharedRows + i % kSharedRows;
-  slot[1] = (long long)own_base * kSharedRows + (long long)(c0[1] + problem * a.beams + w) * a.group + e;
+  segment(0, head + (uint32_t)block * shared_line, s.shared_tiles);
+  segment(1, head + (uint32_t)a.n_blocks * shared_line + (w ? s.upto[w - 1] : 0), own_tiles);
+  const size_t slot[2] = {(c0[0] + problem * a.n_blocks + block) * kSharedRows + i % kSharedRows,
+                          own_base * kSharedRows + (c0[1] + problem * a.beams + w) * a.group + e};
   const int all = n[0] + n[1];
-  auto row = [&](int k) { return (size_t)(k < n[0] ? slot[0] + (long long)k * kSharedRows : slot[1] + (long long)(k - n[0]) * a.group); };
-  float M = -INFINITY, L = 0.f;
-  for (int k = lane; k < all; k += 32) M = fmaxf(M, __ldcg(a.part_ml + row(k)).x);
-  M = warp_max(M);
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = warp; k0 < all; k0 += kJoinWarps * kJoinFlight) {
-    float4 v[kJoinFlight];
-    float2 ml[kJoinFlight];
+  auto row = [&](int k) { return k < n[0] ? slot[0] + (size_t)k * kSharedRows : slot[1] + (size_t)(k - n[0]) * a.group; };
+  // a warp takes pieces warp, warp + 8, ..., the first of them under way while the reference is found
+  float4 v[kJoinFlight];
+  float2 ml[kJoinFlight];
+  auto fetch = [&](int k0) {
 #pragma unroll
     for (int k = 0; k < kJoinFlight; ++k) {
       const int at = k0 + kJoinWarps * k;
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      ml[k] = make_float2(M, 0.f);
+      ml[k] = make_float2(-INFINITY, 0.f);
       if (at >= all) continue;
       v[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row(at) * kHeadDim) + lane);
       ml[k] = __ldcg(a.part_ml + row(at));
     }
+  };
+  fetch(warp);
+  float M = -INFINITY, L = 0.f;
+  for (int k = lane; k < all; k += 32) M = fmaxf(M, __ldcg(a.part_ml + row(k)).x);
+  M = warp_max(M);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = warp; k0 < all; k0 += kJoinWarps * kJoinFlight) {
+    if (k0 != warp) fetch(k0);
 #pragma unroll
     for (int k = 0; k < kJoinFlight; ++k) {
-      const float f = M == -INFINITY ? 1.f : fast_exp2(ml[k].x - M);
+      const bool none = ml[k].x == -INFINITY;  // a piece of which the row has seen nothing (or a NaN: its sum)
+      const float f = none ? 1.f : fast_exp2(ml[k].x - ref);
       L = fmaf(ml[k].y, f, L);
       O.x = fmaf(v[k].x, f, O.x);
       O.y = fmaf(v[k].y, f, O.y);
@@ -735,6 +774,7 @@ __global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArg
   *reinterpret_cast<float4*>(&so[warp][4 * lane]) = O;
   if (lane == 0) sl[warp] = L;
   __syncthreads();
+  if (tid >= kHeadDim) return;
   float Os = 0.f, Ls = 0.f;
 #pragma unroll
   for (int k = 0; k < kJoinWarps; ++k) {
@@ -745,7 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArg
   a.out[out_row * kHeadDim + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(val));
   if (a.lse && tid == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
 }
-static_assert(kJoinThreads == kHeadDim, "a thread per dimension");
+static_assert(kJoinThreads >= kHeadDim, "a thread per dimension");
 
 template <int P, bool Q4>
 cudaError_t launch(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {

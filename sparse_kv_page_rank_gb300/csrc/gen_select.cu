@@ -36,7 +36,7 @@ static_assert(kThreads >= LOCKSGEN_MAX_KEEP, "a thread per continuation");
 // The list of a part: members that chunks may add to, and beside them those of the slow
 // way, `keep` threads with all their logits.
 constexpr int kShort = 256;
-constexpr int kTidy = 128;  // more are cut back to `keep` after chunks 1, 3, 7, ...
+constexpr int kTidy = 8;  // so many more than `keep` are cut back after chunks 1, 3, 7, ..., which raises T
 
 __device__ __forceinline__ bool is_live(float score, int ended) { return score > -INFINITY && score < INFINITY && !ended; }
 
@@ -63,6 +63,12 @@ struct Chunk {
   // 16-byte loads of the aligned pieces that cover the row, which begins at element
   // -first of the chunk; the pieces at its ends element by element
   __device__ __forceinline__ void load(const T* base, int first, int vocab) {
+    if (first >= 0 && first + kSize <= vocab) {
+      const uint4* at = reinterpret_cast<const uint4*>(base + first) + threadIdx.x;
+#pragma unroll
+      for (int k = 0; k < LOADS; ++k) raw[k] = __ldg(at + k * kThreads);
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
       const int i = first + (k * kThreads + threadIdx.x) * kVec;
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) part_kernel(const Selec
   constexpr int kMine = C::kMine;
   static_assert(kMine <= 32, "a bit per logit");
   __shared__ unsigned long long list[kShort + LOCKSGEN_MAX_KEEP * kMine], best_of[kThreads], tidy[LOCKSGEN_MAX_KEEP], thresh;
-  __shared__ float sm_m[kThreads / 32], sm_l[kThreads / 32];
+  __shared__ float sm_m[kThreads / 32], sm_l[kThreads / 32], first_t;
   __shared__ uint32_t top[kThreads];
   __shared__ int n_list;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -175,33 +181,39 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) part_kernel(const Selec
         for (int o = 1; o < kGroupLanes; o *= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
         if (lane % kGroupLanes == 0) top[tid / kGroupLanes] = orderable_key(g);
         __syncthreads();
-        const uint32_t v = top[lane];
-        int rank = 0;
+        if (warp == 0) {
+          const uint32_t v = top[lane];
+          int rank = 0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint32_t w = __shfl_sync(0xffffffffu, v, j);
-          rank += w > v || (w == v && j < lane);
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t w = __shfl_sync(0xffffffffu, v, j);
+            rank += w > v || (w == v && j < lane);
+          }
+          if (rank == a.keep - 1) first_t = below(v);
         }
-        t = below(__shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, rank == a.keep - 1)) - 1));
       } else {
         top[tid] = orderable_key(mine);
         __syncthreads();
-        // every warp: halving until about `keep` threads reach T
-        uint32_t v[kThreads / 32];
+        if (warp == 0) {
+          // halving until about `keep` threads reach T
+          uint32_t v[kThreads / 32];
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) v[i] = top[32 * i + lane];
-        uint32_t lo = 0, hi = 0xffffffffu;  // at least `keep` reach lo
-        while (lo < hi) {
-          const uint32_t mid = lo + (hi - lo) / 2 + 1;
-          int count = 0;
+          for (int i = 0; i < kThreads / 32; ++i) v[i] = top[32 * i + lane];
+          uint32_t lo = 0, hi = 0xffffffffu;  // at least `keep` reach lo
+          while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2 + 1;
+            int count = 0;
 #pragma unroll
-          for (int i = 0; i < kThreads / 32; ++i) count += __popc(__ballot_sync(0xffffffffu, v[i] >= mid));
-          if (count >= a.keep) lo = mid;
-          else hi = mid - 1;
-          if (count >= a.keep && count <= a.keep + 4) break;
+            for (int i = 0; i < kThreads / 32; ++i) count += __popc(__ballot_sync(0xffffffffu, v[i] >= mid));
+            if (count >= a.keep) lo = mid;
+            else hi = mid - 1;
+            if (count >= a.keep && count <= a.keep + 4) break;
+          }
+          if (lane == 0) first_t = below(lo);
         }
-        t = below(lo);
       }
+      __syncthreads();
+      t = first_t;
     }
     if (mine > t) {
       uint32_t mask = 0;
@@ -218,10 +230,17 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) part_kernel(const Selec
       const float was = m;
       m = fmaxf(m, mine);
       const float ref = m == -INFINITY ? 0.f : m;  // (-infinity less itself is no number)
-      float sum = 0.f;
+      const uint64_t less = f32x2(-ref, -ref), factor = f32x2(kLog2e, kLog2e);
+      uint64_t sum = f32x2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) sum += exp_of(x[j] - ref);
-      l = c == 0 ? sum : fmaf(l, exp_of(was - ref), sum);
+      for (int j = 0; j < kMine; j += 2) {
+        float e0, e1;
+        unpack_f32x2(mul_f32x2(add_f32x2(f32x2(x[j], x[j + 1]), less), factor), e0, e1);
+        sum = add_f32x2(sum, f32x2(fast_exp2(e0), fast_exp2(e1)));
+      }
+      float s0, s1;
+      unpack_f32x2(sum, s0, s1);
+      l = c == 0 ? s0 + s1 : fmaf(l, exp_of(was - ref), s0 + s1);
     }
     if (c == 0 && !last) {
       // Members are at least `keep` now, or else every number is one.  What is equal to T
@@ -235,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) part_kernel(const Selec
       __syncthreads();
       const int n = n_list;
       __syncthreads();
-      if (n > kTidy && n <= kShort && cut(n) == a.keep) t = key_logit((uint32_t)(tidy[a.keep - 1] >> 32));
+      if (n > a.keep + kTidy && n <= kShort && cut(n) == a.keep) t = key_logit((uint32_t)(tidy[a.keep - 1] >> 32));
     }
   }
   __syncthreads();
