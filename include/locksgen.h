@@ -144,8 +144,10 @@ LOCKS_API locks_status_t locksgen_attend_workspace_size(const locks_cache_t* cac
  * heads of a KV head) and not once per row.  No row may be shorter than what it shares: the count is
  * cut to the shortest row's full pages.  Where the columns differ after all,
  * LOCKS_DEVERR_BLOCK_TABLE is set and the request's results are those of some row's pages.
- * Logits, sums and outputs are accumulated in float32; the softmax weights (for
- * 4-bit pages times their scale) are rounded to bf16, 2^-9 of each. */
+ * Logits, sums and outputs are accumulated in float32; the softmax weights are
+ * rounded to bf16 for bf16 pages (2^-8 of each) and to half precision for 4-bit
+ * ones (2^-11, and 2^-32 of the row's largest), whose values s * code are rounded
+ * to half precision too. */
 LOCKS_API locks_status_t locksgen_attend(const locks_cache_t* cache, const locks_params_t* params, int32_t beams,
                                          const int32_t* shared_pages, const void* q, void* out, float* lse, void* ws,
                                          size_t ws_bytes, void* stream);

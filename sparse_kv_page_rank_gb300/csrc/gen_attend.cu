@@ -13,13 +13,12 @@
 // 16 w + 15, with the softmax and the outputs of its tokens in registers; the warps' states
 // meet in shared memory at the end of a piece.  The queries stay in shared memory (their
 // fragments would take 64 more registers than there are).  bf16 pages: ldmatrix.
-// 4-bit pages: the codes are bf16 numbers (exact), keys get their scale on the four
-// partial sums of a logit, values theirs on the weights, in fp32 before those are
-// rounded to bf16, whose range needs no care.
+// 4-bit pages: keys' codes are bf16 numbers (exact) and get their scale on the four partial
+// sums of a logit; values are s * code rounded to half precision (2^-11), and so are the weights.
 //
 // Work split.  All 64-token tiles of all problems lie in one line: request by request, KV
 // head by head, first the shared pages (once per block of 32 rows), then each row's own.  Every
-// CTA gets an equal part of it, two CTAs per SM; a segment counts kSegment tiles more
+// CTA gets an equal part of it, two CTAs per SM; a segment counts a few tiles more
 // than it has, which is what its queries, its first copies and its merge cost.  A piece
 // (the part of a segment that a CTA has) leaves its state in the workspace at place
 // CTA + segment, which no two pieces share; a second, dependent kernel joins them.
@@ -35,7 +34,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kSegment = 2;
+// Places that a segment has beyond its tiles.  Measured (2, 3, 4): bf16 pages, 131,000 shared
+// tokens 99, 91, 93 us, 32 K 34.4, 33.6, 33.6; 4-bit, four requests of 16 K 51.5, 52.9, 54.1.
+constexpr int kSegmentBf16 = 3, kSegmentQ4 = 2;
 constexpr int kHalfTile = 64 * 128;   // bytes of a 64-row x 64-column bf16 box
 constexpr int kTile = 2 * kHalfTile;  // 64 tokens of K (or V)
 constexpr int kQueryBytes = kSharedRows * kHeadDim * 2;
@@ -65,20 +66,22 @@ __device__ __forceinline__ int row_length(const GroupArgs& a, int row, bool says
 // alone shares with nobody.
 __device__ __forceinline__ int shared_of(int given, int full, int live) { return live > 1 ? max(0, min(given, full)) : 0; }
 __device__ __forceinline__ int tiles_of(int tokens) { return (tokens + kPage - 1) / kPage; }
-__device__ __forceinline__ int line_of(int tiles) { return tiles > 0 ? tiles + kSegment : 0; }
+__device__ __forceinline__ int segment_of(const GroupArgs& a) { return a.q4 ? kSegmentQ4 : kSegmentBf16; }
+__device__ __forceinline__ int line_of(const GroupArgs& a, int tiles) { return tiles > 0 ? tiles + segment_of(a) : 0; }
 
 // One thread: the places in the line of one KV head of request g.
 __device__ __forceinline__ int head_line(const GroupArgs& a, int g) {
+  const int given = __ldg(a.shared_pages + g), base = g * a.beams;
   int full = INT_MAX, live = 0;
-  const int base = g * a.beams;
 #pragma unroll 8
   for (int w = 0; w < a.beams; ++w) {
     const int len = row_length(a, base + w, false);
     if (len > 0) full = min(full, len / a.page_size), ++live;
   }
-  const int sp = shared_of(__ldg(a.shared_pages + g), full, live);
-  int n = a.n_blocks * line_of(tiles_of(sp * a.page_size));
-  for (int w = 0; w < a.beams; ++w) n += line_of(tiles_of(row_length(a, base + w, false) - sp * a.page_size));
+  const int sp = shared_of(given, full, live);
+  int n = a.n_blocks * line_of(a, tiles_of(sp * a.page_size));
+#pragma unroll 8
+  for (int w = 0; w < a.beams; ++w) n += line_of(a, tiles_of(row_length(a, base + w, false) - sp * a.page_size));
   return n;
 }
 
@@ -90,12 +93,12 @@ struct Group {
 };
 // One warp.
 __device__ void load_group(const GroupArgs& a, int g, Group& s, bool says) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, given = __ldg(a.shared_pages + g);
   const int len = lane < a.beams ? row_length(a, g * a.beams + lane, says) : 0;
   const uint32_t live = __ballot_sync(0xffffffffu, len > 0);
   const int full = __reduce_min_sync(0xffffffffu, len > 0 ? len / a.page_size : INT_MAX);
-  const int sp = shared_of(__ldg(a.shared_pages + g), full, __popc(live));
-  int upto = line_of(tiles_of(len > 0 ? len - sp * a.page_size : 0));
+  const int sp = shared_of(given, full, __popc(live));
+  int upto = line_of(a, tiles_of(len > 0 ? len - sp * a.page_size : 0));
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     const int other = __shfl_up_sync(0xffffffffu, upto, d);
@@ -108,7 +111,7 @@ __device__ void load_group(const GroupArgs& a, int g, Group& s, bool says) {
     s.sp = sp;
     s.first = live ? __ffs(live) - 1 : 0;
     s.shared_tiles = tiles_of(sp * a.page_size);
-    s.line = upto + a.n_blocks * line_of(s.shared_tiles);
+    s.line = upto + a.n_blocks * line_of(a, s.shared_tiles);
   }
 }
 static_assert(LOCKSGEN_MAX_BEAMS == 32, "a lane per row");
@@ -144,12 +147,14 @@ struct Piece {
   const int32_t* table;
 };
 
+constexpr int kFewGroups = 2 * kWarps;
 struct Shared {
   uint64_t full[8], empty[8];
   int left[8][4];  // per stage (and page of it): tokens of the tile to be seen
   float m[kWarps][kSharedRows], l[kWarps][kSharedRows];
   Group grp;
-  uint32_t offset, scan[kWarps];
+  Group few[kWarps];
+  uint32_t offset, scan[kWarps], lines[kFewGroups];
   int group, abort;
 };
 
@@ -178,9 +183,14 @@ __device__ __forceinline__ uint32_t pair_mask(int t, int len) {
   return (t < len ? 0x0000ffffu : 0u) | (t + 1 < len ? 0xffff0000u : 0u);
 }
 
-// A warp's softmax state and outputs for its tokens: rows 16 i + g, 16 i + g + 8.
-template <int MT>
+// A warp's softmax state and outputs for its tokens: rows 16 i + g, 16 i + g + 8.  m is the
+// reference of a row's weights 2^(s - m): the largest logit when it was set, less kBelow.
+// It moves only when a weight would exceed 2^kLimit, so the usual tile needs no maximum
+// across lanes, only a vote.  bf16 weights: any range will do.  Half-precision ones: the
+// largest lies between 2^7 and 2^15, so those below 2^-31 of it are what is lost.
+template <int MT, bool Q4>
 struct State {
+  static constexpr float kBelow = Q4 ? 7.f : 0.f, kLimit = Q4 ? 15.f : 8.f;
   float m[MT][2], l[MT][2];
   float o[MT][16][4];
   __device__ __forceinline__ void reset() {
@@ -192,8 +202,7 @@ struct State {
       for (int n = 0; n < 16; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
   }
-  // Logits (unscaled) to weights.  The reference of a row moves only when a logit exceeds it
-  // by more than 2^8, so the usual tile needs no maximum across lanes, only a vote.
+  // Logits (unscaled) to weights.
   __device__ __forceinline__ void weigh(float (&s)[MT][2][4], float scale_log2) {
     bool moved = false;
     float top[MT][2];
@@ -202,7 +211,7 @@ struct State {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         top[i][k] = fmaxf(fmaxf(s[i][0][2 * k], s[i][0][2 * k + 1]), fmaxf(s[i][1][2 * k], s[i][1][2 * k + 1])) * scale_log2;
-        moved |= top[i][k] > m[i][k] + 8.f;
+        moved |= top[i][k] > m[i][k] + kLimit;
       }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -211,7 +220,7 @@ struct State {
         for (int k = 0; k < 2; ++k) {
           float t = fmaxf(top[i][k], __shfl_xor_sync(0xffffffffu, top[i][k], 1));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-          t = fmaxf(t, m[i][k]);
+          t = fmaxf(t - kBelow, m[i][k]);
           const float al = t == -INFINITY ? 1.f : fast_exp2(m[i][k] - t);
           m[i][k] = t;
           l[i][k] *= al;
@@ -242,7 +251,7 @@ struct State {
 // Tokens 16 warp .. + 15 of a tile of bf16 pages at `base` (keys, then values), of which the
 // first `left` are seen.
 template <int MT, bool WHOLE>
-__device__ __forceinline__ void tile_bf16(State<MT>& st, uint32_t base, uint32_t queries, int left, float scale_log2) {
+__device__ __forceinline__ void tile_bf16(State<MT, false>& st, uint32_t base, uint32_t queries, int left, float scale_log2) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, mi = lane >> 3;
   float s[MT][2][4];
 #pragma unroll
@@ -301,7 +310,7 @@ __device__ __forceinline__ void tile_bf16(State<MT>& st, uint32_t base, uint32_t
 // i dimension 32 j + 4 n + i of column n: output block 4 j + i, whose columns 2c and 2c + 1 are
 // dimensions 32 j + 8 c + i and 32 j + 8 c + 4 + i.
 template <int P, int MT, bool WHOLE>
-__device__ __forceinline__ void tile_q4(State<MT>& st, uint32_t base, uint32_t queries, int left, float scale_log2) {
+__device__ __forceinline__ void tile_q4(State<MT, true>& st, uint32_t base, uint32_t queries, int left, float scale_log2) {
   using At = Q4Tile<P>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   float s[MT][2][4];
@@ -361,22 +370,26 @@ __device__ __forceinline__ void tile_q4(State<MT>& st, uint32_t base, uint32_t q
   }
   const uint32_t vw0[4] = {v0.x, v0.y, v0.z, v0.w}, vw1[4] = {v1.x, v1.y, v1.z, v1.w};
   const uint32_t zw0[4] = {z0.x, z0.y, z0.z, z0.w}, zw1[4] = {z1.x, z1.y, z1.z, z1.w};
+  uint32_t p[MT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    p[i][0] = pack_f16(s[i][0][0], s[i][0][1]);
+    p[i][1] = pack_f16(s[i][0][2], s[i][0][3]);
+    p[i][2] = pack_f16(s[i][1][0], s[i][1][1]);
+    p[i][3] = pack_f16(s[i][1][2], s[i][1][3]);
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t p[MT][4];
-    const float a0 = f16_lo(zw0[j]), a1 = f16_hi(zw0[j]), b0 = f16_lo(zw1[j]), b1 = f16_hi(zw1[j]);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      p[i][0] = pack_bf16(s[i][0][0] * a0, s[i][0][1] * a1);
-      p[i][1] = pack_bf16(s[i][0][2] * a0, s[i][0][3] * a1);
-      p[i][2] = pack_bf16(s[i][1][0] * b0, s[i][1][1] * b1);
-      p[i][3] = pack_bf16(s[i][1][2] * b0, s[i][1][3] * b1);
-    }
+    uint32_t f[4], h[4];
+    q4_codes01(vw0[j], f[0], f[1]);
+    q4_codes01(vw0[j] >> 8, f[2], f[3]);
+    q4_codes01(vw1[j], h[0], h[1]);
+    q4_codes01(vw1[j] >> 8, h[2], h[3]);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t f0 = u4pair_bf16(vw0[j], 4 * k), f1 = u4pair_bf16(vw1[j], 4 * k);
+      const uint32_t f0 = mul_f16x2(f[k], zw0[j]), f1 = mul_f16x2(h[k], zw1[j]);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) mma_16816(st.o[i][4 * j + k], p[i][0], p[i][1], p[i][2], p[i][3], f0, f1);
+      for (int i = 0; i < MT; ++i) mma_16816_f16(st.o[i][4 * j + k], p[i][0], p[i][1], p[i][2], p[i][3], f0, f1);
     }
   }
 }
@@ -390,28 +403,26 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
   const int nt = p.t1 - p.t0, G = sh.grp.g;
   const uint32_t rbase = smem_u32(ring), qbase = smem_u32(queries);
 
-  // warp 0 asks for the copies; its lanes hold 32 pages' entries, and the next 32
-  int cur = 0, nxt = 0;
-  auto entry = [&](int k) {  // of page k of the piece
-    if (k >= p.pages) return 0;
-    const int lp = p.page0 + k;
-    int phys = __ldg(p.table + lp);
-    if (phys < 0 || phys >= a.pages_total) {
-      set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
-      phys = -1;
+  // The warps take turns at asking for the copies, tile t warp t % kWarps; their lanes hold
+  // 32 pages' entries, and the next 32.
+  int cur = 0, nxt = 0, batch = -2, asked = -1;
+  auto entry = [&](int k) { return k < p.pages ? __ldg(p.table + p.page0 + k) : 0; };  // of page k of the piece
+  auto issue = [&](int t) {  // whole warps: tile t of the piece
+    const int k0 = t * kPPT, need = k0 / kBatch;
+    if (need != batch) {
+      cur = need == batch + 1 ? nxt : entry(need * kBatch + lane);
+      nxt = entry((need + 1) * kBatch + lane);
+      batch = need;
     }
-    return phys;
-  };
-  auto issue = [&](int t) {  // warp 0: tile t of the piece
-    const int k0 = t * kPPT;
-    if (k0 % kBatch == 0) {
-      cur = k0 == 0 ? entry(lane) : nxt;
-      nxt = entry(k0 + kBatch + lane);
-    }
+    asked = t;
     const int stage = (seq + t) % S;
     const int np = min(kPPT, p.pages - k0);
     uint8_t* dst = ring + stage * kStageBytes<Q4>;
-    const int mine = __shfl_sync(0xffffffffu, cur, (k0 + lane % kPPT) % kBatch);  // lane w: page w of the tile
+    int mine = __shfl_sync(0xffffffffu, cur, (k0 + lane % kPPT) % kBatch);  // lane w: page w of the tile
+    if (mine < 0 || mine >= a.pages_total) {
+      if (lane < np) set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
+      mine = -1;
+    }
     if (lane < kPPT) sh.left[stage][lane] = lane < np && mine >= 0 ? min(P, p.limit - (p.page0 + k0 + lane) * P) : 0;
     __syncwarp();  // before the arrival, which releases it
     if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], (uint32_t)np * (Q4 ? LOCKS_KV_Q4_BLOCK_BYTES(P) : 2 * P * kHeadDim * 2));
@@ -434,9 +445,7 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
       }
     }
   };
-  int issued = 0;
-  if (warp == 0)
-    for (; issued < min(S, nt); ++issued) issue(issued);
+  for (int t = warp; t < min(S, nt); t += kWarps) issue(t);
   // the queries; rows past the last are zero
   for (int e = tid; e < MT * 16 * 16; e += kThreads) {
     const int r = e / 16, chunk = e % 16;
@@ -458,15 +467,16 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
   }
   __syncthreads();
 
-  State<MT> st;
+  State<MT, Q4> st;
   st.reset();
   bool ok = true;
   for (int t = 0; t < nt; ++t) {
-    if (warp == 0 && t > 0 && issued < nt) {
-      // the stage of the tile before this one, when all warps are done with it
+    const int ahead = t - 1 + S;
+    if (t > 0 && ahead < nt && ahead % kWarps == warp) {
+      // into the stage of the tile before this one, when all warps are done with it
       ok = mbar_wait(&sh.empty[(seq + t - 1) % S], ((seq + t - 1) / S) & 1);
       if (!ok) break;
-      issue(issued++);
+      issue(ahead);
     }
     const int stage = (seq + t) % S;
     ok = mbar_wait(&sh.full[stage], ((seq + t) / S) & 1);
@@ -484,13 +494,12 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
     if (lane == 0) mbar_arrive(&sh.empty[stage]);
   }
   if (!ok) {
-    // the copies asked for get a bounded time to land
     if (lane == 0) {
       atomicExch(&sh.abort, 1);
       set_error(a.err, kDevErrTimeout);
     }
-    if (warp == 0 && lane == 0)
-      for (int t = max(0, issued - S); t < issued; ++t) (void)mbar_wait(&sh.full[(seq + t) % S], ((seq + t) / S) & 1);
+    // the copies that this warp has asked for get a bounded time to land
+    for (int t = asked; t >= 0 && t > asked - S; t -= kWarps) (void)mbar_wait(&sh.full[(seq + t) % S], ((seq + t) / S) & 1);
   }
   seq += nt;
   // ---- the warps' states, merged ----
@@ -580,6 +589,8 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
     sh.abort = 0;
   }
   pdl_wait();
+  // the join's CTAs start, and read the lengths, as this kernel's first ones finish
+  pdl_launch_dependents();
 
   uint32_t lo, hi;
   if (groups == 1) {
@@ -590,13 +601,25 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
     lo = parts.begin(cta);
     hi = parts.begin(cta + 1);
   } else {
-    // the whole line; with no more requests than threads, each thread's own for good
-    uint32_t own = tid < groups ? (uint32_t)head_line(a, tid) * a.num_kv_heads : 0, mine = own;
-    for (int g = tid + kThreads; g < groups; g += kThreads) mine += (uint32_t)head_line(a, g) * a.num_kv_heads;
-    const uint32_t sum = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0) sh.scan[warp] = sum;
-    __syncthreads();
-    const uint32_t total = sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3];
+    // the whole line; few requests: a warp each, else a thread each
+    uint32_t total = 0;
+    if (groups <= kFewGroups) {
+      for (int g = warp; g < groups; g += kWarps) {
+        load_group(a, g, sh.few[warp], false);
+        __syncwarp();
+        if (lane == 0) sh.lines[g] = (uint32_t)sh.few[warp].line * a.num_kv_heads;
+        __syncwarp();
+      }
+      __syncthreads();
+      for (int g = 0; g < groups; ++g) total += sh.lines[g];
+    } else {
+      uint32_t mine = 0;
+      for (int g = tid; g < groups; g += kThreads) mine += (uint32_t)head_line(a, g) * a.num_kv_heads;
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, mine);
+      if (lane == 0) sh.scan[warp] = sum;
+      __syncthreads();
+      total = sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3];
+    }
     const Parts parts(total, a.n_ctas);
     lo = parts.begin(cta);
     hi = parts.begin(cta + 1);
@@ -604,24 +627,26 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
     uint32_t before = 0;
     for (int g0 = 0; g0 < groups; g0 += kThreads) {
       const int g = g0 + tid;
-      if (g0 > 0) own = g < groups ? (uint32_t)head_line(a, g) * a.num_kv_heads : 0;
+      const uint32_t own = g >= groups ? 0 : groups <= kFewGroups ? sh.lines[g] : (uint32_t)head_line(a, g) * a.num_kv_heads;
       uint32_t upto = own;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
         const uint32_t other = __shfl_up_sync(0xffffffffu, upto, d);
         if (lane >= d) upto += other;
       }
-      __syncthreads();
-      if (lane == 31) sh.scan[warp] = upto;
-      __syncthreads();
-      for (int w = 0; w < kWarps; ++w) upto += w < warp ? sh.scan[w] : 0;
+      if (groups > 32) {
+        __syncthreads();
+        if (lane == 31) sh.scan[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) upto += w < warp ? sh.scan[w] : 0;
+      }
       const uint32_t first = before + upto - own;
       if (lo >= first && lo < first + own) {
         sh.group = g;
         sh.offset = first;
       }
       if (cta == 0 && g < groups) a.offsets[g] = first;
-      before += sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3];
+      if (groups > 32) before += sh.scan[0] + sh.scan[1] + sh.scan[2] + sh.scan[3];
       if (cta != 0 && before > lo) break;
     }
     if (cta == 0 && tid == 0) a.offsets[groups] = total;
@@ -635,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
     __syncthreads();
   };
   if (groups > 1) load();
+  constexpr int kSegment = Q4 ? kSegmentQ4 : kSegmentBf16;
   const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;  // records of shared parts
   while (pos < hi) {
     while (pos >= offset + (uint32_t)sh.grp.line * a.num_kv_heads) {
@@ -648,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
     const uint32_t in = pos - offset;
     p.h = (int)(in / (uint32_t)s.line);
     int x = (int)(in - (uint32_t)p.h * s.line);
-    const int shared_line = line_of(s.shared_tiles), shared_all = a.n_blocks * shared_line;
+    const int shared_line = line_of(a, s.shared_tiles), shared_all = a.n_blocks * shared_line;
     uint32_t start = offset + (uint32_t)p.h * s.line;
     int tiles, end_page;
     p.shared = x < shared_all;
@@ -688,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
     }
     pos = start + kSegment + tiles;
   }
-  pdl_launch_dependents();
 }
 
 // Joins the pieces of one (row, query head).  Grid (batch * Hkv, group).
@@ -719,18 +744,19 @@ __global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArg
   }
   // the CTAs that have pieces of the two segments
   const int i = w * a.group + e, block = i / kSharedRows;
-  const int shared_line = line_of(s.shared_tiles), own_tiles = tiles_of(len - s.sp * a.page_size);
+  const int shared_line = line_of(a, s.shared_tiles), own_tiles = tiles_of(len - s.sp * a.page_size);
   const uint32_t head = (groups == 1 ? 0u : a.offsets[g]) + (uint32_t)h * s.line;
   const size_t problem = (size_t)g * a.num_kv_heads + h;
   const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;
+  const uint32_t extra = segment_of(a);
   uint32_t c0[2] = {0, 0};
   int n[2] = {0, 0};
   auto segment = [&](int k, uint32_t start, int tiles) {
     if (tiles == 0) return;
     c0[k] = parts.owner(start);
-    n[k] = (int)(parts.owner(start + kSegment + tiles - 1) - c0[k]) + 1;
+    n[k] = (int)(parts.owner(start + extra + tiles - 1) - c0[k]) + 1;
     // the first of them may end before the first tile
-    while (parts.begin(c0[k] + 1) <= start + kSegment) ++c0[k], --n[k];
+    while (parts.begin(c0[k] + 1) <= start + extra) ++c0[k], --n[k];
   };
   segment(0, head + (uint32_t)block * shared_line, s.shared_tiles);
   segment(1, head + (uint32_t)a.n_blocks * shared_line + (w ? s.upto[w - 1] : 0), own_tiles);

@@ -3,9 +3,12 @@
 Tolerances, half a step per rounding.  Logits: 128 exact products added in float32, 2^-24 of
 sum |q||k| each (4-bit pages: 32 at a time, then four scaled sums: no more), so a weight is off by
 e = 2^-17 sum |q||k| scale + 2^-21 (the exponential and the exponent's rounding, of at most 2^6 in
-base 2 for a weight that counts); softmax weights (4-bit pages: times their scale) are rounded to
-bf16, 2^-8; the sums over tokens and the joins are float32 (2^-12 for all, up to 2^12 additions in
-turn); the output is rounded to bf16, 2^-8 of itself.  lse: the sum's share of the same."""
+base 2 for a weight that counts).  bf16 pages: the softmax weights are rounded to bf16, 2^-8.  4-bit
+pages: weights and values s * code are rounded to half precision, 2^-11 each; a weight below
+2^-14 is off by half of half precision's smallest step, 2^-25, where the row's largest is at
+least 2^7, so by 2^-32 of that, which is no more than 1: 2^-32 sum |v| over all tokens.  The sums over
+tokens and the joins are float32 (2^-12 for all, up to 2^12 additions in turn); the output is rounded
+to bf16, 2^-8 of itself.  lse: the sum's share of the same."""
 
 import math
 
@@ -40,7 +43,10 @@ def check(case, q, out, lse, scale=None):
             o, l, mean, _, mag = attend64(q[b, s], k[h], v[h], scale=scale)
             e = 2.0 ** -17 * mag + 2.0 ** -21
             assert ((lse[b, s].double() - l).abs() <= e + 2.0 ** -12 + 2.0 ** -24 * l.abs()).all(), (b, h)
-            tol = (2.0 ** -8 + 2.0 ** -12 + 2 * e[:, None]) * mean + 2.0 ** -8 * o.abs()
+            weights = 2.0 ** -8 if case.fmt == "bf16" else 2.0 ** -10
+            tol = (weights + 2.0 ** -12 + 2 * e[:, None]) * mean + 2.0 ** -8 * o.abs()
+            if case.fmt == "q4":
+                tol = tol + 2.0 ** -32 * v[h].abs().sum(dim=0)
             bad = (out[b, s].double() - o).abs() > tol
             assert not bad.any(), (b, h, (out[b, s].double() - o).abs().max())
 
