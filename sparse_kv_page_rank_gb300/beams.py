@@ -127,16 +127,23 @@ class LocksBeams:
             if self.end_token < 0:
                 raise ValueError("ended without an end_token")
         shape = (n, keep)
-        outs = []
-        for x, t, what in ((out_scores, torch.float32, "out_scores"), (out_parents, torch.int32, "out_parents"),
-                           (out_tokens, torch.int32, "out_tokens"), (out_ended, torch.int32, "out_ended")):
-            if x is not None:
-                self._here(x, t, shape, what)
-            elif what != "out_ended" or self.end_token >= 0:
-                x = self._new(shape, t, stream)
-            outs.append(x)
+        if out_scores is None:
+            out_scores = self._new(shape, torch.float32, stream)
+        else:
+            self._here(out_scores, torch.float32, shape, "out_scores")
+        ints = [out_parents, out_tokens, out_ended]
+        if all(x is None for x in ints):  # one allocation
+            ints = list(self._new((3 if self.end_token >= 0 else 2, n, keep), torch.int32, stream).unbind())
+            ints += [None] * (3 - len(ints))
+        else:
+            for i, what in enumerate(("out_parents", "out_tokens", "out_ended")):
+                if ints[i] is not None:
+                    self._here(ints[i], torch.int32, shape, what)
+                elif i < 2 or self.end_token >= 0:
+                    ints[i] = self._new(shape, torch.int32, stream)
+        outs = (out_scores, *ints)
         if n == 0:
-            return tuple(outs)
+            return outs
         choice = L.locksgen_choice_t(logits.data_ptr(), scores.data_ptr(), L._ptr(ended), outs[0].data_ptr(),
                                      outs[1].data_ptr(), outs[2].data_ptr(), L._ptr(outs[3]),
                                      row if n * W > 1 else vocab, n, W, vocab, keep, dtype, self.end_token)
@@ -145,7 +152,7 @@ class LocksBeams:
         if ws is None:
             ws = self._select_ws[key] = self._workspace(L.locksgen_select_workspace_size(choice))
         L.locksgen_select(choice, ws, ws.numel(), handle)
-        return tuple(outs)
+        return outs
 
     def reorder(self, parents: torch.Tensor, stream=None):
         """Every row becomes a copy of its parent (int32 [requests][width], as ``select`` gives them; -1:

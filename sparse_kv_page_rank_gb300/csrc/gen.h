@@ -52,7 +52,7 @@ struct ReorderArgs {
 };
 bool reorder_fits(const ReorderArgs& a, int layers);  // the launch of so many layers
 cudaError_t launch_reorder_plan(const ReorderArgs& a, cudaStream_t s);
-cudaError_t launch_reorder_move(const ReorderArgs& a, bool tables, cudaStream_t s);
+cudaError_t launch_reorder_move(const ReorderArgs& a, bool tables, int sms, cudaStream_t s);
 
 // Attention of rows that share pages (gen_attend.cu).
 constexpr int kSharedRows = 32;  // (row, head) pairs that a pass over the shared pages serves

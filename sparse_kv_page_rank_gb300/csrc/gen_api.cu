@@ -181,7 +181,7 @@ locks_status_t locksgen_reorder(const locks_cache_t* caches, int32_t num_caches,
       a.k_pool[i] = const_cast<void*>(caches[first + i].k_pool);
       a.v_pool[i] = const_cast<void*>(caches[first + i].v_pool);
     }
-    if (launch_reorder_move(a, first == 0, s) != cudaSuccess) return LOCKS_ERR_CUDA;
+    if (launch_reorder_move(a, first == 0, device_sm_count(), s) != cudaSuccess) return LOCKS_ERR_CUDA;
   }
   return LOCKS_OK;
 }

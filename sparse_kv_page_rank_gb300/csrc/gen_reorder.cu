@@ -12,6 +12,8 @@
 // copies the open pages of all layers.
 //
 // What bounds it: the copied pages' bytes, for few the latency of the two launches.
+#include <algorithm>
+
 #include "common.cuh"
 #include "gen.h"
 
@@ -21,7 +23,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kColumnThreads = 64;            // columns of a CTA that permutes tables
-constexpr int kPieceUnits = 4 * kThreads;     // 16-byte units of a CTA that copies
+constexpr int kFlight = 4;                    // 16-byte units that a thread has in flight
+constexpr int kPieceUnits = kFlight * kThreads;
+constexpr int kCopyCtas = 8;                  // per SM
 
 // The n-th set bit (from 0) of m.
 __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
@@ -97,7 +101,8 @@ __global__ void plan_kernel(const ReorderArgs a) {
 }
 
 // The first n_tables CTAs permute tables, `chunks` of columns per request; the others copy:
-// piece by piece of a row's page, row by row, layer by layer.
+// every one finds the rows that have a page to copy, 256 rows at a time, and takes its share
+// of their pages' pieces in all layers.
 __global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ ReorderArgs a, int chunks, int n_tables,
                                                         int pieces) {
   const int tid = threadIdx.x, W = a.beams;
@@ -125,44 +130,64 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ 
       }
     return;
   }
-  const int i = blockIdx.x - n_tables, piece = i % pieces, row = i / pieces % a.batch, layer = i / pieces / a.batch;
-  const ReorderRow r = a.rows[row];
-  if (r.tokens == 0) return;
+  __shared__ ReorderRow todo[kThreads];
+  __shared__ int found[kThreads / 32];
+  const int lane = tid & 31, warp = tid >> 5, n_ctas = gridDim.x - n_tables;
   const int hkv = a.num_kv_heads, P = a.page_size;
-  const int groups = r.tokens / 16;
   const size_t page_bytes = a.q4 ? (size_t)hkv * LOCKS_KV_Q4_BLOCK_BYTES(P) : (size_t)hkv * P * kHeadDim * 2;
-  const int head_units = groups * (a.q4 ? 144 : 256);  // of 16 bytes, per head (and pool)
-  const int units = head_units * hkv * (a.q4 ? 1 : 2);
-  const uint8_t* pools[2] = {static_cast<const uint8_t*>(a.k_pool[layer]), static_cast<const uint8_t*>(a.v_pool[layer])};
-  uint4 v[4];
-  size_t at[4];
-  uint8_t* out[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int u = piece * kPieceUnits + k * kThreads + tid;
-    out[k] = nullptr;
-    if (u >= units) continue;
-    int h = u / head_units, x = u % head_units;
-    const uint8_t* pool = pools[0];
-    if (a.q4) {
-      // four parts of a block, each with those of the first 16 tokens first
-      const int n = groups;
-      int off;
-      if (x < 64 * n) off = 16 * x;
-      else if (x < 72 * n) off = 64 * P + 16 * (x - 64 * n);
-      else if (x < 136 * n) off = 72 * P + 16 * (x - 72 * n);
-      else off = 136 * P + 16 * (x - 136 * n);
-      at[k] = (size_t)h * LOCKS_KV_Q4_BLOCK_BYTES(P) + off;
-    } else {
-      if (h >= hkv) h -= hkv, pool = pools[1];
-      at[k] = (size_t)h * P * kHeadDim * 2 + 16 * (size_t)x;
+  for (int row0 = 0; row0 < a.batch; row0 += kThreads) {
+    ReorderRow mine = {};
+    if (row0 + tid < a.batch) mine = a.rows[row0 + tid];
+    const uint32_t copies = __ballot_sync(0xffffffffu, mine.tokens > 0);
+    __syncthreads();  // the last rows are done with
+    if (lane == 0) found[warp] = __popc(copies);
+    __syncthreads();
+    int at = __popc(copies & ((1u << lane) - 1u)), n = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      at += w < warp ? found[w] : 0;
+      n += found[w];
     }
-    v[k] = *reinterpret_cast<const uint4*>(pool + r.src * page_bytes + at[k]);
-    out[k] = const_cast<uint8_t*>(pool) + r.dst * page_bytes + at[k];
-  }
+    if (mine.tokens > 0) todo[at] = mine;
+    __syncthreads();
+    // piece by piece of a page, page by page, layer by layer
+    const int items = n * pieces * a.n_layers;
+    for (int i = blockIdx.x - n_tables; i < items; i += n_ctas) {
+      const int piece = i % pieces, layer = i / pieces / n;
+      const ReorderRow r = todo[i / pieces % n];
+      const int groups = r.tokens / 16;
+      const int head_units = groups * (a.q4 ? 144 : 256);  // of 16 bytes, per head (and pool)
+      const int units = head_units * hkv * (a.q4 ? 1 : 2);
+      if (piece * kPieceUnits >= units) continue;
+      uint4 v[kFlight];
+      uint8_t* out[kFlight];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (out[k]) *reinterpret_cast<uint4*>(out[k]) = v[k];
+      for (int k = 0; k < kFlight; ++k) {
+        const int u = piece * kPieceUnits + k * kThreads + tid;
+        out[k] = nullptr;
+        if (u >= units) continue;
+        int h = u / head_units;
+        const int x = u - h * head_units;
+        uint8_t* pool = static_cast<uint8_t*>(a.k_pool[layer]);
+        size_t off;
+        if (a.q4) {
+          // four parts of a block, each with those of the first 16 tokens first
+          off = (size_t)h * LOCKS_KV_Q4_BLOCK_BYTES(P);
+          if (x < 64 * groups) off += 16 * x;
+          else if (x < 72 * groups) off += 64 * P + 16 * (x - 64 * groups);
+          else if (x < 136 * groups) off += 72 * P + 16 * (x - 72 * groups);
+          else off += 136 * P + 16 * (x - 136 * groups);
+        } else {
+          if (h >= hkv) h -= hkv, pool = static_cast<uint8_t*>(a.v_pool[layer]);
+          off = (size_t)h * P * kHeadDim * 2 + 16 * (size_t)x;
+        }
+        v[k] = *reinterpret_cast<const uint4*>(pool + r.src * page_bytes + off);
+        out[k] = pool + r.dst * page_bytes + off;
+      }
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k)
+        if (out[k]) *reinterpret_cast<uint4*>(out[k]) = v[k];
+    }
+  }
 }
 
 cudaLaunchConfig_t config(unsigned grid, unsigned block, cudaLaunchAttribute* attr, cudaStream_t s) {
@@ -195,11 +220,15 @@ bool reorder_fits(const ReorderArgs& a, int layers) {
   return (long long)table_chunks(a) * (a.batch / a.beams) + (long long)page_pieces(a) * a.batch * layers <= 0x7fffffffLL;
 }
 
-cudaError_t launch_reorder_move(const ReorderArgs& a, bool tables, cudaStream_t s) {
+cudaError_t launch_reorder_move(const ReorderArgs& a, bool tables, int sms, cudaStream_t s) {
   const int chunks = table_chunks(a), pieces = page_pieces(a);
   const int n_tables = tables ? chunks * (a.batch / a.beams) : 0;
+  // at most all rows of a request but one are copies
+  const long long items = (long long)pieces * (a.batch / a.beams) * (a.beams - 1) * a.n_layers;
+  const int copies = (int)std::min<long long>(items, (long long)kCopyCtas * sms);
+  if (n_tables + copies == 0) return cudaSuccess;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = config((unsigned)(n_tables + pieces * a.batch * a.n_layers), kThreads, attr, s);
+  const cudaLaunchConfig_t cfg = config((unsigned)(n_tables + copies), kThreads, attr, s);
   return cudaLaunchKernelEx(&cfg, move_kernel, a, chunks, n_tables, pieces);
 }
 
