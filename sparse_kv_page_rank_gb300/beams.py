@@ -26,6 +26,9 @@ import torch
 from . import locks as L
 
 
+_LOGITS = {torch.bfloat16: L.LOCKS_DTYPE_BF16, torch.float32: L.LOCKS_DTYPE_F32}
+
+
 class LocksBeams:
     """Beam search with ``width`` beams per request.
 
@@ -51,8 +54,9 @@ class LocksBeams:
                 raise ValueError("beams need a CUDA device")
             self._index = torch.cuda.current_device() if device.index is None else device.index
             self.device = torch.device("cuda", self._index)
-        self._select_ws = {}  # by sizes; kept, since a captured graph may hold their addresses
-        self._held = []
+        self._select_ws = None
+        self._select_need = {}  # bytes by sizes
+        self._held = []         # all workspaces: a captured graph may still use an outgrown one
         if self.runtimes:
             rt = self.runtimes[0]
             if rt.batch % width:
@@ -69,9 +73,10 @@ class LocksBeams:
             self._attend_ws = self._workspace(max(L.locksgen_attend_workspace_size(x.cache, x.params, width)
                                                   for x in self.runtimes))
 
-    def _workspace(self, need: int) -> torch.Tensor:
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("a workspace is missing: run a call of these sizes before the capture")
+    def _workspace(self, need: int, stream=None) -> torch.Tensor:
+        if torch.cuda.is_current_stream_capturing() or (stream is not None and self._on_stream(
+                stream, torch.cuda.is_current_stream_capturing)):
+            raise RuntimeError("a larger workspace is needed: run a call of these sizes before the capture")
         ws = torch.zeros(need + 256, dtype=torch.uint8, device=self.device)
         off = (-ws.data_ptr()) % 256
         torch.cuda.synchronize(self.device)  # before a call on any stream
@@ -86,9 +91,11 @@ class LocksBeams:
     def _new(self, shape, dtype, stream):
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        s = torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
-        with torch.cuda.stream(s):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+        return self._on_stream(stream, lambda: torch.empty(shape, dtype=dtype, device=self.device))
+
+    def _on_stream(self, stream, f):
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream):
+            return f()
 
     def _here(self, x, dtype, shape, what):
         if x.dtype is not dtype or x.shape != shape or x.get_device() != self._index or not x.is_contiguous():
@@ -113,9 +120,8 @@ class LocksBeams:
             row = logits.stride(0) if W == 1 else logits.stride(1)
         else:
             ok = logits.dim() == 2 and logits.shape[0] % W == 0
-            n, vocab = (logits.shape[0] // W, logits.shape[1]) if ok else (0, 0)
-            row = logits.stride(0)
-        dtype = {torch.bfloat16: L.LOCKS_DTYPE_BF16, torch.float32: L.LOCKS_DTYPE_F32}.get(logits.dtype)
+            n, vocab, row = (logits.shape[0] // W, logits.shape[1], logits.stride(0)) if ok else (0, 0, 0)
+        dtype = _LOGITS.get(logits.dtype)
         if not ok or dtype is None or (vocab > 1 and logits.stride(-1) != 1) or logits.get_device() != self._index:
             raise ValueError(f"logits must be bf16 or float32 [requests * {W}][vocab] on the device, a row's elements contiguous")
         if self.runtimes and n != self.requests:
@@ -131,26 +137,31 @@ class LocksBeams:
             out_scores = self._new(shape, torch.float32, stream)
         else:
             self._here(out_scores, torch.float32, shape, "out_scores")
-        ints = [out_parents, out_tokens, out_ended]
-        if all(x is None for x in ints):  # one allocation
-            ints = list(self._new((3 if self.end_token >= 0 else 2, n, keep), torch.int32, stream).unbind())
-            ints += [None] * (3 - len(ints))
+        if out_parents is None:
+            out_parents = self._new(shape, torch.int32, stream)
         else:
-            for i, what in enumerate(("out_parents", "out_tokens", "out_ended")):
-                if ints[i] is not None:
-                    self._here(ints[i], torch.int32, shape, what)
-                elif i < 2 or self.end_token >= 0:
-                    ints[i] = self._new(shape, torch.int32, stream)
-        outs = (out_scores, *ints)
+            self._here(out_parents, torch.int32, shape, "out_parents")
+        if out_tokens is None:
+            out_tokens = self._new(shape, torch.int32, stream)
+        else:
+            self._here(out_tokens, torch.int32, shape, "out_tokens")
+        if out_ended is not None:
+            self._here(out_ended, torch.int32, shape, "out_ended")
+        elif self.end_token >= 0:
+            out_ended = self._new(shape, torch.int32, stream)
+        outs = out_scores, out_parents, out_tokens, out_ended
         if n == 0:
             return outs
-        choice = L.locksgen_choice_t(logits.data_ptr(), scores.data_ptr(), L._ptr(ended), outs[0].data_ptr(),
-                                     outs[1].data_ptr(), outs[2].data_ptr(), L._ptr(outs[3]),
+        choice = L.locksgen_choice_t(logits.data_ptr(), scores.data_ptr(), L._ptr(ended), out_scores.data_ptr(),
+                                     out_parents.data_ptr(), out_tokens.data_ptr(), L._ptr(out_ended),
                                      row if n * W > 1 else vocab, n, W, vocab, keep, dtype, self.end_token)
         key = (n, vocab, keep, dtype)
-        ws = self._select_ws.get(key)
-        if ws is None:
-            ws = self._select_ws[key] = self._workspace(L.locksgen_select_workspace_size(choice))
+        need = self._select_need.get(key)
+        if need is None:
+            need = self._select_need[key] = L.locksgen_select_workspace_size(choice)
+        ws = self._select_ws
+        if ws is None or ws.numel() < need:  # in large steps, so that the outgrown ones are no more than the last
+            ws = self._select_ws = self._workspace(need if ws is None else max(need, 2 * ws.numel()), stream)
         L.locksgen_select(choice, ws, ws.numel(), handle)
         return outs
 

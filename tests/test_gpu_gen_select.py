@@ -197,8 +197,13 @@ def test_the_same_bits_every_time_and_from_a_graph():
         check(out, logits, scores, ended, 2, 12)
     with pytest.raises(RuntimeError, match="before the capture"):
         with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=stream):
-            beams.select(logits, scores, ended, keep=13)
+            beams.select(logits, scores, ended, keep=64)
     torch.cuda.synchronize()
+    # a larger call beside it leaves the graph its workspace
+    beams.select(logits, scores, ended, keep=64)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(out, logits, scores, ended, 2, 12)
     assert beams.device_error() == 0
 
 
