@@ -23,8 +23,8 @@ struct SelectPlan {
   size_t off_parts = 0, off_lists = 0, total = 0;
 };
 
-// A CTA of the merge keeps a byte per list, at most 16 K of them.
 constexpr int kMaxVocab = 1 << 22;
+constexpr long long kMaxLists = 16384;  // of a request: a CTA of the merge keeps two bytes of each
 
 locks_status_t plan_select(const locksgen_choice_t* c, SelectPlan* pl) {
   if (!c || c->batch <= 0 || c->beams <= 0 || c->vocab <= 0 || c->keep <= 0) return LOCKS_ERR_INVALID_ARG;
@@ -40,7 +40,7 @@ locks_status_t plan_select(const locksgen_choice_t* c, SelectPlan* pl) {
   const long long chunks = count(pl->small ? kSelectSmall : kSelectChunk);
   const long long slots = kSelectCtas * sms;
   double best = 1e30;
-  for (long long n = 1; n <= chunks; ++n) {
+  for (long long n = 1; n <= chunks && n * c->beams <= kMaxLists; ++n) {
     const long long each = (chunks + n - 1) / n, waves = (rows * n + slots - 1) / slots;
     const double time = (double)waves * ((double)each + kPartChunks);
     if (time >= best) continue;

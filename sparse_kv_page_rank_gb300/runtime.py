@@ -236,8 +236,8 @@ class LocksRuntime:
         return q_out
 
     def _append_axes(self, k, v, q, q_out, rope, rotary_dim, interleaved, positions, axes, tokens, handle):
-        if rope is None or axes.pairs != rotary_dim // 2:
-            raise ValueError("axes need a rope, of whose pairs each has its axis")
+        if rope is None or getattr(axes, "pairs", None) != rotary_dim // 2:
+            raise ValueError("axes (locks.make_axes) need a rope, of whose pairs each has its axis")
         if (positions is None or positions.dtype is not torch.int32 or positions.dim() != 2
                 or positions.shape[1] != tokens.total or positions.get_device() != self._index
                 or (tokens.total > 1 and positions.stride(1) != 1)):
