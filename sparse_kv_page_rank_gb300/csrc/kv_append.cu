@@ -221,14 +221,14 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvAppen
   };
   const int i0 = warp % WPT;
   load(i0);  // under way while the token's place is looked up
+  // AXES: each lane the table row of one axis, on its way with the rows
+  const int axis_row = AXES ? __ldg(a.positions + (lane < a.num_axes ? lane : 0) * a.axis_stride + t) : 0;
   const bool says = lane == 0 && warp % WPT == 0;
   const TokenPlace tp = token_place(a.tok, t, says);
   if (!tp.ok) return;
   Turn tr;
   if (a.rotary_dim) {
-    // AXES: each lane the row of one axis
-    const int row = AXES ? __ldg(a.positions + (lane < a.num_axes ? lane : 0) * a.axis_stride + t)
-                         : a.positions ? __ldg(a.positions + t) : tp.pos;
+    const int row = AXES ? axis_row : a.positions ? __ldg(a.positions + t) : tp.pos;
     bool outside = row < 0 || row >= a.rope_rows;
     if (AXES) outside = __any_sync(0xffffffffu, outside);
     if (outside) {
