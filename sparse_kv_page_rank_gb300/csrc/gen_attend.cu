@@ -717,15 +717,14 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
 }
 
 // Joins the pieces of one (row, query head).  Grid (batch * Hkv, group).
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinWarps = 8;   // at most
 constexpr int kJoinFlight = 8;  // pieces that a warp loads at once
 
-__global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const GroupArgs a) {
   __shared__ __align__(16) float so[kJoinWarps][kHeadDim];  // (read and written 16 bytes at a time)
   __shared__ float sl[kJoinWarps];
   __shared__ Group s;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int b = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads, e = blockIdx.y;
   const int g = b / a.beams, w = b % a.beams, groups = a.batch / a.beams;
   // (the lengths were complete before the other kernel let this one begin)
@@ -738,7 +737,7 @@ __global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArg
   const int len = s.len[w];
   const size_t out_row = ((size_t)b * a.num_kv_heads + h) * a.group + e;
   if (len == 0) {
-    if (tid < kHeadDim) a.out[out_row * kHeadDim + tid] = 0;
+    for (int d = tid; d < kHeadDim; d += blockDim.x) a.out[out_row * kHeadDim + d] = 0;
     if (a.lse && tid == 0) a.lse[out_row] = -INFINITY;
     return;
   }
@@ -764,13 +763,13 @@ __global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArg
                           own_base * kSharedRows + (c0[1] + problem * a.beams + w) * a.group + e};
   const int all = n[0] + n[1];
   auto row = [&](int k) { return k < n[0] ? slot[0] + (size_t)k * kSharedRows : slot[1] + (size_t)(k - n[0]) * a.group; };
-  // a warp takes pieces warp, warp + 8, ..., the first of them under way while the reference is found
+  // a warp takes every so manieth piece, the first of them under way while the reference is found
   float4 v[kJoinFlight];
   float2 ml[kJoinFlight];
   auto fetch = [&](int k0) {
 #pragma unroll
     for (int k = 0; k < kJoinFlight; ++k) {
-      const int at = k0 + kJoinWarps * k;
+      const int at = k0 + warps * k;
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       ml[k] = make_float2(-INFINITY, 0.f);
       if (at >= all) continue;
@@ -784,7 +783,7 @@ __global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArg
   M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = warp; k0 < all; k0 += kJoinWarps * kJoinFlight) {
+  for (int k0 = warp; k0 < all; k0 += warps * kJoinFlight) {
     if (k0 != warp) fetch(k0);
 #pragma unroll
     for (int k = 0; k < kJoinFlight; ++k) {
@@ -800,18 +799,16 @@ __global__ void __launch_bounds__(kJoinThreads) group_join_kernel(const GroupArg
   *reinterpret_cast<float4*>(&so[warp][4 * lane]) = O;
   if (lane == 0) sl[warp] = L;
   __syncthreads();
-  if (tid >= kHeadDim) return;
-  float Os = 0.f, Ls = 0.f;
-#pragma unroll
-  for (int k = 0; k < kJoinWarps; ++k) {
-    Os += so[k][tid];
-    Ls += sl[k];
+  float Ls = 0.f;
+  for (int k = 0; k < warps; ++k) Ls += sl[k];
+  for (int d = tid; d < kHeadDim; d += blockDim.x) {
+    float Os = 0.f;
+    for (int k = 0; k < warps; ++k) Os += so[k][d];
+    const float val = Ls == 0.f ? 0.f : Os / Ls;  // a NaN stays one
+    a.out[out_row * kHeadDim + d] = __bfloat16_as_ushort(__float2bfloat16_rn(val));
   }
-  const float val = Ls == 0.f ? 0.f : Os / Ls;  // a NaN stays one
-  a.out[out_row * kHeadDim + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(val));
   if (a.lse && tid == 0) a.lse[out_row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
 }
-static_assert(kJoinThreads >= kHeadDim, "a thread per dimension");
 
 template <int P, bool Q4>
 cudaError_t launch(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
@@ -835,13 +832,22 @@ cudaError_t launch(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap&
 
 int group_attend_ctas_per_sm() { return 2; }
 
+// Warps per result: few results take their pieces side by side, many need few warps each.
+// Measured, the whole call in us (8, 4, 2, 1 warps): 128 results of 2 K 11.9, 12.1, 13.2, 14.5; 512
+// of 32 K 46.0, 43.4, 44.6, 45.8; 1024 of 16 K, 4-bit, 54.6, 48.6, 46.0, 47.0; 2048 of 3 K 62.4,
+// 50.3, 47.2, 44.1.
+static int join_warps(const GroupArgs& a) {
+  const long long results = (long long)a.batch * a.num_kv_heads * a.group, n = a.n_ctas;
+  return results <= n ? kJoinWarps : results <= 2 * n ? 4 : results <= 4 * n ? 2 : 1;
+}
+
 cudaError_t launch_group_attend(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   const cudaError_t e = a.q4 ? (a.page_size == 16 ? launch<16, true>(a, tk, tv, s) : launch<64, true>(a, tk, tv, s))
                              : (a.page_size == 16 ? launch<16, false>(a, tk, tv, s) : launch<64, false>(a, tk, tv, s));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.batch * a.num_kv_heads, a.group, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.blockDim = dim3(32 * join_warps(a), 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
