@@ -723,35 +723,43 @@ constexpr int kJoinFlight = 8;  // pieces that a warp loads at once
 __global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const GroupArgs a) {
   __shared__ __align__(16) float so[kJoinWarps][kHeadDim];  // (read and written 16 bytes at a time)
   __shared__ float sl[kJoinWarps];
-  __shared__ Group s;
+  __shared__ Group few[kJoinWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int b = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads, e = blockIdx.y;
   const int g = b / a.beams, w = b % a.beams, groups = a.batch / a.beams;
-  // (the lengths were complete before the other kernel let this one begin)
-  if (warp == 0) load_group(a, g, s, false);
+  // Where the pieces are follows from the lengths, which were complete before the other
+  // kernel let this one begin; a warp per request finds it while that one still runs, and with more
+  // requests it is read from what that one leaves.
+  const bool known = groups <= warps;
+  if (known ? warp < groups : warp == 0) load_group(a, known ? warp : g, few[warp], false);
   __syncthreads();
-  pdl_wait();
-  pdl_launch_dependents();
-  const uint32_t total = groups == 1 ? (uint32_t)s.line * a.num_kv_heads : a.offsets[groups];
+  const Group& s = few[known ? g : 0];
+  uint32_t total = 0, first = 0;
+  if (known) {
+    for (int i = 0; i < groups; ++i) {
+      const uint32_t line = (uint32_t)few[i].line * a.num_kv_heads;
+      first += i < g ? line : 0;
+      total += line;
+    }
+  } else {
+    pdl_wait();
+    total = a.offsets[groups];
+    first = a.offsets[g];
+  }
   const Parts parts(total, a.n_ctas);
   const int len = s.len[w];
   const size_t out_row = ((size_t)b * a.num_kv_heads + h) * a.group + e;
-  if (len == 0) {
-    for (int d = tid; d < kHeadDim; d += blockDim.x) a.out[out_row * kHeadDim + d] = 0;
-    if (a.lse && tid == 0) a.lse[out_row] = -INFINITY;
-    return;
-  }
   // the CTAs that have pieces of the two segments
   const int i = w * a.group + e, block = i / kSharedRows;
   const int shared_line = line_of(a, s.shared_tiles), own_tiles = tiles_of(len - s.sp * a.page_size);
-  const uint32_t head = (groups == 1 ? 0u : a.offsets[g]) + (uint32_t)h * s.line;
+  const uint32_t head = first + (uint32_t)h * s.line;
   const size_t problem = (size_t)g * a.num_kv_heads + h;
   const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;
   const uint32_t extra = segment_of(a);
   uint32_t c0[2] = {0, 0};
   int n[2] = {0, 0};
   auto segment = [&](int k, uint32_t start, int tiles) {
-    if (tiles == 0) return;
+    if (tiles <= 0) return;
     c0[k] = parts.owner(start);
     n[k] = (int)(parts.owner(start + extra + tiles - 1) - c0[k]) + 1;
     // the first of them may end before the first tile
@@ -762,6 +770,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const Group
   const size_t slot[2] = {(c0[0] + problem * a.n_blocks + block) * kSharedRows + i % kSharedRows,
                           own_base * kSharedRows + (c0[1] + problem * a.beams + w) * a.group + e};
   const int all = n[0] + n[1];
+  if (known) pdl_wait();
+  pdl_launch_dependents();
+  if (len == 0) {
+    for (int d = tid; d < kHeadDim; d += blockDim.x) a.out[out_row * kHeadDim + d] = 0;
+    if (a.lse && tid == 0) a.lse[out_row] = -INFINITY;
+    return;
+  }
   auto row = [&](int k) { return k < n[0] ? slot[0] + (size_t)k * kSharedRows : slot[1] + (size_t)(k - n[0]) * a.group; };
   // a warp takes every so manieth piece, the first of them under way while the reference is found
   float4 v[kJoinFlight];
