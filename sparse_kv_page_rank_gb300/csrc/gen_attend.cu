@@ -728,10 +728,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const Group
   const int b = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads, e = blockIdx.y;
   const int g = b / a.beams, w = b % a.beams, groups = a.batch / a.beams;
   // Where the pieces are follows from the lengths, which were complete before the other
-  // kernel let this one begin; a warp per request finds it while that one still runs, and with more
-  // requests it is read from what that one leaves.
-  const bool known = groups <= warps;
-  if (known ? warp < groups : warp == 0) load_group(a, known ? warp : g, few[warp], false);
+  // kernel let this one begin; few requests' are gone through while that one still runs, and with more
+  // it is read from what that one leaves.
+  const bool known = groups <= min(2 * warps, kJoinWarps);
+  if (known)
+    for (int i = warp; i < groups; i += warps) load_group(a, i, few[i], false);
+  else if (warp == 0) load_group(a, g, few[0], false);
   __syncthreads();
   const Group& s = few[known ? g : 0];
   uint32_t total = 0, first = 0;
