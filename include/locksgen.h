@@ -68,10 +68,10 @@ LOCKS_API locks_status_t locksgen_append_axes(const locks_cache_t* cache, const 
  *                (dtype), rows row_stride elements apart (at least vocab),
  *                aligned to an element
  *   scores       float32 [batch][beams]: the hypotheses' log probabilities;
- *                -infinity for a row without a hypothesis, whose logits are
- *                not read
+ *                -infinity for a row without a hypothesis, whose logits may
+ *                be anything
  *   ended        int32 [batch][beams], or NULL: nonzero for a hypothesis that
- *                has ended, whose logits are not read (needs an end_token)
+ *                has ended, whose logits may be anything (needs an end_token)
  *   end_token    the token that ends a hypothesis, or -1 for none
  *   keep         continuations kept per request, 1..LOCKSGEN_MAX_KEEP
  * and what it gives, all [batch][keep], best first:

@@ -139,16 +139,16 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) part_kernel(const Selec
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int part = blockIdx.x, row = blockIdx.y;
   pdl_wait();
+  const T* base = reinterpret_cast<const T*>(a.logits) + (size_t)row * a.row_stride;
+  const int before = (int)((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
+  const int begin = part * a.chunks * C::kSize - before;
+  C next;
+  next.load(base, begin, a.vocab);  // under way while the row's state is looked up
   if (!is_live(__ldg(a.scores + row), a.ended ? __ldg(a.ended + row) : 0)) {
     pdl_launch_dependents();
     return;
   }
   if (tid == 0) n_list = 0;
-  const T* base = reinterpret_cast<const T*>(a.logits) + (size_t)row * a.row_stride;
-  const int before = (int)((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
-  const int begin = part * a.chunks * C::kSize - before;
-  C next;
-  next.load(base, begin, a.vocab);
   float m = -INFINITY, l = 0.f;  // this thread's maximum and sum
   float t = -INFINITY;           // what exceeds it joins the list
   // the best `keep` of the list's n members, in order; the list's size
@@ -215,21 +215,8 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) part_kernel(const Selec
           if (lane == 0) first_t = below(lo);
         }
       }
-      __syncthreads();
-      t = first_t;
     }
-    if (mine > t) {
-      uint32_t mask = 0;
-#pragma unroll
-      for (int j = 0; j < kMine; ++j)
-        if (x[j] > t) mask |= 1u << j;
-      for (; mask; mask &= mask - 1) {
-        const int i = C::token(here, __ffs(mask) - 1);
-        const int at = atomicAdd(&n_list, 1);
-        if (at < kShort) list[at] = part_key(C::logit(base, i), i);
-      }
-    }
-    {
+    {  // (the first chunk's while one warp looks for T)
       const float was = m;
       m = fmaxf(m, mine);
       const float ref = m == -INFINITY ? 0.f : m;  // (-infinity less itself is no number)
@@ -245,14 +232,25 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) part_kernel(const Selec
       unpack_f32x2(sum, s0, s1);
       l = c == 0 ? s0 + s1 : fmaf(l, exp_of(was - ref), s0 + s1);
     }
-    if (c == 0 && !last) {
-      // Members are at least `keep` now, or else every number is one.  What is equal to T
-      // in later chunks comes after those that reach it: from here on T itself must be exceeded.
+    if (c == 0) {
       __syncthreads();
-      const int n = n_list;
-      __syncthreads();  // before anyone adds to it
-      if (n < a.keep) t = -INFINITY;
-      else if (t > -INFINITY) t = key_logit(above(orderable_key(t)));
+      t = first_t;
+    }
+    if (mine > t) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int j = 0; j < kMine; ++j)
+        if (x[j] > t) mask |= 1u << j;
+      for (; mask; mask &= mask - 1) {
+        const int i = C::token(here, __ffs(mask) - 1);
+        const int at = atomicAdd(&n_list, 1);
+        if (at < kShort) list[at] = part_key(C::logit(base, i), i);
+      }
+    }
+    if (c == 0) {
+      // `keep` members reach T (unless T is -infinity), and what is equal to it in later chunks
+      // comes after them: from here on T itself must be exceeded.
+      if (t > -INFINITY) t = key_logit(above(orderable_key(t)));
     } else if ((c & (c + 1)) == 0 && !last) {
       __syncthreads();
       const int n = n_list;
