@@ -71,17 +71,17 @@ __device__ __forceinline__ int row_length(const GroupArgs& a, int row, bool says
 // Shared pages of a request whose `live` rows have at least `full` whole pages: a row
 // alone shares with nobody.
 __device__ __forceinline__ int shared_of(int given, int full, int live) { return live > 1 ? max(0, min(given, full)) : 0; }
-__device__ __forceinline__ int tiles_of(int tokens) { return (tokens + kPage - 1) / kPage; }
+__device__ __forceinline__ int tiles_of(int tokens) { return tokens > 0 ? (tokens - 1) / kPage + 1 : 0; }
 __device__ __forceinline__ int segment_of(const GroupArgs& a) { return a.q4 ? kSegmentQ4 : kSegmentBf16; }
 __device__ __forceinline__ int line_of(const GroupArgs& a, int tiles) { return tiles > 0 ? tiles + segment_of(a) : 0; }
 
 // One thread: the places in the line of one KV head of request g.
-__device__ __forceinline__ int head_line(const GroupArgs& a, int g) {
+__device__ __forceinline__ int head_line(const GroupArgs& a, int g, bool says) {
   const int given = __ldg(a.shared_pages + g), base = g * a.beams;
   int full = INT_MAX, live = 0;
 #pragma unroll 8
   for (int w = 0; w < a.beams; ++w) {
-    const int len = row_length(a, base + w, false);
+    const int len = row_length(a, base + w, says);
     if (len > 0) full = min(full, len / a.page_size), ++live;
   }
   const int sp = shared_of(given, full, live);
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
     uint32_t total = 0;
     if (groups <= kFewGroups) {
       for (int g = warp; g < groups; g += kWarps) {
-        load_group(a, g, sh.few[warp], false);
+        load_group(a, g, sh.few[warp], cta == 0);
         __syncwarp();
         if (lane == 0) sh.lines[g] = (uint32_t)sh.few[warp].line * a.num_kv_heads;
         __syncwarp();
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
       for (int g = 0; g < groups; ++g) total += sh.lines[g];
     } else {
       uint32_t mine = 0;
-      for (int g = tid; g < groups; g += kThreads) mine += (uint32_t)head_line(a, g) * a.num_kv_heads;
+      for (int g = tid; g < groups; g += kThreads) mine += (uint32_t)head_line(a, g, cta == 0) * a.num_kv_heads;
       const uint32_t sum = __reduce_add_sync(0xffffffffu, mine);
       if (lane == 0) sh.scan[warp] = sum;
       __syncthreads();
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
     uint32_t before = 0;
     for (int g0 = 0; g0 < groups; g0 += kThreads) {
       const int g = g0 + tid;
-      const uint32_t own = g >= groups ? 0 : groups <= kFewGroups ? sh.lines[g] : (uint32_t)head_line(a, g) * a.num_kv_heads;
+      const uint32_t own = g >= groups ? 0 : groups <= kFewGroups ? sh.lines[g] : (uint32_t)head_line(a, g, false) * a.num_kv_heads;
       uint32_t upto = own;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
   int g = sh.group;
   uint32_t offset = sh.offset, pos = lo, seq = 0;
   auto load = [&] {
-    if (warp == 0) load_group(a, g, sh.grp, true);
+    if (warp == 0) load_group(a, g, sh.grp, false);
     __syncthreads();
   };
   if (groups > 1) load();
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
       p.limit = s.len[p.w];
       tiles = tiles_of(p.limit - s.sp * P);
       p.rows = a.group;
-      end_page = (p.limit + P - 1) / P;
+      end_page = (p.limit - 1) / P + 1;
       p.table = a.block_table + (size_t)(g * a.beams + p.w) * a.max_pages;
     }
     p.t0 = max(0, (int)(pos - start) - kSegment);

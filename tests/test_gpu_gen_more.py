@@ -44,6 +44,32 @@ def test_attend_of_many_requests(fmt, requests, W):
     check_attend(case, q, out, lse)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+@pytest.mark.parametrize("W,hq,hkv,P", [(32, 16, 1, 64), (32, 32, 2, 16), (31, 15, 1, 64)])
+def test_attend_of_the_widest_requests(fmt, W, hq, hkv, P):
+    """Up to 512 (row, head) pairs over one KV head's shared pages."""
+    tails = [[(7 * w) % 90 for w in range(W)], [None if w % 3 else w for w in range(W)]]
+    case, _, shared = shared_case([260, 100], tails, hq, hkv, P, fmt, seed=W + P)
+    beams = LocksBeams([case.runtime()], width=W)
+    q = case.query(case.B)
+    out, lse = beams.attend(q, shared)
+    assert beams.device_error() == 0
+    check_attend(case, q, out, lse)
+
+
+@pytest.mark.parametrize("requests", [1, 3, 20, 140])
+def test_a_bad_length_among_idle_rows_is_told(requests):
+    case, W, shared = shared_case([50] + [20] * (requests - 1), [[1, 2]] + [[None, None]] * (requests - 1), 2, 1, 16, "bf16", seed=3)
+    beams = LocksBeams([case.runtime()], width=W)
+    q = case.query(case.B)
+    case.seq[-1 if requests > 1 else 0] = -9
+    if requests == 1:
+        case.lens[0] = 0
+    out, lse = beams.attend(q, shared)
+    assert beams.device_error() == L.LOCKS_DEVERR_LENGTHS
+    check_attend(case, q, out, lse)
+
+
 def test_attend_at_the_largest_scale():
     case, W, shared = shared_case([700], [[33, 40, 1]], 4, 1, 64, "q4", seed=3)
     g = torch.Generator().manual_seed(1)
