@@ -310,6 +310,22 @@ __device__ __forceinline__ void tile_bf16(State<MT, false>& st, uint32_t base, u
   }
 }
 
+// Fields i of both halves of w, each holding code + 8, as a bf16 pair of codes: the field under
+// the exponent of 128 is 128 + u exactly, from which 136 is taken.
+template <int I>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  uint32_t d = field_under<0x000f000fu, 0x43004300u>(w >> (4 * I));
+  asm("sub.rn.bf16x2 %0, %0, %1;\n" : "+r"(d) : "r"(0x43084308u));
+  return d;
+}
+// D = A B: the first of a chain of products.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // The same of 4-bit pages.  A key word holds dimensions 32 j + 8 c .. + 7 of one token, field
 // i the pair 8 c + 2 i, + 1, so fields 0 and 1 are one step of a product, 2 and 3 the next; the
 // queries are read in that order.  A value word holds four dimensions of two tokens, field
@@ -330,20 +346,16 @@ __device__ __forceinline__ void tile_q4(State<MT, true>& st, uint32_t base, uint
     const uint32_t za[2][2] = {{z0.x, z0.y}, {z1.x, z1.y}}, zb[2][2] = {{z0.z, z0.w}, {z1.z, z1.w}};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uint32_t f[2][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[0][k] = u4pair_bf16(kw0[j], 4 * k);
-        f[1][k] = u4pair_bf16(kw1[j], 4 * k);
-      }
+      const uint32_t f[2][4] = {{code_pair<0>(kw0[j]), code_pair<1>(kw0[j]), code_pair<2>(kw0[j]), code_pair<3>(kw0[j])},
+                                {code_pair<0>(kw1[j]), code_pair<1>(kw1[j]), code_pair<2>(kw1[j]), code_pair<3>(kw1[j])}};
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const uint4 qa = lds128(query_addr<true>(queries, 16 * i + g, 4 * j + c));
         const uint4 qb = lds128(query_addr<true>(queries, 16 * i + g + 8, 4 * j + c));
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_16816(acc, qa.x, qb.x, qa.y, qb.y, f[n][0], f[n][1]);
+          float acc[4];
+          mma_first(acc, qa.x, qb.x, qa.y, qb.y, f[n][0], f[n][1]);
           mma_16816(acc, qa.z, qb.z, qa.w, qb.w, f[n][2], f[n][3]);
           const float s0 = j & 1 ? f16_hi(za[n][j >> 1]) : f16_lo(za[n][j >> 1]);
           const float s1 = j & 1 ? f16_hi(zb[n][j >> 1]) : f16_lo(zb[n][j >> 1]);
