@@ -36,9 +36,10 @@ class LocksBeams:
     n_summarized (the same tensors) and have one page format; or none, with a
     ``device``, for ``select`` alone.  ``end_token`` ends a hypothesis (-1: none).
 
-    One workspace serves all calls of a kind: the caller orders calls that are on
-    different streams, and replays of graphs that hold them (or has a LocksBeams
-    for each).
+    One workspace serves all calls of a kind, and so do the outputs that are not given
+    (as those of a ``LocksRuntime``'s decode calls): the next call of the same sizes
+    overwrites them.  The caller orders calls that are on different streams, and
+    replays of graphs that hold them (or has a LocksBeams for each).
     """
 
     def __init__(self, runtimes=None, width: int = 1, *, device=None, end_token: int = -1):
@@ -56,6 +57,7 @@ class LocksBeams:
             self.device = torch.device("cuda", self._index)
         self._select_ws = None
         self._select_need = {}  # bytes by sizes
+        self._outs = {}         # outputs by sizes
         self._held = []         # all workspaces: a captured graph may still use an outgrown one
         if self.runtimes:
             rt = self.runtimes[0]
@@ -88,11 +90,6 @@ class LocksBeams:
             raise ValueError(f"the beams are on {self.device}, which is not the current device")
         return L._stream(stream, self._index)
 
-    def _new(self, shape, dtype, stream):
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        return self._on_stream(stream, lambda: torch.empty(shape, dtype=dtype, device=self.device))
-
     def _on_stream(self, stream, f):
         with torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream):
             return f()
@@ -110,8 +107,8 @@ class LocksBeams:
         hypothesis; ended: int32 [requests][width], nonzero for a hypothesis that has
         ended, which continues as it is with the token ``end_token``.  Returns scores, parents, tokens
         and ended (None without an end_token), [requests][keep], best first; where there is no
-        continuation the score is -inf and parent and token are -1.  The outputs are new tensors
-        unless given; out_scores and out_ended may be scores and ended where keep is width."""
+        continuation the score is -inf and parent and token are -1.  The outputs are the object's
+        own unless given; they may be given back as scores and ended where keep is width."""
         handle = self._launch_on(stream)
         W = self.width
         if logits.dim() == 3:
@@ -127,28 +124,34 @@ class LocksBeams:
         if self.runtimes and n != self.requests:
             raise ValueError(f"logits of {self.requests} requests are needed")
         keep = W if keep is None else int(keep)
+        if not 0 < keep <= L.LOCKSGEN_MAX_KEEP:
+            raise L.LocksError(L.LOCKS_ERR_INVALID_ARG if keep <= 0 else L.LOCKS_ERR_UNSUPPORTED, "locksgen_select")
         self._here(scores, torch.float32, (n, W), "scores")
         if ended is not None:
             self._here(ended, torch.int32, (n, W), "ended")
             if self.end_token < 0:
                 raise ValueError("ended without an end_token")
         shape = (n, keep)
+        own = self._outs.get(shape)
+        if own is None:
+            own = self._outs[shape] = tuple(torch.empty(shape, dtype=t, device=self.device)
+                                            for t in (torch.float32, torch.int32, torch.int32, torch.int32))
         if out_scores is None:
-            out_scores = self._new(shape, torch.float32, stream)
+            out_scores = own[0]
         else:
             self._here(out_scores, torch.float32, shape, "out_scores")
         if out_parents is None:
-            out_parents = self._new(shape, torch.int32, stream)
+            out_parents = own[1]
         else:
             self._here(out_parents, torch.int32, shape, "out_parents")
         if out_tokens is None:
-            out_tokens = self._new(shape, torch.int32, stream)
+            out_tokens = own[2]
         else:
             self._here(out_tokens, torch.int32, shape, "out_tokens")
         if out_ended is not None:
             self._here(out_ended, torch.int32, shape, "out_ended")
         elif self.end_token >= 0:
-            out_ended = self._new(shape, torch.int32, stream)
+            out_ended = own[3]
         outs = out_scores, out_parents, out_tokens, out_ended
         if n == 0:
             return outs
@@ -180,7 +183,7 @@ class LocksBeams:
         """``LocksRuntime.dense_decode`` of layer ``layer`` for rows that share pages: the first
         shared_pages[r] (int32 [requests]) columns of the block table are the same in all rows of
         request r and are read once.  q bf16 [requests * width][Hq][128] -> out bf16 of the same
-        shape, lse float32 [requests * width][Hq] (new tensors by default)."""
+        shape, lse float32 [requests * width][Hq] (the runtime's own by default, as there)."""
         handle = self._launch_on(stream)
         if not self.runtimes:
             raise ValueError("these beams have no caches")
@@ -189,11 +192,11 @@ class LocksBeams:
         self._here(q, torch.bfloat16, shape, "q")
         self._here(shared_pages, torch.int32, (self.requests,), "shared_pages")
         if out is None:
-            out = self._new(shape, torch.bfloat16, stream)
+            out = rt.out
         else:
             self._here(out, torch.bfloat16, shape, "out")
         if lse is None:
-            lse = self._new(shape[:2], torch.float32, stream)
+            lse = rt.lse
         else:
             self._here(lse, torch.float32, shape[:2], "lse")
         L.locksgen_attend(rt.cache, rt.params, self.width, shared_pages, q, out, lse, self._attend_ws,

@@ -25,7 +25,7 @@
 //
 // Measured, 32 query / 8 KV heads (floor by bytes): eight rows that share 32 K tokens of bf16
 // pages and have 300 of their own 33.9 us (21.2; every row by itself 83); 131 K shared 89 us (79.6; 274);
-// four rows of 2 K 11 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 42 us, 16-token
+// four rows of 2 K 11 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 41 us, 16-token
 // ones 45 us (8.1; 72 and 79): 32 rows per key make the instructions the bound there (35% of the issue
 // slots with two warps per scheduler, which is what 255 registers leave).
 #include <algorithm>

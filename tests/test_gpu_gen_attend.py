@@ -78,7 +78,7 @@ def test_cases(fmt, prompts, tails, hq, hkv, P):
     case, W, shared = shared_case(prompts, tails, hq, hkv, P, fmt, seed=hq + P + len(prompts))
     beams = LocksBeams([case.runtime()], width=W)
     q = case.query(case.B)
-    out, lse = beams.attend(q, shared)
+    out, lse = (x.clone() for x in beams.attend(q, shared))
     assert beams.device_error() == 0
     check(case, q, out, lse)
     # any smaller count of shared pages is right too, and a larger one is cut to the shortest row's
@@ -118,7 +118,7 @@ def test_numbers_that_are_not_finite(fmt):
     case, W, shared = shared_case([100, 100], [[30, 40], [30, 40]], 4, 1, 64, fmt, seed=12)
     q = case.query(case.B)
     beams = LocksBeams([case.runtime()], width=W)
-    clean, _ = beams.attend(q, shared)
+    clean = beams.attend(q, shared)[0].clone()
     page, slot = int(case.table[1, 2]), 3  # token 131 of row 1
     if fmt == "bf16":
         case.v[page, 0, slot, 7] = float("nan")
@@ -144,7 +144,7 @@ def test_bad_pages_and_lengths_are_skipped(fmt):
     case, W, shared = shared_case([300, 200], [[10, 10], [5, 6]], 4, 2, 64, fmt, seed=5)
     beams = LocksBeams([case.runtime()], width=W)
     q = case.query(case.B)
-    good, _ = beams.attend(q, shared)
+    good = beams.attend(q, shared)[0].clone()
     case.table[0, 4] = 1 << 24   # a page of row 0's own
     out, _ = beams.attend(q, shared)
     assert beams.device_error() == L.LOCKS_DEVERR_BLOCK_TABLE and torch.equal(out[1:], good[1:])

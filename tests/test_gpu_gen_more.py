@@ -89,7 +89,7 @@ def test_lengths_that_the_table_cannot_hold(fmt):
     case, W, shared = shared_case([300], [[10, 10]], 4, 2, 64, fmt, seed=5)
     beams = LocksBeams([case.runtime()], width=W)
     q = case.query(case.B)
-    good, _ = beams.attend(q, shared)
+    good = beams.attend(q, shared)[0].clone()
     cols = case.table.shape[1]
     case.seq[1] = 1 << 30
     case.table[1].clamp_(min=0)
@@ -170,18 +170,24 @@ def test_two_searches_on_two_streams():
     searches = [LocksBeams([c.runtime()], width=W) for c, W, _ in cases]
     qs = [c.query(c.B) for c, _, _ in cases]
     logits, scores, _ = make(16, 4, 50000, torch.bfloat16, seed=4)
-    want = [s.attend(q, c[2]) for s, q, c in zip(searches, qs, cases)]
+    want = [[x.clone() for x in s.attend(q, c[2])] for s, q, c in zip(searches, qs, cases)]
     pick = [LocksBeams(width=4) for _ in range(2)]
-    best = [p.select(logits, scores) for p in pick]
+    best = [[x.clone() for x in p.select(logits, scores)[:3]] for p in pick]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
     got = []
     for _ in range(20):
         for i, st in enumerate(streams):
-            got.append((i, searches[i].attend(qs[i], cases[i][2], stream=st), pick[i].select(logits, scores, stream=st)))
+            with torch.cuda.stream(st):
+                outs = dict(out=torch.empty_like(qs[i]), lse=torch.empty(4, 16, device="cuda"))
+                some = dict(out_scores=torch.empty(16, 4, device="cuda"),
+                            out_tokens=torch.empty(16, 4, dtype=torch.int32, device="cuda"),
+                            out_parents=torch.empty(16, 4, dtype=torch.int32, device="cuda"))
+            got.append((i, searches[i].attend(qs[i], cases[i][2], stream=st, **outs),
+                        pick[i].select(logits, scores, stream=st, **some)))
     torch.cuda.synchronize()
     for i, a, b in got:
-        assert all(torch.equal(x, y) for x, y in zip(a, want[i])) and all(torch.equal(x, y) for x, y in zip(b[:3], best[i][:3]))
+        assert all(torch.equal(x, y) for x, y in zip(a, want[i])) and all(torch.equal(x, y) for x, y in zip(b[:3], best[i]))
 
 
 def test_tensors_of_another_device_are_refused(monkeypatch):

@@ -147,9 +147,13 @@ def test_ended_hypotheses(dtype):
     check(got, x, scores, ended, end, W)
     assert got[3][1].all() and int(got[3][2, 0]) == 1 and int(got[2][2, 0]) == end
     # in place
-    s2, e2 = scores.clone(), ended.clone()
+    s2, e2, want = scores.clone(), ended.clone(), [x.clone() for x in got]
     again = beams.select(logits, s2, e2, out_scores=s2, out_ended=e2)
-    assert all(torch.equal(a, b) for a, b in zip(again, got)) and again[0] is s2 and again[3] is e2
+    assert all(torch.equal(a, b) for a, b in zip(again, want)) and again[0] is s2 and again[3] is e2
+    # and the object's own outputs handed back
+    second = beams.select(logits, got[0], got[3])
+    assert all(a is b for a, b in zip(second, got))
+    check(second, x, want[0], want[3], end, W)
 
 
 def test_bad_numbers_are_told_and_kept_out():
@@ -183,7 +187,7 @@ def test_the_same_bits_every_time_and_from_a_graph():
     logits, scores, _ = make(7, 6, 33333, torch.bfloat16, seed=5)
     beams = LocksBeams(width=6, end_token=2)
     ended = torch.zeros(7, 6, dtype=torch.int32).cuda()
-    first = beams.select(logits, scores, ended, keep=12)
+    first = [x.clone() for x in beams.select(logits, scores, ended, keep=12)]
     for _ in range(20):
         assert all(torch.equal(a, b) for a, b in zip(first, beams.select(logits, scores, ended, keep=12)))
     graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
