@@ -18,9 +18,10 @@
  * page that the row's next token goes to) a row's pages are its own.  That is
  * how locksgen_reorder leaves them, without a page being allocated or counted:
  * a beam that is continued twice gives its copy the pages of one that is not
- * continued.  So a request begins with its prompt in row 0 and the other rows
- * idle (length 0): they hold the prompt's full pages, by reference or not at
- * all, and pages of their own from the prompt's open page on, and the
+ * continued.  A full page that no live row refers to any more is the caller's to
+ * give out again.  So a request begins with its prompt in row 0 and the other
+ * rows idle (length 0): they hold the prompt's full pages, by reference or not
+ * at all, and pages of their own from the prompt's open page on, and the
  * scores of rows other than 0 are -infinity.
  */
 #ifndef LOCKSGEN_H_

@@ -134,8 +134,11 @@ class LocksBeams:
         shape = (n, keep)
         own = self._outs.get(shape)
         if own is None:
-            own = self._outs[shape] = tuple(torch.empty(shape, dtype=t, device=self.device)
-                                            for t in (torch.float32, torch.int32, torch.int32, torch.int32))
+            def make():
+                return tuple(torch.empty(shape, dtype=t, device=self.device)
+                             for t in (torch.float32, torch.int32, torch.int32, torch.int32))
+            # memory that its first use follows on the same stream
+            own = self._outs[shape] = make() if stream is None else self._on_stream(stream, make)
         if out_scores is None:
             out_scores = own[0]
         else:

@@ -61,7 +61,7 @@ static_assert(kWarps * kSharedRows * kOStride<true> * 4 <= kStages<true> * kStag
 // ---- lengths, and what follows from them ----------------------------------------------
 
 __device__ __forceinline__ int row_length(const GroupArgs& a, int row, bool says) {
-  int len = __ldg(a.seq_lens + row);
+  int len = a.seq_lens[row];  // (plain loads where the kernel before may have written)
   if (len < 0 || len > a.max_pages * a.page_size) {
     if (says) set_error(a.err, LOCKS_DEVERR_LENGTHS);
     len = len < 0 ? 0 : a.max_pages * a.page_size;
@@ -77,7 +77,7 @@ __device__ __forceinline__ int line_of(const GroupArgs& a, int tiles) { return t
 
 // One thread: the places in the line of one KV head of request g.
 __device__ __forceinline__ int head_line(const GroupArgs& a, int g, bool says) {
-  const int given = __ldg(a.shared_pages + g), base = g * a.beams;
+  const int given = a.shared_pages[g], base = g * a.beams;
   int full = INT_MAX, live = 0;
 #pragma unroll 8
   for (int w = 0; w < a.beams; ++w) {
@@ -99,7 +99,7 @@ struct Group {
 };
 // One warp.
 __device__ void load_group(const GroupArgs& a, int g, Group& s, bool says) {
-  const int lane = threadIdx.x & 31, given = __ldg(a.shared_pages + g);
+  const int lane = threadIdx.x & 31, given = a.shared_pages[g];
   const int len = lane < a.beams ? row_length(a, g * a.beams + lane, says) : 0;
   const uint32_t live = __ballot_sync(0xffffffffu, len > 0);
   const int full = __reduce_min_sync(0xffffffffu, len > 0 ? len / a.page_size : INT_MAX);
@@ -193,7 +193,7 @@ __device__ __forceinline__ uint32_t pair_mask(int t, int len) {
 // reference of a row's weights 2^(s - m): the largest logit when it was set, less kBelow.
 // It moves only when a weight would exceed 2^kLimit, so the usual tile needs no maximum
 // across lanes, only a vote.  bf16 weights: any range will do.  Half-precision ones: the
-// largest lies between 2^7 and 2^15, so those below 2^-31 of it are what is lost.
+// largest lies between 2^7 and 2^15, so those below 2^-32 of it are what is lost.
 template <int MT, bool Q4>
 struct State {
   static constexpr float kBelow = Q4 ? 7.f : 0.f, kLimit = Q4 ? 15.f : 8.f;
@@ -424,7 +424,7 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
   // The warps take turns at asking for the copies, tile t warp t % kWarps; their lanes hold
   // 32 pages' entries, and the next 32.
   int cur = 0, nxt = 0, batch = -2, asked = -1;
-  auto entry = [&](int k) { return k < p.pages ? __ldg(p.table + p.page0 + k) : 0; };  // of page k of the piece
+  auto entry = [&](int k) { return k < p.pages ? p.table[p.page0 + k] : 0; };  // of page k of the piece
   auto issue = [&](int t) {  // whole warps: tile t of the piece
     const int k0 = t * kPPT, need = k0 / kBatch;
     if (need != batch) {
@@ -468,7 +468,7 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
   for (int e = tid; e < MT * 16 * 16; e += kThreads) {
     const int r = e / 16, chunk = e % 16;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < p.rows) v = __ldg(reinterpret_cast<const uint4*>(a.q + query_row(a, p, G, r) * kHeadDim) + chunk);
+    if (r < p.rows) v = *(reinterpret_cast<const uint4*>(a.q + query_row(a, p, G, r) * kHeadDim) + chunk);
     const uint32_t at = query_addr<Q4>(qbase, r, chunk);
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
   }
@@ -477,9 +477,9 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
     bool differs = false;
     for (int k = lane; k < p.pages; k += 32) {
       const int32_t* column = a.block_table + (size_t)G * a.beams * a.max_pages + p.page0 + k;
-      const int phys = __ldg(p.table + p.page0 + k);
+      const int phys = p.table[p.page0 + k];
 #pragma unroll 8
-      for (int w = 0; w < a.beams; ++w) differs |= __ldg(column + (size_t)w * a.max_pages) != phys && sh.grp.len[w] > 0;
+      for (int w = 0; w < a.beams; ++w) differs |= column[(size_t)w * a.max_pages] != phys && sh.grp.len[w] > 0;
     }
     if (differs) set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
   }

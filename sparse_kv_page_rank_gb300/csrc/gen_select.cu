@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, kSelectCtas) part_kernel(const Selec
   const int begin = part * a.chunks * C::kSize - before;
   C next;
   next.load(base, begin, a.vocab);  // under way while the row's state is looked up
-  if (!is_live(__ldg(a.scores + row), a.ended ? __ldg(a.ended + row) : 0)) {
+  if (!is_live(a.scores[row], a.ended ? a.ended[row] : 0)) {  // (plain loads: the choice before may have written them)
     pdl_launch_dependents();
     return;
   }

@@ -226,3 +226,20 @@ def test_many_rows_move():
     g = torch.Generator().manual_seed(2)
     rows.run(torch.randint(0, 3, (200, 3), generator=g).tolist())
     assert rows.beams.device_error() == 0
+
+
+def test_own_outputs_on_another_stream():
+    """Outputs that a call on another stream makes are not memory that work on the current one still writes."""
+    logits, scores, _ = make(2, 4, 500, torch.float32, 5)
+    beams, side = LocksBeams(width=4), torch.cuda.Stream()
+    beams.select(logits, scores, keep=3, stream=side)  # the workspace
+    torch.cuda.synchronize()
+    before = [torch.zeros(2, 4, dtype=torch.int32, device="cuda") for _ in range(8)]
+    torch.cuda._sleep(200_000_000)
+    for x in before:
+        x.fill_(7)
+    del x, before
+    got = beams.select(logits, scores, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    check_select(got, logits, scores, None, -1, 4)
