@@ -76,7 +76,7 @@ struct GroupArgs {
   float scale_log2;
   int q4;
 };
-int group_attend_ctas_per_sm();
+int group_attend_ctas_per_sm(bool q4);
 cudaError_t launch_group_attend(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
 
 }  // namespace locks

@@ -9,27 +9,32 @@
 // What bounds it: the bytes of the shared pages once and of the rows' own pages.
 //
 // Layout.  mma.sync m16n8k16 with one or two tiles of 16 rows: a CTA of four warps takes
-// 64 tokens at a time from a ring that bulk and tensor copies fill, warp w tokens 16 w ..
-// 16 w + 15, with the softmax and the outputs of its tokens in registers; the warps' states
-// meet in shared memory at the end of a piece.  The queries stay in shared memory (their
-// fragments would take 64 more registers than there are).  bf16 pages: ldmatrix.
-// 4-bit pages: keys' codes are bf16 numbers (exact) and get their scale on the four partial
-// sums of a logit; values are s * code rounded to half precision (2^-11), and so are the weights.
+// 64 tokens at a time from a ring that bulk and tensor copies fill.  Warp w has the logits and weights
+// of tokens 16 w .. 16 w + 15; the weights go to the other warps by shared memory, and a warp has 32 columns
+// of the outputs for all tokens.  So every value is loaded, and every code taken apart, once, a piece ends
+// without a merge of outputs, and 170 registers suffice.  With all 128 columns of its own
+// tokens in each warp (255 registers): 34.1 us for the 32.3 below (32 K, bf16; 16-token pages 36.3 for 33.3), 4-bit
+// pages 45.7 for 42.0; but 43.3 for 44.1 where 64 rows share 32 K tokens.
+// bf16 pages: ldmatrix.  4-bit pages: keys' codes are bf16 numbers (exact) and get their scale on the
+// four partial sums of a logit; values are s * code rounded to half precision (2^-11), and so are the
+// weights.  Four CTAs of 128 registers, some of them spilt, took 47.2 us for 42.0; the queries in
+// registers, 45.7.
 //
 // Work split.  All 64-token tiles of all problems lie in one line: request by request, KV
 // head by head, first the shared pages (once per block of 32 rows), then each row's own.  Every
-// CTA gets an equal part of it, two CTAs per SM; a segment counts a few tiles more
+// CTA gets an equal part of it; a segment counts a few tiles more
 // than it has, which is what its queries, its first copies and its merge cost.  A piece
 // (the part of a segment that a CTA has) leaves its state in the workspace at place
 // CTA + segment, which no two pieces share; a second, dependent kernel joins them.
 //
 // Measured, 32 query / 8 KV heads (floor by bytes): eight rows that share 32 K tokens of bf16
-// pages and have 300 of their own 33.9 us (21.2; every row by itself 83); 131 K shared 89 us (79.6; 274);
-// four rows of 2 K 11 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 41 us, 16-token
-// ones 45 us (8.1; 72 and 79): 32 rows per key make the instructions the bound there (35% of the issue
-// slots with two warps per scheduler, which is what 255 registers leave).
+// pages and have 60 of their own 32.3 us (20.1), 300 33.6 (21.2; every row by itself 83); 131 K shared 87.6 us
+// (79.6; 274); four rows of 2 K 10.5 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 41 us,
+// 16-token ones 42 us (8.1; 72 and 79): 32 rows per key make the instructions the bound there, some 900
+// per warp and 64 tokens, of which the SM issues 46% of what it could (no pipe is above 37%).
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "gen.h"
 #include "kv_q4.cuh"
@@ -40,23 +45,32 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// Places that a segment has beyond its tiles.  Measured (2, 3, 4): bf16 pages, 131,000 shared
-// tokens 99, 91, 93 us, 32 K 34.4, 33.6, 33.6; 4-bit, four requests of 16 K 51.5, 52.9, 54.1.
+// Places that a segment has beyond its tiles.  Measured: bf16 pages (2, 3, 4), 131,000 shared
+// tokens 89.4, 87.6, 89.5 us, 64 rows 44.8, 44.1, 44.3; 4-bit, four requests of 16 K (1, 2, 3) 46.1, 42.2, 43.1.
 constexpr int kSegmentBf16 = 3, kSegmentQ4 = 2;
 constexpr int kHalfTile = 64 * 128;   // bytes of a 64-row x 64-column bf16 box
 constexpr int kTile = 2 * kHalfTile;  // 64 tokens of K (or V)
 constexpr int kQueryBytes = kSharedRows * kHeadDim * 2;
 template <bool Q4>
-constexpr int kOStride = Q4 ? 132 : 136;  // padded row of a warp's outputs (floats): no two lanes' stores meet in a bank
+constexpr int kOStride = Q4 ? 132 : 136;  // padded row of outputs (floats), against bank conflicts
 template <bool Q4>
 constexpr int kStageBytes = Q4 ? kQ4Slot : 2 * kTile;
+// Measured for 4 bits (3, 4, 6 stages): 49.7, 42.2, 43.0 us.
 template <bool Q4>
-constexpr int kStages = Q4 ? 8 : 3;
+constexpr int kStages = Q4 ? 4 : 3;
 template <bool Q4>
-constexpr int kSmem = kStages<Q4> * kStageBytes<Q4> + kQueryBytes + 1024;
-static_assert(kWarps * kSharedRows * kOStride<true> * 4 <= kStages<true> * kStageBytes<true> &&
-                  kWarps * kSharedRows * kOStride<false> * 4 <= kStages<false> * kStageBytes<false>,
-              "the merge fits the ring");
+constexpr int kCtas = Q4 ? 3 : 2;  // per SM
+// Whether the warps take turns at asking for a tile; warps that ask for one.
+template <int P, bool Q4>
+constexpr bool kTurns = Q4 && P == kPage;
+template <int P, bool Q4>
+constexpr int kAsking = kTurns<P, Q4> ? 1 : kWarps;
+constexpr int kWeightBytes = kWarps * 2 * 32 * 16;  // weights of a tile
+template <bool Q4>
+constexpr int kSmem = kStages<Q4> * kStageBytes<Q4> + kQueryBytes + kWeightBytes + 1024;
+static_assert(kSharedRows * kOStride<true> * 4 <= kStages<true> * kStageBytes<true> &&
+                  kSharedRows * kOStride<false> * 4 <= kStages<false> * kStageBytes<false>,
+              "the outputs fit the ring");
 
 // ---- lengths, and what follows from them ----------------------------------------------
 
@@ -155,7 +169,7 @@ struct Piece {
 
 constexpr int kFewGroups = 2 * kWarps;
 struct Shared {
-  uint64_t full[8], empty[8];
+  uint64_t full[8];
   int left[8][4];  // per stage (and page of it): tokens of the tile to be seen
   float m[kWarps][kSharedRows], l[kWarps][kSharedRows];
   Group grp;
@@ -189,29 +203,29 @@ __device__ __forceinline__ uint32_t pair_mask(int t, int len) {
   return (t < len ? 0x0000ffffu : 0u) | (t + 1 < len ? 0xffff0000u : 0u);
 }
 
-// A warp's softmax state and outputs for its tokens: rows 16 i + g, 16 i + g + 8.  m is the
+// A warp's sums for its tokens and outputs for its columns: rows 16 i + g, 16 i + g + 8.  m is the
 // reference of a row's weights 2^(s - m): the largest logit when it was set, less kBelow.
-// It moves only when a weight would exceed 2^kLimit, so the usual tile needs no maximum
-// across lanes, only a vote.  bf16 weights: any range will do.  Half-precision ones: the
+// It is the same in all warps and moves only when a weight would exceed 2^kLimit, so the usual tile
+// needs no maximum across lanes, only a vote.  bf16 weights: any range will do.  Half-precision ones: the
 // largest lies between 2^7 and 2^15, so those below 2^-32 of it are what is lost.
 template <int MT, bool Q4>
 struct State {
   static constexpr float kBelow = Q4 ? 7.f : 0.f, kLimit = Q4 ? 15.f : 8.f;
+  static constexpr int kBlocks = 4;  // of eight output columns
   float m[MT][2], l[MT][2];
-  float o[MT][16][4];
+  float o[MT][kBlocks][4];
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       m[i][0] = m[i][1] = -INFINITY;
       l[i][0] = l[i][1] = 0.f;
 #pragma unroll
-      for (int n = 0; n < 16; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+      for (int n = 0; n < kBlocks; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
   }
-  // Logits (unscaled) to weights.
-  __device__ __forceinline__ void weigh(float (&s)[MT][2][4], float scale_log2) {
+  // This lane's largest logits (s: unscaled); whether one of them moves its row's reference.
+  __device__ __forceinline__ bool look(const float (&s)[MT][2][4], float scale_log2, float (&top)[MT][2]) const {
     bool moved = false;
-    float top[MT][2];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -219,24 +233,27 @@ struct State {
         top[i][k] = fmaxf(fmaxf(s[i][0][2 * k], s[i][0][2 * k + 1]), fmaxf(s[i][1][2 * k], s[i][1][2 * k + 1])) * scale_log2;
         moved |= top[i][k] > m[i][k] + kLimit;
       }
-    if (__any_sync(0xffffffffu, moved)) {
+    return moved;
+  }
+  // The largest logit of a row among the lanes that hold it.
+  __device__ __forceinline__ static float row_top(float t) {
+    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    return fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+  }
+  // The reference of a row of which logit t is to be seen.
+  __device__ __forceinline__ void move(int i, int k, float t) {
+    t = fmaxf(t - kBelow, m[i][k]);
+    const float al = t == -INFINITY ? 1.f : fast_exp2(m[i][k] - t);
+    m[i][k] = t;
+    l[i][k] *= al;
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float t = fmaxf(top[i][k], __shfl_xor_sync(0xffffffffu, top[i][k], 1));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-          t = fmaxf(t - kBelow, m[i][k]);
-          const float al = t == -INFINITY ? 1.f : fast_exp2(m[i][k] - t);
-          m[i][k] = t;
-          l[i][k] *= al;
-#pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            o[i][n][2 * k] *= al;
-            o[i][n][2 * k + 1] *= al;
-          }
-        }
+    for (int n = 0; n < kBlocks; ++n) {
+      o[i][n][2 * k] *= al;
+      o[i][n][2 * k + 1] *= al;
     }
+  }
+  // Logits to weights.
+  __device__ __forceinline__ void weigh(float (&s)[MT][2][4], float scale_log2) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -254,12 +271,11 @@ struct State {
   }
 };
 
-// Tokens 16 warp .. + 15 of a tile of bf16 pages at `base` (keys, then values), of which the
-// first `left` are seen.
-template <int MT, bool WHOLE>
-__device__ __forceinline__ void tile_bf16(State<MT, false>& st, uint32_t base, uint32_t queries, int left, float scale_log2) {
+// The logits of tokens 16 warp .. + 15 of a tile of bf16 pages at `base` (keys, then values), of
+// which the first `left` are seen.
+template <int MT>
+__device__ __forceinline__ void logits_bf16(float (&s)[MT][2][4], uint32_t base, uint32_t queries, int left) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, mi = lane >> 3;
-  float s[MT][2][4];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -277,7 +293,7 @@ __device__ __forceinline__ void tile_bf16(State<MT, false>& st, uint32_t base, u
       mma_16816(s[i][1], a0, a1, a2, a3, b2, b3);
     }
   }
-  if constexpr (!WHOLE) {
+  if (left < 16) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -286,26 +302,27 @@ __device__ __forceinline__ void tile_bf16(State<MT, false>& st, uint32_t base, u
         for (int e = 0; e < 4; ++e)
           if (8 * n + 2 * c + (e & 1) >= left) s[i][n][e] = -INFINITY;
   }
-  st.weigh(s, scale_log2);
-  uint32_t p[MT][4];
+}
+// The weights of 16 tokens (a fragment each lane: `weights`) times this warp's 32 columns of their values.
+template <int MT, bool WHOLE>
+__device__ __forceinline__ void values_bf16(State<MT, false>& st, uint32_t base, int group, uint32_t weights, int left) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, mi = lane >> 3;
+  const int vrow = 16 * group + (mi & 1) * 8 + (lane & 7);
+  uint4 p[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    p[i][0] = pack_bf16(s[i][0][0], s[i][0][1]);
-    p[i][1] = pack_bf16(s[i][0][2], s[i][0][3]);
-    p[i][2] = pack_bf16(s[i][1][0], s[i][1][1]);
-    p[i][3] = pack_bf16(s[i][1][2], s[i][1][3]);
-  }
-  const int vrow = 16 * warp + (mi & 1) * 8 + (lane & 7);
-  const uint32_t k0 = WHOLE ? ~0u : pair_mask(2 * c, left), k1 = WHOLE ? ~0u : pair_mask(8 + 2 * c, left);
+  for (int i = 0; i < MT; ++i) p[i] = lds128(weights + ((group * MT + i) * 32 + lane) * 16);
 #pragma unroll
-  for (int dn = 0; dn < 8; ++dn) {
+  for (int n = 0; n < 2; ++n) {
     uint32_t v0, v1, v2, v3;
-    ldmatrix_x4_trans(v0, v1, v2, v3, tile_addr(base + kTile, vrow, 2 * dn + (mi >> 1)));
-    if constexpr (!WHOLE) v0 &= k0, v1 &= k1, v2 &= k0, v3 &= k1;  // what lies past the end may be anything
+    ldmatrix_x4_trans(v0, v1, v2, v3, tile_addr(base + kTile, vrow, 4 * warp + 2 * n + (mi >> 1)));
+    if constexpr (!WHOLE) {  // what lies past the end may be anything
+      const uint32_t k0 = pair_mask(2 * c, left), k1 = pair_mask(8 + 2 * c, left);
+      v0 &= k0, v1 &= k1, v2 &= k0, v3 &= k1;
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      mma_16816(st.o[i][2 * dn], p[i][0], p[i][1], p[i][2], p[i][3], v0, v1);
-      mma_16816(st.o[i][2 * dn + 1], p[i][0], p[i][1], p[i][2], p[i][3], v2, v3);
+      mma_16816(st.o[i][2 * n], p[i].x, p[i].y, p[i].z, p[i].w, v0, v1);
+      mma_16816(st.o[i][2 * n + 1], p[i].x, p[i].y, p[i].z, p[i].w, v2, v3);
     }
   }
 }
@@ -326,16 +343,13 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// The same of 4-bit pages.  A key word holds dimensions 32 j + 8 c .. + 7 of one token, field
-// i the pair 8 c + 2 i, + 1, so fields 0 and 1 are one step of a product, 2 and 3 the next; the
-// queries are read in that order.  A value word holds four dimensions of two tokens, field
-// i dimension 32 j + 4 n + i of column n: output block 4 j + i, whose columns 2c and 2c + 1 are
-// dimensions 32 j + 8 c + i and 32 j + 8 c + 4 + i.
-template <int P, int MT, bool WHOLE>
-__device__ __forceinline__ void tile_q4(State<MT, true>& st, uint32_t base, uint32_t queries, int left, float scale_log2) {
+// 4-bit pages: the logits of tokens 16 warp .. + 15, of which the first `left` are seen.  A key
+// word holds dimensions 32 j + 8 c .. + 7 of one token, field i the pair 8 c + 2 i, + 1, so fields 0
+// and 1 are one step of a product, 2 and 3 the next; the queries are read in that order.
+template <int P, int MT>
+__device__ __forceinline__ void logits_q4(float (&s)[MT][2][4], uint32_t base, uint32_t queries, int left) {
   using At = Q4Tile<P>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  float s[MT][2][4];
   {
     // keys: tokens g and 8 + g for the products, their scales for columns 2c, 2c + 1
     const uint32_t kb = base + At::key_codes(warp), sb = base + At::key_scales(warp);
@@ -367,7 +381,7 @@ __device__ __forceinline__ void tile_q4(State<MT, true>& st, uint32_t base, uint
       }
     }
   }
-  if constexpr (!WHOLE) {
+  if (left < 16) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -376,38 +390,46 @@ __device__ __forceinline__ void tile_q4(State<MT, true>& st, uint32_t base, uint
         for (int e = 0; e < 4; ++e)
           if (8 * n + 2 * c + (e & 1) >= left) s[i][n][e] = -INFINITY;
   }
-  st.weigh(s, scale_log2);
-  const uint32_t vb = base + At::value_codes(warp), zb = base + At::value_scales(warp);
-  const uint4 v0 = lds128(vb + lane * 16), v1 = lds128(vb + 512 + lane * 16);
-  uint4 z0 = lds128(zb + c * 32), z1 = lds128(zb + c * 32 + 16);
+}
+// The weights of 16 tokens (a fragment each lane: `weights`) times their values, of which this
+// warp has a quarter of the dimensions.  A value word holds four dimensions of two tokens, field
+// i dimension 32 j + 4 n + i of column n.  The warp takes two neighbouring words and two
+// neighbouring fields, j0, j0 + 1 and i0, i0 + 1: output block 2 y + x, whose columns 2c and
+// 2c + 1 are dimensions 32 (j0 + y) + 8 c + i0 + x and 4 more.
+__device__ __forceinline__ int first_word() { return 2 * (threadIdx.x >> 5 & 1); }
+__device__ __forceinline__ int first_field() { return 2 * (threadIdx.x >> 6); }
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+template <int P, int MT, bool WHOLE>
+__device__ __forceinline__ void values_q4(State<MT, true>& st, uint32_t base, int group, uint32_t weights, int left) {
+  using At = Q4Tile<P>;
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  const uint32_t vb = base + At::value_codes(group) + 4 * first_word(), zb = base + At::value_scales(group) + 4 * first_word();
+  const uint2 v0 = lds64(vb + lane * 16), v1 = lds64(vb + 512 + lane * 16);
+  uint2 z0 = lds64(zb + c * 32), z1 = lds64(zb + c * 32 + 16);
   if constexpr (!WHOLE) {
     // scales past the end may be anything, a NaN too
     const uint32_t m0 = pair_mask(2 * c, left), m1 = pair_mask(8 + 2 * c, left);
-    z0.x &= m0; z0.y &= m0; z0.z &= m0; z0.w &= m0;
-    z1.x &= m1; z1.y &= m1; z1.z &= m1; z1.w &= m1;
+    z0.x &= m0; z0.y &= m0;
+    z1.x &= m1; z1.y &= m1;
   }
-  const uint32_t vw0[4] = {v0.x, v0.y, v0.z, v0.w}, vw1[4] = {v1.x, v1.y, v1.z, v1.w};
-  const uint32_t zw0[4] = {z0.x, z0.y, z0.z, z0.w}, zw1[4] = {z1.x, z1.y, z1.z, z1.w};
-  uint32_t p[MT][4];
+  const uint32_t vw0[2] = {v0.x, v0.y}, vw1[2] = {v1.x, v1.y}, zw0[2] = {z0.x, z0.y}, zw1[2] = {z1.x, z1.y};
+  uint4 p[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    p[i][0] = pack_f16(s[i][0][0], s[i][0][1]);
-    p[i][1] = pack_f16(s[i][0][2], s[i][0][3]);
-    p[i][2] = pack_f16(s[i][1][0], s[i][1][1]);
-    p[i][3] = pack_f16(s[i][1][2], s[i][1][3]);
-  }
+  for (int i = 0; i < MT; ++i) p[i] = lds128(weights + ((group * MT + i) * 32 + lane) * 16);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t f[4], h[4];
-    q4_codes01(vw0[j], f[0], f[1]);
-    q4_codes01(vw0[j] >> 8, f[2], f[3]);
-    q4_codes01(vw1[j], h[0], h[1]);
-    q4_codes01(vw1[j] >> 8, h[2], h[3]);
+  for (int y = 0; y < 2; ++y) {
+    uint32_t f[2], h[2];
+    q4_codes01(vw0[y] >> (4 * first_field()), f[0], f[1]);
+    q4_codes01(vw1[y] >> (4 * first_field()), h[0], h[1]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t f0 = mul_f16x2(f[k], zw0[j]), f1 = mul_f16x2(h[k], zw1[j]);
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t f0 = mul_f16x2(f[x], zw0[y]), f1 = mul_f16x2(h[x], zw1[y]);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) mma_16816_f16(st.o[i][4 * j + k], p[i][0], p[i][1], p[i][2], p[i][3], f0, f1);
+      for (int i = 0; i < MT; ++i) mma_16816_f16(st.o[i][2 * y + x], p[i].x, p[i].y, p[i].z, p[i].w, f0, f1);
     }
   }
 }
@@ -416,16 +438,18 @@ __device__ __forceinline__ void tile_q4(State<MT, true>& st, uint32_t base, uint
 template <int P, bool Q4, int MT>
 __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const Piece& p, Shared& sh,
                                           uint8_t* ring, uint8_t* queries, uint32_t& seq, float* part_o, float2* part_ml) {
+  // (a tile's weights follow the queries)
   constexpr int kPPT = kPage / P, S = kStages<Q4>, kBatch = 32;  // pages of a tile; page entries a warp looks up at once
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int nt = p.t1 - p.t0, G = sh.grp.g;
   const uint32_t rbase = smem_u32(ring), qbase = smem_u32(queries);
 
-  // The warps take turns at asking for the copies, tile t warp t % kWarps; their lanes hold
-  // 32 pages' entries, and the next 32.
+  // Every warp asks for its quarter of a tile: one of four 16-token pages, or one box of a 64-token one
+  // (of which 4-bit ones are one copy: the warps take turns).  Its lanes hold 32 pages' entries, and the next 32.
   int cur = 0, nxt = 0, batch = -2, asked = -1;
   auto entry = [&](int k) { return k < p.pages ? p.table[p.page0 + k] : 0; };  // of page k of the piece
   auto issue = [&](int t) {  // whole warps: tile t of the piece
+    if (kTurns<P, Q4> && t % kWarps != warp) return;
     const int k0 = t * kPPT, need = k0 / kBatch;
     if (need != batch) {
       cur = need == batch + 1 ? nxt : entry(need * kBatch + lane);
@@ -433,37 +457,34 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
       batch = need;
     }
     asked = t;
-    const int stage = (seq + t) % S;
-    const int np = min(kPPT, p.pages - k0);
-    uint8_t* dst = ring + stage * kStageBytes<Q4>;
-    int mine = __shfl_sync(0xffffffffu, cur, (k0 + lane % kPPT) % kBatch);  // lane w: page w of the tile
-    if (mine < 0 || mine >= a.pages_total) {
-      if (lane < np) set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
-      mine = -1;
+    const int stage = (seq + t) % S, w = P == kPage ? 0 : warp, k = k0 + w;
+    const int phys = __shfl_sync(0xffffffffu, cur, k % kBatch);
+    if (lane != 0) return;
+    const bool there = k < p.pages, good = there && phys >= 0 && phys < a.pages_total;
+    if (there && !good) set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
+    if (P != kPage || kTurns<P, Q4> || warp == 0) sh.left[stage][w] = good ? min(P, p.limit - (p.page0 + k) * P) : 0;
+    if (!there) {
+      mbar_arrive(&sh.full[stage]);
+      return;
     }
-    if (lane < kPPT) sh.left[stage][lane] = lane < np && mine >= 0 ? min(P, p.limit - (p.page0 + k0 + lane) * P) : 0;
-    __syncwarp();  // before the arrival, which releases it
-    if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], (uint32_t)np * (Q4 ? LOCKS_KV_Q4_BLOCK_BYTES(P) : 2 * P * kHeadDim * 2));
-#pragma unroll
-    for (int w = 0; w < kPPT; ++w) {
-      const int phys = __shfl_sync(0xffffffffu, mine, w);
-      if (lane == 0 && w < np) {
-        const size_t ph = (size_t)max(phys, 0) * a.num_kv_heads + p.h;  // (a page outside the pool: any, unseen)
-        if constexpr (Q4) {
-          bulk_load(smem_u32(dst + w * LOCKS_KV_Q4_BLOCK_BYTES(P)), a.blocks + ph * LOCKS_KV_Q4_BLOCK_BYTES(P),
-                    LOCKS_KV_Q4_BLOCK_BYTES(P), &sh.full[stage]);
-        } else {
-          const int y = (int)(ph * P);
-          uint8_t* d = dst + w * (P * 128);
-          tma_load_2d(d, &tk, &sh.full[stage], 0, y);
-          tma_load_2d(d + kHalfTile, &tk, &sh.full[stage], 64, y);
-          tma_load_2d(d + kTile, &tv, &sh.full[stage], 0, y);
-          tma_load_2d(d + kTile + kHalfTile, &tv, &sh.full[stage], 64, y);
-        }
-      }
+    const size_t ph = (size_t)(good ? phys : 0) * a.num_kv_heads + p.h;  // (a page outside the pool: any, unseen)
+    uint8_t* dst = ring + stage * kStageBytes<Q4>;
+    mbar_arrive_expect_tx(&sh.full[stage], kStageBytes<Q4> / kAsking<P, Q4>);
+    if constexpr (Q4) {
+      constexpr int kBytes = LOCKS_KV_Q4_BLOCK_BYTES(P);
+      bulk_load(smem_u32(dst + w * kBytes), a.blocks + ph * kBytes, kBytes, &sh.full[stage]);
+    } else if constexpr (P == kPage) {
+      tma_load_2d(dst + warp * kHalfTile, warp < 2 ? &tk : &tv, &sh.full[stage], 64 * (warp & 1), (int)(ph * P));
+    } else {
+      const int y = (int)(ph * P);
+      uint8_t* d = dst + w * (P * 128);
+      tma_load_2d(d, &tk, &sh.full[stage], 0, y);
+      tma_load_2d(d + kHalfTile, &tk, &sh.full[stage], 64, y);
+      tma_load_2d(d + kTile, &tv, &sh.full[stage], 0, y);
+      tma_load_2d(d + kTile + kHalfTile, &tv, &sh.full[stage], 64, y);
     }
   };
-  for (int t = warp; t < min(S, nt); t += kWarps) issue(t);
+  for (int t = 0; t < min(S, nt); ++t) issue(t);
   // the queries; rows past the last are zero
   for (int e = tid; e < MT * 16 * 16; e += kThreads) {
     const int r = e / 16, chunk = e % 16;
@@ -488,28 +509,76 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
   State<MT, Q4> st;
   st.reset();
   bool ok = true;
+  const uint32_t weights = qbase + kQueryBytes;
   for (int t = 0; t < nt; ++t) {
-    const int ahead = t - 1 + S;
-    if (t > 0 && ahead < nt && ahead % kWarps == warp) {
-      // into the stage of the tile before this one, when all warps are done with it
-      ok = mbar_wait(&sh.empty[(seq + t - 1) % S], ((seq + t - 1) / S) & 1);
-      if (!ok) break;
-      issue(ahead);
-    }
     const int stage = (seq + t) % S;
-    ok = mbar_wait(&sh.full[stage], ((seq + t) / S) & 1);
-    if (!ok) break;
-    const int left = P == kPage ? min(16, sh.left[stage][0] - 16 * warp) : sh.left[stage][P == kPage ? 0 : warp];
     const uint32_t base = rbase + stage * kStageBytes<Q4>;
-    if constexpr (Q4) {
-      if (left >= 16) tile_q4<P, MT, true>(st, base, qbase, 16, a.scale_log2);
-      else if (left > 0) tile_q4<P, MT, false>(st, base, qbase, left, a.scale_log2);
-    } else {
-      if (left >= 16) tile_bf16<MT, true>(st, base, qbase, 16, a.scale_log2);
-      else if (left > 0) tile_bf16<MT, false>(st, base, qbase, left, a.scale_log2);
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[stage], ((seq + t) / S) & 1))) {
+      if (lane == 0) atomicExch(&sh.abort, 1);
+      ok = false;
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.empty[stage]);
+    // tokens of 16 that are seen
+    auto left_of = [&](int group) { return P == kPage ? min(16, sh.left[stage][0] - 16 * group) : sh.left[stage][P == kPage ? 0 : group]; };
+    const int left = left_of(warp);
+    float s[MT][2][4], top[MT][2];
+    if (ok && left > 0) {
+      if constexpr (Q4) logits_q4<P, MT>(s, base, qbase, left);
+      else logits_bf16<MT>(s, base, qbase, left);
+    } else {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][0][e] = s[i][1][e] = -INFINITY;
+    }
+    // the reference of a row is the same in all warps
+    const bool moved = __syncthreads_or(st.look(s, a.scale_log2, top));
+    ok = *reinterpret_cast<volatile int*>(&sh.abort) == 0;  // (set before the barrier, and not again before the next one)
+    if (!ok) break;
+    // all warps are done with the tile before this one, and its stage is free
+    if (t > 0 && t - 1 + S < nt) issue(t - 1 + S);
+    if (moved) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float x = st.row_top(top[i][k]);
+          if (c == 0) sh.m[warp][16 * i + 8 * k + g] = x;
+        }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) x = fmaxf(x, sh.m[w][16 * i + 8 * k + g]);
+          st.move(i, k, x);
+        }
+    }
+    st.weigh(s, a.scale_log2);
+    auto packed = [](float x, float y) { return Q4 ? pack_f16(x, y) : pack_bf16(x, y); };
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(weights + ((warp * MT + i) * 32 + lane) * 16),
+                   "r"(packed(s[i][0][0], s[i][0][1])), "r"(packed(s[i][0][2], s[i][0][3])),
+                   "r"(packed(s[i][1][0], s[i][1][1])), "r"(packed(s[i][1][2], s[i][1][3]))
+                   : "memory");
+    __syncthreads();
+    auto values = [&](auto all, int w, int left_w) {
+      if constexpr (Q4) values_q4<P, MT, decltype(all)::value>(st, base, w, weights, left_w);
+      else values_bf16<MT, decltype(all)::value>(st, base, w, weights, left_w);
+    };
+    bool whole = true;
+#pragma unroll
+    for (int w = 0; w < kPPT; ++w) whole &= sh.left[stage][w] >= P;
+    if (whole) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) values(std::true_type(), w, 16);
+    } else {
+#pragma unroll 1
+      for (int w = 0; w < kWarps; ++w)
+        if (left_of(w) > 0) values(std::false_type(), w, left_of(w));
+    }
   }
   if (!ok) {
     if (lane == 0) {
@@ -517,10 +586,10 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
       set_error(a.err, kDevErrTimeout);
     }
     // the copies that this warp has asked for get a bounded time to land
-    for (int t = asked; t >= 0 && t > asked - S; t -= kWarps) (void)mbar_wait(&sh.full[(seq + t) % S], ((seq + t) / S) & 1);
+    for (int t = asked; t >= 0 && t > asked - S; --t) (void)mbar_wait(&sh.full[(seq + t) % S], ((seq + t) / S) & 1);
   }
   seq += nt;
-  // ---- the warps' states, merged ----
+  // ---- the piece's state ----
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -528,55 +597,38 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
       st.l[i][k] += __shfl_xor_sync(0xffffffffu, st.l[i][k], 1);
       st.l[i][k] += __shfl_xor_sync(0xffffffffu, st.l[i][k], 2);
       if (c == 0) {
-        sh.m[warp][16 * i + 8 * k + g] = st.m[i][k];
+        if (warp == 0) sh.m[0][16 * i + 8 * k + g] = st.m[i][k];
         sh.l[warp][16 * i + 8 * k + g] = st.l[i][k];
       }
     }
   __syncthreads();  // every warp is done with the ring
   float* so = reinterpret_cast<float*>(ring);
+  // of one reference, and each warp has its own columns; the sums are left
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int r = 16 * i + 8 * k + g;
-      float M = -INFINITY;
+      float* row = so + (16 * i + 8 * k + g) * kOStride<Q4>;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][r]);
-      const float f = M == -INFINITY ? 1.f : fast_exp2(st.m[i][k] - M);
-      float* row = so + (warp * kSharedRows + r) * kOStride<Q4>;
-      if constexpr (Q4) {
+      for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float4*>(row + 32 * j + 8 * c + 4 * e) =
-                make_float4(f * st.o[i][4 * j][2 * k + e], f * st.o[i][4 * j + 1][2 * k + e],
-                            f * st.o[i][4 * j + 2][2 * k + e], f * st.o[i][4 * j + 3][2 * k + e]);
-      } else {
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-          *reinterpret_cast<float2*>(row + 8 * n + 2 * c) = make_float2(f * st.o[i][n][2 * k], f * st.o[i][n][2 * k + 1]);
-      }
+        for (int e = 0; e < 2; ++e)
+          if constexpr (Q4)
+            *reinterpret_cast<float2*>(row + 32 * (first_word() + y) + 8 * c + 4 * e + first_field()) =
+                make_float2(st.o[i][2 * y][2 * k + e], st.o[i][2 * y + 1][2 * k + e]);
+          else
+            *reinterpret_cast<float2*>(row + 32 * warp + 16 * y + 8 * e + 2 * c) =
+                make_float2(st.o[i][2 * y + e][2 * k], st.o[i][2 * y + e][2 * k + 1]);
     }
   if (tid < p.rows) {
-    float M = -INFINITY, L = 0.f;
+    float L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][tid]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) L = fmaf(sh.l[w][tid], M == -INFINITY ? 1.f : fast_exp2(sh.m[w][tid] - M), L);
-    part_ml[tid] = make_float2(M, L);
+    for (int w = 0; w < kWarps; ++w) L += sh.l[w][tid];
+    part_ml[tid] = make_float2(sh.m[0][tid], L);
   }
   __syncthreads();
-  for (int e = tid; e < p.rows * (kHeadDim / 4); e += kThreads) {
-    const float* at = so + e / (kHeadDim / 4) * kOStride<Q4> + e % (kHeadDim / 4) * 4;
-    float4 O = *reinterpret_cast<const float4*>(at);
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      const float4 v = *reinterpret_cast<const float4*>(at + w * kSharedRows * kOStride<Q4>);
-      O = make_float4(O.x + v.x, O.y + v.y, O.z + v.z, O.w + v.w);
-    }
-    reinterpret_cast<float4*>(part_o)[e] = O;
-  }
+  for (int e = tid; e < p.rows * (kHeadDim / 4); e += kThreads)
+    reinterpret_cast<float4*>(part_o)[e] = *reinterpret_cast<const float4*>(so + e / (kHeadDim / 4) * kOStride<Q4> + e % (kHeadDim / 4) * 4);
   // the ring was written with ordinary stores: before the next copies into it
   fence_proxy_async();
   __syncthreads();
@@ -584,7 +636,7 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
 }
 
 template <int P, bool Q4>
-__global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_constant__ CUtensorMap tk,
+__global__ void __launch_bounds__(kThreads, kCtas<Q4>) group_attend_kernel(const __grid_constant__ CUtensorMap tk,
                                                                    const __grid_constant__ CUtensorMap tv,
                                                                    const GroupArgs a) {
   constexpr int kPPT = kPage / P;
@@ -599,10 +651,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_attend_kernel(const __grid_
       prefetch_tmap(&tk);
       prefetch_tmap(&tv);
     }
-    for (int s = 0; s < kStages<Q4>; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], kWarps);
-    }
+    for (int s = 0; s < kStages<Q4>; ++s) mbar_init(&sh.full[s], kAsking<P, Q4>);
     fence_mbar_init();
     sh.abort = 0;
   }
@@ -865,7 +914,7 @@ cudaError_t launch(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap&
 
 }  // namespace
 
-int group_attend_ctas_per_sm() { return 2; }
+int group_attend_ctas_per_sm(bool q4) { return q4 ? kCtas<true> : kCtas<false>; }
 
 // Warps per result: few results take their pieces side by side, many need few warps each.
 // Measured, the whole call in us (8, 4, 2, 1 warps): 128 results of 2 K 11.9, 12.1, 13.2, 14.5; 512
