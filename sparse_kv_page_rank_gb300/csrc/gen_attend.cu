@@ -31,7 +31,7 @@
 // pages and have 60 of their own 32.3 us (20.1), 300 33.6 (21.2; every row by itself 83); 131 K shared 87.6 us
 // (79.6; 274); four rows of 2 K 10.5 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 41 us,
 // 16-token ones 42 us (8.1; 72 and 79): 32 rows per key make the instructions the bound there, some 900
-// per warp and 64 tokens, of which the SM issues 46% of what it could (no pipe is above 37%).
+// per warp and 64 tokens, of which the SM issues 45% of what it could (no pipe is above 37%).
 #include <algorithm>
 #include <climits>
 #include <type_traits>
