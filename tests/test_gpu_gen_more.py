@@ -243,3 +243,20 @@ def test_own_outputs_on_another_stream():
     side.synchronize()
     torch.cuda.synchronize()
     check_select(got, logits, scores, None, -1, 4)
+
+
+@pytest.mark.parametrize("fmt,P", [("bf16", 64), ("bf16", 16), ("q4", 64), ("q4", 16)])
+@pytest.mark.parametrize("prompts,W,hq,hkv", [([3000, 5, 1111], 8, 16, 4), ([9000], 16, 16, 2)])
+def test_attend_gives_the_same_bits_every_time(fmt, P, prompts, W, hq, hkv):
+    """The split follows the lengths alone, and nothing depends on which warp comes first."""
+    tails = [[(11 * w + 3 * r) % 70 for w in range(W)] for r in range(len(prompts))]
+    case, _, shared = shared_case(prompts, tails, hq, hkv, P, fmt, seed=W + P)
+    beams = LocksBeams([case.runtime()], width=W)
+    q = case.query(case.B)
+    first = [x.clone() for x in beams.attend(q, shared)]
+    check_attend(case, q, *first)
+    differs = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        out, lse = beams.attend(q, shared)
+        differs += (out.view(torch.int16) != first[0].view(torch.int16)).sum() + (lse != first[1]).sum()
+    assert differs.item() == 0 and beams.device_error() == 0
