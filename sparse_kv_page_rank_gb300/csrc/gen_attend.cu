@@ -189,12 +189,16 @@ __device__ __forceinline__ size_t query_row(const GroupArgs& a, const Piece& p, 
   return ((size_t)(g * a.beams + w) * a.num_kv_heads + p.h) * a.group + e;
 }
 
-// Address of 16 bytes (chunk) of a query: bf16 pages read them by ldmatrix, 8 rows of one
-// chunk together; 4-bit pages as 16 bytes per lane, two rows of four chunks.
-template <bool Q4>
+// Address of 16 bytes (chunk) of a query, for ldmatrix.
 __device__ __forceinline__ uint32_t query_addr(uint32_t base, int row, int chunk) {
-  return base + row * 256 + ((chunk ^ (Q4 ? (row & 1) * 4 : row & 7)) << 4);
+  return base + row * 256 + ((chunk ^ (row & 7)) << 4);
 }
+// For 4-bit pages queries lie as the products take them, 16 bytes a lane: of row tile i and
+// dimensions 32 j + .., the first or second step.
+__device__ __forceinline__ uint32_t fragment_addr(uint32_t base, int i, int j, int step, int lane) {
+  return base + ((i * 4 + j) * 2 + step) * 512 + lane * 16;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory"); }
 __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int row, int chunk) {
   return base + (chunk >> 3) * kHalfTile + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
@@ -288,7 +292,7 @@ __device__ __forceinline__ void logits_bf16(float (&s)[MT][2][4], uint32_t base,
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       uint32_t a0, a1, a2, a3;
-      ldmatrix_x4(a0, a1, a2, a3, query_addr<false>(queries, 16 * i + (mi & 1) * 8 + (lane & 7), 2 * kk + (mi >> 1)));
+      ldmatrix_x4(a0, a1, a2, a3, query_addr(queries, 16 * i + (mi & 1) * 8 + (lane & 7), 2 * kk + (mi >> 1)));
       mma_16816(s[i][0], a0, a1, a2, a3, b0, b1);
       mma_16816(s[i][1], a0, a1, a2, a3, b2, b3);
     }
@@ -349,7 +353,7 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 template <int P, int MT>
 __device__ __forceinline__ void logits_q4(float (&s)[MT][2][4], uint32_t base, uint32_t queries, int left) {
   using At = Q4Tile<P>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3;
   {
     // keys: tokens g and 8 + g for the products, their scales for columns 2c, 2c + 1
     const uint32_t kb = base + At::key_codes(warp), sb = base + At::key_scales(warp);
@@ -364,13 +368,12 @@ __device__ __forceinline__ void logits_q4(float (&s)[MT][2][4], uint32_t base, u
                                 {code_pair<0>(kw1[j]), code_pair<1>(kw1[j]), code_pair<2>(kw1[j]), code_pair<3>(kw1[j])}};
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const uint4 qa = lds128(query_addr<true>(queries, 16 * i + g, 4 * j + c));
-        const uint4 qb = lds128(query_addr<true>(queries, 16 * i + g + 8, 4 * j + c));
+        const uint4 q0 = lds128(fragment_addr(queries, i, j, 0, lane)), q1 = lds128(fragment_addr(queries, i, j, 1, lane));
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           float acc[4];
-          mma_first(acc, qa.x, qb.x, qa.y, qb.y, f[n][0], f[n][1]);
-          mma_16816(acc, qa.z, qb.z, qa.w, qb.w, f[n][2], f[n][3]);
+          mma_first(acc, q0.x, q0.y, q0.z, q0.w, f[n][0], f[n][1]);
+          mma_16816(acc, q1.x, q1.y, q1.z, q1.w, f[n][2], f[n][3]);
           const float s0 = j & 1 ? f16_hi(za[n][j >> 1]) : f16_lo(za[n][j >> 1]);
           const float s1 = j & 1 ? f16_hi(zb[n][j >> 1]) : f16_lo(zb[n][j >> 1]);
           s[i][n][0] = j == 0 ? s0 * acc[0] : fmaf(s0, acc[0], s[i][n][0]);
@@ -490,8 +493,17 @@ __device__ __forceinline__ bool run_piece(const GroupArgs& a, const CUtensorMap&
     const int r = e / 16, chunk = e % 16;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (r < p.rows) v = *(reinterpret_cast<const uint4*>(a.q + query_row(a, p, G, r) * kHeadDim) + chunk);
-    const uint32_t at = query_addr<Q4>(qbase, r, chunk);
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    if constexpr (Q4) {
+      // row g (or g + 8) of its tile, dimensions 32 j + 8 c ..: words 0 and 1 for the first step, 2 and 3 for the second
+      const uint32_t at = fragment_addr(qbase, r / 16, chunk / 4, 0, r % 8 * 4 + chunk % 4) + r / 8 % 2 * 4;
+      sts32(at, v.x);
+      sts32(at + 8, v.y);
+      sts32(at + 512, v.z);
+      sts32(at + 520, v.w);
+    } else {
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(query_addr(qbase, r, chunk)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                   : "memory");
+    }
   }
   // one head's last warp sees, while the first copies are under way, whether the rows do share
   if (p.shared && p.h == 0 && p.block == 0 && warp == kWarps - 1) {
