@@ -13,12 +13,12 @@
 // of tokens 16 w .. 16 w + 15; the weights go to the other warps by shared memory, and a warp has 32 columns
 // of the outputs for all tokens.  So every value is loaded, and every code taken apart, once, a piece ends
 // without a merge of outputs, and 170 registers suffice.  With all 128 columns of its own
-// tokens in each warp (255 registers): 34.1 us for the 32.3 below (32 K, bf16; 16-token pages 36.3 for 33.3), 4-bit
-// pages 45.7 for 42.0; but 43.3 for 44.1 where 64 rows share 32 K tokens.
+// tokens in each warp (255 registers) 32 K tokens in bf16 took 34.1 us for the 32.3 below, 16-token pages 36.3
+// for 33.3, 4-bit ones 45.7 for 42; but 43.3 for 44.1 where 64 rows share 32 K tokens.
 // bf16 pages: ldmatrix.  4-bit pages: keys' codes are bf16 numbers (exact) and get their scale on the
 // four partial sums of a logit; values are s * code rounded to half precision (2^-11), and so are the
-// weights.  Four CTAs of 128 registers, some of them spilt, took 47.2 us for 42.0; the queries in
-// registers, 45.7.
+// weights.  The queries lie in shared memory in the order of the products' registers (42 us to 39.8); three
+// CTAs per SM, four of 128 registers take 40.1.
 //
 // Work split.  All 64-token tiles of all problems lie in one line: request by request, KV
 // head by head, first the shared pages (once per block of 32 rows), then each row's own.  Every
@@ -29,9 +29,9 @@
 //
 // Measured, 32 query / 8 KV heads (floor by bytes): eight rows that share 32 K tokens of bf16
 // pages and have 60 of their own 32.3 us (20.1), 300 33.6 (21.2; every row by itself 83); 131 K shared 87.6 us
-// (79.6; 274); four rows of 2 K 10.5 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 41 us,
-// 16-token ones 42 us (8.1; 72 and 79): 32 rows per key make the instructions the bound there, some 900
-// per warp and 64 tokens, of which the SM issues 45% of what it could (no pipe is above 37%).
+// (79.6; 274); four rows of 2 K 10.5 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 37 us,
+// 16-token ones 39 us (8.1; 72 and 79): 32 rows per key make the instructions the bound there, some 800
+// per warp and 64 tokens.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -45,9 +45,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// Places that a segment has beyond its tiles.  Measured: bf16 pages (2, 3, 4), 131,000 shared
-// tokens 89.4, 87.6, 89.5 us, 64 rows 44.8, 44.1, 44.3; 4-bit, four requests of 16 K (1, 2, 3) 46.1, 42.2, 43.1.
-constexpr int kSegmentBf16 = 3, kSegmentQ4 = 2;
+// Places that a segment has beyond its tiles.  Measured (2, 3, 4): bf16 pages, 131,000 shared
+// tokens 89.4, 87.6, 89.5 us, 64 rows 44.8, 44.1, 44.3; 4-bit, four requests of 16 K (1, 2, 3) 40.5, 37.8, 37.2.
+constexpr int kSegment = 3;
 constexpr int kHalfTile = 64 * 128;   // bytes of a 64-row x 64-column bf16 box
 constexpr int kTile = 2 * kHalfTile;  // 64 tokens of K (or V)
 constexpr int kQueryBytes = kSharedRows * kHeadDim * 2;
@@ -55,7 +55,7 @@ template <bool Q4>
 constexpr int kOStride = Q4 ? 132 : 136;  // padded row of outputs (floats), against bank conflicts
 template <bool Q4>
 constexpr int kStageBytes = Q4 ? kQ4Slot : 2 * kTile;
-// Measured for 4 bits (3, 4, 6 stages): 49.7, 42.2, 43.0 us.
+// Measured for 4 bits, four requests of 16 K (3, 4, 5, 6 stages) 43.7, 37.8, 37.4, 37.6 us, 131 K 76.8, 77.4, 78.1, 78.8.
 template <bool Q4>
 constexpr int kStages = Q4 ? 4 : 3;
 template <bool Q4>
@@ -86,8 +86,7 @@ __device__ __forceinline__ int row_length(const GroupArgs& a, int row, bool says
 // alone shares with nobody.
 __device__ __forceinline__ int shared_of(int given, int full, int live) { return live > 1 ? max(0, min(given, full)) : 0; }
 __device__ __forceinline__ int tiles_of(int tokens) { return tokens > 0 ? (tokens - 1) / kPage + 1 : 0; }
-__device__ __forceinline__ int segment_of(const GroupArgs& a) { return a.q4 ? kSegmentQ4 : kSegmentBf16; }
-__device__ __forceinline__ int line_of(const GroupArgs& a, int tiles) { return tiles > 0 ? tiles + segment_of(a) : 0; }
+__device__ __forceinline__ int line_of(int tiles) { return tiles > 0 ? tiles + kSegment : 0; }
 
 // One thread: the places in the line of one KV head of request g.
 __device__ __forceinline__ int head_line(const GroupArgs& a, int g, bool says) {
@@ -99,9 +98,9 @@ __device__ __forceinline__ int head_line(const GroupArgs& a, int g, bool says) {
     if (len > 0) full = min(full, len / a.page_size), ++live;
   }
   const int sp = shared_of(given, full, live);
-  int n = a.n_blocks * line_of(a, tiles_of(sp * a.page_size));
+  int n = a.n_blocks * line_of(tiles_of(sp * a.page_size));
 #pragma unroll 8
-  for (int w = 0; w < a.beams; ++w) n += line_of(a, tiles_of(row_length(a, base + w, false) - sp * a.page_size));
+  for (int w = 0; w < a.beams; ++w) n += line_of(tiles_of(row_length(a, base + w, false) - sp * a.page_size));
   return n;
 }
 
@@ -118,7 +117,7 @@ __device__ void load_group(const GroupArgs& a, int g, Group& s, bool says) {
   const uint32_t live = __ballot_sync(0xffffffffu, len > 0);
   const int full = __reduce_min_sync(0xffffffffu, len > 0 ? len / a.page_size : INT_MAX);
   const int sp = shared_of(given, full, __popc(live));
-  int upto = line_of(a, tiles_of(len > 0 ? len - sp * a.page_size : 0));
+  int upto = line_of(tiles_of(len > 0 ? len - sp * a.page_size : 0));
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     const int other = __shfl_up_sync(0xffffffffu, upto, d);
@@ -131,7 +130,7 @@ __device__ void load_group(const GroupArgs& a, int g, Group& s, bool says) {
     s.sp = sp;
     s.first = live ? __ffs(live) - 1 : 0;
     s.shared_tiles = tiles_of(sp * a.page_size);
-    s.line = upto + a.n_blocks * line_of(a, s.shared_tiles);
+    s.line = upto + a.n_blocks * line_of(s.shared_tiles);
   }
 }
 static_assert(LOCKSGEN_MAX_BEAMS == 32, "a lane per row");
@@ -739,7 +738,6 @@ __global__ void __launch_bounds__(kThreads, kCtas<Q4>) group_attend_kernel(const
     __syncthreads();
   };
   if (groups > 1) load();
-  constexpr int kSegment = Q4 ? kSegmentQ4 : kSegmentBf16;
   const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;  // records of shared parts
   while (pos < hi) {
     while (pos >= offset + (uint32_t)sh.grp.line * a.num_kv_heads) {
@@ -753,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<Q4>) group_attend_kernel(const
     const uint32_t in = pos - offset;
     p.h = (int)(in / (uint32_t)s.line);
     int x = (int)(in - (uint32_t)p.h * s.line);
-    const int shared_line = line_of(a, s.shared_tiles), shared_all = a.n_blocks * shared_line;
+    const int shared_line = line_of(s.shared_tiles), shared_all = a.n_blocks * shared_line;
     uint32_t start = offset + (uint32_t)p.h * s.line;
     int tiles, end_page;
     p.shared = x < shared_all;
@@ -832,11 +830,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) group_join_kernel(const Group
   const size_t out_row = ((size_t)b * a.num_kv_heads + h) * a.group + e;
   // the CTAs that have pieces of the two segments
   const int i = w * a.group + e, block = i / kSharedRows;
-  const int shared_line = line_of(a, s.shared_tiles), own_tiles = tiles_of(len - s.sp * a.page_size);
+  const int shared_line = line_of(s.shared_tiles), own_tiles = tiles_of(len - s.sp * a.page_size);
   const uint32_t head = first + (uint32_t)h * s.line;
   const size_t problem = (size_t)g * a.num_kv_heads + h;
   const size_t own_base = (size_t)a.n_ctas + (size_t)groups * a.num_kv_heads * a.n_blocks;
-  const uint32_t extra = segment_of(a);
+  constexpr uint32_t extra = kSegment;
   uint32_t c0[2] = {0, 0};
   int n[2] = {0, 0};
   auto segment = [&](int k, uint32_t start, int tiles) {
