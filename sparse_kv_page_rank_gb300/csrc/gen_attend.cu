@@ -29,7 +29,7 @@
 //
 // Measured, 32 query / 8 KV heads (floor by bytes): eight rows that share 32 K tokens of bf16
 // pages and have 60 of their own 32.3 us (20.1), 300 33.6 (21.2; every row by itself 83); 131 K shared 87.6 us
-// (79.6; 274); four rows of 2 K 10.5 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 37 us,
+// (79.6; 274); of 2 K 10.5 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 37 us,
 // 16-token ones 39 us (8.1; 72 and 79): 32 rows per key make the instructions the bound there, some 800
 // per warp and 64 tokens.
 #include <algorithm>
@@ -927,9 +927,9 @@ cudaError_t launch(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap&
 int group_attend_ctas_per_sm(bool q4) { return q4 ? kCtas<true> : kCtas<false>; }
 
 // Warps per result: few results take their pieces side by side, many need few warps each.
-// Measured, the whole call in us (8, 4, 2, 1 warps): 128 results of 2 K 11.9, 12.1, 13.2, 14.5; 512
-// of 32 K 46.0, 43.4, 44.6, 45.8; 1024 of 16 K, 4-bit, 54.6, 48.6, 46.0, 47.0; 2048 of 3 K 62.4,
-// 50.3, 47.2, 44.1.
+// Measured, the whole call in us (8, 4, 2, 1 warps): 256 results of 2 K 10.5, 10.3, 11.4, 12.6, of 32 K
+// in 4 bits 27.9, 28.7, 30.8, 35.4; 512 of 32 K 47.0, 44.0, 45.6, 47.1; 1024 of 16 K, 4-bit, 46.6, 41.1, 38.8,
+// 41.5; 2048 of 3 K 62.5, 50.8, 47.3, 44.5.
 static int join_warps(const GroupArgs& a) {
   const long long results = (long long)a.batch * a.num_kv_heads * a.group, n = a.n_ctas;
   return results <= n ? kJoinWarps : results <= 2 * n ? 4 : results <= 4 * n ? 2 : 1;
