@@ -184,7 +184,7 @@ __device__ void cluster_select(const AttendArgs& a, int b, int bh, int ns, int k
       for (int h = 0; h < 16; ++h)
         if (h < G) sv[h] = __ldcg(row + h);
     }
-    phys = __ldg(a.block_table + (size_t)b * a.max_pages + j);
+    phys = a.block_table[(size_t)b * a.max_pages + j];
   }
   {
     const float2* pb = a.part + (size_t)bh * a.n_scan_chunks * G;
@@ -408,11 +408,11 @@ __global__ void __launch_bounds__(kAttendThreads) attend_kernel(const __grid_con
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
       const int d0 = 16 * kk + 2 * c;
-      qf[kk][0] = (g < G) ? __ldg(reinterpret_cast<const uint32_t*>(qb + g * kHeadDim + d0)) : 0u;
-      qf[kk][1] = (g + 8 < G) ? __ldg(reinterpret_cast<const uint32_t*>(qb + (g + 8) * kHeadDim + d0)) : 0u;
-      qf[kk][2] = (g < G) ? __ldg(reinterpret_cast<const uint32_t*>(qb + g * kHeadDim + d0 + 8)) : 0u;
+      qf[kk][0] = (g < G) ? *reinterpret_cast<const uint32_t*>(qb + g * kHeadDim + d0) : 0u;
+      qf[kk][1] = (g + 8 < G) ? *reinterpret_cast<const uint32_t*>(qb + (g + 8) * kHeadDim + d0) : 0u;
+      qf[kk][2] = (g < G) ? *reinterpret_cast<const uint32_t*>(qb + g * kHeadDim + d0 + 8) : 0u;
       qf[kk][3] =
-          (g + 8 < G) ? __ldg(reinterpret_cast<const uint32_t*>(qb + (g + 8) * kHeadDim + d0 + 8)) : 0u;
+          (g + 8 < G) ? *reinterpret_cast<const uint32_t*>(qb + (g + 8) * kHeadDim + d0 + 8) : 0u;
     }
   }
   int L = a.seq_lens[b];

@@ -210,7 +210,7 @@ struct Q4Warp {
       for (int j = 0; j < 4; ++j) {
         raw[j] = make_uint4(0, 0, 0, 0);
         if (h < G)
-          raw[j] = __ldg(reinterpret_cast<const uint4*>(row(h) + 32 * j + 8 * c));
+          raw[j] = *reinterpret_cast<const uint4*>(row(h) + 32 * j + 8 * c);
         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));

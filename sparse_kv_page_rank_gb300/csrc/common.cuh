@@ -110,6 +110,10 @@ __device__ __forceinline__ void set_error(int* err, int bit) {
 }
 
 // ---- programmatic dependent launch ------------------------------------------
+// A kernel that begins before the one ahead of it has ended reads global memory by ordinary
+// loads only.  Read-only ones (__ldg) are for what does not change while the kernel lives, and
+// may be moved ahead of this wait; but lengths, tables, queries and pages may be written by
+// the kernel that it waits for (appends, reordered beams).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");

@@ -69,25 +69,25 @@ struct Chunk {
     if (first >= 0 && first + kSize <= vocab) {
       const uint4* at = reinterpret_cast<const uint4*>(base + first) + threadIdx.x;
 #pragma unroll
-      for (int k = 0; k < LOADS; ++k) raw[k] = __ldg(at + k * kThreads);
+      for (int k = 0; k < LOADS; ++k) raw[k] = at[k * kThreads];
       return;
     }
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
       const int i = first + (k * kThreads + threadIdx.x) * kVec;
       if (i >= 0 && i + kVec <= vocab) {
-        raw[k] = __ldg(reinterpret_cast<const uint4*>(base + i));
+        raw[k] = *reinterpret_cast<const uint4*>(base + i);
       } else {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (sizeof(T) == 2) {
             const int j = i + 2 * e;
-            const uint32_t lo = j >= 0 && j < vocab ? __ldg(reinterpret_cast<const uint16_t*>(base) + j) : 0xff80u;
-            const uint32_t hi = j + 1 >= 0 && j + 1 < vocab ? __ldg(reinterpret_cast<const uint16_t*>(base) + j + 1) : 0xff80u;
+            const uint32_t lo = j >= 0 && j < vocab ? reinterpret_cast<const uint16_t*>(base)[j] : 0xff80u;
+            const uint32_t hi = j + 1 >= 0 && j + 1 < vocab ? reinterpret_cast<const uint16_t*>(base)[j + 1] : 0xff80u;
             w[e] = lo | hi << 16;
           } else {
-            w[e] = i + e >= 0 && i + e < vocab ? __ldg(reinterpret_cast<const uint32_t*>(base) + i + e) : 0xff800000u;
+            w[e] = i + e >= 0 && i + e < vocab ? reinterpret_cast<const uint32_t*>(base)[i + e] : 0xff800000u;
           }
         }
         raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -110,8 +110,8 @@ struct Chunk {
     }
   }
   __device__ __forceinline__ static float logit(const T* base, int i) {
-    if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(base) + i) << 16);
-    else return __ldg(reinterpret_cast<const float*>(base) + i);
+    if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[i] << 16);
+    else return reinterpret_cast<const float*>(base)[i];
   }
   __device__ __forceinline__ static int token(int first, int j) {
     return first + ((j / kVec) * kThreads + threadIdx.x) * kVec + j % kVec;

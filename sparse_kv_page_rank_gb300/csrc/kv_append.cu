@@ -56,12 +56,12 @@ __device__ __forceinline__ TokenPlace token_place(const KvTokenArgs& a, int t, b
     const int lane = threadIdx.x & 31;
     r.b = 0;
     for (int b0 = 1; b0 <= a.batch; b0 += 32) {
-      const int n = __popc(__ballot_sync(0xffffffffu, b0 + lane <= a.batch && __ldg(a.cu_tokens + b0 + lane) <= t));
+      const int n = __popc(__ballot_sync(0xffffffffu, b0 + lane <= a.batch && a.cu_tokens[b0 + lane] <= t));
       r.b += n;
       if (n < 32) break;
     }
     if (r.b >= a.batch) return r;  // a row behind the last sequence
-    const int c0 = __ldg(a.cu_tokens + r.b), c1 = __ldg(a.cu_tokens + r.b + 1);
+    const int c0 = a.cu_tokens[r.b], c1 = a.cu_tokens[r.b + 1];
     n_b = c1 - c0;
     i = t - c0;
     if (i < 0 || i >= n_b || i >= a.max_tokens) {
@@ -69,7 +69,7 @@ __device__ __forceinline__ TokenPlace token_place(const KvTokenArgs& a, int t, b
       return r;
     }
   }
-  const int len = __ldg(a.seq_lens + r.b);
+  const int len = a.seq_lens[r.b];
   if (!a.cu_tokens && len == 0) return r;  // an idle slot of a padded batch
   const long long pos = (long long)len - n_b + i;
   if (pos < 0 || pos >= (long long)a.max_pages * a.page_size) {
@@ -79,7 +79,7 @@ __device__ __forceinline__ TokenPlace token_place(const KvTokenArgs& a, int t, b
   r.pos = (int)pos;
   const int lp = r.pos / a.page_size;
   r.slot = r.pos - lp * a.page_size;
-  r.phys = __ldg(a.block_table + (size_t)r.b * a.max_pages + lp);
+  r.phys = a.block_table[(size_t)r.b * a.max_pages + lp];
   if (r.phys < 0 || r.phys >= a.pages_total) {
     if (report) set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
     return r;
@@ -178,14 +178,14 @@ __device__ __forceinline__ void axis_pairs(const KvAppendArgs& a, int row, int p
   const int half = a.rotary_dim / 2;
   const float* t0 = a.rope + (size_t)r0 * a.rotary_dim + p;
   if (r0 == r1 && r0 == r2 && r0 == r3) {
-    c = __ldg(reinterpret_cast<const float4*>(t0));
-    s = __ldg(reinterpret_cast<const float4*>(t0 + half));
+    c = *reinterpret_cast<const float4*>(t0);
+    s = *reinterpret_cast<const float4*>(t0 + half);
   } else {
     const float* t1 = a.rope + (size_t)r1 * a.rotary_dim + p + 1;
     const float* t2 = a.rope + (size_t)r2 * a.rotary_dim + p + 2;
     const float* t3 = a.rope + (size_t)r3 * a.rotary_dim + p + 3;
-    c = make_float4(__ldg(t0), __ldg(t1), __ldg(t2), __ldg(t3));
-    s = make_float4(__ldg(t0 + half), __ldg(t1 + half), __ldg(t2 + half), __ldg(t3 + half));
+    c = make_float4(*t0, *t1, *t2, *t3);
+    s = make_float4(t0[half], t1[half], t2[half], t3[half]);
   }
 }
 
@@ -222,13 +222,13 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvAppen
   const int i0 = warp % WPT;
   load(i0);  // under way while the token's place is looked up
   // AXES: each lane the table row of one axis, on its way with the rows
-  const int axis_row = AXES ? __ldg(a.positions + (lane < a.num_axes ? lane : 0) * a.axis_stride + t) : 0;
+  const int axis_row = AXES ? a.positions[(lane < a.num_axes ? lane : 0) * a.axis_stride + t] : 0;
   const bool says = lane == 0 && warp % WPT == 0;
   const TokenPlace tp = token_place(a.tok, t, says);
   if (!tp.ok) return;
   Turn tr;
   if (a.rotary_dim) {
-    const int row = AXES ? axis_row : a.positions ? __ldg(a.positions + t) : tp.pos;
+    const int row = AXES ? axis_row : a.positions ? a.positions[t] : tp.pos;
     bool outside = row < 0 || row >= a.rope_rows;
     if (AXES) outside = __any_sync(0xffffffffu, outside);
     if (outside) {
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const KvAppen
         if constexpr (AXES) {
           axis_pairs(a, row, p0 + 4 * k, turns, c, s);
         } else {
-          c = __ldg(reinterpret_cast<const float4*>(cs) + k);
-          s = __ldg(reinterpret_cast<const float4*>(cs + half) + k);
+          c = reinterpret_cast<const float4*>(cs)[k];
+          s = reinterpret_cast<const float4*>(cs + half)[k];
         }
         if constexpr (PAIRS_NEXT) {
           const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};

@@ -231,11 +231,11 @@ __device__ __forceinline__ size_t part_of(const PromptArgs& a, int tile, int spl
 // One value of the cache (bf16 pages: any; 4-bit pages: with its scale).
 template <bool Q4, int P>
 __device__ float value_at(const PromptArgs& a, const PromptPlace& w, int t, int d) {
-  const int phys = __ldg(a.block_table + (size_t)w.b * a.max_pages + t / P);
+  const int phys = a.block_table[(size_t)w.b * a.max_pages + t / P];
   const size_t ph = (size_t)phys * a.num_kv_heads + w.hkv;
   const int slot = t % P;
   if (!Q4) {
-    const uint16_t x = __ldg(static_cast<const uint16_t*>(a.v_pool) + (ph * P + slot) * kHeadDim + d);
+    const uint16_t x = static_cast<const uint16_t*>(a.v_pool)[(ph * P + slot) * kHeadDim + d];
     return __uint_as_float((uint32_t)x << 16);
   }
   const int u = slot & 15, j = d / 32;
@@ -264,7 +264,7 @@ __device__ void load_role(const PromptArgs& a, const PromptPlace& w, const CUten
     const int lp = jb * kPPB + lane;
     int phys = -1;
     if (lp < n_pages && lp < w.j1 * kPPB) {
-      phys = __ldg(a.block_table + (size_t)w.b * a.max_pages + lp);
+      phys = a.block_table[(size_t)w.b * a.max_pages + lp];
       if (phys < 0 || phys >= a.pages_total) {
         set_error(a.err, LOCKS_DEVERR_BLOCK_TABLE);
         phys = -1;
@@ -487,30 +487,32 @@ __global__ void __launch_bounds__(128) planes_kernel(const PromptArgs a) {
   const int tile = P == 64 ? warp : 0;
   const size_t plane = (size_t)a.batch * a.num_kv_heads * a.plane_rows * kHeadDim;
   uint16_t* dst = a.planes + ((size_t)blockIdx.y * a.plane_rows + t0) * kHeadDim;
-  {
-    const int c = lane & 3;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = 8 * k + (lane >> 2);
-      convert_keys(__ldg(reinterpret_cast<const uint4*>(block + At::key_codes(tile) + 64 * r + 16 * c)),
-                   __ldg(reinterpret_cast<const uint2*>(block + At::key_scales(tile) + 8 * r)),
-                   [&](int j, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
-                     uint16_t* at = dst + r * kHeadDim + 32 * j + 8 * c;
-                     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                     *reinterpret_cast<uint4*>(at + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                   });
-    }
-  }
   const int g = lane >> 2, c = lane & 3;
+  uint4 kw[2], vw[2], vs[2];  // all loads before the first store
+  uint2 ks[2];
 #pragma unroll
-  for (int hi = 0; hi < 2; ++hi) {
-    uint16_t* row = dst + 2 * plane + (8 * hi + 2 * c) * kHeadDim + 4 * g;
-    convert_values(__ldg(reinterpret_cast<const uint4*>(block + At::value_codes(tile) + 512 * hi + 16 * lane)),
-                   __ldg(reinterpret_cast<const uint4*>(block + At::value_scales(tile) + 32 * c + 16 * hi)),
-                   [&](int j, uint2 x0, uint2 x1) {
-                     *reinterpret_cast<uint2*>(row + 32 * j) = x0;
-                     *reinterpret_cast<uint2*>(row + kHeadDim + 32 * j) = x1;
-                   });
+  for (int k = 0; k < 2; ++k) {
+    kw[k] = *reinterpret_cast<const uint4*>(block + At::key_codes(tile) + 64 * (8 * k + g) + 16 * c);
+    ks[k] = *reinterpret_cast<const uint2*>(block + At::key_scales(tile) + 8 * (8 * k + g));
+    vw[k] = *reinterpret_cast<const uint4*>(block + At::value_codes(tile) + 512 * k + 16 * lane);
+    vs[k] = *reinterpret_cast<const uint4*>(block + At::value_scales(tile) + 32 * c + 16 * k);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = 8 * k + g;
+    convert_keys(kw[k], ks[k], [&](int j, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+      uint16_t* at = dst + r * kHeadDim + 32 * j + 8 * c;
+      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(at + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    });
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint16_t* row = dst + 2 * plane + (8 * k + 2 * c) * kHeadDim + 4 * g;
+    convert_values(vw[k], vs[k], [&](int j, uint2 x0, uint2 x1) {
+      *reinterpret_cast<uint2*>(row + 32 * j) = x0;
+      *reinterpret_cast<uint2*>(row + kHeadDim + 32 * j) = x1;
+    });
   }
 }
 
@@ -533,8 +535,8 @@ __global__ void __launch_bounds__(128) bf16_planes_kernel(const PromptArgs a) {
   uint4 x[2 * kSteps];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    x[i] = __ldg(k + 32 * i);
-    x[kSteps + i] = __ldg(v + 32 * i);
+    x[i] = k[32 * i];
+    x[kSteps + i] = v[32 * i];
   }
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
@@ -682,7 +684,7 @@ __device__ void softmax_role(const PromptArgs& a, const PromptPlace& w, PromptSh
     uint4 x[16];
     uint32_t qt[2][32];  // one tile: the row in tensor memory
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + k) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < 16; ++k) x[k] = valid ? reinterpret_cast<const uint4*>(src)[k] : make_uint4(0, 0, 0, 0);
     float down = 1.f;
     if (Q4) {
       uint32_t m = 0;  // largest magnitude, as bf16 bits

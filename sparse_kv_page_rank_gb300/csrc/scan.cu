@@ -498,10 +498,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const ScanArgs a)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         qa[s] = (qr < G && (!GRP2 || g < 8))
-                    ? __ldg(reinterpret_cast<const uint4*>(qrow + qr * kHeadDim + 32 * s + 8 * c))
+                    ? *reinterpret_cast<const uint4*>(qrow + qr * kHeadDim + 32 * s + 8 * c)
                     : make_uint4(0, 0, 0, 0);
         qb[s] = (G16 && g + 8 < G)
-                    ? __ldg(reinterpret_cast<const uint4*>(qrow + (g + 8) * kHeadDim + 32 * s + 8 * c))
+                    ? *reinterpret_cast<const uint4*>(qrow + (g + 8) * kHeadDim + 32 * s + 8 * c)
                     : make_uint4(0, 0, 0, 0);
       }
     }

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kTopkThreads, 1) topk_kernel(const TopkArgs a)
 #pragma unroll
     for (int p = 0; p < IPT; ++p) {
       const int j = j0 + tid + kTopkThreads * p;
-      if (j < a.max_pages) idx[j - j0] = __ldg(a.block_table + (size_t)b * a.max_pages + j);
+      if (j < a.max_pages) idx[j - j0] = a.block_table[(size_t)b * a.max_pages + j];
     }
   }
   pdl_wait();
