@@ -243,10 +243,12 @@ struct State {
     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
     return fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
   }
-  // The reference of a row of which logit t is to be seen.
+  // The reference of a row of which logit t is the largest in sight.  It moves for the row's own
+  // logits alone, so that no other row, an idle one whose query is whatever memory held least
+  // of all, has a part in how this one's weights are rounded.
   __device__ __forceinline__ void move(int i, int k, float t) {
-    t = fmaxf(t - kBelow, m[i][k]);
-    const float al = t == -INFINITY ? 1.f : fast_exp2(m[i][k] - t);
+    t = t > m[i][k] + kLimit ? t - kBelow : m[i][k];
+    const float al = t == m[i][k] ? 1.f : fast_exp2(m[i][k] - t);
     m[i][k] = t;
     l[i][k] *= al;
 #pragma unroll
