@@ -40,6 +40,9 @@ extern "C" {
 /* Most rows of a request, and most continuations kept of one. */
 #define LOCKSGEN_MAX_BEAMS 32
 #define LOCKSGEN_MAX_KEEP 64
+/* Most rows (batch * beams) and tokens of a choice. */
+#define LOCKSGEN_MAX_ROWS 65535
+#define LOCKSGEN_MAX_VOCAB (1 << 22)
 /* Most axes of a position. */
 #define LOCKSGEN_MAX_AXES 4
 
@@ -93,7 +96,9 @@ typedef struct locksgen_choice {
   int32_t dtype, end_token;
 } locksgen_choice_t;
 
-/* Bytes of workspace locksgen_select needs for these sizes. */
+/* Bytes of workspace locksgen_select needs for these sizes.  It is no bound for smaller
+ * ones: few rows are cut into more parts, so ask for each set of sizes (the pointers
+ * and row_stride do not matter).  What exceeds a limit above is LOCKS_ERR_UNSUPPORTED. */
 LOCKS_API locks_status_t locksgen_select_workspace_size(const locksgen_choice_t* choice, size_t* bytes);
 
 /* The best continuations of every request: token v of live beam w scores

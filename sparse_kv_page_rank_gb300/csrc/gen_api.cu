@@ -23,15 +23,14 @@ struct SelectPlan {
   size_t off_parts = 0, off_lists = 0, total = 0;
 };
 
-constexpr int kMaxVocab = 1 << 22;
 constexpr long long kMaxLists = 16384;  // of a request: a CTA of the merge keeps two bytes of each
 
 locks_status_t plan_select(const locksgen_choice_t* c, SelectPlan* pl) {
   if (!c || c->batch <= 0 || c->beams <= 0 || c->vocab <= 0 || c->keep <= 0) return LOCKS_ERR_INVALID_ARG;
   if (c->dtype != LOCKS_DTYPE_BF16 && c->dtype != LOCKS_DTYPE_F32) return LOCKS_ERR_INVALID_ARG;
-  if (c->beams > LOCKSGEN_MAX_BEAMS || c->keep > LOCKSGEN_MAX_KEEP || c->vocab > kMaxVocab) return LOCKS_ERR_UNSUPPORTED;
+  if (c->beams > LOCKSGEN_MAX_BEAMS || c->keep > LOCKSGEN_MAX_KEEP || c->vocab > LOCKSGEN_MAX_VOCAB) return LOCKS_ERR_UNSUPPORTED;
   const long long rows = (long long)c->batch * c->beams;
-  if (rows > 65535) return LOCKS_ERR_UNSUPPORTED;  // the launch's second dimension
+  if (rows > LOCKSGEN_MAX_ROWS) return LOCKS_ERR_UNSUPPORTED;  // the launch's second dimension
   // a row may begin inside its first 16 bytes
   const int vec = c->dtype == LOCKS_DTYPE_BF16 ? 8 : 4;
   const long long span = c->vocab + vec - 1, sms = device_sm_count();

@@ -56,6 +56,8 @@ LOCKSGEN_DEVERR_LOGITS = 0x40
 LOCKSGEN_DEVERR_PARENT = 0x80
 LOCKSGEN_MAX_BEAMS = 32
 LOCKSGEN_MAX_KEEP = 64
+LOCKSGEN_MAX_ROWS = 65535
+LOCKSGEN_MAX_VOCAB = 1 << 22
 LOCKSGEN_MAX_AXES = 4
 
 
