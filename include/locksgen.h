@@ -104,10 +104,12 @@ LOCKS_API locks_status_t locksgen_select_workspace_size(const locksgen_choice_t*
 /* The best continuations of every request: token v of live beam w scores
  *   scores[w] + x_v - ln sum_u exp(x_u)        (x: the beam's logits)
  * where x_v is above -infinity; a beam that has ended continues as it is, with
- * its own score and the token end_token.  Out come the `keep` largest, ties to
- * the lower w * vocab + v; places for which there is no continuation get the
- * score -infinity, parent and token -1 and ended 0.  Scores are compared in 64
- * bits (the sums of exponentials are float32) and rounded once.  A live beam
+ * its own score and the token end_token.  Out come the `keep` largest.  Ties go
+ * to the lower beam, and within a beam to the larger logit (logits that differ
+ * may score the same), then to the lower token.  Places for which there is no
+ * continuation get the score -infinity, parent and token -1 and ended 0.  Scores are
+ * compared in 64 bits, of which the sums of exponentials are float32 (two beams'
+ * continuations closer than 2^-16 may change places), and rounded once.  A live beam
  * with a NaN or +infinity among its logits, or with such a score, has no
  * continuation and sets LOCKSGEN_DEVERR_LOGITS.  `ws`: 256-byte aligned, its
  * first word the device error word, zeroed once before its first use. */

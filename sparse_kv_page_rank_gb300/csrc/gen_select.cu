@@ -329,11 +329,21 @@ __device__ __forceinline__ unsigned long long orderable(double d) {
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
 
+// The order among equal scores is that of the places, lower is better: the beam, then the logit's
+// key turned round, then the token.  Logits that differ may score the same in 64 bits, and a
+// part's list has been cut by logit and token, so the merge goes by them too.
 struct Head {
   unsigned long long score;  // orderable, 0 for none
-  unsigned long long place;  // beam, then token
+  unsigned long long place;
 };
-__device__ __forceinline__ unsigned long long place_of(int beam, uint32_t token) { return ((unsigned long long)beam << 32) | token; }
+constexpr int kTokenBits = 22;
+static_assert(LOCKSGEN_MAX_VOCAB <= 1 << kTokenBits && LOCKSGEN_MAX_BEAMS <= 1 << (64 - 32 - kTokenBits), "a place is 64 bits");
+__device__ __forceinline__ unsigned long long place_of(int beam, uint32_t key, uint32_t token) {
+  return ((unsigned long long)beam << (32 + kTokenBits)) | ((unsigned long long)~key << kTokenBits) | token;
+}
+__device__ __forceinline__ int beam_of(unsigned long long place) { return (int)(place >> (32 + kTokenBits)); }
+__device__ __forceinline__ int token_of(unsigned long long place) { return (int)(place & ((1u << kTokenBits) - 1)); }
+constexpr uint32_t kEndedKey = 0xffffffffu;  // an ended beam has one continuation
 __device__ __forceinline__ bool better(const Head& x, const Head& y) {
   return x.score > y.score || (x.score == y.score && x.place < y.place);
 }
@@ -457,9 +467,9 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const SelectArgs a) {
     if (r.error < 0.f || r.value + r.error < t) return;
     const int w = e / a.keep / a.n_parts;
     const double d = (double)score[w] + ((double)key_logit(v.x) - lse[w]);
-    if (d > -INFINITY) add(d, place_of(w, v.y));
+    if (d > -INFINITY) add(d, place_of(w, v.x, v.y));
   };
-  if (tid < W && state[tid] == 2) add((double)score[tid], place_of(tid, (uint32_t)a.end_token));
+  if (tid < W && state[tid] == 2) add((double)score[tid], place_of(tid, kEndedKey, (uint32_t)a.end_token));
 #pragma unroll
   for (int k = 0; k < kEager; ++k) consider(place(k), first[k], eager[k]);
   for (int k = kEager; k * kThreads < entries; ++k)
@@ -471,7 +481,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const SelectArgs a) {
   const int n = n_list;
   auto put = [&](int k, const Head& h) {
     const size_t at = (size_t)b * a.keep + k;
-    const int w = (int)(h.place >> 32), token = (int)(uint32_t)h.place;
+    const int w = beam_of(h.place), token = token_of(h.place);
     const unsigned long long bits = h.score >> 63 ? h.score & 0x7fffffffffffffffull : ~h.score;
     a.out_scores[at] = (float)__longlong_as_double((long long)bits);
     a.out_parents[at] = w;
@@ -500,11 +510,11 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const SelectArgs a) {
     Head h = {0, ~0ull};
     const int w = i / a.n_parts, at = taken[i];
     if (state[w] == 2) {
-      if (i % a.n_parts == 0 && at == 0) h = {orderable((double)score[w]), place_of(w, (uint32_t)a.end_token)};
+      if (i % a.n_parts == 0 && at == 0) h = {orderable((double)score[w]), place_of(w, kEndedKey, (uint32_t)a.end_token)};
     } else if (state[w] == 1 && at < counts[i]) {
       const uint2 e = __ldcg(all + (size_t)i * a.keep + at);
       const double d = (double)score[w] + ((double)key_logit(e.x) - lse[w]);
-      if (d > -INFINITY) h = {orderable(d), place_of(w, e.y)};
+      if (d > -INFINITY) h = {orderable(d), place_of(w, e.x, e.y)};
     }
     return h;
   };
