@@ -82,7 +82,7 @@ LOCKS_API locks_status_t locksgen_append_axes(const locks_cache_t* cache, const 
  *   out_scores   float32;  out_parents  int32: the beam, 0..beams-1;
  *   out_tokens   int32;    out_ended    int32, or NULL: 1 where the hypothesis
  *                has ended now (its parent had, or its token is end_token)
- * out_scores and out_ended may be scores and ended where keep is beams. */
+ * out_scores and out_ended may be scores and ended where keep is beams or batch is 1. */
 typedef struct locksgen_choice {
   const void* logits;
   const float* scores;

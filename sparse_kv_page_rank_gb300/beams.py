@@ -108,7 +108,8 @@ class LocksBeams:
         ended, which continues as it is with the token ``end_token``.  Returns scores, parents, tokens
         and ended (None without an end_token), [requests][keep], best first; where there is no
         continuation the score is -inf and parent and token are -1.  The outputs are the object's
-        own unless given; they may be given back as scores and ended where keep is width."""
+        own unless given; they may be given back as scores and ended where keep is width, or of one request
+        the first width of them (``scores[:, :width]``)."""
         handle = self._launch_on(stream)
         W = self.width
         if logits.dim() == 3:

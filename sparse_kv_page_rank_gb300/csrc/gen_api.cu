@@ -108,7 +108,8 @@ locks_status_t locksgen_select(const locksgen_choice_t* c, void* ws, size_t ws_b
   const size_t element = c->dtype == LOCKS_DTYPE_BF16 ? 2 : 4;
   if (c->row_stride < c->vocab || (reinterpret_cast<uintptr_t>(c->logits) & (element - 1))) return LOCKS_ERR_INVALID_ARG;
   if (c->end_token < -1 || c->end_token >= c->vocab || (c->ended && c->end_token < 0)) return LOCKS_ERR_INVALID_ARG;
-  if (c->keep != c->beams && (c->out_scores == c->scores || (c->ended && c->out_ended == c->ended))) return LOCKS_ERR_INVALID_ARG;
+  // (a request's rows are read before its continuations are written, but not before another's are)
+  if (c->keep != c->beams && c->batch > 1 && (c->out_scores == c->scores || (c->ended && c->out_ended == c->ended))) return LOCKS_ERR_INVALID_ARG;
   if ((st = check_ws(ws, ws_bytes, pl.total)) != LOCKS_OK) return st;
   SelectArgs a;
   a.logits = c->logits;
