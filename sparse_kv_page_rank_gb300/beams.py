@@ -9,6 +9,7 @@ layers have a ``LocksRuntime`` each, over one block table and one set of lengths
         q = rt.append(k, v, q, rope=cos_sin)
         out, lse = beams.attend(q, shared_pages, layer=i)    # or rt.decode_step(q)
     scores, parents, tokens, ended = beams.select(logits, scores, ended)
+    trail.append((parents.clone(), tokens.clone()))           # the next call overwrites them
     beams.reorder(parents)
     seq_lens += seq_lens > 0                                  # the chosen tokens come next
 
@@ -108,7 +109,8 @@ class LocksBeams:
         ended, which continues as it is with the token ``end_token``.  Returns scores, parents, tokens
         and ended (None without an end_token), [requests][keep], best first; where there is no
         continuation the score is -inf and parent and token are -1.  The outputs are the object's
-        own unless given; they may be given back as scores and ended where keep is width, or of one request
+        own unless given, and the next call of these sizes overwrites them: copy the parents and
+        tokens that are to be kept.  They may be given back as scores and ended where keep is width, or of one request
         the first width of them (``scores[:, :width]``)."""
         handle = self._launch_on(stream)
         W = self.width
