@@ -18,11 +18,16 @@
  * page that the row's next token goes to) a row's pages are its own.  That is
  * how locksgen_reorder leaves them, without a page being allocated or counted:
  * a beam that is continued twice gives its copy the pages of one that is not
- * continued.  A full page that no live row refers to any more is the caller's to
- * give out again.  So a request begins with its prompt in row 0 and the other
- * rows idle (length 0): they hold the prompt's full pages, by reference or not
- * at all, and pages of their own from the prompt's open page on, and the
- * scores of rows other than 0 are -infinity.
+ * continued, from the open page on.  So a request begins with its prompt in row 0
+ * and the other rows idle (length 0): they hold the prompt's full pages, by
+ * reference or not at all, and pages of their own from the prompt's open page on,
+ * and the scores of rows other than 0 are -infinity.  From then on every row, an
+ * idle one too, has to have a page of its own in the column of the live rows' open
+ * page when the rows are reordered.  What the row that gives its pages held before
+ * that column leaves the tables: full pages, and, where it had ended or been idle for
+ * a while, the open page it was left with and those after it.  A page, full or not,
+ * is the caller's to give out again when no row's table holds it any more, or only
+ * idle rows', in columns before the open pages of all live rows of the request.
  */
 #ifndef LOCKSGEN_H_
 #define LOCKSGEN_H_
