@@ -74,7 +74,7 @@ locks_status_t plan_group(const locks_cache_t* c, const locks_params_t* p, int b
   pl->n_blocks = (beams * G + kSharedRows - 1) / kSharedRows;
   const long long segments = groups * hkv * pl->n_blocks + rows;
   const long long tiles = ((long long)c->max_pages * c->page_size + kPage - 1) / kPage;
-  if (segments * (tiles + 3) > 0x7fffffffLL) return LOCKS_ERR_UNSUPPORTED;  // places of the line are 32-bit numbers
+  if (segments * (tiles + kSegment) > 0x7fffffffLL) return LOCKS_ERR_UNSUPPORTED;  // places of the line are 32-bit numbers
   pl->n_ctas = (int)std::min<long long>((long long)group_attend_ctas_per_sm(is_q4(c)) * device_sm_count(), segments * tiles);
   const size_t parts = (size_t)(pl->n_ctas + groups * hkv * pl->n_blocks) * kSharedRows + (size_t)(pl->n_ctas + rows) * G;
   size_t off = kAlign;  // the error word

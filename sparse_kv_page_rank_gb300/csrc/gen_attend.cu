@@ -45,9 +45,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// Places that a segment has beyond its tiles.  Measured (2, 3, 4): bf16 pages, 131,000 shared
-// tokens 89.4, 87.6, 89.5 us, 64 rows 44.8, 44.1, 44.3; 4-bit, four requests of 16 K (1, 2, 3) 40.5, 37.8, 37.2.
-constexpr int kSegment = 3;
 constexpr int kHalfTile = 64 * 128;   // bytes of a 64-row x 64-column bf16 box
 constexpr int kTile = 2 * kHalfTile;  // 64 tokens of K (or V)
 constexpr int kQueryBytes = kSharedRows * kHeadDim * 2;

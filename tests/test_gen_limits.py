@@ -7,7 +7,7 @@ import pytest
 
 from sparse_kv_page_rank_gb300 import locks as L
 from tests.test_gen_abi import _choice, lib  # noqa: F401
-from tests.test_kv_layout import _status
+from tests.test_kv_layout import _cache, _status
 
 HEADER = (Path(__file__).resolve().parents[1] / "include" / "locksgen.h").read_text()
 
@@ -43,3 +43,17 @@ def test_a_workspace_is_for_its_sizes(lib):  # noqa: F811
     b = later[0]
     choice = _choice(batch=b, beams=1, vocab=50000, row_stride=50000, keep=64)
     assert _status(lambda: L.locksgen_select(choice, 0x100, sizes[b], stream=0)) == L.LOCKS_ERR_WORKSPACE
+
+
+def test_the_line_of_shared_pages_fits_32_bits(lib):  # noqa: F811
+    """Every row's part is a segment of its tiles and a few places more, and there is one more per request."""
+    csrc = Path(L.__file__).parent / "csrc"
+    found = [int(n) for f in csrc.iterdir() for n in re.findall(r"constexpr int kSegment = (\d+);", f.read_text())]
+    assert len(found) == 1  # one place says how many
+    params = L.make_params(1, 0)
+    for rows in (1 << 10, 1 << 15):
+        tiles = (1 << 31) // (2 * rows) - found[0]  # 2 rows segments of so many: 2^31 places
+        def size(n, rows=rows):
+            return L.locksgen_attend_workspace_size(_cache(batch=rows, num_kv_heads=1, max_pages=n, page_size=64, pages_total=10), params, 1)
+        assert size(tiles - 1) > 0
+        assert _status(lambda: size(tiles)) == L.LOCKS_ERR_UNSUPPORTED
