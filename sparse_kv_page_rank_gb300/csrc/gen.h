@@ -56,8 +56,9 @@ cudaError_t launch_reorder_move(const ReorderArgs& a, bool tables, int sms, cuda
 
 // Attention of rows that share pages (gen_attend.cu).
 constexpr int kSharedRows = 32;  // (row, head) pairs that a pass over the shared pages serves
-// Places that a segment has beyond its tiles.  Measured (2, 3, 4): bf16 pages, 131,000 shared
-// tokens 89.4, 87.6, 89.5 us, 64 rows 44.8, 44.1, 44.3; 4-bit, four requests of 16 K (1, 2, 3) 40.5, 37.8, 37.2.
+// Places that a segment has beyond its tiles.  Measured (1, 2, 3, 4): bf16 pages, 131,000 shared
+// tokens 98.6, 92.7, 89.0, 90.6 us, 64 rows of 32 K 54.7, 48.0, 47.2, 46.9; 4-bit, four requests of 16 K, 64-token pages
+// 44.0, 40.1, 39.5, 40.9, 16-token ones 45.3, 41.3, 41.2, 42.5.
 constexpr int kSegment = 3;
 struct GroupArgs {
   const uint16_t* q;  // bf16 [batch][Hq][d]

@@ -12,13 +12,15 @@
 // 64 tokens at a time from a ring that bulk and tensor copies fill.  Warp w has the logits and weights
 // of tokens 16 w .. 16 w + 15; the weights go to the other warps by shared memory, and a warp has 32 columns
 // of the outputs for all tokens.  So every value is loaded, and every code taken apart, once, a piece ends
-// without a merge of outputs, and 170 registers suffice.  With all 128 columns of its own
-// tokens in each warp (255 registers) 32 K tokens in bf16 took 34.1 us for the 32.3 below, 16-token pages 36.3
-// for 33.3, 4-bit ones 45.7 for 42; but 43.3 for 44.1 where 64 rows share 32 K tokens.
+// without a merge of outputs, and 172 registers suffice (168 at 4 bits, where the
+// kernel of 16-token pages spills 8 bytes).  With all 128 columns of its own
+// tokens in each warp (255 registers) 32 K tokens in bf16 took 34.1 us for 32.3, 16-token pages 36.3
+// for 33.3, 4-bit ones 45.7 for 42; but 43.3 for 44.1 where 64 rows share 32 K tokens (one set of inputs,
+// of which L2 holds a part).
 // bf16 pages: ldmatrix.  4-bit pages: keys' codes are bf16 numbers (exact) and get their scale on the
 // four partial sums of a logit; values are s * code rounded to half precision (2^-11), and so are the
-// weights.  The queries lie in shared memory in the order of the products' registers (42 us to 39.8); three
-// CTAs per SM, four of 128 registers take 40.1.
+// weights.  The queries lie in shared memory in the order of the products' registers (42 us to 39.8 on one
+// set of inputs); three CTAs per SM, four of 128 registers take 43.6 us for 41.2 (the last case below).
 //
 // Work split.  All 64-token tiles of all problems lie in one line: request by request, KV
 // head by head, first the shared pages (once per block of 32 rows), then each row's own.  Every
@@ -27,11 +29,11 @@
 // (the part of a segment that a CTA has) leaves its state in the workspace at place
 // CTA + segment, which no two pieces share; a second, dependent kernel joins them.
 //
-// Measured, 32 query / 8 KV heads (floor by bytes): eight rows that share 32 K tokens of bf16
-// pages and have 60 of their own 32.3 us (20.1), 300 33.6 (21.2; every row by itself 83); 131 K shared 87.6 us
-// (79.6; 274); of 2 K 10.5 us.  Four requests of eight rows, up to 16 K tokens of 4-bit pages 37 us,
-// 16-token ones 39 us (8.1; 72 and 79): 32 rows per key make the instructions the bound there, some 800
-// per warp and 64 tokens.
+// Measured, 32 query / 8 KV heads, in a graph, on inputs that change and exceed L2 (floor by bytes; every row
+// by itself): eight rows that share 32 K tokens of bf16 pages and have 60 of their own 33.3 us (20.1; 82.7), 300
+// 34.1 (21.2; 82.8); 131 K shared 89.1 us (79.6; 274); of 2 K 12.2 us, four rows 10.5.  Four requests of eight rows, up to
+// 16 K tokens of 4-bit pages 39.4 us, 16-token ones 41.2 us (8.1; 74 and 81): 32 rows per key make the instructions
+// the bound there, some 730 per warp and 64 tokens.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -52,7 +54,8 @@ template <bool Q4>
 constexpr int kOStride = Q4 ? 132 : 136;  // padded row of outputs (floats), against bank conflicts
 template <bool Q4>
 constexpr int kStageBytes = Q4 ? kQ4Slot : 2 * kTile;
-// Measured for 4 bits, four requests of 16 K (3, 4, 5, 6 stages) 43.7, 37.8, 37.4, 37.6 us, 131 K 76.8, 77.4, 78.1, 78.8.
+// Measured for 4 bits (3, 4, 5, 6 stages): four requests of 16 K, 64-token pages 41.9, 39.5, 40.3, 40.8 us, 16-token ones
+// 42.3, 41.2, 41.6, 42.1; 131 K 77.3, 77.5, 78.7, 79.5; one request of 32 K 28.8, 29.2, 29.8, 30.4.
 template <bool Q4>
 constexpr int kStages = Q4 ? 4 : 3;
 template <bool Q4>
@@ -926,9 +929,9 @@ cudaError_t launch(const GroupArgs& a, const CUtensorMap& tk, const CUtensorMap&
 int group_attend_ctas_per_sm(bool q4) { return q4 ? kCtas<true> : kCtas<false>; }
 
 // Warps per result: few results take their pieces side by side, many need few warps each.
-// Measured, the whole call in us (8, 4, 2, 1 warps): 256 results of 2 K 10.5, 10.3, 11.4, 12.6, of 32 K
-// in 4 bits 27.9, 28.7, 30.8, 35.4; 512 of 32 K 47.0, 44.0, 45.6, 47.1; 1024 of 16 K, 4-bit, 46.6, 41.1, 38.8,
-// 41.5; 2048 of 3 K 62.5, 50.8, 47.3, 44.5.
+// Measured, the whole call in us (8, 4, 2, 1 warps): 256 results of 2 K 12.2, 11.9, 13.1, 14.1, of 32 K
+// in 4 bits 29.3, 30.4, 32.6, 36.9; 512 of 32 K 50.5, 47.2, 48.4, 50.0; 1024 of 16 K, 4-bit, 49.2, 43.6, 41.2,
+// 44.5; 2048 of 3 K 62.9, 51.0, 47.6, 44.8.
 static int join_warps(const GroupArgs& a) {
   const long long results = (long long)a.batch * a.num_kv_heads * a.group, n = a.n_ctas;
   return results <= n ? kJoinWarps : results <= 2 * n ? 4 : results <= 4 * n ? 2 : 1;

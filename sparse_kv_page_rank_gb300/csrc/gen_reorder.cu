@@ -13,7 +13,7 @@
 //
 // What bounds it: the copied pages' bytes, for few the latency of the two launches.
 // Measured (floor by bytes), in a graph: 16 requests of 8 beams, four layers of bf16 pages 13.1 us
-// (6.4); 32 of 8, 16 layers 67 us (51.6); one request of 4 beams, a table of 2048 columns 3.9 us.
+// (6.4); 32 of 8, 16 layers 69.6 us (53.1); one request of 4 beams, a table of 2048 columns 3.5 us.
 #include <algorithm>
 
 #include "common.cuh"

@@ -19,10 +19,10 @@
 // sorted lists, `keep` times.
 //
 // What bounds it: the logits' bytes and one exponential each; for few rows the latency of
-// the two launches.  Measured (floor by bytes), in a graph: 32 requests of 4 beams, 128,256
-// bf16 logits 16.3 us (4.3); 24 of 8, 100,003 float32 logits, 16 kept, 24.4 us (11.3); one request of 4
-// beams, 32,000 logits 7.1 us.  One kernel, whose last CTA of a request merges, took 17.9, 26.2
-// and 8.7.
+// the two launches.  Measured (floor by bytes), in a graph, on inputs that change and
+// exceed L2: 32 requests of 4 beams, 128,256 bf16 logits, some ended, 16.5 us (4.3); 24 of 8, 100,003
+// float32 logits, 16 kept, 24.4 us (11.3); one request of 4 beams, 32,000 logits 7.1 us.  One kernel, whose
+// last CTA of a request merges, took 17.9, 26.2 and 8.7 where two took 16.5, 25.1 and 7.2.
 #include "common.cuh"
 #include "gen.h"
 
