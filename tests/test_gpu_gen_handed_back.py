@@ -56,7 +56,7 @@ def test_several_requests_are_refused():
 
 
 def test_back_pointers_are_copied_to_be_kept():
-    """What README's loop does: the object's own outputs are the next call's too, copies are not."""
+    """As in the module's example: the object's own outputs are the next call's too, copies are not."""
     W, V, steps = 3, 400, 5
     beams = LocksBeams(width=W)
     scores = torch.zeros(2, W, device="cuda")
